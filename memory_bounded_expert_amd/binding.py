@@ -10,6 +10,7 @@ not built.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -21,6 +22,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoebound.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 HEADERS = (os.path.join(INCLUDE, "moebound.h"), os.path.join(INCLUDE, "cce.h"))
+# the operators around the layer
+OPERATOR_HEADERS = (os.path.join(INCLUDE, "route.h"),)
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, 1, 2, 3, 4
 STAGES = {"router": 0, "topk": 1, "plan": 2, "gather": 3, "gemm_up": 4, "gemm_down": 5,
@@ -28,6 +31,7 @@ STAGES = {"router": 0, "topk": 1, "plan": 2, "gather": 3, "gemm_up": 4, "gemm_do
 BSTAGES = {"zero": 0, "transpose": 1, "plan": 2, "recompute": 3, "dh": 4, "wgrad_down": 5,
            "wgrad_gate_up": 6, "dx": 7, "combine_bwd": 8, "dwr": 9}
 MOE_F32, MOE_BF16 = 0, 1
+ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 CCE_STAGES = {"logits": 0, "fold": 1, "grad": 2, "dx": 3, "dw": 4}
 
 _c = ctypes
@@ -63,6 +67,15 @@ class CcePlan(_c.Structure):
         ("H", _c.c_int32), ("v_chunk", _c.c_int32), ("S", _c.c_int32), ("reserved0", _c.c_int32),
         ("strip_bound_bytes", _c.c_int64), ("unchunked_logit_bytes", _c.c_int64),
         ("fwd_workspace_bytes", _c.c_int64), ("bwd_workspace_bytes", _c.c_int64),
+    ]
+
+
+class RoutePlan(_c.Structure):
+    _fields_ = [
+        ("magic", _c.c_uint32), ("score", _c.c_int32), ("N", _c.c_int64), ("E", _c.c_int32),
+        ("k", _c.c_int32), ("n_group", _c.c_int32), ("topk_group", _c.c_int32),
+        ("group_top", _c.c_int32), ("renorm", _c.c_int32), ("scale", _c.c_float),
+        ("reserved0", _c.c_int32),
     ]
 
 
@@ -120,16 +133,37 @@ def lib() -> ctypes.CDLL:
     L.cce_debug_stage.restype = _c.c_int
     L.cce_debug_stage.argtypes = [_c.POINTER(CcePlan), _c.c_int32, _c.c_int32] + [_vp] * 8 + [
         _vp, _c.c_size_t, _vp]
+    L.route_plan.restype = _c.c_int
+    L.route_plan.argtypes = [_c.c_int64] + [_c.c_int32] * 7 + [_c.c_float, _c.POINTER(RoutePlan)]
+    L.route_forward.restype = _c.c_int
+    L.route_forward.argtypes = [_c.POINTER(RoutePlan)] + [_vp] * 5
+    L.route_backward.restype = _c.c_int
+    L.route_backward.argtypes = [_c.POINTER(RoutePlan)] + [_vp] * 5
+    L.moe_routed_forward.restype = _c.c_int
+    L.moe_routed_forward.argtypes = [_c.POINTER(MoePlan)] + [_vp] * 8 + [_c.c_size_t, _vp,
+                                                                       _c.POINTER(MoeStats)]
+    L.moe_routed_backward.restype = _c.c_int
+    L.moe_routed_backward.argtypes = [_c.POINTER(MoePlan)] + [_vp] * 13 + [_c.c_size_t, _vp,
+                                                                         _c.POINTER(MoeStats)]
     _LIB = L
     return L
 
 
 def declared_functions() -> list:
     """Function names declared in include/moebound.h and include/cce.h."""
+    return _declared(HEADERS, "moe|cce")
+
+
+def declared_operators() -> list:
+    """Function names declared in the headers of the operators around the layer."""
+    return _declared(OPERATOR_HEADERS, "moe|route")
+
+
+def _declared(headers, prefixes) -> list:
     names = set()
-    for h in HEADERS:
+    for h in headers:
         text = re.sub(r"/\*.*?\*/", "", open(h).read(), flags=re.S)
-        names |= set(re.findall(r"\b((?:moe|cce)_[a-z_]+)\s*\(", text))
+        names |= set(re.findall(r"\b((?:%s)_[a-z_]+)\s*\(" % prefixes, text))
     return sorted(names)
 
 
@@ -175,6 +209,22 @@ def _stream(device, stream):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return _vp(stream.cuda_stream)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device, stream):
+    """Context in which a call on ``device`` and ``stream`` (None: the device's
+    current stream) allocates and launches: outputs and workspaces then belong
+    to the stream that writes them, whatever device or stream is current."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, not on {device}")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream on {stream.device}, tensors on {device}")
+        return torch.cuda.stream(stream)
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def moe_plan_chunks(N: int, H: int, F: int, E: int, k: int, c: int, K_max: int,
@@ -416,3 +466,107 @@ def cce_debug_stage(plan: CcePlan, stage: str, strip: int, X, W, targets, loss, 
                                  _ptr(targets), _ptr(loss), _ptr(lse), _ptr(dloss), _ptr(dX),
                                  _ptr(dW), _ptr(ws), ws.numel(), _stream(X.device, stream)),
            "cce_debug_stage")
+
+
+# ---- routing by scores, and the layer under a given routing
+
+
+def route_plan(N: int, E: int, k: int, score: str = "softmax", n_group: int = 1,
+               topk_group: int = 1, group_top: int = 2, renorm: bool = True,
+               scale: float = 1.0) -> RoutePlan:
+    """Routing of N tokens to k of E experts; score "softmax" or "sigmoid"."""
+    if score not in ROUTE_SCORES:
+        raise ValueError(f"score {score!r} is not one of {sorted(ROUTE_SCORES)}")
+    plan = RoutePlan()
+    _check(lib().route_plan(N, E, k, ROUTE_SCORES[score], n_group, topk_group, group_top,
+                            int(renorm), scale, ctypes.byref(plan)), "route_plan")
+    return plan
+
+
+def route_forward(plan: RoutePlan, logits, bias=None, topk_idx=None, gates=None, stream=None):
+    """Returns (topk_idx [N, k] int32, gates [N, k] fp32)."""
+    dev = logits.device
+    N, E, k = plan.N, plan.E, plan.k
+    _expect(logits, "logits", (N, E), torch.float32, dev)
+    if bias is not None:
+        _expect(bias, "bias", (E,), torch.float32, dev)
+    with _on(dev, stream):
+        topk_idx = torch.empty((N, k), dtype=torch.int32, device=dev) if topk_idx is None else topk_idx
+        gates = torch.empty((N, k), dtype=torch.float32, device=dev) if gates is None else gates
+        _expect(topk_idx, "topk_idx", (N, k), torch.int32, dev)
+        _expect(gates, "gates", (N, k), torch.float32, dev)
+        _check(lib().route_forward(ctypes.byref(plan), _ptr(logits), _ptr(bias), _ptr(topk_idx),
+                                   _ptr(gates), _stream(dev, None)), "route_forward")
+    return topk_idx, gates
+
+
+def route_backward(plan: RoutePlan, logits, topk_idx, dgates, dlogits=None, stream=None):
+    """Returns dlogits [N, E] fp32."""
+    dev = logits.device
+    N, E, k = plan.N, plan.E, plan.k
+    _expect(logits, "logits", (N, E), torch.float32, dev)
+    _expect(topk_idx, "topk_idx", (N, k), torch.int32, dev)
+    _expect(dgates, "dgates", (N, k), torch.float32, dev)
+    with _on(dev, stream):
+        dlogits = torch.empty((N, E), dtype=torch.float32, device=dev) if dlogits is None else dlogits
+        _expect(dlogits, "dlogits", (N, E), torch.float32, dev)
+        _check(lib().route_backward(ctypes.byref(plan), _ptr(logits), _ptr(topk_idx), _ptr(dgates),
+                                    _ptr(dlogits), _stream(dev, None)), "route_backward")
+    return dlogits
+
+
+def moe_routed_forward(plan: MoePlan, X, W_gate, W_up, W_down, topk_idx, gates, Y=None, ws=None,
+                       stream=None):
+    """The layer's experts under a given routing.  Returns (Y, stats dict)."""
+    dev = X.device
+    dt = torch_dtype(plan.dtype)
+    N, H, F, E, k = plan.N, plan.H, plan.F, plan.E, plan.k
+    for t, n, s, d in ((X, "X", (N, H), dt), (W_gate, "W_gate", (E, H, F), dt),
+                       (W_up, "W_up", (E, H, F), dt), (W_down, "W_down", (E, F, H), dt),
+                       (topk_idx, "topk_idx", (N, k), torch.int32),
+                       (gates, "gates", (N, k), torch.float32)):
+        _expect(t, n, s, d, dev)
+    with _on(dev, stream):
+        Y = torch.empty((N, H), dtype=dt, device=dev) if Y is None else Y
+        _expect(Y, "Y", (N, H), dt, dev)
+        ws = workspace(plan, "fwd", dev) if ws is None else ws
+        st = MoeStats()
+        _check(lib().moe_routed_forward(
+            ctypes.byref(plan), _ptr(X), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(topk_idx),
+            _ptr(gates), _ptr(Y), _ptr(ws), ws.numel(), _stream(dev, None), ctypes.byref(st)),
+            "moe_routed_forward")
+    return Y, st.as_dict()
+
+
+def moe_routed_backward(plan: MoePlan, X, W_gate, W_up, W_down, dY, topk_idx, gates, dX=None,
+                        dW_gate=None, dW_up=None, dW_down=None, dgates=None, ws=None, stream=None):
+    """Returns dict with dX (the experts' share), dW_gate, dW_up, dW_down, dgates, stats."""
+    dev = X.device
+    dt = torch_dtype(plan.dtype)
+    N, H, F, E, k = plan.N, plan.H, plan.F, plan.E, plan.k
+    f32 = torch.float32
+    for t, n, s, d in ((X, "X", (N, H), dt), (W_gate, "W_gate", (E, H, F), dt),
+                       (W_up, "W_up", (E, H, F), dt), (W_down, "W_down", (E, F, H), dt),
+                       (dY, "dY", (N, H), dt), (topk_idx, "topk_idx", (N, k), torch.int32),
+                       (gates, "gates", (N, k), f32)):
+        _expect(t, n, s, d, dev)
+    with _on(dev, stream):
+        new = lambda shape, d=f32: torch.empty(shape, dtype=d, device=dev)
+        dX = new((N, H), dt) if dX is None else dX
+        dW_gate = new((E, H, F)) if dW_gate is None else dW_gate
+        dW_up = new((E, H, F)) if dW_up is None else dW_up
+        dW_down = new((E, F, H)) if dW_down is None else dW_down
+        dgates = new((N, k)) if dgates is None else dgates
+        for t, n, s, d in ((dX, "dX", (N, H), dt), (dW_gate, "dW_gate", (E, H, F), f32),
+                           (dW_up, "dW_up", (E, H, F), f32), (dW_down, "dW_down", (E, F, H), f32),
+                           (dgates, "dgates", (N, k), f32)):
+            _expect(t, n, s, d, dev)
+        ws = workspace(plan, "bwd", dev) if ws is None else ws
+        st = MoeStats()
+        _check(lib().moe_routed_backward(
+            ctypes.byref(plan), _ptr(X), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(dY),
+            _ptr(topk_idx), _ptr(gates), _ptr(dX), _ptr(dW_gate), _ptr(dW_up), _ptr(dW_down),
+            _ptr(dgates), _ptr(ws), ws.numel(), _stream(dev, None), ctypes.byref(st)),
+            "moe_routed_backward")
+    return dict(dX=dX, dW_gate=dW_gate, dW_up=dW_up, dW_down=dW_down, dgates=dgates,
+                stats=st.as_dict())

@@ -16,6 +16,7 @@
 #include <cstring>
 
 #include "moe_internal.h"
+#include "route.h"
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
 
@@ -227,24 +228,13 @@ int check_forward_args(const moe_plan_t* plan, const void* X, const void* W_r,
   return MOE_OK;
 }
 
-int forward_impl(const moe_plan_t& P, const void* X, const void* W_r, const float* router_bias,
-                 const void* W_gate, const void* W_up, const void* W_down, void* Y,
-                 int32_t* topk_idx, float* gates, float* logits, void* workspace,
-                 hipStream_t st, moe_stats_t* stats) {
-  if (P.N == 0) {
-    fill_stats(stats, P, 0, 0, 0);
-    return MOE_OK;
-  }
-  const Layout L = make_layout(P, Pass::Forward, logits == nullptr, false);
-  char* ws = (char*)workspace;
-  float* lg = logits ? logits : (float*)(ws + L.logits);
-  int launches = 0;
-  (void)hipGetLastError();
-
-  const int rs = router_splits(P);
-  float* rparts = rs > 1 ? (float*)(ws + L.rparts) : nullptr;
-  MOE_CHECK(gemm_router(P.dtype, X, W_r, router_bias, lg, P.N, P.H, P.E, st, rparts, rs));
-  MOE_CHECK(launch_topk(lg, P.N, P.E, P.k, topk_idx, gates, st, rparts, rs, router_bias));
+// The forward call from the chunk plan on: the permutations of the given
+// routing, then the chunks; the workspace is laid out by L and `launches`
+// kernels are enqueued already.
+static int experts_forward(const moe_plan_t& P, const Layout& L, const void* X, const void* W_gate,
+                           const void* W_up, const void* W_down, const int32_t* topk_idx,
+                           const float* gates, void* Y, char* ws, hipStream_t st, int launches,
+                           moe_stats_t* stats) {
   const PlanBuffers pb = plan_buffers(ws, L, nullptr, nullptr, nullptr);
   if (launch_plan(topk_idx, P.N, P.K, P.k, P.E, pb, st, gates, &launches) != hipSuccess)
     return MOE_EHIP;
@@ -284,6 +274,28 @@ int forward_impl(const moe_plan_t& P, const void* X, const void* W_r, const floa
   return MOE_OK;
 }
 
+int forward_impl(const moe_plan_t& P, const void* X, const void* W_r, const float* router_bias,
+                 const void* W_gate, const void* W_up, const void* W_down, void* Y,
+                 int32_t* topk_idx, float* gates, float* logits, void* workspace,
+                 hipStream_t st, moe_stats_t* stats) {
+  if (P.N == 0) {
+    fill_stats(stats, P, 0, 0, 0);
+    return MOE_OK;
+  }
+  const Layout L = make_layout(P, Pass::Forward, logits == nullptr, false);
+  char* ws = (char*)workspace;
+  float* lg = logits ? logits : (float*)(ws + L.logits);
+  int launches = 0;
+  (void)hipGetLastError();
+
+  const int rs = router_splits(P);
+  float* rparts = rs > 1 ? (float*)(ws + L.rparts) : nullptr;
+  MOE_CHECK(gemm_router(P.dtype, X, W_r, router_bias, lg, P.N, P.H, P.E, st, rparts, rs));
+  MOE_CHECK(launch_topk(lg, P.N, P.E, P.k, topk_idx, gates, st, rparts, rs, router_bias));
+  return experts_forward(P, L, X, W_gate, W_up, W_down, topk_idx, gates, Y, ws, st, launches,
+                         stats);
+}
+
 }  // namespace moe
 
 MOE_API int moe_plan_set_flags(moe_plan_t* plan, int32_t flags) {
@@ -311,10 +323,31 @@ MOE_API int moe_bounded_forward(const moe_plan_t* plan, const void* X, const voi
                       workspace, (hipStream_t)stream, stats);
 }
 
+MOE_API int moe_routed_forward(const moe_plan_t* plan, const void* X, const void* W_gate,
+                               const void* W_up, const void* W_down, const int32_t* topk_idx,
+                               const float* gates, void* Y, void* workspace,
+                               size_t workspace_bytes, void* stream, moe_stats_t* stats) {
+  if (int s = check_forward_args(plan, X, X, W_gate, W_up, W_down, Y, topk_idx, gates)) return s;
+  const moe_plan_t& P = *plan;
+  if (P.N == 0) {
+    fill_stats(stats, P, 0, 0, 0);
+    return MOE_OK;
+  }
+  if (!workspace) return MOE_EINVAL;
+  if ((uintptr_t)workspace % 256) return MOE_EINVAL;
+  if (workspace_bytes < (size_t)P.fwd_workspace_bytes) return MOE_EWORKSPACE;
+  (void)hipGetLastError();
+  const Layout L = make_layout(P, Pass::Forward, false, false);
+  return experts_forward(P, L, X, W_gate, W_up, W_down, topk_idx, gates, Y, (char*)workspace,
+                         (hipStream_t)stream, 0, stats);
+}
+
 namespace moe {
 namespace {
 
-// Everything one backward call's kernels read and write, resolved once.
+// Everything one backward call's kernels read and write, resolved once.  W_r,
+// dlogits and dW_r are null in a call under a given routing, which has no
+// router stages.
 struct BwdCall {
   const moe_plan_t* P;
   Layout L;
@@ -422,7 +455,7 @@ hipError_t bwd_stage(const BwdCall& c, int stage, int i, int* launches) {
     return err;
   }
   if (stage == MOE_BSTAGE_TRANSPOSE) {
-    run(launch_transpose(P.dtype, c.W_r, c.wrt, P.H, P.E, st));
+    if (c.W_r) run(launch_transpose(P.dtype, c.W_r, c.wrt, P.H, P.E, st));
     return err;
   }
   if (stage == kBStageExactZero) {
@@ -538,7 +571,7 @@ hipError_t bwd_stage(const BwdCall& c, int stage, int i, int* launches) {
       run(gemm_dx(P.dtype, rg, c.a, c.u, c.W_gate, c.W_up, c.o, P.H, P.F, st));
       break;
     case MOE_BSTAGE_COMBINE_BWD:
-      run(launch_combine_bwd(P.dtype, c.o, c.wrt, c.topk_idx, c.pb.pos, c.gates, c.dg, c.dX,
+      run(launch_combine_bwd(P.dtype, c.o, c.W_r ? c.wrt : nullptr, c.topk_idx, c.pb.pos, c.gates, c.dg, c.dX,
                              c.dlogits, P.N, P.K, i, g.n, P.k, P.E, P.H, st,
                              c.fused_swiglu ? c.dgp : nullptr,
                              c.fused_swiglu ? dh_ntiles(rg, P.F) : 0, (int64_t)P.k * P.c_eff));
@@ -554,28 +587,11 @@ hipError_t bwd_stage(const BwdCall& c, int stage, int i, int* launches) {
   return err;
 }
 
-}  // namespace
-}  // namespace moe
-
-MOE_API int moe_bounded_backward(const moe_plan_t* plan, const void* X, const void* W_r,
-                                 const void* W_gate, const void* W_up, const void* W_down,
-                                 const void* dY, const int32_t* topk_idx, const float* gates,
-                                 void* dX, float* dW_gate, float* dW_up, float* dW_down,
-                                 float* dlogits, float* dgates, float* dW_r, void* workspace,
-                                 size_t workspace_bytes, void* stream, moe_stats_t* stats) {
-  if (!plan_ok(plan)) return MOE_EINVAL;
-  const moe_plan_t& P = *plan;
-  if (!dW_gate || !dW_up || !dW_down) return MOE_EINVAL;
-  if (P.N > 0 && (!X || !W_r || !W_gate || !W_up || !W_down || !dY || !topk_idx || !gates ||
-                  !dX || !dlogits || !workspace))
-    return MOE_EINVAL;
-  if (P.N > 0 && (uintptr_t)workspace % 256) return MOE_EINVAL;
-  if (workspace_bytes < (size_t)P.bwd_workspace_bytes) return MOE_EWORKSPACE;
+// The whole backward call: zeroing, the permutations, then the chunks.
+int run_backward(const BwdCall& c, moe_stats_t* stats) {
+  const moe_plan_t& P = *c.P;
   int launches = 0;
   (void)hipGetLastError();
-  const BwdCall c = bwd_call(P, X, W_r, W_gate, W_up, W_down, dY, topk_idx, gates, dX, dW_gate,
-                             dW_up, dW_down, dlogits, dgates, dW_r, workspace,
-                             (hipStream_t)stream);
   if (bwd_stage(c, MOE_BSTAGE_ZERO, 0, &launches) != hipSuccess) return MOE_EHIP;
   if (P.N == 0) {
     fill_stats(stats, P, launches, 0, 0);
@@ -600,6 +616,49 @@ MOE_API int moe_bounded_backward(const moe_plan_t* plan, const void* X, const vo
              (size_t)P.k * P.c_eff * P.F * (3 * elem_bytes(P.dtype) + (c.fused_swiglu ? 0 : 4)),
              c.fused ? 1 : 2);
   return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+MOE_API int moe_bounded_backward(const moe_plan_t* plan, const void* X, const void* W_r,
+                                 const void* W_gate, const void* W_up, const void* W_down,
+                                 const void* dY, const int32_t* topk_idx, const float* gates,
+                                 void* dX, float* dW_gate, float* dW_up, float* dW_down,
+                                 float* dlogits, float* dgates, float* dW_r, void* workspace,
+                                 size_t workspace_bytes, void* stream, moe_stats_t* stats) {
+  if (!plan_ok(plan)) return MOE_EINVAL;
+  const moe_plan_t& P = *plan;
+  if (!dW_gate || !dW_up || !dW_down) return MOE_EINVAL;
+  if (P.N > 0 && (!X || !W_r || !W_gate || !W_up || !W_down || !dY || !topk_idx || !gates ||
+                  !dX || !dlogits || !workspace))
+    return MOE_EINVAL;
+  if (P.N > 0 && (uintptr_t)workspace % 256) return MOE_EINVAL;
+  if (workspace_bytes < (size_t)P.bwd_workspace_bytes) return MOE_EWORKSPACE;
+  const BwdCall c = bwd_call(P, X, W_r, W_gate, W_up, W_down, dY, topk_idx, gates, dX, dW_gate,
+                             dW_up, dW_down, dlogits, dgates, dW_r, workspace,
+                             (hipStream_t)stream);
+  return run_backward(c, stats);
+}
+
+MOE_API int moe_routed_backward(const moe_plan_t* plan, const void* X, const void* W_gate,
+                                const void* W_up, const void* W_down, const void* dY,
+                                const int32_t* topk_idx, const float* gates, void* dX,
+                                float* dW_gate, float* dW_up, float* dW_down, float* dgates,
+                                void* workspace, size_t workspace_bytes, void* stream,
+                                moe_stats_t* stats) {
+  if (!plan_ok(plan)) return MOE_EINVAL;
+  const moe_plan_t& P = *plan;
+  if (!dW_gate || !dW_up || !dW_down) return MOE_EINVAL;
+  if (P.N > 0 && (!X || !W_gate || !W_up || !W_down || !dY || !topk_idx || !gates || !dX ||
+                  !dgates || !workspace))
+    return MOE_EINVAL;
+  if (P.N > 0 && (uintptr_t)workspace % 256) return MOE_EINVAL;
+  if (workspace_bytes < (size_t)P.bwd_workspace_bytes) return MOE_EWORKSPACE;
+  const BwdCall c = bwd_call(P, X, nullptr, W_gate, W_up, W_down, dY, topk_idx, gates, dX, dW_gate,
+                             dW_up, dW_down, nullptr, dgates, nullptr, workspace,
+                             (hipStream_t)stream);
+  return run_backward(c, stats);
 }
 
 MOE_API int moe_debug_stage_bwd(const moe_plan_t* plan, int32_t stage, int32_t chunk,

@@ -185,6 +185,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_bwd_kernel(
 //   experts and 0 elsewhere,
 //   dX[t] = sum_s dXp[pos[t,s]] + sum_s dl_s W_r^T[S_t[s]]  (fp32, slot order,
 //   one rounding).
+// Without WrT (a routing given from outside) there is no router: dlogits is
+// not written and dX holds the experts' rows only.
 // With dgp set, slot s's dgate is first summed over the nparts shares
 // dgp[nt][pos[t,s]] (nt ascending) and stored to dgates.
 template <typename T>
@@ -228,11 +230,13 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(
       for (int s = 0; s < k; ++s) dl[s] = gs[s] * (dgs[s] - sdot);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kThreads) {
-      float v = 0.f;
-      for (int s = 0; s < k; ++s)
-        if (ex[s] == e) v = dl[s];
-      dlogits[t * E + e] = v;
+    if (WrT) {
+      for (int e = threadIdx.x; e < E; e += kThreads) {
+        float v = 0.f;
+        for (int s = 0; s < k; ++s)
+          if (ex[s] == e) v = dl[s];
+        dlogits[t * E + e] = v;
+      }
     }
     for (int c = threadIdx.x; c < cpr; c += kThreads) {
       float acc[EPC];
@@ -244,7 +248,7 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(
 #pragma unroll
         for (int q = 0; q < EPC; ++q) acc[q] += v[q];
       }
-      for (int s = 0; s < k; ++s) {
+      for (int s = 0; WrT && s < k; ++s) {
         float w[EPC];
         unpack16(reinterpret_cast<const u32x4_t*>(WrT + (int64_t)ex[s] * H)[c], w, T());
 #pragma unroll

@@ -39,3 +39,10 @@ from .ce_oracle import (  # noqa: F401,E402
     ce_backward_tokens,
     ce_backward_tokens_rows,
 )
+
+from .route_oracle import (  # noqa: F401,E402
+    route_log_scores,
+    route_select,
+    route_gates,
+    route_backward,
+)

@@ -1,0 +1,137 @@
+"""The operators around the layer on the host, without a GPU: exports, struct
+layouts, plans, and argument errors before anything is enqueued."""
+
+import ctypes
+import os
+import re
+import subprocess
+import tempfile
+
+import pytest
+import torch
+
+from memory_bounded_expert_amd import binding as B
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+pytestmark = pytest.mark.skipif(not os.path.exists(B.LIB_PATH),
+                                reason="libmoebound.so not built (run __graft_entry__.build())")
+
+FAKE = ctypes.c_void_p(0x100000)  # never dereferenced: every check below fails first
+PLANS = {"route_plan_t": B.RoutePlan}
+
+
+def test_exports_and_argument_counts():
+    L = B.lib()
+    names = B.declared_operators()
+    assert {"route_plan", "route_forward", "route_backward", "moe_routed_forward",
+            "moe_routed_backward"} <= set(names)
+    for h in B.OPERATOR_HEADERS:
+        text = re.sub(r"/\*.*?\*/", "", open(h).read(), flags=re.S)
+        for m in re.finditer(r"\bint ([a-z]+_[a-z_]+)\s*\(([^;{]*?)\)\s*;", text, flags=re.S):
+            name, params = m.group(1), m.group(2).strip()
+            assert name in names
+            assert len(getattr(L, name).argtypes) == params.count(",") + 1, name
+
+
+@pytest.mark.parametrize("struct", sorted(PLANS))
+def test_struct_layout_matches_c(struct):
+    cls = PLANS[struct]
+    src = ["#include <stdio.h>", "#include <stddef.h>"]
+    src += ['#include "%s"' % os.path.basename(h) for h in B.OPERATOR_HEADERS]
+    src += ["int main(void) {", 'printf("size %%zu\\n", sizeof(%s));' % struct]
+    src += ['printf("%s %%zu\\n", offsetof(%s, %s));' % (n, struct, n) for n, _ in cls._fields_]
+    src += ["return 0; }"]
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "t.c"), os.path.join(d, "t")
+        open(c, "w").write("\n".join(src) + "\n")
+        subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"),
+                        c, "-o", exe], check=True)
+        got = dict(l.split() for l in subprocess.run([exe], capture_output=True, text=True,
+                                                     check=True).stdout.splitlines())
+    assert int(got.pop("size")) == ctypes.sizeof(cls)
+    for n, off in got.items():
+        assert int(off) == getattr(cls, n).offset, n
+
+
+# ---- routing
+
+ROUTE_OK = dict(N=10, E=64, k=8, score=0, n_group=8, topk_group=4, group_top=2, renorm=1, scale=1.0)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(N=-1), B.MOE_EINVAL), (dict(E=0, n_group=1), B.MOE_EINVAL), (dict(k=0), B.MOE_EINVAL),
+    (dict(k=65), B.MOE_EINVAL), (dict(score=2), B.MOE_EINVAL), (dict(n_group=0), B.MOE_EINVAL),
+    (dict(n_group=7), B.MOE_EINVAL), (dict(topk_group=0), B.MOE_EINVAL),
+    (dict(topk_group=9), B.MOE_EINVAL), (dict(k=9, topk_group=1), B.MOE_EINVAL),
+    (dict(group_top=0), B.MOE_EINVAL), (dict(group_top=3), B.MOE_EINVAL),
+    (dict(renorm=2), B.MOE_EINVAL), (dict(scale=0.0), B.MOE_EINVAL),
+    (dict(scale=-1.0), B.MOE_EINVAL), (dict(scale=float("inf")), B.MOE_EINVAL),
+    (dict(scale=float("nan")), B.MOE_EINVAL),
+    (dict(E=1032, n_group=1, topk_group=1), B.MOE_EUNSUPPORTED),
+    (dict(E=128, k=65, n_group=1, topk_group=1), B.MOE_EUNSUPPORTED),
+    (dict(E=130, k=2, n_group=65, topk_group=1), B.MOE_EUNSUPPORTED),
+    (dict(N=2**31), B.MOE_EUNSUPPORTED),
+])
+def test_route_plan_errors(change, status):
+    a = {**ROUTE_OK, **change}
+    assert B.lib().route_plan(*a.values(), ctypes.byref(B.RoutePlan())) == status
+
+
+def test_route_argument_errors():
+    L, ref = B.lib(), ctypes.byref
+    assert L.route_plan(*ROUTE_OK.values(), None) == B.MOE_EINVAL
+    with pytest.raises(ValueError):
+        B.route_plan(4, 8, 2, score="cosine")
+    bad, p = B.RoutePlan(), B.route_plan(4, 8, 2)
+    assert L.route_forward(ref(bad), FAKE, None, FAKE, FAKE, None) == B.MOE_EINVAL
+    assert L.route_backward(ref(bad), FAKE, FAKE, FAKE, FAKE, None) == B.MOE_EINVAL
+    for i in (0, 2, 3):
+        args = [FAKE, None, FAKE, FAKE]
+        args[i] = None
+        assert L.route_forward(ref(p), *args, None) == B.MOE_EINVAL
+    for i in range(4):
+        args = [FAKE] * 4
+        args[i] = None
+        assert L.route_backward(ref(p), *args, None) == B.MOE_EINVAL
+    p0 = B.route_plan(0, 8, 2)
+    assert L.route_forward(ref(p0), *[None] * 5) == B.MOE_OK
+    assert L.route_backward(ref(p0), *[None] * 5) == B.MOE_OK
+
+
+def test_routed_layer_argument_errors():
+    L, ref = B.lib(), ctypes.byref
+    p = B.moe_plan_chunks(256, 64, 128, 8, 2, 64, 8, B.MOE_F32)
+    fwd, bwd = [FAKE] * 7, [FAKE] * 12
+    assert L.moe_routed_forward(ref(B.MoePlan()), *fwd, FAKE, 1 << 30, None, None) == B.MOE_EINVAL
+    for i in range(7):
+        args = list(fwd)
+        args[i] = None
+        assert L.moe_routed_forward(ref(p), *args, FAKE, 1 << 30, None, None) == B.MOE_EINVAL
+    for i in range(12):
+        args = list(bwd)
+        args[i] = None
+        assert L.moe_routed_backward(ref(p), *args, FAKE, 1 << 30, None, None) == B.MOE_EINVAL
+    off = ctypes.c_void_p(0x100010)
+    assert L.moe_routed_forward(ref(p), *fwd, off, 1 << 30, None, None) == B.MOE_EINVAL
+    assert L.moe_routed_backward(ref(p), *bwd, off, 1 << 30, None, None) == B.MOE_EINVAL
+    assert L.moe_routed_forward(ref(p), *fwd, FAKE, p.fwd_workspace_bytes - 1, None, None) == B.MOE_EWORKSPACE
+    assert L.moe_routed_backward(ref(p), *bwd, FAKE, p.bwd_workspace_bytes - 1, None, None) == B.MOE_EWORKSPACE
+    p0 = B.moe_plan_chunks(0, 64, 64, 8, 2, 4, 4, B.MOE_F32)
+    st = B.MoeStats()
+    assert L.moe_routed_forward(ref(p0), *[None] * 8, 0, None, ref(st)) == B.MOE_OK
+    assert st.launches == 0
+
+
+def test_binding_refuses_wrong_tensors():
+    p = B.route_plan(4, 8, 2)
+    l = torch.zeros(4, 8)
+    for bad in (l[:3], l.double(), l.t().contiguous().t(), torch.zeros(8, 8)[::2]):
+        with pytest.raises(ValueError):
+            B.route_forward(p, bad)
+    with pytest.raises(ValueError):  # not on a GPU
+        B.route_forward(p, l)
+    with pytest.raises(ValueError):
+        B.route_forward(p, l, torch.zeros(7))
+    with pytest.raises(ValueError):
+        B.route_backward(p, l, torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 2))
