@@ -72,7 +72,7 @@ typedef struct route_plan {
  *   unknown, n_group < 1, E not a multiple of n_group, topk_group outside
  *   [1, n_group], k > topk_group * (E / n_group), group_top not 1 or 2,
  *   renorm not 0 or 1, or scale not a finite number above 0.
- *   MOE_EUNSUPPORTED if E > 1024, k > 64, n_group > 64 or N >= 2^31.
+ *   MOE_EUNSUPPORTED if E > 1024, k > 64, n_group > 64 or N >= 2^26.
  */
 int route_plan(int64_t N, int32_t E, int32_t k, int32_t score, int32_t n_group,
                int32_t topk_group, int32_t group_top, int32_t renorm, float scale,

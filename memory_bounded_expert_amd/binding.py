@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(PKG, "libmoebound.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 HEADERS = (os.path.join(INCLUDE, "moebound.h"), os.path.join(INCLUDE, "cce.h"))
 # the operators around the layer
-OPERATOR_HEADERS = (os.path.join(INCLUDE, "route.h"),)
+OPERATOR_HEADERS = (os.path.join(INCLUDE, "route.h"), os.path.join(INCLUDE, "lnorm.h"))
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, 1, 2, 3, 4
 STAGES = {"router": 0, "topk": 1, "plan": 2, "gather": 3, "gemm_up": 4, "gemm_down": 5,
@@ -76,6 +76,13 @@ class RoutePlan(_c.Structure):
         ("k", _c.c_int32), ("n_group", _c.c_int32), ("topk_group", _c.c_int32),
         ("group_top", _c.c_int32), ("renorm", _c.c_int32), ("scale", _c.c_float),
         ("reserved0", _c.c_int32),
+    ]
+
+
+class LnormPlan(_c.Structure):
+    _fields_ = [
+        ("magic", _c.c_uint32), ("dtype", _c.c_int32), ("N", _c.c_int64), ("H", _c.c_int32),
+        ("eps", _c.c_float), ("bwd_workspace_bytes", _c.c_int64),
     ]
 
 
@@ -145,6 +152,12 @@ def lib() -> ctypes.CDLL:
     L.moe_routed_backward.restype = _c.c_int
     L.moe_routed_backward.argtypes = [_c.POINTER(MoePlan)] + [_vp] * 13 + [_c.c_size_t, _vp,
                                                                          _c.POINTER(MoeStats)]
+    L.lnorm_plan.restype = _c.c_int
+    L.lnorm_plan.argtypes = [_c.c_int64, _c.c_int32, _c.c_int32, _c.c_float, _c.POINTER(LnormPlan)]
+    L.lnorm_forward.restype = _c.c_int
+    L.lnorm_forward.argtypes = [_c.POINTER(LnormPlan)] + [_vp] * 7
+    L.lnorm_backward.restype = _c.c_int
+    L.lnorm_backward.argtypes = [_c.POINTER(LnormPlan)] + [_vp] * 9 + [_c.c_size_t, _vp]
     _LIB = L
     return L
 
@@ -156,7 +169,7 @@ def declared_functions() -> list:
 
 def declared_operators() -> list:
     """Function names declared in the headers of the operators around the layer."""
-    return _declared(OPERATOR_HEADERS, "moe|route")
+    return _declared(OPERATOR_HEADERS, "moe|route|lnorm")
 
 
 def _declared(headers, prefixes) -> list:
@@ -246,7 +259,8 @@ def moe_plan_set_flags(plan: MoePlan, flags: int) -> MoePlan:
 
 
 def workspace(plan, kind: str, device) -> torch.Tensor:
-    """Workspace of a MoePlan ("fwd", "bwd", "debug") or CcePlan ("fwd", "bwd")."""
+    """Workspace of a MoePlan ("fwd", "bwd", "debug"), CcePlan ("fwd", "bwd") or
+    LnormPlan ("bwd")."""
     n = getattr(plan, {"fwd": "fwd_workspace_bytes", "bwd": "bwd_workspace_bytes",
                        "debug": "debug_workspace_bytes"}[kind])
     return torch.empty(max(int(n), 1), dtype=torch.uint8, device=device)
@@ -570,3 +584,58 @@ def moe_routed_backward(plan: MoePlan, X, W_gate, W_up, W_down, dY, topk_idx, ga
             "moe_routed_backward")
     return dict(dX=dX, dW_gate=dW_gate, dW_up=dW_up, dW_down=dW_down, dgates=dgates,
                 stats=st.as_dict())
+
+
+# ---- layer norm
+
+
+def lnorm_plan(N: int, H: int, dtype: int = MOE_BF16, eps: float = 1e-5) -> LnormPlan:
+    plan = LnormPlan()
+    _check(lib().lnorm_plan(N, H, dtype, eps, ctypes.byref(plan)), "lnorm_plan")
+    return plan
+
+
+def lnorm_forward(plan: LnormPlan, X, gamma, beta=None, Y=None, mean=None, rstd=None, stream=None):
+    """Returns (Y [N, H], mean [N], rstd [N])."""
+    dev = X.device
+    dt, f32 = torch_dtype(plan.dtype), torch.float32
+    N, H = plan.N, plan.H
+    _expect(X, "X", (N, H), dt, dev)
+    _expect(gamma, "gamma", (H,), f32, dev)
+    if beta is not None:
+        _expect(beta, "beta", (H,), f32, dev)
+    with _on(dev, stream):
+        Y = torch.empty((N, H), dtype=dt, device=dev) if Y is None else Y
+        mean = torch.empty(N, dtype=f32, device=dev) if mean is None else mean
+        rstd = torch.empty(N, dtype=f32, device=dev) if rstd is None else rstd
+        _expect(Y, "Y", (N, H), dt, dev)
+        _expect(mean, "mean", (N,), f32, dev)
+        _expect(rstd, "rstd", (N,), f32, dev)
+        _check(lib().lnorm_forward(ctypes.byref(plan), _ptr(X), _ptr(gamma), _ptr(beta), _ptr(Y),
+                                   _ptr(mean), _ptr(rstd), _stream(dev, None)), "lnorm_forward")
+    return Y, mean, rstd
+
+
+def lnorm_backward(plan: LnormPlan, X, gamma, dY, mean, rstd, dX=None, dgamma=None, dbeta=None,
+                   want_dbeta=True, ws=None, stream=None):
+    """Returns (dX [N, H], dgamma [H], dbeta [H] or None)."""
+    dev = X.device
+    dt, f32 = torch_dtype(plan.dtype), torch.float32
+    N, H = plan.N, plan.H
+    for t, n, s, d in ((X, "X", (N, H), dt), (gamma, "gamma", (H,), f32), (dY, "dY", (N, H), dt),
+                       (mean, "mean", (N,), f32), (rstd, "rstd", (N,), f32)):
+        _expect(t, n, s, d, dev)
+    with _on(dev, stream):
+        dX = torch.empty((N, H), dtype=dt, device=dev) if dX is None else dX
+        dgamma = torch.empty(H, dtype=f32, device=dev) if dgamma is None else dgamma
+        if dbeta is None and want_dbeta:
+            dbeta = torch.empty(H, dtype=f32, device=dev)
+        _expect(dX, "dX", (N, H), dt, dev)
+        _expect(dgamma, "dgamma", (H,), f32, dev)
+        if dbeta is not None:
+            _expect(dbeta, "dbeta", (H,), f32, dev)
+        ws = workspace(plan, "bwd", dev) if ws is None else ws
+        _check(lib().lnorm_backward(ctypes.byref(plan), _ptr(X), _ptr(gamma), _ptr(dY), _ptr(mean),
+                                    _ptr(rstd), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws),
+                                    ws.numel(), _stream(dev, None)), "lnorm_backward")
+    return dX, dgamma, dbeta

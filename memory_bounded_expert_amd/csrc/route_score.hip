@@ -255,7 +255,7 @@ MOE_API int route_plan(int64_t N, int32_t E, int32_t k, int32_t score, int32_t n
   if ((int64_t)k > (int64_t)topk_group * (E / n_group)) return MOE_EINVAL;
   if ((group_top != 1 && group_top != 2) || (renorm != 0 && renorm != 1)) return MOE_EINVAL;
   if (!(scale > 0.f) || !std::isfinite(scale)) return MOE_EINVAL;
-  if (E > kRouteMaxE || k > kRouteMaxK || n_group > kRouteMaxGroups || N >= ((int64_t)1 << 31))
+  if (E > kRouteMaxE || k > kRouteMaxK || n_group > kRouteMaxGroups || N >= ((int64_t)1 << 26))
     return MOE_EUNSUPPORTED;
   route_plan_t p{};
   p.magic = kRouteMagic;

@@ -18,14 +18,14 @@ pytestmark = pytest.mark.skipif(not os.path.exists(B.LIB_PATH),
                                 reason="libmoebound.so not built (run __graft_entry__.build())")
 
 FAKE = ctypes.c_void_p(0x100000)  # never dereferenced: every check below fails first
-PLANS = {"route_plan_t": B.RoutePlan}
+PLANS = {"route_plan_t": B.RoutePlan, "lnorm_plan_t": B.LnormPlan}
 
 
 def test_exports_and_argument_counts():
     L = B.lib()
     names = B.declared_operators()
     assert {"route_plan", "route_forward", "route_backward", "moe_routed_forward",
-            "moe_routed_backward"} <= set(names)
+            "moe_routed_backward", "lnorm_plan", "lnorm_forward", "lnorm_backward"} <= set(names)
     for h in B.OPERATOR_HEADERS:
         text = re.sub(r"/\*.*?\*/", "", open(h).read(), flags=re.S)
         for m in re.finditer(r"\bint ([a-z]+_[a-z_]+)\s*\(([^;{]*?)\)\s*;", text, flags=re.S):
@@ -71,7 +71,7 @@ ROUTE_OK = dict(N=10, E=64, k=8, score=0, n_group=8, topk_group=4, group_top=2, 
     (dict(E=1032, n_group=1, topk_group=1), B.MOE_EUNSUPPORTED),
     (dict(E=128, k=65, n_group=1, topk_group=1), B.MOE_EUNSUPPORTED),
     (dict(E=130, k=2, n_group=65, topk_group=1), B.MOE_EUNSUPPORTED),
-    (dict(N=2**31), B.MOE_EUNSUPPORTED),
+    (dict(N=2**26), B.MOE_EUNSUPPORTED),
 ])
 def test_route_plan_errors(change, status):
     a = {**ROUTE_OK, **change}
@@ -135,3 +135,49 @@ def test_binding_refuses_wrong_tensors():
         B.route_forward(p, l, torch.zeros(7))
     with pytest.raises(ValueError):
         B.route_backward(p, l, torch.zeros(4, 2, dtype=torch.int64), torch.zeros(4, 2))
+
+
+# ---- layer norm
+
+
+@pytest.mark.parametrize("args,status", [
+    ((-1, 64, 0, 1e-5), B.MOE_EINVAL), ((4, 0, 0, 1e-5), B.MOE_EINVAL), ((4, 64, 2, 1e-5), B.MOE_EINVAL),
+    ((4, 64, 0, 0.0), B.MOE_EINVAL), ((4, 64, 0, float("nan")), B.MOE_EINVAL),
+    ((4, 64, 0, float("inf")), B.MOE_EINVAL), ((4, 65537, 0, 1e-5), B.MOE_EUNSUPPORTED),
+    ((2**31, 64, 0, 1e-5), B.MOE_EUNSUPPORTED),
+])
+def test_lnorm_plan_errors(args, status):
+    assert B.lib().lnorm_plan(*args, ctypes.byref(B.LnormPlan())) == status
+
+
+def test_lnorm_argument_errors():
+    L, ref = B.lib(), ctypes.byref
+    assert L.lnorm_plan(4, 64, 0, 1e-5, None) == B.MOE_EINVAL
+    p, big = B.lnorm_plan(4, 64, B.MOE_F32), 1 << 30
+    assert L.lnorm_forward(ref(B.LnormPlan()), *[FAKE] * 6, None) == B.MOE_EINVAL
+    assert L.lnorm_backward(ref(B.LnormPlan()), *[FAKE] * 9, big, None) == B.MOE_EINVAL
+    for i in (0, 1, 3, 4, 5):
+        args = [FAKE] * 6
+        args[i] = None
+        assert L.lnorm_forward(ref(p), *args, None) == B.MOE_EINVAL
+    for i in (0, 1, 2, 3, 4, 5, 6, 8):
+        args = [FAKE] * 9
+        args[i] = None
+        assert L.lnorm_backward(ref(p), *args, big, None) == B.MOE_EINVAL
+    assert L.lnorm_backward(ref(p), *[FAKE] * 8, ctypes.c_void_p(0x100080), big, None) == B.MOE_EINVAL
+    assert L.lnorm_backward(ref(p), *[FAKE] * 9, p.bwd_workspace_bytes - 1, None) == B.MOE_EWORKSPACE
+    p0 = B.lnorm_plan(0, 64, B.MOE_F32)
+    assert L.lnorm_forward(ref(p0), *[None] * 7) == B.MOE_OK
+    assert L.lnorm_backward(ref(p0), *[None] * 9, 0, None) == B.MOE_EINVAL  # dgamma
+
+
+def test_lnorm_binding_refuses_wrong_tensors():
+    p = B.lnorm_plan(4, 64, B.MOE_F32)
+    x, g = torch.zeros(4, 64), torch.zeros(64)
+    for bad in (x[:3], x.bfloat16(), torch.zeros(4, 128)[:, ::2], torch.zeros(64, 4).t()):
+        with pytest.raises(ValueError):
+            B.lnorm_forward(p, bad, g)
+    with pytest.raises(ValueError):
+        B.lnorm_forward(p, x, g.bfloat16())
+    with pytest.raises(ValueError):  # not on a GPU
+        B.lnorm_forward(p, x, g)
