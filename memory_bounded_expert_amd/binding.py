@@ -23,7 +23,8 @@ LIB_PATH = os.path.join(PKG, "libmoebound.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 HEADERS = (os.path.join(INCLUDE, "moebound.h"), os.path.join(INCLUDE, "cce.h"))
 # the operators around the layer
-OPERATOR_HEADERS = (os.path.join(INCLUDE, "route.h"), os.path.join(INCLUDE, "lnorm.h"))
+OPERATOR_HEADERS = tuple(os.path.join(INCLUDE, n) for n in
+                         ("route.h", "lnorm.h", "embed.h", "distill.h"))
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, 1, 2, 3, 4
 STAGES = {"router": 0, "topk": 1, "plan": 2, "gather": 3, "gemm_up": 4, "gemm_down": 5,
@@ -83,6 +84,23 @@ class LnormPlan(_c.Structure):
     _fields_ = [
         ("magic", _c.c_uint32), ("dtype", _c.c_int32), ("N", _c.c_int64), ("H", _c.c_int32),
         ("eps", _c.c_float), ("bwd_workspace_bytes", _c.c_int64),
+    ]
+
+
+class EmbedPlan(_c.Structure):
+    _fields_ = [
+        ("magic", _c.c_uint32), ("dtype", _c.c_int32), ("N", _c.c_int64), ("V", _c.c_int64),
+        ("H", _c.c_int32), ("scale", _c.c_float), ("bwd_workspace_bytes", _c.c_int64),
+    ]
+
+
+class KdPlan(_c.Structure):
+    _fields_ = [
+        ("magic", _c.c_uint32), ("dtype", _c.c_int32), ("N", _c.c_int64), ("V", _c.c_int64),
+        ("H", _c.c_int32), ("v_chunk", _c.c_int32), ("K", _c.c_int32),
+        ("temperature", _c.c_float), ("dw_dtype", _c.c_int32), ("S", _c.c_int32),
+        ("strip_bound_bytes", _c.c_int64), ("fwd_workspace_bytes", _c.c_int64),
+        ("bwd_workspace_bytes", _c.c_int64),
     ]
 
 
@@ -158,6 +176,21 @@ def lib() -> ctypes.CDLL:
     L.lnorm_forward.argtypes = [_c.POINTER(LnormPlan)] + [_vp] * 7
     L.lnorm_backward.restype = _c.c_int
     L.lnorm_backward.argtypes = [_c.POINTER(LnormPlan)] + [_vp] * 9 + [_c.c_size_t, _vp]
+    L.embed_plan.restype = _c.c_int
+    L.embed_plan.argtypes = [_c.c_int64, _c.c_int64, _c.c_int32, _c.c_int32, _c.c_float,
+                             _c.POINTER(EmbedPlan)]
+    L.embed_forward.restype = _c.c_int
+    L.embed_forward.argtypes = [_c.POINTER(EmbedPlan)] + [_vp] * 4
+    L.embed_backward.restype = _c.c_int
+    L.embed_backward.argtypes = [_c.POINTER(EmbedPlan)] + [_vp] * 3 + [_c.c_int32, _vp, _c.c_size_t,
+                                                                     _vp]
+    L.kd_plan.restype = _c.c_int
+    L.kd_plan.argtypes = [_c.c_int64, _c.c_int32, _c.c_int64, _c.c_int32, _c.c_int32, _c.c_float,
+                          _c.c_int32, _c.c_int32, _c.POINTER(KdPlan)]
+    L.kd_forward.restype = _c.c_int
+    L.kd_forward.argtypes = [_c.POINTER(KdPlan)] + [_vp] * 8 + [_c.c_size_t, _vp]
+    L.kd_backward.restype = _c.c_int
+    L.kd_backward.argtypes = [_c.POINTER(KdPlan)] + [_vp] * 10 + [_c.c_size_t, _vp]
     _LIB = L
     return L
 
@@ -169,7 +202,7 @@ def declared_functions() -> list:
 
 def declared_operators() -> list:
     """Function names declared in the headers of the operators around the layer."""
-    return _declared(OPERATOR_HEADERS, "moe|route|lnorm")
+    return _declared(OPERATOR_HEADERS, "moe|route|lnorm|embed|kd")
 
 
 def _declared(headers, prefixes) -> list:
@@ -259,10 +292,13 @@ def moe_plan_set_flags(plan: MoePlan, flags: int) -> MoePlan:
 
 
 def workspace(plan, kind: str, device) -> torch.Tensor:
-    """Workspace of a MoePlan ("fwd", "bwd", "debug"), CcePlan ("fwd", "bwd") or
-    LnormPlan ("bwd")."""
-    n = getattr(plan, {"fwd": "fwd_workspace_bytes", "bwd": "bwd_workspace_bytes",
-                       "debug": "debug_workspace_bytes"}[kind])
+    """Workspace of a MoePlan ("fwd", "bwd", "debug"), CcePlan or KdPlan ("fwd", "bwd"),
+    LnormPlan or EmbedPlan ("bwd"); "both" is large enough for "fwd" and "bwd"."""
+    if kind == "both":
+        n = max(plan.fwd_workspace_bytes, plan.bwd_workspace_bytes)
+    else:
+        n = getattr(plan, {"fwd": "fwd_workspace_bytes", "bwd": "bwd_workspace_bytes",
+                           "debug": "debug_workspace_bytes"}[kind])
     return torch.empty(max(int(n), 1), dtype=torch.uint8, device=device)
 
 
@@ -639,3 +675,102 @@ def lnorm_backward(plan: LnormPlan, X, gamma, dY, mean, rstd, dX=None, dgamma=No
                                     _ptr(rstd), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws),
                                     ws.numel(), _stream(dev, None)), "lnorm_backward")
     return dX, dgamma, dbeta
+
+
+# ---- token embedding
+
+
+def embed_plan(N: int, V: int, H: int, dtype: int = MOE_BF16, scale: float = 1.0) -> EmbedPlan:
+    plan = EmbedPlan()
+    _check(lib().embed_plan(N, V, H, dtype, scale, ctypes.byref(plan)), "embed_plan")
+    return plan
+
+
+def embed_forward(plan: EmbedPlan, W, ids, Y=None, stream=None):
+    """Returns Y [N, H] = scale W[ids] (0 for an id outside [0, V))."""
+    dev = W.device
+    dt = torch_dtype(plan.dtype)
+    N, V, H = plan.N, plan.V, plan.H
+    _expect(W, "W", (V, H), dt, dev)
+    _expect(ids, "ids", (N,), torch.int32, dev)
+    with _on(dev, stream):
+        Y = torch.empty((N, H), dtype=dt, device=dev) if Y is None else Y
+        _expect(Y, "Y", (N, H), dt, dev)
+        _check(lib().embed_forward(ctypes.byref(plan), _ptr(W), _ptr(ids), _ptr(Y),
+                                   _stream(dev, None)), "embed_forward")
+    return Y
+
+
+def embed_backward(plan: EmbedPlan, ids, dY, dW=None, accumulate=False, ws=None, stream=None):
+    """Returns dW [V, H] fp32; with accumulate the gradient is added to the dW given."""
+    dev = dY.device
+    N, V, H = plan.N, plan.V, plan.H
+    _expect(ids, "ids", (N,), torch.int32, dev)
+    _expect(dY, "dY", (N, H), torch_dtype(plan.dtype), dev)
+    if accumulate and dW is None:
+        raise ValueError("accumulate needs the dW to add to")
+    with _on(dev, stream):
+        dW = torch.empty((V, H), dtype=torch.float32, device=dev) if dW is None else dW
+        _expect(dW, "dW", (V, H), torch.float32, dev)
+        ws = workspace(plan, "bwd", dev) if ws is None else ws
+        _check(lib().embed_backward(ctypes.byref(plan), _ptr(ids), _ptr(dY), _ptr(dW),
+                                    int(bool(accumulate)), _ptr(ws), ws.numel(),
+                                    _stream(dev, None)), "embed_backward")
+    return dW
+
+
+# ---- distillation from a teacher's top logits over vocabulary strips
+
+
+def kd_plan(N: int, H: int, V: int, v_chunk: int, K: int, temperature: float = 1.0,
+            dtype: int = MOE_BF16, dw_dtype: int = MOE_F32) -> KdPlan:
+    plan = KdPlan()
+    _check(lib().kd_plan(N, H, V, v_chunk, K, temperature, dtype, dw_dtype, ctypes.byref(plan)),
+           "kd_plan")
+    return plan
+
+
+def kd_forward(plan: KdPlan, X, W, t_idx, t_logit, loss=None, lse=None, y_top=None, ws=None,
+               stream=None):
+    """Returns (loss [N], lse [N], y_top [N, K]) fp32."""
+    dev = X.device
+    N, H, V, K = plan.N, plan.H, plan.V, plan.K
+    f32 = torch.float32
+    for t, n, s, d in ((X, "X", (N, H), torch.bfloat16), (W, "W", (V, H), torch.bfloat16),
+                       (t_idx, "t_idx", (N, K), torch.int32), (t_logit, "t_logit", (N, K), f32)):
+        _expect(t, n, s, d, dev)
+    with _on(dev, stream):
+        loss = torch.empty(N, dtype=f32, device=dev) if loss is None else loss
+        lse = torch.empty(N, dtype=f32, device=dev) if lse is None else lse
+        y_top = torch.empty((N, K), dtype=f32, device=dev) if y_top is None else y_top
+        _expect(loss, "loss", (N,), f32, dev)
+        _expect(lse, "lse", (N,), f32, dev)
+        _expect(y_top, "y_top", (N, K), f32, dev)
+        ws = workspace(plan, "fwd", dev) if ws is None else ws
+        _check(lib().kd_forward(ctypes.byref(plan), _ptr(X), _ptr(W), _ptr(t_idx), _ptr(t_logit),
+                                _ptr(loss), _ptr(lse), _ptr(y_top), _ptr(ws), ws.numel(),
+                                _stream(dev, None)), "kd_forward")
+    return loss, lse, y_top
+
+
+def kd_backward(plan: KdPlan, X, W, t_idx, t_logit, lse, y_top, dloss, dX=None, dW=None, ws=None,
+                stream=None):
+    """Returns (dX [N, H] bf16, dW [V, H] in the plan's dw_dtype)."""
+    dev = X.device
+    N, H, V, K = plan.N, plan.H, plan.V, plan.K
+    f32, bf16, wt = torch.float32, torch.bfloat16, torch_dtype(plan.dw_dtype)
+    for t, n, s, d in ((X, "X", (N, H), bf16), (W, "W", (V, H), bf16),
+                       (t_idx, "t_idx", (N, K), torch.int32), (t_logit, "t_logit", (N, K), f32),
+                       (lse, "lse", (N,), f32), (y_top, "y_top", (N, K), f32),
+                       (dloss, "dloss", (N,), f32)):
+        _expect(t, n, s, d, dev)
+    with _on(dev, stream):
+        dX = torch.empty((N, H), dtype=bf16, device=dev) if dX is None else dX
+        dW = torch.empty((V, H), dtype=wt, device=dev) if dW is None else dW
+        _expect(dX, "dX", (N, H), bf16, dev)
+        _expect(dW, "dW", (V, H), wt, dev)
+        ws = workspace(plan, "bwd", dev) if ws is None else ws
+        _check(lib().kd_backward(ctypes.byref(plan), _ptr(X), _ptr(W), _ptr(t_idx), _ptr(t_logit),
+                                 _ptr(lse), _ptr(y_top), _ptr(dloss), _ptr(dX), _ptr(dW), _ptr(ws),
+                                 ws.numel(), _stream(dev, None)), "kd_backward")
+    return dX, dW

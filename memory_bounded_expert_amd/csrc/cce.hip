@@ -36,12 +36,6 @@ struct CceLayout {
   size_t total = 0;
 };
 
-// Columns of the strip buffers: the widest strip rounded up to whole
-// 256-column logit tiles (v_chunk itself unless the vocabulary is narrower).
-int strip_cols(int64_t V, int v_chunk) {
-  return (int)std::min<int64_t>(v_chunk, ceil_div(V, 256) * 256);
-}
-
 CceLayout cce_layout(int64_t N, int H, int cols, bool backward) {
   CceLayout L;
   size_t cur = 0;
@@ -107,6 +101,7 @@ __global__ __launch_bounds__(kFoldThreads) void cce_fold_kernel(
   if (last) {
     const float l = mm + logf(zz);
     lse[t] = l;
+    if (!loss) return;  // only the normaliser is wanted
     const int tg = targets[t];
     loss[t] = (tg >= 0 && (int64_t)tg < V) ? l - ytgt[t] : 0.f;
   } else {
@@ -144,6 +139,21 @@ unsigned blocks(int64_t n) { return (unsigned)ceil_div(n, kCceThreads); }
 bool plan_ok(const cce_plan_t* p) { return p != nullptr && p->magic == kCceMagic; }
 
 }  // namespace
+
+hipError_t launch_cce_fold(const float* pmax, const float* psum, int nslices, int64_t N, float* m,
+                           float* z, bool first, bool last, const float* ytgt,
+                           const int32_t* targets, int64_t V, float* loss, float* lse,
+                           hipStream_t st) {
+  cce_fold_kernel<<<(unsigned)ceil_div(N, kFoldThreads), kFoldThreads, 0, st>>>(
+      pmax, psum, nslices, N, m, z, first, last, ytgt, targets, V, loss, lse);
+  return hipGetLastError();
+}
+
+hipError_t launch_cce_round(const float* src, void* dst, int64_t n, hipStream_t st) {
+  cce_round_kernel<<<blocks(n / 4), kCceThreads, 0, st>>>(src, (bf16_t*)dst, n / 4);
+  return hipGetLastError();
+}
+
 }  // namespace moe
 
 using namespace moe;
@@ -204,9 +214,8 @@ MOE_API int cce_forward(const cce_plan_t* plan, const void* X, const void* W,
                               nullptr, nullptr, 0, st));
     // slices the GEMM wrote: whole 256-column tiles, two slices each
     const int nsl = (int)ceil_div(w, 256) * (256 / kCceSlice);
-    cce_fold_kernel<<<(unsigned)ceil_div(P.N, kFoldThreads), kFoldThreads, 0, st>>>(
-        pmax, psum, nsl, P.N, m, z, s == 0, s == P.S - 1, ytgt, targets, P.V, loss, lse);
-    CCE_CHECK(hipGetLastError());
+    CCE_CHECK(launch_cce_fold(pmax, psum, nsl, P.N, m, z, s == 0, s == P.S - 1, ytgt, targets, P.V,
+                              loss, lse, st));
   }
   return MOE_OK;
 }
@@ -243,9 +252,7 @@ MOE_API int cce_backward(const cce_plan_t* plan, const void* X, const void* W,
     CCE_CHECK(gemm_cce_dx(G, cols, Ws, P.N, P.H, w, dx, s == 0, st));
     CCE_CHECK(gemm_cce_dw(G, cols, X, P.N, P.H, w, dW + v0 * P.H, st));
   }
-  const int64_t n4 = P.N * P.H / 4;
-  cce_round_kernel<<<blocks(n4), kCceThreads, 0, st>>>(dx, (bf16_t*)dX, n4);
-  CCE_CHECK(hipGetLastError());
+  CCE_CHECK(launch_cce_round(dx, dX, P.N * P.H, st));
   return MOE_OK;
 }
 
@@ -281,11 +288,10 @@ MOE_API int cce_debug_stage(const cce_plan_t* plan, int32_t stage, int32_t strip
       break;
     case CCE_STAGE_FOLD: {
       const int nsl = (int)ceil_div(w, 256) * (256 / kCceSlice);
-      cce_fold_kernel<<<(unsigned)ceil_div(P.N, kFoldThreads), kFoldThreads, 0, st>>>(
-          (float*)(ws + L.pmax), (float*)(ws + L.psum), nsl, P.N, (float*)(ws + L.m),
-          (float*)(ws + L.z), strip == 0, strip == P.S - 1, (float*)(ws + L.ytgt), targets, P.V,
-          loss, lse);
-      CCE_CHECK(hipGetLastError());
+      CCE_CHECK(launch_cce_fold((float*)(ws + L.pmax), (float*)(ws + L.psum), nsl, P.N,
+                                (float*)(ws + L.m), (float*)(ws + L.z), strip == 0,
+                                strip == P.S - 1, (float*)(ws + L.ytgt), targets, P.V, loss, lse,
+                                st));
       break;
     }
     case CCE_STAGE_GRAD:

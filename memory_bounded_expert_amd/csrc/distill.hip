@@ -1,0 +1,328 @@
+// Distillation from a teacher's top logits through the vocabulary projection
+// (include/distill.h).
+//
+// The strips and their GEMMs are the cross-entropy's (cce.hip, gemm_cce.hip)
+// on logits scaled by 1 / T.  What the teacher's list adds is sparse, K of V
+// entries per token: the forward pass takes their logits as dot products of
+// gathered rows of W, and the backward pass overwrites their values in the
+// strip's logit gradient from those logits, in fp32 before the one rounding.
+#include <algorithm>
+#include <cmath>
+
+#include "device_common.hpp"
+#include "distill.h"
+#include "moe_internal.h"
+#include "wave_ops.hpp"
+
+#define MOE_API extern "C" __attribute__((visibility("default")))
+
+namespace moe {
+namespace {
+
+constexpr uint32_t kKdMagic = 0x4b445331u;  // "KDS1"
+constexpr int kMaxList = 256;
+constexpr int kPer = kMaxList / 64;  // list entries per lane
+constexpr int kWaves = kThreads / 64;
+constexpr int kDots = 4;             // rows of W a wave multiplies at a time
+
+struct KdArgs {
+  const bf16_t* X;
+  const bf16_t* W;
+  const int32_t* t_idx;
+  const float* t_logit;
+  const float* lse;
+  int64_t N, V;
+  int H, K;
+  float T;
+};
+
+// The teacher's probabilities of token t's list: lane l holds entries l + 64 q.
+// p is -1 for an entry that is no part of the list; returns whether any is.
+__device__ __forceinline__ bool list_softmax(const KdArgs& a, int64_t t, int lane, int32_t (&id)[kPer],
+                                             float (&p)[kPer], float (&logp)[kPer]) {
+  float top = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    const int j = lane + 64 * q;
+    id[q] = -1;
+    logp[q] = -INFINITY;
+    if (j < a.K) {
+      const int32_t v = a.t_idx[t * a.K + j];
+      const float l = a.t_logit[t * a.K + j] / a.T;
+      if (v >= 0 && v < a.V && l > -INFINITY) {
+        id[q] = v;
+        logp[q] = l;
+      }
+    }
+    top = fmaxf(top, logp[q]);
+  }
+  top = run_max<64>(top);
+  const bool any = top > -INFINITY;
+  float z = 0.f;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    p[q] = id[q] >= 0 ? expf(logp[q] - top) : 0.f;
+    z += p[q];
+  }
+  z = run_sum<64>(z);
+  const float logz = any ? logf(z) : 0.f;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    p[q] = id[q] >= 0 ? p[q] / z : -1.f;
+    logp[q] = logp[q] - top - logz;
+  }
+  return any;
+}
+
+// One work-group per token: the list entries' logits, a wave taking kDots
+// rows of W at a time, then the loss.
+__global__ __launch_bounds__(kThreads) void kd_loss_kernel(const KdArgs a, float* __restrict__ loss,
+                                                           float* __restrict__ y_top) {
+  __shared__ float ys[kMaxList];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t t = blockIdx.x;
+  const u32x4_t* x = reinterpret_cast<const u32x4_t*>(a.X + t * a.H);
+  for (int j0 = w * kDots; j0 < a.K; j0 += kWaves * kDots) {
+    const u32x4_t* row[kDots];
+    bool real[kDots];
+    float acc[kDots];
+#pragma unroll
+    for (int u = 0; u < kDots; ++u) {
+      const int32_t v = j0 + u < a.K ? a.t_idx[t * a.K + j0 + u] : -1;
+      real[u] = v >= 0 && v < a.V && a.t_logit[t * a.K + j0 + u] / a.T > -INFINITY;
+      row[u] = reinterpret_cast<const u32x4_t*>(a.W + (int64_t)(real[u] ? v : 0) * a.H);
+      acc[u] = 0.f;
+    }
+    for (int c = lane; c < a.H / 8; c += 64) {
+      u32x4_t raw[kDots];
+#pragma unroll
+      for (int u = 0; u < kDots; ++u) raw[u] = row[u][c];
+      float xv[8], wv[8];
+      unpack16(x[c], xv, bf16_t());
+#pragma unroll
+      for (int u = 0; u < kDots; ++u) {
+        unpack16(raw[u], wv, bf16_t());
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[u] = fmaf(xv[e], wv[e], acc[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kDots; ++u) {
+      acc[u] = real[u] ? run_sum<64>(acc[u]) : 0.f;
+      if (lane == 0 && j0 + u < a.K) {
+        ys[j0 + u] = acc[u];
+        y_top[t * a.K + j0 + u] = acc[u];
+      }
+    }
+  }
+  __syncthreads();
+  if (w != 0) return;
+  int32_t id[kPer];
+  float p[kPer], logp[kPer];
+  const bool any = list_softmax(a, t, lane, id, p, logp);
+  float s = 0.f;
+#pragma unroll
+  for (int q = 0; q < kPer; ++q)
+    if (p[q] > 0.f) s = fmaf(p[q], logp[q] - (ys[lane + 64 * q] / a.T - a.lse[t]), s);
+  s = run_sum<64>(s);
+  if (lane == 0) loss[t] = any ? a.T * a.T * s : 0.f;
+}
+
+// Per token: dl = dloss T (0 for an empty list), and for each entry the sum of
+// p over the entries with its index (-1: no part of the list).
+__global__ __launch_bounds__(kThreads) void kd_prep_kernel(const KdArgs a,
+                                                           const float* __restrict__ dloss,
+                                                           float* __restrict__ dl,
+                                                           float* __restrict__ psum) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
+  if (t >= a.N) return;  // whole wave leaves together
+  int32_t id[kPer];
+  float p[kPer], logp[kPer], s[kPer];
+  const bool any = list_softmax(a, t, lane, id, p, logp);
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) s[q] = 0.f;
+#pragma unroll
+  for (int r = 0; r < kPer; ++r)
+    for (int l = 0; l < min(64, a.K - 64 * r); ++l) {
+      const int32_t v = __shfl(id[r], l);
+      const float pv = __shfl(p[r], l);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) s[q] += id[q] == v ? pv : 0.f;
+    }
+#pragma unroll
+  for (int q = 0; q < kPer; ++q)
+    if (lane + 64 * q < a.K) psum[t * a.K + lane + 64 * q] = id[q] >= 0 ? s[q] : -1.f;
+  if (lane == 0) dl[t] = any ? dloss[t] * a.T : 0.f;
+}
+
+// The strip's list entries: G[t][i - v0] = dl (q - p), from the entries' own
+// logits (entries of one index write the same value).
+__global__ __launch_bounds__(kThreads) void kd_entries_kernel(
+    const KdArgs a, const float* __restrict__ y_top, const float* __restrict__ dl,
+    const float* __restrict__ psum, int64_t v0, int w, bf16_t* __restrict__ G, int ldg) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= a.N * a.K) return;
+  const int64_t v = (int64_t)a.t_idx[i] - v0;
+  if (v < 0 || v >= w) return;
+  const float p = psum[i];
+  if (p < 0.f) return;
+  const int64_t t = i / a.K;
+  G[t * ldg + v] = f2bf(dl[t] * (expf(y_top[i] / a.T - a.lse[t]) - p));
+}
+
+struct KdLayout {
+  size_t pmax = 0, psum = 0, m = 0, z = 0;      // forward
+  size_t g = 0, dx = 0, dl = 0, p = 0;          // backward
+  size_t total = 0;
+};
+
+KdLayout kd_layout(int64_t N, int H, int cols, int K, bool backward) {
+  KdLayout L;
+  size_t cur = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = cur;
+    cur = (cur + bytes + 255) & ~(size_t)255;
+    return o;
+  };
+  const size_t n = (size_t)N;
+  if (!backward) {
+    const size_t nsl = (size_t)cols / kCceSlice;
+    L.pmax = take(nsl * n * 4);
+    L.psum = take(nsl * n * 4);
+    L.m = take(n * 4);
+    L.z = take(n * 4);
+  } else {
+    L.g = take(n * (size_t)cols * 2);
+    L.dx = take(n * (size_t)H * 4);
+    L.dl = take(n * 4);
+    L.p = take(n * (size_t)K * 4);
+  }
+  L.total = cur;
+  return L;
+}
+
+bool plan_ok(const kd_plan_t* p) { return p != nullptr && p->magic == kKdMagic; }
+
+KdArgs kd_args(const kd_plan_t& P, const void* X, const void* W, const int32_t* t_idx,
+               const float* t_logit, const float* lse) {
+  return KdArgs{(const bf16_t*)X, (const bf16_t*)W, t_idx, t_logit, lse, P.N, P.V, P.H, P.K,
+                P.temperature};
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+#define KD_CHECK(call)                         \
+  do {                                         \
+    if ((call) != hipSuccess) return MOE_EHIP; \
+  } while (0)
+
+MOE_API int kd_plan(int64_t N, int32_t H, int64_t V, int32_t v_chunk, int32_t K, float temperature,
+                    int32_t dtype, int32_t dw_dtype, kd_plan_t* out) {
+  if (!out || N < 0 || V < 1 || H < 1 || v_chunk < 1 || K < 1) return MOE_EINVAL;
+  if (!(temperature > 0.f) || !std::isfinite(temperature)) return MOE_EINVAL;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EINVAL;
+  if (dw_dtype != MOE_F32 && dw_dtype != MOE_BF16) return MOE_EINVAL;
+  if (dtype != MOE_BF16 || H % 128 != 0 || v_chunk % 256 != 0 || K > kMaxList) return MOE_EUNSUPPORTED;
+  const int64_t lim = (int64_t)1 << 30;
+  if (N >= lim || N * (int64_t)H >= lim || N * (int64_t)v_chunk >= lim ||
+      (int64_t)v_chunk * H >= lim || V >= 2 * lim)
+    return MOE_EUNSUPPORTED;
+  kd_plan_t p{};
+  p.magic = kKdMagic;
+  p.dtype = dtype;
+  p.N = N;
+  p.V = V;
+  p.H = H;
+  p.v_chunk = v_chunk;
+  p.K = K;
+  p.temperature = temperature;
+  p.dw_dtype = dw_dtype;
+  p.S = N == 0 ? 0 : (int32_t)ceil_div(V, v_chunk);
+  p.strip_bound_bytes = N * std::min<int64_t>(v_chunk, V) * 2;
+  const int cols = strip_cols(V, v_chunk);
+  p.fwd_workspace_bytes = N == 0 ? 0 : (int64_t)kd_layout(N, H, cols, K, false).total;
+  p.bwd_workspace_bytes = N == 0 ? 0 : (int64_t)kd_layout(N, H, cols, K, true).total;
+  *out = p;
+  return MOE_OK;
+}
+
+MOE_API int kd_forward(const kd_plan_t* plan, const void* X, const void* W, const int32_t* t_idx,
+                       const float* t_logit, float* loss, float* lse, float* y_top,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  if (!plan_ok(plan)) return MOE_EINVAL;
+  const kd_plan_t& P = *plan;
+  if (P.N == 0) return MOE_OK;
+  if (!X || !W || !t_idx || !t_logit || !loss || !lse || !y_top || !workspace) return MOE_EINVAL;
+  if ((uintptr_t)workspace % 256) return MOE_EINVAL;
+  if (workspace_bytes < (size_t)P.fwd_workspace_bytes) return MOE_EWORKSPACE;
+  const KdLayout L = kd_layout(P.N, P.H, strip_cols(P.V, P.v_chunk), P.K, false);
+  hipStream_t st = (hipStream_t)stream;
+  char* ws = (char*)workspace;
+  float* pmax = (float*)(ws + L.pmax);
+  float* psum = (float*)(ws + L.psum);
+  (void)hipGetLastError();
+  for (int s = 0; s < P.S; ++s) {
+    const int64_t v0 = (int64_t)s * P.v_chunk;
+    const int w = (int)std::min<int64_t>(P.v_chunk, P.V - v0);
+    KD_CHECK(gemm_kd_logits(false, X, (const bf16_t*)W + v0 * P.H, P.N, P.H, w, 1.f / P.temperature,
+                            pmax, psum, nullptr, nullptr, nullptr, 0, st));
+    const int nsl = (int)ceil_div(w, 256) * (256 / kCceSlice);
+    KD_CHECK(launch_cce_fold(pmax, psum, nsl, P.N, (float*)(ws + L.m), (float*)(ws + L.z), s == 0,
+                             s == P.S - 1, nullptr, nullptr, P.V, nullptr, lse, st));
+  }
+  kd_loss_kernel<<<(unsigned)P.N, kThreads, 0, st>>>(kd_args(P, X, W, t_idx, t_logit, lse), loss,
+                                                     y_top);
+  KD_CHECK(hipGetLastError());
+  return MOE_OK;
+}
+
+MOE_API int kd_backward(const kd_plan_t* plan, const void* X, const void* W, const int32_t* t_idx,
+                        const float* t_logit, const float* lse, const float* y_top,
+                        const float* dloss, void* dX, void* dW, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  if (!plan_ok(plan)) return MOE_EINVAL;
+  const kd_plan_t& P = *plan;
+  if (!dW) return MOE_EINVAL;
+  if (P.N > 0 && (!X || !W || !t_idx || !t_logit || !lse || !y_top || !dloss || !dX || !workspace))
+    return MOE_EINVAL;
+  if (P.N > 0 && (uintptr_t)workspace % 256) return MOE_EINVAL;
+  if (workspace_bytes < (size_t)P.bwd_workspace_bytes) return MOE_EWORKSPACE;
+  hipStream_t st = (hipStream_t)stream;
+  const size_t dwb = P.dw_dtype == MOE_BF16 ? 2 : 4;
+  (void)hipGetLastError();
+  if (P.N == 0) {  // no tokens: dW = 0
+    KD_CHECK(launch_fill_zero(dW, (size_t)P.V * P.H * dwb, st));
+    return MOE_OK;
+  }
+  const int cols = strip_cols(P.V, P.v_chunk);
+  const KdLayout L = kd_layout(P.N, P.H, cols, P.K, true);
+  char* ws = (char*)workspace;
+  bf16_t* G = (bf16_t*)(ws + L.g);
+  float* dx = (float*)(ws + L.dx);
+  float* dl = (float*)(ws + L.dl);
+  float* psum = (float*)(ws + L.p);
+  const KdArgs a = kd_args(P, X, W, t_idx, t_logit, lse);
+  kd_prep_kernel<<<(unsigned)ceil_div(P.N, kWaves), kThreads, 0, st>>>(a, dloss, dl, psum);
+  KD_CHECK(hipGetLastError());
+  for (int s = 0; s < P.S; ++s) {
+    const int64_t v0 = (int64_t)s * P.v_chunk;
+    const int w = (int)std::min<int64_t>(P.v_chunk, P.V - v0);
+    const bf16_t* Ws = (const bf16_t*)W + v0 * P.H;
+    KD_CHECK(gemm_kd_logits(true, X, Ws, P.N, P.H, w, 1.f / P.temperature, nullptr, nullptr, lse,
+                            dl, G, cols, st));
+    kd_entries_kernel<<<(unsigned)ceil_div(P.N * P.K, kThreads), kThreads, 0, st>>>(
+        a, y_top, dl, psum, v0, w, G, cols);
+    KD_CHECK(hipGetLastError());
+    KD_CHECK(gemm_cce_dx(G, cols, Ws, P.N, P.H, w, dx, s == 0, st));
+    if (P.dw_dtype == MOE_BF16)
+      KD_CHECK(gemm_kd_dw_bf16(G, cols, X, P.N, P.H, w, (bf16_t*)dW + v0 * P.H, st));
+    else
+      KD_CHECK(gemm_cce_dw(G, cols, X, P.N, P.H, w, (float*)dW + v0 * P.H, st));
+  }
+  KD_CHECK(launch_cce_round(dx, dX, P.N * P.H, st));
+  return MOE_OK;
+}

@@ -70,4 +70,39 @@ hipError_t gemm_cce_dw(const void* G, int ldg, const void* X, int64_t N, int H, 
   return launch_lds<Mode::Expert, Shape<128, 128, 2, 4, 64, 1>, false, false, false, false, Epi::AccF32>(p, grid, st);
 }
 
+hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, int H, int w,
+                          float inv_t, float* pmax, float* psum, const float* lse, const float* dl,
+                          void* G, int ldg, hipStream_t st) {
+  if (N == 0 || w == 0) return hipSuccess;
+  Params p{};
+  p.A = X; p.lda = H;
+  p.B = Ws; p.ldb = H;
+  p.M = (int)N; p.N = w; p.K = H;
+  p.ce_scale = inv_t;
+  const dim3 grid((unsigned)ceil_div(N, Logit::BM), (unsigned)ceil_div(w, Logit::BN));
+  if (!grad) {
+    p.ce_pmax = pmax; p.ce_psum = psum;
+    return launch_lds<Mode::Dense, Logit, false, true, true, false, Epi::KDStats>(p, grid, st);
+  }
+  p.ce_lse = lse; p.ce_dl = dl;
+  p.C = G; p.ldc = ldg;
+  return launch_lds<Mode::Dense, Logit, false, true, true, false, Epi::KDGrad>(p, grid, st);
+}
+
+hipError_t gemm_kd_dw_bf16(const void* G, int ldg, const void* X, int64_t N, int H, int w,
+                           void* dws, hipStream_t st) {
+  if (w == 0) return hipSuccess;
+  Params p{};
+  p.A = G; p.lda = ldg;
+  p.B = X; p.ldb = H;
+  p.C = dws; p.ldc = H;
+  p.M = w; p.N = H; p.K = (int)N;
+  p.tile_group = kCceDwGroup;  // as gemm_cce_dw
+  const int bn = H % 256 == 0 ? 256 : 128;
+  const dim3 grid((unsigned)ceil_div(w, 128), (unsigned)(H / bn), 1u);
+  if (bn == 256)
+    return launch_lds<Mode::Expert, Shape<128, 256, 2, 2, 32, 2>, false, false, false, false, Epi::Store>(p, grid, st);
+  return launch_lds<Mode::Expert, Shape<128, 128, 2, 4, 64, 1>, false, false, false, false, Epi::Store>(p, grid, st);
+}
+
 }  // namespace moe

@@ -49,9 +49,11 @@ namespace gemm {
 enum class Mode { Rows, Dense, Expert, ExpertIdx, ExpertIdxB };
 // CEStats and CEGrad are the vocabulary-strip cross-entropy epilogues (LDS
 // pipeline, Dense mode only).
+// KDStats and KDGrad are their forms for distillation: logits times ce_scale,
+// no targets.
 // SwiGLUBwd is the SwiGLU backward fused into dY W_down^T (LDS pipeline,
 // Rows mode only).
-enum class Epi { Store, SwiGLU, SwiGLUSave, F32, BiasF32, AccF32, CEStats, CEGrad, SwiGLUBwd };
+enum class Epi { Store, SwiGLU, SwiGLUSave, F32, BiasF32, AccF32, CEStats, CEGrad, KDStats, KDGrad, SwiGLUBwd };
 
 struct Params {
   const void* A;
@@ -97,6 +99,7 @@ struct Params {
   float* ce_ytgt;          // CEStats: [M] the target's logit (its slice writes it)
   const float* ce_lse;     // CEGrad: [M] log-normaliser
   const float* ce_dl;      // CEGrad: [M] upstream gradient, 0 for ignored rows
+  float ce_scale;          // KDStats, KDGrad: factor on the logits, 1 / temperature
   // Epi::SwiGLUBwd: C = h (then g h), C2 = a (then da), C3 = u (then du),
   // row r's pair sw_perm[r] (< sw_nk) and its gate; sw_dgp[n-tile][row]
   // (row stride sw_rows) receives the tile's share of sum_f dh' h.

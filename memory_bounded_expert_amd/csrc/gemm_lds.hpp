@@ -831,7 +831,7 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
     return;
   }
 
-  if constexpr (EPI == Epi::CEStats) {
+  if constexpr (EPI == Epi::CEStats || EPI == Epi::KDStats) {
     // Vocabulary-strip cross-entropy, forward: the tile's logits stay on
     // chip.  Per row, each wave reduces its WN-column slice (columns past N,
     // the ragged end of the strip, excluded) to the slice's max m and
@@ -840,7 +840,12 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
     // (commutative pairwise steps, so every lane ends with the same bits).
     // Slice s of the strip covers columns [s WN, (s + 1) WN), the same
     // vocabulary columns whatever the strip width.  The lane holding the
-    // row's target column also writes that logit.
+    // row's target column also writes that logit.  KDStats: the same of the
+    // logits times ce_scale, without targets.
+    constexpr bool KD = EPI == Epi::KDStats;
+    auto logit = [&](int i, int j, int q) __attribute__((always_inline)) {
+      return KD ? acc[0][i][j][q] * p.ce_scale : acc[0][i][j][q];
+    };
     const int col0 = n0 + wn * WN;
     const int slice = col0 / WN;
     const int64_t M = p.M;
@@ -852,13 +857,13 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
         float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-          if (col0 + j * 16 + l16 < p.N) mx = fmaxf(mx, acc[0][i][j][q]);
+          if (col0 + j * 16 + l16 < p.N) mx = fmaxf(mx, logit(i, j, q));
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
         float sm = 0.f;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-          if (col0 + j * 16 + l16 < p.N) sm += __expf(acc[0][i][j][q] - mx);
+          if (col0 + j * 16 + l16 < p.N) sm += __expf(logit(i, j, q) - mx);
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) sm += __shfl_xor(sm, o);
         if (row < row_end) {
@@ -866,13 +871,15 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
             p.ce_pmax[slice * M + row] = mx;
             p.ce_psum[slice * M + row] = sm;
           }
-          const int64_t rel = (int64_t)p.ce_targets[row] - p.ce_col0 - col0;
-          if (rel >= 0 && rel < WN && (int)(rel & 15) == l16) {
-            float v = 0.f;
+          if constexpr (!KD) {
+            const int64_t rel = (int64_t)p.ce_targets[row] - p.ce_col0 - col0;
+            if (rel >= 0 && rel < WN && (int)(rel & 15) == l16) {
+              float v = 0.f;
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
-              if ((int)(rel >> 4) == j) v = acc[0][i][j][q];
-            p.ce_ytgt[row] = v;
+              for (int j = 0; j < FN; ++j)
+                if ((int)(rel >> 4) == j) v = acc[0][i][j][q];
+              p.ce_ytgt[row] = v;
+            }
           }
         }
       }
@@ -996,7 +1003,8 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
 
   if constexpr ((MODE == Mode::Rows && (EPI == Epi::Store || EPI == Epi::SwiGLU ||
                                        EPI == Epi::SwiGLUSave || EPI == Epi::F32)) ||
-                (MODE == Mode::Dense && EPI == Epi::CEGrad)) {
+                (MODE == Mode::Dense && (EPI == Epi::CEGrad || EPI == Epi::KDGrad)) ||
+                (MODE == Mode::Expert && EPI == Epi::Store)) {
     // Row-grouped outputs go out through LDS: each wave parks its fragment
     // values (computed exactly as below) in the free operand stages, slab by
     // slab of wave row slices, and the work-group then writes the slab with
@@ -1050,6 +1058,22 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) rg[i][q] = __shfl(row_scale_lane, i * 16 + 4 * lg + q, 64);
       stage_store(static_cast<T*>(p.C), [&](int i, int j, int q) { return f2bf(acc[0][i][j][q] * rg[i][q]); });
+    } else if constexpr (EPI == Epi::KDGrad) {
+      // Distillation, backward: dl_row exp(ce_scale logit - lse_row), bf16 (the
+      // teacher's entries are corrected afterwards); zeros as for CEGrad.
+      float rlse[FM][4], rdl[FM][4];
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = min(m0 + wm * WM + i * 16 + 4 * lg + q, row_end - 1);
+          rlse[i][q] = p.ce_lse[row];
+          rdl[i][q] = p.ce_dl[row];
+        }
+      stage_store(static_cast<T*>(p.C), [&](int i, int j, int q) {
+        const float gv = rdl[i][q] * __expf(fmaf(acc[0][i][j][q], p.ce_scale, -rlse[i][q]));
+        return f2bf(n0 + wn * WN + j * 16 + l16 < p.N ? gv : 0.f);
+      });
     } else if constexpr (EPI == Epi::CEGrad) {
       // Vocabulary-strip cross-entropy, backward: the strip's logit gradient
       // dl_row (exp(logit - lse_row) - [column == target_row]), bf16;

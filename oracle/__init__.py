@@ -46,3 +46,10 @@ from .route_oracle import (  # noqa: F401,E402
     route_gates,
     route_backward,
 )
+
+from .distill_oracle import (  # noqa: F401,E402
+    kd_list,
+    kd_forward,
+    kd_dlogits,
+    kd_backward,
+)

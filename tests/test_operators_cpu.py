@@ -18,14 +18,16 @@ pytestmark = pytest.mark.skipif(not os.path.exists(B.LIB_PATH),
                                 reason="libmoebound.so not built (run __graft_entry__.build())")
 
 FAKE = ctypes.c_void_p(0x100000)  # never dereferenced: every check below fails first
-PLANS = {"route_plan_t": B.RoutePlan, "lnorm_plan_t": B.LnormPlan}
+PLANS = {"route_plan_t": B.RoutePlan, "lnorm_plan_t": B.LnormPlan, "embed_plan_t": B.EmbedPlan,
+         "kd_plan_t": B.KdPlan}
 
 
 def test_exports_and_argument_counts():
     L = B.lib()
     names = B.declared_operators()
-    assert {"route_plan", "route_forward", "route_backward", "moe_routed_forward",
-            "moe_routed_backward", "lnorm_plan", "lnorm_forward", "lnorm_backward"} <= set(names)
+    assert set(names) == {p + s for p in ("route_", "lnorm_", "embed_", "kd_")
+                          for s in ("plan", "forward", "backward")} | {"moe_routed_forward",
+                                                                       "moe_routed_backward"}
     for h in B.OPERATOR_HEADERS:
         text = re.sub(r"/\*.*?\*/", "", open(h).read(), flags=re.S)
         for m in re.finditer(r"\bint ([a-z]+_[a-z_]+)\s*\(([^;{]*?)\)\s*;", text, flags=re.S):
@@ -181,3 +183,105 @@ def test_lnorm_binding_refuses_wrong_tensors():
         B.lnorm_forward(p, x, g.bfloat16())
     with pytest.raises(ValueError):  # not on a GPU
         B.lnorm_forward(p, x, g)
+
+
+# ---- token embedding
+
+
+@pytest.mark.parametrize("args,status", [
+    ((-1, 10, 64, 0, 1.0), B.MOE_EINVAL), ((4, 0, 64, 0, 1.0), B.MOE_EINVAL),
+    ((4, 10, 0, 0, 1.0), B.MOE_EINVAL), ((4, 10, 64, 3, 1.0), B.MOE_EINVAL),
+    ((4, 10, 64, 0, float("nan")), B.MOE_EINVAL), ((4, 10, 64, 0, float("inf")), B.MOE_EINVAL),
+    ((2**26, 10, 64, 0, 1.0), B.MOE_EUNSUPPORTED), ((4, 2**30, 64, 0, 1.0), B.MOE_EUNSUPPORTED),
+    ((4, 10, 65537, 0, 1.0), B.MOE_EUNSUPPORTED),
+])
+def test_embed_plan_errors(args, status):
+    assert B.lib().embed_plan(*args, ctypes.byref(B.EmbedPlan())) == status
+
+
+def test_embed_argument_errors():
+    L, ref = B.lib(), ctypes.byref
+    assert L.embed_plan(4, 10, 64, 0, 1.0, None) == B.MOE_EINVAL
+    p, big = B.embed_plan(4, 10, 64, B.MOE_F32), 1 << 30
+    assert L.embed_forward(ref(B.EmbedPlan()), *[FAKE] * 3, None) == B.MOE_EINVAL
+    assert L.embed_backward(ref(B.EmbedPlan()), *[FAKE] * 3, 0, FAKE, big, None) == B.MOE_EINVAL
+    for i in range(3):
+        args = [FAKE] * 3
+        args[i] = None
+        assert L.embed_forward(ref(p), *args, None) == B.MOE_EINVAL
+        assert L.embed_backward(ref(p), *args, 0, FAKE, big, None) == B.MOE_EINVAL
+    assert L.embed_backward(ref(p), *[FAKE] * 3, 0, None, big, None) == B.MOE_EINVAL
+    assert L.embed_backward(ref(p), *[FAKE] * 3, 0, ctypes.c_void_p(0x100004), big, None) == B.MOE_EINVAL
+    assert L.embed_backward(ref(p), *[FAKE] * 3, 0, FAKE, p.bwd_workspace_bytes - 1, None) == B.MOE_EWORKSPACE
+    p0 = B.embed_plan(0, 10, 64, B.MOE_F32)
+    assert L.embed_forward(ref(p0), *[None] * 4) == B.MOE_OK
+    assert L.embed_backward(ref(p0), *[None] * 3, 0, None, 0, None) == B.MOE_EINVAL  # dW
+    assert L.embed_backward(ref(p0), None, None, FAKE, 1, None, 0, None) == B.MOE_OK
+
+
+def test_embed_binding_refuses_wrong_tensors():
+    p = B.embed_plan(4, 10, 64, B.MOE_F32)
+    W, ids = torch.zeros(10, 64), torch.zeros(4, dtype=torch.int32)
+    for w, i in ((W[:9], ids), (W.bfloat16(), ids), (W, ids.long()), (W, ids[:3]), (W, ids)):
+        with pytest.raises(ValueError):  # the last pair is not on a GPU
+            B.embed_forward(p, w, i)
+    with pytest.raises(ValueError):
+        B.embed_backward(p, ids, torch.zeros(4, 64), accumulate=True)
+
+
+# ---- distillation
+
+KD_OK = dict(N=8, H=128, V=1000, v_chunk=256, K=16, temperature=1.0, dtype=1, dw_dtype=0)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(N=-1), B.MOE_EINVAL), (dict(H=0), B.MOE_EINVAL), (dict(V=0), B.MOE_EINVAL),
+    (dict(v_chunk=0), B.MOE_EINVAL), (dict(K=0), B.MOE_EINVAL), (dict(temperature=0.0), B.MOE_EINVAL),
+    (dict(temperature=-2.0), B.MOE_EINVAL), (dict(temperature=float("nan")), B.MOE_EINVAL),
+    (dict(temperature=float("inf")), B.MOE_EINVAL), (dict(dtype=2), B.MOE_EINVAL),
+    (dict(dw_dtype=5), B.MOE_EINVAL), (dict(dtype=0), B.MOE_EUNSUPPORTED),
+    (dict(H=192), B.MOE_EUNSUPPORTED), (dict(v_chunk=300), B.MOE_EUNSUPPORTED),
+    (dict(K=257), B.MOE_EUNSUPPORTED), (dict(N=2**23), B.MOE_EUNSUPPORTED),
+    (dict(v_chunk=2**23), B.MOE_EUNSUPPORTED), (dict(V=2**31), B.MOE_EUNSUPPORTED),
+    (dict(N=2**16, v_chunk=2**14), B.MOE_EUNSUPPORTED),
+])
+def test_kd_plan_errors(change, status):
+    assert B.lib().kd_plan(*{**KD_OK, **change}.values(), ctypes.byref(B.KdPlan())) == status
+
+
+def test_kd_strips_and_workspace():
+    p = B.kd_plan(8192, 7168, 200_000, 8192, 32)
+    c = B.cce_plan(8192, 7168, 200_000, 8192)
+    assert (p.S, p.strip_bound_bytes) == (c.S, c.strip_bound_bytes) == (25, 8192 * 8192 * 2)
+    # beside the cross-entropy's: the list's probabilities
+    assert p.bwd_workspace_bytes <= c.bwd_workspace_bytes + 8192 * 32 * 4 + 256
+    assert p.fwd_workspace_bytes <= c.fwd_workspace_bytes
+
+
+def test_kd_argument_errors():
+    L, ref = B.lib(), ctypes.byref
+    assert L.kd_plan(*KD_OK.values(), None) == B.MOE_EINVAL
+    p, big = B.kd_plan(**KD_OK), 1 << 30
+    assert L.kd_forward(ref(B.KdPlan()), *[FAKE] * 8, big, None) == B.MOE_EINVAL
+    assert L.kd_backward(ref(B.KdPlan()), *[FAKE] * 10, big, None) == B.MOE_EINVAL
+    for n, f in ((8, L.kd_forward), (10, L.kd_backward)):
+        for i in range(n):
+            args = [FAKE] * n
+            args[i] = None
+            assert f(ref(p), *args, big, None) == B.MOE_EINVAL
+        assert f(ref(p), *[FAKE] * (n - 1), ctypes.c_void_p(0x100080), big, None) == B.MOE_EINVAL
+    assert L.kd_forward(ref(p), *[FAKE] * 8, p.fwd_workspace_bytes - 1, None) == B.MOE_EWORKSPACE
+    assert L.kd_backward(ref(p), *[FAKE] * 10, p.bwd_workspace_bytes - 1, None) == B.MOE_EWORKSPACE
+    p0 = B.kd_plan(**{**KD_OK, "N": 0})
+    assert L.kd_forward(ref(p0), *[None] * 8, 0, None) == B.MOE_OK
+    assert L.kd_backward(ref(p0), *[None] * 10, 0, None) == B.MOE_EINVAL  # dW
+
+
+def test_kd_binding_refuses_wrong_tensors():
+    p = B.kd_plan(**KD_OK)
+    ok = dict(X=torch.zeros(8, 128).bfloat16(), W=torch.zeros(1000, 128).bfloat16(),
+              t_idx=torch.zeros(8, 16, dtype=torch.int32), t_logit=torch.zeros(8, 16))
+    for change in (dict(X=torch.zeros(8, 128)), dict(W=ok["W"][:999]), dict(t_idx=ok["t_idx"].long()),
+                   dict(t_logit=ok["t_logit"][:, :8]), dict()):  # the last: not on a GPU
+        with pytest.raises(ValueError):
+            B.kd_forward(p, **{**ok, **change})
