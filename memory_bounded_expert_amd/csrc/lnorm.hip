@@ -1,11 +1,16 @@
 // Layer norm and its gradient (include/lnorm.h).
 //
-// Forward: one work-group per row; the mean, then the centred squares, then
-// the output.  Backward: one work-group per slab of rows keeps the slab's
-// shares of dgamma and dbeta in the workspace and writes dX row by row; a
-// second launch adds the slabs up in order.
+// Both passes move a few bytes per operation and are bound by HBM, so a row is
+// read once and held in registers: W waves per row, C vectors of 16 bytes per
+// lane (single elements where rows do not start on 16-byte steps).  A
+// work-group walks over rows with gamma, beta (or the shares of dgamma and
+// dbeta) in registers and the next row's loads in flight.  The backward pass
+// writes each work-group's shares of dgamma and dbeta to the workspace, and a
+// second launch adds them up in order.  Rows wider than the registers hold go
+// through kernels that read the row again for each step.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "device_common.hpp"
 #include "lnorm.h"
@@ -18,8 +23,11 @@ namespace moe {
 namespace {
 
 constexpr uint32_t kLnormMagic = 0x4c4e4d31u;  // "LNM1"
-constexpr int kMaxSlabs = 512;
+constexpr int kMaxSlabs = 1024;
 constexpr unsigned kMaxRowGrid = 1u << 16;
+// Waves over which the rows are spread: two per SIMD, what the registers of
+// the backward pass allow.
+constexpr int kRowWaves = 2048;
 
 // Sum over the work-group; every thread gets it.  `red` holds one float per wave.
 __device__ __forceinline__ float group_sum(float v, float* red) {
@@ -31,6 +39,252 @@ __device__ __forceinline__ float group_sum(float v, float* red) {
 #pragma unroll
   for (int w = 0; w < kThreads / 64; ++w) s += red[w];
   return s;
+}
+
+// One lane's part of a row: C vectors of EPC elements, vector c at c * 64 W + its
+// place in the row's lanes.
+template <typename T, int EPC, int W, int C>
+struct RowPart {
+  static constexpr int COLS = EPC * C;
+  using Raw = std::conditional_t<EPC == 1, T, u32x4_t>;
+  Raw raw[C];
+
+  __device__ __forceinline__ void load(const T* row, int place, int vecs) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      raw[c] = c * 64 * W + place < vecs ? reinterpret_cast<const Raw*>(row)[c * 64 * W + place] : Raw{};
+  }
+  __device__ __forceinline__ void get(int c, float* v) const {
+    if constexpr (EPC == 1)
+      v[0] = Elem<T>::to_f(raw[c]);
+    else
+      unpack16(raw[c], v, T());
+  }
+  __device__ static __forceinline__ void put(T* row, int at, const float* v) {
+    if constexpr (EPC == 1)
+      row[at] = Elem<T>::from_f(v[0]);
+    else
+      reinterpret_cast<u32x4_t*>(row)[at] = pack16(v, T());
+  }
+};
+
+template <int EPC, int W, int C>
+__device__ __forceinline__ void load_cols(const float* p, int place, int vecs, float* out) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int at = c * 64 * W + place;
+    if constexpr (EPC == 1) {
+      out[c] = p && at < vecs ? p[at] : 0.f;
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPC; e += 4) {
+        // gamma and beta may start off a 16-byte step
+#pragma unroll
+        for (int f = 0; f < 4; ++f) out[c * EPC + e + f] = p && at < vecs ? p[at * EPC + e + f] : 0.f;
+      }
+    }
+  }
+}
+
+// Sums over the W waves of a row (a work-group of W waves, or one wave); `red`
+// alternates between two halves, so one barrier per sum is enough.
+template <int W, int NV>
+__device__ __forceinline__ void row_sums(float (&v)[NV], float (*red)[NV][16], int& half) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = run_sum<64>(v[i]);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) red[half][i][threadIdx.x >> 6] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) s += red[half][i][w];
+      v[i] = s;
+    }
+    half ^= 1;
+  }
+}
+
+// The next row's loads fly ahead, except where 16 waves leave each 128 registers.
+template <int W>
+constexpr bool kAhead = W < 16;
+template <int W>
+constexpr int kGroup = W == 1 ? kThreads : 64 * W;  // threads of a work-group
+
+template <typename T, int EPC, int W, int C>
+__global__ __launch_bounds__(kGroup<W>) void lnorm_rows_forward_kernel(
+    const T* X, const float* __restrict__ gamma, const float* __restrict__ beta, T* Y,
+    float* __restrict__ mean, float* __restrict__ rstd, int64_t N, int H, float eps) {
+  using Part = RowPart<T, EPC, W, C>;
+  __shared__ float red[2][1][16];
+  constexpr int RPG = kGroup<W> / (64 * W);  // rows of a work-group at a time
+  const int place = threadIdx.x % (64 * W);
+  const int vecs = H / EPC;
+  const float inv = 1.f / H;
+  float ga[Part::COLS], be[Part::COLS];
+  load_cols<EPC, W, C>(gamma, place, vecs, ga);
+  load_cols<EPC, W, C>(beta, place, vecs, be);
+  int half = 0;
+  int64_t t = (int64_t)blockIdx.x * RPG + threadIdx.x / (64 * W);
+  const int64_t step = (int64_t)gridDim.x * RPG;
+  Part cur;
+  if (kAhead<W> && t < N) cur.load(X + t * H, place, vecs);
+  for (; t < N; t += step) {
+    Part next;
+    if constexpr (kAhead<W>) {
+      if (t + step < N) next.load(X + (t + step) * H, place, vecs);
+    } else {
+      cur.load(X + t * H, place, vecs);
+    }
+    float s[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float v[EPC];
+      cur.get(c, v);
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) s[0] += v[e];
+    }
+    row_sums<W>(s, red, half);
+    const float m = s[0] * inv;
+    s[0] = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (c * 64 * W + place < vecs) {
+        float v[EPC];
+        cur.get(c, v);
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) s[0] = fmaf(v[e] - m, v[e] - m, s[0]);
+      }
+    }
+    row_sums<W>(s, red, half);
+    const float r = 1.f / sqrtf(s[0] * inv + eps);
+    if (place == 0) {
+      mean[t] = m;
+      rstd[t] = r;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (c * 64 * W + place < vecs) {
+        float v[EPC];
+        cur.get(c, v);
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) v[e] = fmaf((v[e] - m) * r, ga[c * EPC + e], be[c * EPC + e]);
+        Part::put(Y + t * H, c * 64 * W + place, v);
+      }
+    }
+    if constexpr (kAhead<W>) cur = next;
+  }
+}
+
+// part: [work-group][2][H], its rows' shares of dgamma and dbeta.
+template <typename T, int EPC, int W, int C>
+__global__ __launch_bounds__(kGroup<W>) void lnorm_rows_backward_kernel(
+    const T* __restrict__ X, const float* __restrict__ gamma, const T* dY,
+    const float* __restrict__ mean, const float* __restrict__ rstd, T* dX,
+    float* __restrict__ part, int64_t N, int H) {
+  using Part = RowPart<T, EPC, W, C>;
+  constexpr int RPG = kGroup<W> / (64 * W);
+  __shared__ float red[2][2][16];
+  const int place = threadIdx.x % (64 * W);
+  const int vecs = H / EPC;
+  const float inv = 1.f / H;
+  float ga[Part::COLS], dg[Part::COLS], db[Part::COLS];
+  load_cols<EPC, W, C>(gamma, place, vecs, ga);
+#pragma unroll
+  for (int i = 0; i < Part::COLS; ++i) dg[i] = db[i] = 0.f;
+  int half = 0;
+  int64_t t = (int64_t)blockIdx.x * RPG + threadIdx.x / (64 * W);
+  const int64_t step = (int64_t)gridDim.x * RPG;
+  Part x, dy;
+  float m = 0.f, r = 0.f;
+  auto load = [&](int64_t u, Part& px, Part& pd, float& pm, float& pr) {
+    px.load(X + u * H, place, vecs);
+    pd.load(dY + u * H, place, vecs);
+    pm = mean[u];
+    pr = rstd[u];
+  };
+  if (kAhead<W> && t < N) load(t, x, dy, m, r);
+  for (; t < N; t += step) {
+    Part x2, dy2;
+    float m2 = 0.f, r2 = 0.f;
+    if constexpr (kAhead<W>) {
+      if (t + step < N) load(t + step, x2, dy2, m2, r2);
+    } else {
+      load(t, x, dy, m, r);
+    }
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      // lanes past the row's end hold x = dy = gamma = 0
+      float v[EPC], d[EPC];
+      x.get(c, v);
+      dy.get(c, d);
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) {
+        const int i = c * EPC + e;
+        const float xh = (v[e] - m) * r, q = d[e] * ga[i];
+        s[0] += q;
+        s[1] = fmaf(q, xh, s[1]);
+        dg[i] = fmaf(d[e], xh, dg[i]);
+        db[i] += d[e];
+      }
+    }
+    row_sums<W>(s, red, half);
+    const float a = s[0] * inv, b = s[1] * inv;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (c * 64 * W + place < vecs) {
+        float v[EPC], d[EPC];
+        x.get(c, v);
+        dy.get(c, d);
+#pragma unroll
+        for (int e = 0; e < EPC; ++e)
+          d[e] = r * (fmaf(d[e], ga[c * EPC + e], -a) - (v[e] - m) * r * b);
+        Part::put(dX + t * H, c * 64 * W + place, d);
+      }
+    }
+    if constexpr (kAhead<W>) {
+      x = x2;
+      dy = dy2;
+      m = m2;
+      r = r2;
+    }
+  }
+  float* pg = part + (int64_t)blockIdx.x * 2 * H;
+  if constexpr (RPG == 1) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int at = c * 64 * W + place;
+      if (at < vecs)
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) {
+          pg[at * EPC + e] = dg[c * EPC + e];
+          pg[H + at * EPC + e] = db[c * EPC + e];
+        }
+    }
+  } else {
+    // the work-group's waves add their shares up in order
+    __shared__ float sum[2][64 * C * EPC];
+    for (int w = 0; w < RPG; ++w) {
+      if ((int)threadIdx.x >> 6 == w) {
+#pragma unroll
+        for (int i = 0; i < Part::COLS; ++i) {
+          // column of element i of this lane
+          const int at = (i / EPC * 64 + place) * EPC + i % EPC;
+          sum[0][at] = w == 0 ? dg[i] : sum[0][at] + dg[i];
+          sum[1][at] = w == 0 ? db[i] : sum[1][at] + db[i];
+        }
+      }
+      __syncthreads();
+    }
+    for (int h = threadIdx.x; h < H; h += kThreads) {
+      pg[h] = sum[0][h];
+      pg[H + h] = sum[1][h];
+    }
+  }
 }
 
 template <typename T>
@@ -90,30 +344,122 @@ __global__ __launch_bounds__(kThreads) void lnorm_backward_kernel(
   }
 }
 
-// dgamma, dbeta = sum of the slabs' shares, slabs in order.  64 columns per
-// work-group, its waves taking every fourth slab.
-__global__ __launch_bounds__(kThreads) void lnorm_fold_kernel(const float* __restrict__ part,
-                                                              int slabs, int H,
-                                                              float* __restrict__ dgamma,
-                                                              float* __restrict__ dbeta) {
-  __shared__ float red[kThreads];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+// dgamma, dbeta = sum of the slabs' shares.  64 columns per work-group; wave w
+// takes slabs w, w + 16, ... in order, then the waves' sums are added in order.
+constexpr int kFoldWaves = 16;
+__global__ __launch_bounds__(64 * kFoldWaves) void lnorm_fold_kernel(const float* __restrict__ part,
+                                                                     int slabs, int H,
+                                                                     float* __restrict__ dgamma,
+                                                                     float* __restrict__ dbeta) {
+  __shared__ float red[kFoldWaves][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
   const int width = 2 * H;
   float s = 0.f;
-  if (c < width)
-    for (int p = w; p < slabs; p += kThreads / 64) s += part[(int64_t)p * width + c];
-  red[threadIdx.x] = s;
+  if (c < width) {
+    const float* q = part + c;
+#pragma unroll 8
+    for (int p = w; p < slabs; p += kFoldWaves) s += q[(int64_t)p * width];
+  }
+  red[w][lane] = s;
   __syncthreads();
   if (w != 0 || c >= width) return;
 #pragma unroll
-  for (int v = 1; v < kThreads / 64; ++v) s += red[v * 64 + threadIdx.x];
+  for (int v = 1; v < kFoldWaves; ++v) s += red[v][lane];
   if (c < H)
     dgamma[c] = s;
   else if (dbeta)
     dbeta[c - H] = s;
 }
 
-int slabs_of(int64_t N) { return (int)std::min<int64_t>(N, kMaxSlabs); }
+// How a row is held: EPC elements per vector, W waves, C vectors per lane.  The
+// smallest W, then the smallest C, that hold it; at most four vectors per lane
+// (16 single elements), which with gamma and two sums fills the registers of
+// two waves per SIMD.  W = 0: too wide.
+struct Holding {
+  int epc, W, C;
+};
+Holding holding(const lnorm_plan_t& P, bool aligned) {
+  const int epc = 16 / elem_bytes(P.dtype);
+  if (!aligned || P.H % epc) {
+    for (int W : {1, 4, 16})
+      for (int C : {4, 16})
+        if ((W == 1 || C == 16) && P.H <= 64 * W * C) return {1, W, C};
+    return {1, 0, 0};
+  }
+  for (int W : {1, 2, 4, 8, 16})
+    for (int C : {1, 2, 4})
+      if ((W == 1 || C == 4) && (W < 16 || epc == 4) && P.H / epc <= 64 * W * C) return {epc, W, C};
+  return {1, 0, 0};
+}
+int rows_per_group(int W) { return W == 1 ? kThreads / 64 : 1; }
+int waves_per_group(int W) { return W == 1 ? kThreads / 64 : W; }
+
+// Work-groups of a pass over the rows (the backward pass's slabs).
+int row_groups(int64_t N, int W) {
+  if (W == 0) return (int)std::min<int64_t>(N, 512);
+  return (int)std::min<int64_t>(ceil_div(N, rows_per_group(W)), std::max(256, kRowWaves / waves_per_group(W)));
+}
+
+// Calls f with the holding as template arguments.
+template <typename T, typename F>
+void with_holding(const Holding& h, F f) {
+  constexpr int EPC = Elem<T>::kPer16B;
+  auto is = [&](int epc, int W, int C) { return h.epc == epc && h.W == W && h.C == C; };
+  using std::integral_constant;
+#define LNORM_CASE(e, w, c) \
+  if (is(e, w, c)) return f(integral_constant<int, e>(), integral_constant<int, w>(), integral_constant<int, c>());
+  LNORM_CASE(EPC, 1, 1)
+  LNORM_CASE(EPC, 1, 2)
+  LNORM_CASE(EPC, 1, 4)
+  LNORM_CASE(EPC, 2, 4)
+  LNORM_CASE(EPC, 4, 4)
+  LNORM_CASE(EPC, 8, 4)
+  if constexpr (EPC == 4) {
+    LNORM_CASE(EPC, 16, 4)
+  }
+  LNORM_CASE(1, 1, 4)
+  LNORM_CASE(1, 1, 16)
+  LNORM_CASE(1, 4, 16)
+  LNORM_CASE(1, 16, 16)
+#undef LNORM_CASE
+}
+
+template <typename T>
+hipError_t run_forward(const lnorm_plan_t& P, const void* X, const float* gamma, const float* beta,
+                       void* Y, float* mean, float* rstd, hipStream_t st) {
+  const Holding h = holding(P, ((uintptr_t)X | (uintptr_t)Y) % 16 == 0);
+  if (h.W == 0) {
+    const unsigned grid = (unsigned)std::min<int64_t>(P.N, kMaxRowGrid);
+    lnorm_forward_kernel<T><<<grid, kThreads, 0, st>>>((const T*)X, gamma, beta, (T*)Y, mean, rstd,
+                                                       P.N, P.H, P.eps);
+  } else {
+    const int grid = row_groups(P.N, h.W);
+    with_holding<T>(h, [&](auto e, auto w, auto c) {
+      lnorm_rows_forward_kernel<T, e.value, w.value, c.value><<<grid, kGroup<w.value>, 0, st>>>(
+          (const T*)X, gamma, beta, (T*)Y, mean, rstd, P.N, P.H, P.eps);
+    });
+  }
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run_backward(const lnorm_plan_t& P, const void* X, const float* gamma, const void* dY,
+                        const float* mean, const float* rstd, void* dX, float* part, int* slabs,
+                        hipStream_t st) {
+  const Holding h = holding(P, ((uintptr_t)X | (uintptr_t)dY | (uintptr_t)dX) % 16 == 0);
+  const int grid = *slabs = row_groups(P.N, h.W);
+  if (h.W == 0) {
+    lnorm_backward_kernel<T><<<grid, kThreads, 0, st>>>((const T*)X, gamma, (const T*)dY, mean, rstd,
+                                                        (T*)dX, part, P.N, P.H);
+  } else {
+    with_holding<T>(h, [&](auto e, auto w, auto c) {
+      lnorm_rows_backward_kernel<T, e.value, w.value, c.value><<<grid, kGroup<w.value>, 0, st>>>(
+          (const T*)X, gamma, (const T*)dY, mean, rstd, (T*)dX, part, P.N, P.H);
+    });
+  }
+  return hipGetLastError();
+}
 
 bool plan_ok(const lnorm_plan_t* p) { return p != nullptr && p->magic == kLnormMagic; }
 
@@ -132,7 +478,7 @@ MOE_API int lnorm_plan(int64_t N, int32_t H, int32_t dtype, float eps, lnorm_pla
   p.N = N;
   p.H = H;
   p.eps = eps;
-  p.bwd_workspace_bytes = (int64_t)slabs_of(N) * 2 * H * sizeof(float);
+  p.bwd_workspace_bytes = std::min<int64_t>(N, kMaxSlabs) * 2 * H * sizeof(float);
   *out = p;
   return MOE_OK;
 }
@@ -145,14 +491,10 @@ MOE_API int lnorm_forward(const lnorm_plan_t* plan, const void* X, const float* 
   if (!X || !gamma || !Y || !mean || !rstd) return MOE_EINVAL;
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
-  const unsigned grid = (unsigned)std::min<int64_t>(P.N, kMaxRowGrid);
-  if (P.dtype == MOE_BF16)
-    lnorm_forward_kernel<bf16_t><<<grid, kThreads, 0, st>>>(
-        (const bf16_t*)X, gamma, beta, (bf16_t*)Y, mean, rstd, P.N, P.H, P.eps);
-  else
-    lnorm_forward_kernel<float><<<grid, kThreads, 0, st>>>((const float*)X, gamma, beta, (float*)Y,
-                                                           mean, rstd, P.N, P.H, P.eps);
-  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
+  const hipError_t err = P.dtype == MOE_BF16
+                             ? run_forward<bf16_t>(P, X, gamma, beta, Y, mean, rstd, st)
+                             : run_forward<float>(P, X, gamma, beta, Y, mean, rstd, st);
+  return err == hipSuccess ? MOE_OK : MOE_EHIP;
 }
 
 MOE_API int lnorm_backward(const lnorm_plan_t* plan, const void* X, const float* gamma,
@@ -167,18 +509,16 @@ MOE_API int lnorm_backward(const lnorm_plan_t* plan, const void* X, const float*
   if (workspace_bytes < (size_t)P.bwd_workspace_bytes) return MOE_EWORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
-  const int slabs = slabs_of(P.N);
+  int slabs = 0;
   float* part = (float*)workspace;
   if (P.N > 0) {
-    if (P.dtype == MOE_BF16)
-      lnorm_backward_kernel<bf16_t><<<slabs, kThreads, 0, st>>>(
-          (const bf16_t*)X, gamma, (const bf16_t*)dY, mean, rstd, (bf16_t*)dX, part, P.N, P.H);
-    else
-      lnorm_backward_kernel<float><<<slabs, kThreads, 0, st>>>(
-          (const float*)X, gamma, (const float*)dY, mean, rstd, (float*)dX, part, P.N, P.H);
-    if (hipGetLastError() != hipSuccess) return MOE_EHIP;
+    const hipError_t err =
+        P.dtype == MOE_BF16
+            ? run_backward<bf16_t>(P, X, gamma, dY, mean, rstd, dX, part, &slabs, st)
+            : run_backward<float>(P, X, gamma, dY, mean, rstd, dX, part, &slabs, st);
+    if (err != hipSuccess) return MOE_EHIP;
   }
-  lnorm_fold_kernel<<<(unsigned)ceil_div(2 * (int64_t)P.H, 64), kThreads, 0, st>>>(part, slabs, P.H,
-                                                                                  dgamma, dbeta);
+  lnorm_fold_kernel<<<(unsigned)ceil_div(2 * (int64_t)P.H, 64), 64 * kFoldWaves, 0, st>>>(
+      part, slabs, P.H, dgamma, dbeta);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
 }
