@@ -68,6 +68,8 @@ struct RowPart {
   }
 };
 
+// A lane's columns of gamma or beta; 0 past the row's end and without p.
+// Vectors start on 16-byte steps (checked by the host).
 template <int EPC, int W, int C>
 __device__ __forceinline__ void load_cols(const float* p, int place, int vecs, float* out) {
 #pragma unroll
@@ -78,9 +80,10 @@ __device__ __forceinline__ void load_cols(const float* p, int place, int vecs, f
     } else {
 #pragma unroll
       for (int e = 0; e < EPC; e += 4) {
-        // gamma and beta may start off a 16-byte step
+        f32x4_t v{0.f, 0.f, 0.f, 0.f};
+        if (p && at < vecs) v = *reinterpret_cast<const f32x4_t*>(p + at * EPC + e);
 #pragma unroll
-        for (int f = 0; f < 4; ++f) out[c * EPC + e + f] = p && at < vecs ? p[at * EPC + e + f] : 0.f;
+        for (int f = 0; f < 4; ++f) out[c * EPC + e + f] = v[f];
       }
     }
   }
@@ -428,7 +431,7 @@ void with_holding(const Holding& h, F f) {
 template <typename T>
 hipError_t run_forward(const lnorm_plan_t& P, const void* X, const float* gamma, const float* beta,
                        void* Y, float* mean, float* rstd, hipStream_t st) {
-  const Holding h = holding(P, ((uintptr_t)X | (uintptr_t)Y) % 16 == 0);
+  const Holding h = holding(P, ((uintptr_t)X | (uintptr_t)Y | (uintptr_t)gamma | (uintptr_t)beta) % 16 == 0);
   if (h.W == 0) {
     const unsigned grid = (unsigned)std::min<int64_t>(P.N, kMaxRowGrid);
     lnorm_forward_kernel<T><<<grid, kThreads, 0, st>>>((const T*)X, gamma, beta, (T*)Y, mean, rstd,
@@ -447,7 +450,7 @@ template <typename T>
 hipError_t run_backward(const lnorm_plan_t& P, const void* X, const float* gamma, const void* dY,
                         const float* mean, const float* rstd, void* dX, float* part, int* slabs,
                         hipStream_t st) {
-  const Holding h = holding(P, ((uintptr_t)X | (uintptr_t)dY | (uintptr_t)dX) % 16 == 0);
+  const Holding h = holding(P, ((uintptr_t)X | (uintptr_t)dY | (uintptr_t)dX | (uintptr_t)gamma) % 16 == 0);
   const int grid = *slabs = row_groups(P.N, h.W);
   if (h.W == 0) {
     lnorm_backward_kernel<T><<<grid, kThreads, 0, st>>>((const T*)X, gamma, (const T*)dY, mean, rstd,
