@@ -56,7 +56,7 @@ __device__ __forceinline__ bool list_softmax(const KdArgs& a, int64_t t, int lan
     }
     top = fmaxf(top, logp[q]);
   }
-  top = run_max<64>(top);
+  top = run_maxf<64>(top);
   const bool any = top > -INFINITY;
   float z = 0.f;
 #pragma unroll

@@ -2,13 +2,21 @@
 // softmax or sigmoid scores with a bias and a group limit, the gates, and the
 // gradient of the logits.
 //
-// One wave per token; lane l holds the logits of experts l, l + 64, ....  The
-// selection runs k rounds; a round takes the largest remaining rank over the
-// wave, then the lowest expert index that holds it.  Ranks are compared as
-// unsigned integers that order as the values do (0: not to be selected), so
-// any input, NaN included, gives k distinct experts.
-#include <climits>
+// The bytes are few (a row of logits in, k pairs out), so the selection's
+// instructions decide.  A token takes 16 lanes of up to 16 experts each (64
+// lanes past 256 experts), so that a wave selects for four tokens at once and
+// every reduction stays inside a row of lanes, in DPP operands.  The selection
+// runs k rounds: the largest remaining rank, then the lowest expert that holds
+// it.  Ranks are unsigned integers that order as the values do (0: not to be
+// selected), so any input, NaN included, gives k distinct experts.
+//
+// Logits rank exactly as they are.  Scores with a bias, and group strengths,
+// are formed in 32 bits first; a token where two values that decide something
+// are nearer than their error bound is selected again in 64 bits by its whole
+// wave (route_exact).
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "device_common.hpp"
 #include "moe_internal.h"
@@ -40,19 +48,26 @@ __device__ __forceinline__ uint64_t order_of(double v) {
   const uint64_t o = b ^ ((b >> 63) ? ~0ull : 1ull << 63);
   return o ? o : 1ull;
 }
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  const uint32_t o = b ^ ((b >> 31) ? ~0u : 1u << 31);
+  return o ? o : 1u;
+}
+// The value that ranks as o (o != 0).
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o ^ ((o >> 31) ? 1u << 31 : ~0u));
+}
 
 __device__ __forceinline__ bool is_masked(float l) { return !(l > -INFINITY); }
 
+// One token's selection in 64 bits by the whole wave (every lane of it calls):
+// lane s returns slot s's expert.  lds: E + n_group doubles of the wave's own.
 template <int V>
-__global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs a) {
-  extern __shared__ double smem[];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kWaves + w;
-  if (t >= a.N) return;  // whole wave leaves together; no work-group barrier below
+__device__ __noinline__ int route_exact(const RouteArgs& a, int64_t t, double* lds) {
+  const int lane = threadIdx.x & 63;
   const float* row = a.logits + t * a.E;
   const int per = a.E / a.n_group;
-  float l[V];
-  float top = -INFINITY;
+  float l[V], top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int e = lane + 64 * j;
@@ -60,47 +75,45 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     if (is_masked(l[j])) l[j] = -INFINITY;
     top = fmaxf(top, l[j]);
   }
-  top = run_max<64>(top);
-  // v_e, in 64 bits
-  double v[V], z = 0.0;
+  top = run_maxf<64>(top);
+  double v[V];
   if (a.sigmoid) {
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] = 1.0 / (1.0 + exp(-(double)l[j]));
   } else {
+    double z = 0.0;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       v[j] = is_masked(l[j]) ? 0.0 : exp((double)l[j] - (double)top);
       z += v[j];
     }
-    z = run_sum64<64>(z);
+    z = wave_sum(z);
     const double inv = z > 0.0 ? 1.0 / z : 0.0;
 #pragma unroll
     for (int j = 0; j < V; ++j) v[j] *= inv;
   }
-  if (a.bias) {
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (lane + 64 * j < a.E) v[j] += (double)a.bias[lane + 64 * j];
-  }
   uint64_t rank[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-    rank[j] = lane + 64 * j >= a.E ? 0ull
-              : is_masked(l[j])    ? order_of(-INFINITY)
-                                   : order_of(a.bias ? v[j] : (double)l[j]);
+  for (int j = 0; j < V; ++j) {
+    const int e = lane + 64 * j;
+    if (a.bias && e < a.E) v[j] += (double)a.bias[e];
+    rank[j] = e >= a.E            ? 0ull
+              : is_masked(l[j])   ? order_of(-(double)INFINITY)
+                                  : order_of(a.bias ? v[j] : (double)l[j]);
+  }
   if (a.n_group > 1) {
     // group strengths: lane g sums group g's best values out of LDS
-    double* val = smem + w * (kRouteMaxE + kRouteMaxGroups);
-    double* strength = val + kRouteMaxE;
+    double* strength = lds + a.E;
+    wave_lds_order();  // earlier uses of the wave's LDS are done
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (lane + 64 * j < a.E) val[lane + 64 * j] = is_masked(l[j]) ? -INFINITY : v[j];
+      if (lane + 64 * j < a.E) lds[lane + 64 * j] = is_masked(l[j]) ? -INFINITY : v[j];
     wave_lds_order();
     double mine = -INFINITY;
     if (lane < a.n_group) {
       double b1 = -INFINITY, b2 = -INFINITY;
       for (int i = 0; i < per; ++i) {
-        const double x = val[lane * per + i];
+        const double x = lds[lane * per + i];
         b2 = fmax(b2, fmin(b1, x));
         b1 = fmax(b1, x);
       }
@@ -110,8 +123,9 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     wave_lds_order();
     int before = 0;
     for (int h = 0; h < a.n_group; ++h)
-      before += strength[h] > mine || (!(mine > strength[h]) && h < lane) ? 1 : 0;
+      before += strength[h] > mine || (strength[h] == mine && h < lane) ? 1 : 0;
     const uint64_t kept = __ballot(lane < a.n_group && before < a.topk_group);
+    wave_lds_order();
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if (lane + 64 * j < a.E && !((kept >> ((lane + 64 * j) / per)) & 1)) rank[j] = 0ull;
@@ -121,41 +135,231 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     uint64_t best = 0ull;
 #pragma unroll
     for (int j = 0; j < V; ++j) best = rank[j] > best ? rank[j] : best;
-    best = run_max<64>(best);
-    int at = INT_MAX;
+    best = wave_max(best);
+    uint32_t at = ~0u;
 #pragma unroll
     for (int j = V - 1; j >= 0; --j)
       if (rank[j] == best) at = lane + 64 * j;
-    at = run_min<64>(at);
+    at = run_minu<64>(at);
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (at == lane + 64 * j) rank[j] = 0ull;
-    if (lane == s) my_i = at;
+      if ((int)at == lane + 64 * j) rank[j] = 0ull;
+    if (lane == s) my_i = (int)at;
   }
-  // gates of the selected, lane s for slot s
-  float ls = -INFINITY;
-  if (lane < a.k) {
-    ls = row[my_i];
-    if (is_masked(ls)) ls = -INFINITY;
+  return my_i;
+}
+
+enum RouteMode { kByLogit, kByScore, kGrouped };  // kByScore: with a bias
+
+// LDS of one wave: four tokens' values, padded by one a group so that lanes
+// that read one group each meet different banks, and strengths; or
+// route_exact's doubles.
+template <int G>
+size_t route_lds(int E, int n_group) {
+  if (n_group == 1) return 0;
+  const size_t fast = (64 / G) * (size_t)(E + 2 * n_group) * sizeof(float);
+  const size_t exact = (size_t)(E + n_group) * sizeof(double);
+  return (std::max(fast, exact) + 15) / 16 * 16;
+}
+
+// G lanes per token, V experts per lane, up to SLOTS slots per lane.  Lane ln
+// holds expert (j / 4) 4 G + (vec ? 4 ln + j % 4 : ln + (j % 4) G) as its j-th:
+// ascending in j, and 16 bytes at a time where rows start on 16-byte steps.
+template <int G, int V, int MODE, int SLOTS>
+__global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs a, int vec,
+                                                                 uint32_t per_mul, int wave_lds) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  constexpr int TPW = 64 / G;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int ln = lane % G, sub = lane / G;
+  const int64_t t0 = ((int64_t)blockIdx.x * kWaves + w) * TPW;
+  if (t0 >= a.N) return;  // whole wave leaves together; no work-group barrier below
+  const bool valid = t0 + sub < a.N;
+  const int64_t t = min(t0 + sub, a.N - 1);
+  const float* row = a.logits + t * a.E;
+  const int mine = vec ? 4 * ln : ln, step = vec ? 1 : G;
+  auto place = [&](int j) { return (j / 4) * 4 * G + (j % 4) * step; };  // expert j's index, less `mine`
+
+  float l[V];
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      f32x4_t q{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (mine + place(j) < a.E) q = *reinterpret_cast<const f32x4_t*>(row + mine + place(j));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) l[j + i] = q[i];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) l[j] = mine + place(j) < a.E ? row[mine + place(j)] : -INFINITY;
   }
-  float g;
+  float top = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    if (is_masked(l[j])) l[j] = -INFINITY;  // NaN
+    top = fmaxf(top, l[j]);
+  }
+  float inv_z = 0.f;
+  if (!a.sigmoid && (MODE != kByLogit || !a.renorm)) {
+    top = run_maxf<G>(top);
+    float z = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) z += is_masked(l[j]) ? 0.f : __expf(l[j] - top);
+    z = run_sum<G>(z);
+    inv_z = z > 0.f ? 1.f / z : 0.f;
+  }
+
+  uint32_t rank[V];
+  bool near = false;  // two values that decide something are too near for 32 bits
+  if constexpr (MODE == kByLogit) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) rank[j] = mine + place(j) < a.E ? order_of(l[j]) : 0u;
+  } else {
+    // v_e.  A score is off by less than 5e-7 (its exponential's argument is
+    // rounded, which costs at most max x exp(-x) = 0.37 of a step; a sum of up
+    // to 1024 terms, 22 steps), adding the bias rounds once more.
+    float v[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      v[j] = a.sigmoid ? logistic(l[j]) : is_masked(l[j]) ? 0.f : __expf(l[j] - top) * inv_z;
+      if (a.bias && mine + place(j) < a.E) v[j] += a.bias[mine + place(j)];
+      rank[j] = mine + place(j) >= a.E ? 0u
+                : is_masked(l[j])      ? order_of(-INFINITY)
+                                       : order_of(a.bias ? v[j] : l[j]);
+    }
+    if constexpr (MODE == kGrouped) {
+      const int per = a.E / a.n_group;
+      float* val = reinterpret_cast<float*>(smem + w * wave_lds) + sub * (a.E + 2 * a.n_group);
+      float* strength = val + a.E + a.n_group;
+      int grp[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int e = mine + place(j);
+        grp[j] = (int)(((uint32_t)e * per_mul) >> 20);
+        if (e < a.E) val[e + grp[j]] = is_masked(l[j]) ? -INFINITY : v[j];
+      }
+      wave_lds_order();
+      for (int g = ln; g < a.n_group; g += G) {
+        float b1 = -INFINITY, b2 = -INFINITY;
+        const float* q = val + g * (per + 1);
+        for (int i = 0; i < per; ++i) {
+          b2 = __builtin_amdgcn_fmed3f(b2, b1, q[i]);  // b2 <= b1: the second largest of the three
+          b1 = fmaxf(b1, q[i]);
+        }
+        strength[g] = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+      }
+      wave_lds_order();
+      uint32_t lo = 0u, hi = 0u;
+      float weakest = INFINITY, next = -INFINITY;  // of the kept, the best of the others
+      for (int g = ln; g < a.n_group; g += G) {
+        const float x = strength[g];
+        int before = 0;
+        for (int h = 0; h < a.n_group; ++h)
+          before += strength[h] > x || (strength[h] == x && h < g) ? 1 : 0;
+        if (before < a.topk_group) {
+          weakest = fminf(weakest, x);
+          if (g < 32) lo |= 1u << g; else hi |= 1u << (g - 32);
+        } else {
+          next = fmaxf(next, x);
+        }
+      }
+      lo = run_or<G>(lo);
+      hi = run_or<G>(hi);
+      weakest = run_minf<G>(weakest);
+      next = run_maxf<G>(next);
+      near = next > -INFINITY && !(weakest - next > 4e-6f * (1.f + fabsf(next)));
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (!(((grp[j] < 32 ? lo : hi) >> (grp[j] & 31)) & 1)) rank[j] = 0u;
+    }
+  }
+
+  int my_i[SLOTS];
+#pragma unroll
+  for (int q = 0; q < SLOTS; ++q) my_i[q] = 0;
+  const bool close = MODE != kByLogit && a.bias;  // ranks are scores, not exact
+  float prev = INFINITY;
+  for (int s = 0; s < a.k + (close ? 1 : 0); ++s) {
+    uint32_t best = 0u;
+#pragma unroll
+    for (int j = 0; j < V; ++j) best = max(best, rank[j]);
+    best = run_maxu<G>(best);
+    if (close) {
+      const float x = best ? value_of(best) : -INFINITY;
+      near |= x > -INFINITY && !(prev - x > 2e-6f * (1.f + fabsf(x)));
+      prev = x;
+      if (s == a.k) break;
+    }
+    uint32_t at = ~0u;
+#pragma unroll
+    for (int j = V - 1; j >= 0; --j)
+      if (rank[j] == best) at = place(j);
+    at = run_minu<G>(at == ~0u ? at : at + mine);
+    const uint32_t mine_at = at - mine;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if ((int)mine_at == place(j)) rank[j] = 0u;
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q)
+      if (ln + G * q == s) my_i[q] = (int)at;
+  }
+  if constexpr (MODE != kByLogit) {
+    uint64_t again = __ballot(near && valid && ln == 0);
+    while (again) {
+      const int first = __builtin_ctzll(again);
+      again &= again - 1;
+      const int at = route_exact<(G * V + 63) / 64>(a, t0 + first / G,
+                                                    reinterpret_cast<double*>(smem + w * wave_lds));
+#pragma unroll
+      for (int q = 0; q < SLOTS; ++q) {
+        const int x = __shfl(at, (ln + G * q) & 63);
+        if (sub == first / G) my_i[q] = x;
+      }
+    }
+  }
+
+  // gates, lane ln for slots ln + G q
+  float ls[SLOTS], g[SLOTS], m = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < SLOTS; ++q) {
+    ls[q] = -INFINITY;
+    if (ln + G * q < a.k) {
+      ls[q] = row[my_i[q]];
+      if (is_masked(ls[q])) ls[q] = -INFINITY;
+    }
+    m = fmaxf(m, ls[q]);
+  }
   if (a.renorm) {
     // scores relative to the largest one selected: no sum underflows
-    const float m = run_max<64>(ls);
+    m = run_maxf<G>(m);
     const float c = a.sigmoid ? fminf(m, 0.f) : m;
-    float r = 0.f;
-    if (ls > -INFINITY)
-      r = !a.sigmoid ? expf(ls - c) : ls < 0.f ? expf(ls - c) / (1.f + expf(ls)) : 1.f / (1.f + expf(-ls));
-    const float sum = run_sum<64>(r);
-    g = sum > 0.f ? a.scale * (r / sum) : 0.f;
-  } else if (a.sigmoid) {
-    g = a.scale * (ls < 0.f ? expf(ls) / (1.f + expf(ls)) : 1.f / (1.f + expf(-ls)));
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) {
+      g[q] = 0.f;
+      if (ls[q] > -INFINITY)
+        g[q] = !a.sigmoid ? expf(ls[q] - c) : ls[q] < 0.f ? expf(ls[q] - c) / (1.f + expf(ls[q])) : 1.f / (1.f + expf(-ls[q]));
+      sum += g[q];
+    }
+    sum = run_sum<G>(sum);
+    const float f = sum > 0.f ? a.scale / sum : 0.f;
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) g[q] *= f;
   } else {
-    g = ls > -INFINITY ? a.scale * (expf(ls - top) / (float)z) : 0.f;
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) {
+      if (a.sigmoid)
+        g[q] = a.scale * (ls[q] < 0.f ? expf(ls[q]) / (1.f + expf(ls[q])) : 1.f / (1.f + expf(-ls[q])));
+      else
+        g[q] = ls[q] > -INFINITY ? a.scale * (expf(ls[q] - top) * inv_z) : 0.f;
+    }
   }
-  if (lane < a.k) {
-    a.idx[t * a.k + lane] = my_i;
-    a.gates[t * a.k + lane] = g;
+#pragma unroll
+  for (int q = 0; q < SLOTS; ++q) {
+    if (valid && ln + G * q < a.k) {
+      a.idx[t * a.k + ln + G * q] = my_i[q];
+      a.gates[t * a.k + ln + G * q] = g[q];
+    }
   }
 }
 
@@ -169,74 +373,161 @@ struct RouteBwdArgs {
   float scale;
 };
 
-// One wave per token: lane s works out slot s's share, the row goes through
-// LDS (zeros or the softmax's dense part, then the selected experts' shares
-// added) and out.
-template <int V>
-__global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteBwdArgs a) {
-  __shared__ float out[kWaves][kRouteMaxE];
+// G lanes per token as in the forward pass: lane ln works out the shares of
+// slots ln + G q, the row goes through LDS (zeros or the softmax's dense part,
+// then the selected experts' shares added) and out.
+template <int G, int V, int SLOTS>
+__global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteBwdArgs a, int vec) {
+  constexpr int TPW = 64 / G;
+  __shared__ __attribute__((aligned(16))) float rows[kWaves * TPW][G * V];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kWaves + w;
-  if (t >= a.N) return;  // whole wave leaves together
+  const int ln = lane % G, sub = lane / G;
+  const int64_t t0 = ((int64_t)blockIdx.x * kWaves + w) * TPW;
+  if (t0 >= a.N) return;  // whole wave leaves together
+  const bool valid = t0 + sub < a.N;
+  const int64_t t = min(t0 + sub, a.N - 1);
   const float* row = a.logits + t * a.E;
+  float* out = rows[w * TPW + sub];
+  const int mine = vec ? 4 * ln : ln, step = vec ? 1 : G;
+  auto place = [&](int j) { return (j / 4) * 4 * G + (j % 4) * step; };
+
+  int e[SLOTS];
+  float ls[SLOTS], dg[SLOTS], wgt[SLOTS], m = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < SLOTS; ++q) {
+    e[q] = -1;
+    ls[q] = -INFINITY;
+    dg[q] = 0.f;
+    if (ln + G * q < a.k) {
+      e[q] = a.idx[t * a.k + ln + G * q];
+      dg[q] = a.dgates[t * a.k + ln + G * q];
+      if ((unsigned)e[q] < (unsigned)a.E) ls[q] = row[e[q]];
+      if (is_masked(ls[q])) {  // a gate fixed at 0
+        ls[q] = -INFINITY;
+        e[q] = -1;
+        dg[q] = 0.f;
+      }
+    }
+    m = fmaxf(m, ls[q]);
+  }
   const bool dense = !a.sigmoid && !a.renorm;
-  float l[V], top = -INFINITY, z = 0.f;
+  float l[V], top = -INFINITY, inv_z = 0.f;
   if (dense) {
+    if (vec) {
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        f32x4_t q{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (mine + place(j) < a.E) q = *reinterpret_cast<const f32x4_t*>(row + mine + place(j));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) l[j + i] = q[i];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) l[j] = mine + place(j) < a.E ? row[mine + place(j)] : -INFINITY;
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      l[j] = lane + 64 * j < a.E ? row[lane + 64 * j] : -INFINITY;
       if (is_masked(l[j])) l[j] = -INFINITY;
       top = fmaxf(top, l[j]);
     }
-    top = run_max<64>(top);
+    top = run_maxf<G>(top);
+    float z = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      l[j] = is_masked(l[j]) ? 0.f : expf(l[j] - top);
+      l[j] = is_masked(l[j]) ? 0.f : __expf(l[j] - top);
       z += l[j];
     }
-    z = run_sum<64>(z);
-    z = z > 0.f ? 1.f / z : 0.f;
+    z = run_sum<G>(z);
+    inv_z = z > 0.f ? 1.f / z : 0.f;
   }
-  int e = -1;
-  float ls = -INFINITY, dg = 0.f;
-  if (lane < a.k) {
-    e = a.idx[t * a.k + lane];
-    if ((unsigned)e < (unsigned)a.E) {
-      ls = row[e];
-      if (is_masked(ls)) ls = -INFINITY;
-    } else {
-      e = -1;
-    }
-    dg = a.dgates[t * a.k + lane];
-  }
-  const bool live = ls > -INFINITY;
-  if (!live) dg = 0.f;  // a gate fixed at 0
-  const float sig = ls < 0.f ? expf(ls) / (1.f + expf(ls)) : 1.f / (1.f + expf(-ls));
-  const float one_less = ls < 0.f ? 1.f / (1.f + expf(ls)) : expf(-ls) / (1.f + expf(-ls));
-  float wgt = 0.f;  // g / scale
+  // w_s = g_s / scale
   if (a.renorm) {
-    const float m = run_max<64>(ls);
+    m = run_maxf<G>(m);
     const float c = a.sigmoid ? fminf(m, 0.f) : m;
-    float r = 0.f;
-    if (live) r = !a.sigmoid ? expf(ls - c) : ls < 0.f ? expf(ls - c) / (1.f + expf(ls)) : sig;
-    const float sum = run_sum<64>(r);
-    wgt = sum > 0.f ? r / sum : 0.f;
-  } else if (live) {
-    wgt = a.sigmoid ? sig : expf(ls - top) * z;
+    float sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) {
+      wgt[q] = 0.f;
+      if (e[q] >= 0)
+        wgt[q] = !a.sigmoid ? expf(ls[q] - c) : ls[q] < 0.f ? expf(ls[q] - c) / (1.f + expf(ls[q])) : 1.f / (1.f + expf(-ls[q]));
+      sum += wgt[q];
+    }
+    sum = run_sum<G>(sum);
+    const float f = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) wgt[q] *= f;
+  } else {
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) {
+      if (a.sigmoid)
+        wgt[q] = ls[q] < 0.f ? expf(ls[q]) / (1.f + expf(ls[q])) : 1.f / (1.f + expf(-ls[q]));
+      else
+        wgt[q] = e[q] >= 0 ? expf(ls[q] - top) * inv_z : 0.f;
+    }
   }
-  // d_s = scale dg_s - sum_j g_j dg_j
-  const float dot = a.sigmoid && !a.renorm ? 0.f : a.scale * run_sum<64>(wgt * dg);
-  float d = wgt * (a.scale * dg - (dense ? 0.f : dot));
-  if (a.sigmoid) d *= one_less;
+  float dot = 0.f;  // sum_j g_j dg_j
+  if (!a.sigmoid || a.renorm) {
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-    if (lane + 64 * j < a.E) out[w][lane + 64 * j] = dense ? -(l[j] * z) * dot : 0.f;
-  wave_lds_order();
-  if (e >= 0 && live) out[w][e] += d;
+    for (int q = 0; q < SLOTS; ++q) dot = fmaf(wgt[q], dg[q], dot);
+    dot = a.scale * run_sum<G>(dot);
+  }
+#pragma unroll
+  for (int j = 0; j < V; j += 4) {
+    f32x4_t q{0.f, 0.f, 0.f, 0.f};
+    if (dense)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = -(l[j + i] * inv_z) * dot;
+    if (vec) {
+      *reinterpret_cast<f32x4_t*>(out + mine + place(j)) = q;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[mine + place(j + i)] = q[i];
+    }
+  }
   wave_lds_order();
 #pragma unroll
-  for (int j = 0; j < V; ++j)
-    if (lane + 64 * j < a.E) a.dlogits[t * a.E + lane + 64 * j] = out[w][lane + 64 * j];
+  for (int q = 0; q < SLOTS; ++q) {
+    if (e[q] >= 0) {
+      float d = wgt[q] * (a.scale * dg[q] - (dense ? 0.f : dot));
+      if (a.sigmoid)  // 1 - s
+        d *= ls[q] < 0.f ? 1.f / (1.f + expf(ls[q])) : expf(-ls[q]) / (1.f + expf(-ls[q]));
+      out[e[q]] += d;
+    }
+  }
+  wave_lds_order();
+  if (!valid) return;
+  float* to = a.dlogits + t * a.E;
+  if (vec) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4)
+      if (mine + place(j) < a.E)
+        *reinterpret_cast<f32x4_t*>(to + mine + place(j)) = *reinterpret_cast<const f32x4_t*>(out + mine + place(j));
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (mine + place(j) < a.E) to[mine + place(j)] = out[mine + place(j)];
+  }
+}
+
+// Calls f with lanes per token, experts per lane and slots per lane.
+template <typename F>
+void with_shape(int E, int k, F f) {
+  using std::integral_constant;
+#define ROUTE_SHAPE(g, v, s) f(integral_constant<int, g>(), integral_constant<int, v>(), integral_constant<int, s>())
+  if (E > 512) return ROUTE_SHAPE(64, 16, 1);
+  if (E > 256) return ROUTE_SHAPE(64, 8, 1);
+  if (k > 16) {
+    if (E > 64) return ROUTE_SHAPE(16, 16, 4);
+    return ROUTE_SHAPE(16, 4, 4);
+  }
+  if (E > 128) return ROUTE_SHAPE(16, 16, 1);
+  if (E > 64) return ROUTE_SHAPE(16, 8, 1);
+  return ROUTE_SHAPE(16, 4, 1);
+#undef ROUTE_SHAPE
+}
+
+bool rows_aligned(int E, const void* p, const void* q) {
+  return E % 4 == 0 && ((uintptr_t)p | (uintptr_t)q) % 16 == 0;
 }
 
 bool plan_ok(const route_plan_t* p) { return p != nullptr && p->magic == kRouteMagic; }
@@ -280,17 +571,24 @@ MOE_API int route_forward(const route_plan_t* plan, const float* logits, const f
   if (!logits || !topk_idx || !gates) return MOE_EINVAL;
   const RouteArgs a{logits, bias,      topk_idx,     gates,       P.N,      P.E,    P.k,
                     P.score, P.n_group, P.topk_group, P.group_top, P.renorm, P.scale};
-  const unsigned grid = (unsigned)ceil_div(P.N, kWaves);
-  const size_t lds = P.n_group > 1 ? kWaves * (kRouteMaxE + kRouteMaxGroups) * sizeof(double) : 0;
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
-  const int vpl = (P.E + 63) / 64;
-  if (vpl <= 1)
-    route_forward_kernel<1><<<grid, kThreads, lds, st>>>(a);
-  else if (vpl <= 4)
-    route_forward_kernel<4><<<grid, kThreads, lds, st>>>(a);
-  else
-    route_forward_kernel<16><<<grid, kThreads, lds, st>>>(a);
+  const int vec = rows_aligned(P.E, logits, nullptr);
+  const int mode = P.n_group > 1 ? kGrouped : bias ? kByScore : kByLogit;
+  const int per = P.E / P.n_group;
+  // e / per as a product: exact for e < 1024, per < 1024
+  const uint32_t per_mul = ((1u << 20) + per - 1) / per;
+  with_shape(P.E, P.k, [&](auto g, auto v, auto s) {
+    constexpr int G = g.value, V = v.value, S = s.value;
+    const unsigned grid = (unsigned)ceil_div(P.N, kWaves * (64 / G));
+    const size_t lds = route_lds<G>(P.E, P.n_group);
+    if (mode == kByLogit)
+      route_forward_kernel<G, V, kByLogit, S><<<grid, kThreads, 0, st>>>(a, vec, per_mul, 0);
+    else if (mode == kByScore)
+      route_forward_kernel<G, V, kByScore, S><<<grid, kThreads, 0, st>>>(a, vec, per_mul, 0);
+    else
+      route_forward_kernel<G, V, kGrouped, S><<<grid, kThreads, kWaves * lds, st>>>(a, vec, per_mul, (int)lds);
+  });
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
 }
 
@@ -301,15 +599,13 @@ MOE_API int route_backward(const route_plan_t* plan, const float* logits, const 
   if (P.N == 0) return MOE_OK;
   if (!logits || !topk_idx || !dgates || !dlogits) return MOE_EINVAL;
   const RouteBwdArgs a{logits, topk_idx, dgates, dlogits, P.N, P.E, P.k, P.score, P.renorm, P.scale};
-  const unsigned grid = (unsigned)ceil_div(P.N, kWaves);
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
-  const int vpl = (P.E + 63) / 64;
-  if (vpl <= 1)
-    route_backward_kernel<1><<<grid, kThreads, 0, st>>>(a);
-  else if (vpl <= 4)
-    route_backward_kernel<4><<<grid, kThreads, 0, st>>>(a);
-  else
-    route_backward_kernel<16><<<grid, kThreads, 0, st>>>(a);
+  const int vec = rows_aligned(P.E, logits, dlogits);
+  with_shape(P.E, P.k, [&](auto g, auto v, auto s) {
+    constexpr int G = g.value, V = v.value, S = s.value;
+    const unsigned grid = (unsigned)ceil_div(P.N, kWaves * (64 / G));
+    route_backward_kernel<G, V, S><<<grid, kThreads, 0, st>>>(a, vec);
+  });
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
 }

@@ -19,35 +19,66 @@ __device__ __forceinline__ void wave_lds_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Reductions over aligned runs of G lanes by xor butterflies: commutative
-// pairwise steps, so every lane of the run ends with the same bits.
-template <int G>
-__device__ __forceinline__ float run_sum(float v) {
-#pragma unroll
-  for (int o = 1; o < G; o <<= 1) v += __shfl_xor(v, o);
-  return v;
+// v of the lane n places around the lane's row of 16 (a DPP operand, no LDS).
+template <int n, typename V>
+__device__ __forceinline__ V row_ror(V v) {
+  static_assert(sizeof(V) == 4, "one register");
+  return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + n, 0xf, 0xf, false));
 }
-template <int G, typename V>
-__device__ __forceinline__ V run_sum64(V v) {
-#pragma unroll
-  for (int o = 1; o < G; o <<= 1) v += __shfl_xor(v, o);
-  return v;
-}
-template <int G, typename V>
-__device__ __forceinline__ V run_max(V v) {
-#pragma unroll
-  for (int o = 1; o < G; o <<= 1) {
-    const V w = __shfl_xor(v, o);
-    v = w > v ? w : v;
+
+// Reductions over aligned runs of G = 16 or 64 lanes; every lane of the run ends
+// with the same bits.  Within a row of 16 by rotations, whose pairs are
+// combined commutatively step by step; the four rows through lanes 0, 16, 32,
+// 48 in order.
+template <int G, typename V, typename Op>
+__device__ __forceinline__ V run_reduce(V v, Op op) {
+  static_assert(G == 16 || G == 64, "a row or a wave");
+  v = op(v, row_ror<8>(v));
+  v = op(v, row_ror<4>(v));
+  v = op(v, row_ror<2>(v));
+  v = op(v, row_ror<1>(v));
+  if constexpr (G == 64) {
+    auto lane = [&](int l) { return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
+    v = op(op(lane(0), lane(16)), op(lane(32), lane(48)));
   }
   return v;
 }
-template <int G, typename V>
-__device__ __forceinline__ V run_min(V v) {
+template <int G>
+__device__ __forceinline__ float run_sum(float v) {
+  return run_reduce<G>(v, [](float a, float b) { return a + b; });
+}
+template <int G>
+__device__ __forceinline__ float run_maxf(float v) {
+  return run_reduce<G>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int G>
+__device__ __forceinline__ float run_minf(float v) {
+  return run_reduce<G>(v, [](float a, float b) { return fminf(a, b); });
+}
+template <int G>
+__device__ __forceinline__ uint32_t run_maxu(uint32_t v) {
+  return run_reduce<G>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int G>
+__device__ __forceinline__ uint32_t run_minu(uint32_t v) {
+  return run_reduce<G>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+template <int G>
+__device__ __forceinline__ uint32_t run_or(uint32_t v) {
+  return run_reduce<G>(v, [](uint32_t a, uint32_t b) { return a | b; });
+}
+
+// 64-bit values over a wave, by xor butterflies.
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
-  for (int o = 1; o < G; o <<= 1) {
-    const V w = __shfl_xor(v, o);
-    v = w < v ? w : v;
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint64_t w = __shfl_xor(v, o);
+    v = w > v ? w : v;
   }
   return v;
 }

@@ -131,6 +131,23 @@ def test_near_ties_are_told_apart(score, groups):
         check(l, bias, up, k, score, *groups, 2, True, 1.0, ("near", score, bias is None))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(64, (1, 1)), (64, (8, 2)), (512, (16, 3)), (256, (64, 2))])
+def test_infinite_logits_still_give_distinct_experts(E, groups, score):
+    require_lib()
+    l = torch.randn(64, E, device=DEV)
+    l[torch.rand(64, E, device=DEV) < 0.2] = float("inf")
+    l[torch.rand(64, E, device=DEV) < 0.2] = float("-inf")
+    l[torch.rand(64, E, device=DEV) < 0.1] = float("nan")
+    for bias in (None, torch.randn(E, device=DEV)):
+        for renorm in (True, False):
+            plan = B.route_plan(64, E, 7, score, *groups, 2, renorm)
+            idx, gates = B.route_forward(plan, l, bias)
+            B.route_backward(plan, l, idx, torch.randn(64, 7, device=DEV))
+            i = idx.cpu().numpy()
+            assert i.min() >= 0 and i.max() < E and all(len(set(r)) == 7 for r in i.tolist())
+
+
 def test_unaligned_rows_other_stream_and_untouched_neighbours():
     require_lib()
     rng = np.random.default_rng(9)
