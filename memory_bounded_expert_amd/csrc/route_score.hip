@@ -112,6 +112,7 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, int64_t t, double* l
     double mine = -INFINITY;
     if (lane < a.n_group) {
       double b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll 8
       for (int i = 0; i < per; ++i) {
         const double x = lds[lane * per + i];
         b2 = fmax(b2, fmin(b1, x));
@@ -132,10 +133,13 @@ __device__ __noinline__ int route_exact(const RouteArgs& a, int64_t t, double* l
   }
   int my_i = 0;
   for (int s = 0; s < a.k; ++s) {
-    uint64_t best = 0ull;
+    uint64_t own = 0ull;
 #pragma unroll
-    for (int j = 0; j < V; ++j) best = rank[j] > best ? rank[j] : best;
-    best = wave_max(best);
+    for (int j = 0; j < V; ++j) own = rank[j] > own ? rank[j] : own;
+    // the largest over the wave, its high half first
+    const uint32_t hi = run_maxu<64>((uint32_t)(own >> 32));
+    const uint32_t lo = run_maxu<64>((uint32_t)(own >> 32) == hi ? (uint32_t)own : 0u);
+    const uint64_t best = (uint64_t)hi << 32 | lo;
     uint32_t at = ~0u;
 #pragma unroll
     for (int j = V - 1; j >= 0; --j)
@@ -169,6 +173,7 @@ template <int G, int V, int MODE, int SLOTS>
 __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs a, int vec,
                                                                  uint32_t per_mul, int wave_lds) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  __shared__ uint64_t lists[kWaves][SLOTS == 1 ? 64 : 1];
   constexpr int TPW = 64 / G;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int ln = lane % G, sub = lane / G;
@@ -242,6 +247,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
       for (int g = ln; g < a.n_group; g += G) {
         float b1 = -INFINITY, b2 = -INFINITY;
         const float* q = val + g * (per + 1);
+#pragma unroll 8
         for (int i = 0; i < per; ++i) {
           b2 = __builtin_amdgcn_fmed3f(b2, b1, q[i]);  // b2 <= b1: the second largest of the three
           b1 = fmaxf(b1, q[i]);
@@ -275,17 +281,90 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
   }
 
   int my_i[SLOTS];
+  float my_v[SLOTS];  // the values they rank by
 #pragma unroll
-  for (int q = 0; q < SLOTS; ++q) my_i[q] = 0;
+  for (int q = 0; q < SLOTS; ++q) my_i[q] = 0, my_v[q] = -INFINITY;
   const bool close = MODE != kByLogit && a.bias;  // ranks are scores, not exact
+  bool done = false;
+  if constexpr (SLOTS == 1) {
+    // The wanted ranks are among few candidates: with `want` of the lanes'
+    // largest at or above T, so are the `want` largest of all.  T is taken per
+    // row of 16 lanes, from how many of the row's lanes have a larger largest.
+    // The candidates, one a lane, then count those before them.
+    constexpr int ROWS = G / 16;
+    const int want = (a.k + (close ? 1 : 0) + ROWS - 1) / ROWS;
+    if (want <= 16) {
+      uint32_t own = 0u;
+#pragma unroll
+      for (int j = 0; j < V; ++j) own = max(own, rank[j]);
+      int above = 0;
+#define ROUTE_ROTATE(n) above += row_ror<n>(own) > own ? 1 : 0;
+      ROUTE_ROTATE(1) ROUTE_ROTATE(2) ROUTE_ROTATE(3) ROUTE_ROTATE(4) ROUTE_ROTATE(5)
+      ROUTE_ROTATE(6) ROUTE_ROTATE(7) ROUTE_ROTATE(8) ROUTE_ROTATE(9) ROUTE_ROTATE(10)
+      ROUTE_ROTATE(11) ROUTE_ROTATE(12) ROUTE_ROTATE(13) ROUTE_ROTATE(14) ROUTE_ROTATE(15)
+#undef ROUTE_ROTATE
+      const uint32_t T = max(1u, run_minu<G>(above < want ? own : ~0u));
+      uint64_t* list = lists[w] + sub * G;  // (rank, ~expert), larger is earlier
+      int count = 0;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const bool in = rank[j] >= T;
+        const uint64_t all = __ballot(in);
+        int at;
+        if constexpr (G == 64) {
+          at = count + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0u));
+          count += __popcll(all);
+        } else {
+          const uint32_t mates = (uint32_t)(all >> (16 * sub)) & 0xffffu;
+          at = count + __popc(mates & ((1u << ln) - 1u));
+          count += __popc(mates);
+        }
+        if (in && at < G) list[at] = (uint64_t)rank[j] << 32 | (uint32_t)~(mine + place(j));
+      }
+      if (!__any(count > G)) {
+        done = true;
+        wave_lds_order();
+        const uint64_t cand = ln < count ? list[ln] : 0ull;
+        wave_lds_order();
+        int before = 0;
+        if constexpr (G == 64) {
+          for (int c = 0; c < count; ++c) {
+            const uint64_t o = (uint64_t)__builtin_amdgcn_readlane((int)(cand >> 32), c) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((int)cand, c);
+            before += o > cand ? 1 : 0;
+          }
+        } else {
+#define ROUTE_ROTATE(n)                                                                       \
+  before += ((uint64_t)row_ror<n>((uint32_t)(cand >> 32)) << 32 | row_ror<n>((uint32_t)cand)) > cand ? 1 : 0;
+          ROUTE_ROTATE(1) ROUTE_ROTATE(2) ROUTE_ROTATE(3) ROUTE_ROTATE(4) ROUTE_ROTATE(5)
+          ROUTE_ROTATE(6) ROUTE_ROTATE(7) ROUTE_ROTATE(8) ROUTE_ROTATE(9) ROUTE_ROTATE(10)
+          ROUTE_ROTATE(11) ROUTE_ROTATE(12) ROUTE_ROTATE(13) ROUTE_ROTATE(14) ROUTE_ROTATE(15)
+#undef ROUTE_ROTATE
+        }
+        if (ln < count) list[before] = cand;
+        wave_lds_order();
+        const uint64_t sel = ln < count ? list[ln] : 0ull;
+        if (ln < a.k) {
+          my_i[0] = (int)~(uint32_t)sel;
+          my_v[0] = value_of((uint32_t)(sel >> 32));
+        }
+        if (close) {
+          const uint64_t next = ln + 1 < count ? list[ln + 1] : 0ull;
+          const float x = next ? value_of((uint32_t)(next >> 32)) : -INFINITY;
+          const bool pair = ln < a.k && x > -INFINITY && !(my_v[0] - x > 2e-6f * (1.f + fabsf(x)));
+          near |= run_or<G>(pair ? 1u : 0u) != 0u;
+        }
+      }
+    }
+  }
   float prev = INFINITY;
-  for (int s = 0; s < a.k + (close ? 1 : 0); ++s) {
+  for (int s = 0; !done && s < a.k + (close ? 1 : 0); ++s) {
     uint32_t best = 0u;
 #pragma unroll
     for (int j = 0; j < V; ++j) best = max(best, rank[j]);
     best = run_maxu<G>(best);
+    const float x = best ? value_of(best) : -INFINITY;
     if (close) {
-      const float x = best ? value_of(best) : -INFINITY;
       near |= x > -INFINITY && !(prev - x > 2e-6f * (1.f + fabsf(x)));
       prev = x;
       if (s == a.k) break;
@@ -301,8 +380,9 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
       if ((int)mine_at == place(j)) rank[j] = 0u;
 #pragma unroll
     for (int q = 0; q < SLOTS; ++q)
-      if (ln + G * q == s) my_i[q] = (int)at;
+      if (ln + G * q == s) my_i[q] = (int)at, my_v[q] = x;
   }
+  bool by_logit = MODE == kByLogit || !a.bias;  // my_v holds logits
   if constexpr (MODE != kByLogit) {
     uint64_t again = __ballot(near && valid && ln == 0);
     while (again) {
@@ -315,6 +395,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
         const int x = __shfl(at, (ln + G * q) & 63);
         if (sub == first / G) my_i[q] = x;
       }
+      by_logit = false;
     }
   }
 
@@ -324,7 +405,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
   for (int q = 0; q < SLOTS; ++q) {
     ls[q] = -INFINITY;
     if (ln + G * q < a.k) {
-      ls[q] = row[my_i[q]];
+      ls[q] = by_logit ? my_v[q] : row[my_i[q]];
       if (is_masked(ls[q])) ls[q] = -INFINITY;
     }
     m = fmaxf(m, ls[q]);

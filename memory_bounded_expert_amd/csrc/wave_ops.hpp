@@ -68,18 +68,10 @@ __device__ __forceinline__ uint32_t run_or(uint32_t v) {
   return run_reduce<G>(v, [](uint32_t a, uint32_t b) { return a | b; });
 }
 
-// 64-bit values over a wave, by xor butterflies.
+// Sum over a wave by xor butterflies; every lane ends with the same bits.
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
-  return v;
-}
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint64_t w = __shfl_xor(v, o);
-    v = w > v ? w : v;
-  }
   return v;
 }
 
