@@ -63,7 +63,7 @@ __device__ __forceinline__ bool is_masked(float l) { return !(l > -INFINITY); }
 // One token's selection in 64 bits by the whole wave (every lane of it calls):
 // lane s returns slot s's expert.  lds: E + n_group doubles of the wave's own.
 template <int V>
-__device__ __noinline__ int route_exact(const RouteArgs& a, int64_t t, double* lds) {
+__device__ __forceinline__ int route_exact(const RouteArgs& a, int64_t t, double* lds) {
   const int lane = threadIdx.x & 63;
   const float* row = a.logits + t * a.E;
   const int per = a.E / a.n_group;
@@ -189,14 +189,16 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
   if (vec) {
 #pragma unroll
     for (int j = 0; j < V; j += 4) {
-      f32x4_t q{-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (mine + place(j) < a.E) q = *reinterpret_cast<const f32x4_t*>(row + mine + place(j));
+      const f32x4_t q = *reinterpret_cast<const f32x4_t*>(row + min(mine + place(j), a.E - 4));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) l[j + i] = q[i];
+      for (int i = 0; i < 4; ++i) l[j + i] = mine + place(j) < a.E ? q[i] : -INFINITY;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j) l[j] = mine + place(j) < a.E ? row[mine + place(j)] : -INFINITY;
+    for (int j = 0; j < V; ++j) {
+      l[j] = row[min(mine + place(j), a.E - 1)];
+      l[j] = mine + place(j) < a.E ? l[j] : -INFINITY;
+    }
   }
   float top = -INFINITY;
 #pragma unroll
@@ -223,14 +225,35 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     // v_e.  A score is off by less than 5e-7 (its exponential's argument is
     // rounded, which costs at most max x exp(-x) = 0.37 of a step; a sum of up
     // to 1024 terms, 22 steps), adding the bias rounds once more.
-    float v[V];
+    // (Loads and the choice of score stand outside the loops: a branch per
+    // element would wait for each load by itself.)
+    float v[V], b[V];
+    if (a.sigmoid) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = logistic(l[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = is_masked(l[j]) ? 0.f : __expf(l[j] - top) * inv_z;
+    }
+    if (a.bias) {
+      if (vec) {
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+          const f32x4_t q = *reinterpret_cast<const f32x4_t*>(a.bias + min(mine + place(j), a.E - 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) b[j + i] = q[i];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) b[j] = a.bias[min(mine + place(j), a.E - 1)];
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] += b[j];
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      v[j] = a.sigmoid ? logistic(l[j]) : is_masked(l[j]) ? 0.f : __expf(l[j] - top) * inv_z;
-      if (a.bias && mine + place(j) < a.E) v[j] += a.bias[mine + place(j)];
-      rank[j] = mine + place(j) >= a.E ? 0u
-                : is_masked(l[j])      ? order_of(-INFINITY)
-                                       : order_of(a.bias ? v[j] : l[j]);
+      const uint32_t o = order_of(is_masked(l[j]) || !a.bias ? l[j] : v[j]);
+      rank[j] = mine + place(j) < a.E ? o : 0u;
     }
     if constexpr (MODE == kGrouped) {
       const int per = a.E / a.n_group;
@@ -654,7 +677,7 @@ MOE_API int route_forward(const route_plan_t* plan, const float* logits, const f
                     P.score, P.n_group, P.topk_group, P.group_top, P.renorm, P.scale};
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
-  const int vec = rows_aligned(P.E, logits, nullptr);
+  const int vec = rows_aligned(P.E, logits, bias);
   const int mode = P.n_group > 1 ? kGrouped : bias ? kByScore : kByLogit;
   const int per = P.E / P.n_group;
   // e / per as a product: exact for e < 1024, per < 1024
