@@ -153,7 +153,9 @@ __device__ __forceinline__ int route_exact(const RouteArgs& a, int64_t t, double
   return my_i;
 }
 
-enum RouteMode { kByLogit, kByScore, kGrouped };  // kByScore: with a bias
+// kByScore: with a bias.  kQuads: groups, and every four experts that a lane
+// holds next to each other are of one group.
+enum RouteMode { kByLogit, kByScore, kGrouped, kQuads };
 
 // LDS of one wave: four tokens' values, padded by one a group so that lanes
 // that read one group each meet different banks, and strengths; or
@@ -173,7 +175,7 @@ template <int G, int V, int MODE, int SLOTS>
 __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs a, int vec,
                                                                  uint32_t per_mul, int wave_lds) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  __shared__ uint64_t lists[kWaves][SLOTS == 1 ? 64 : 1];
+  __shared__ uint32_t lists[kWaves][SLOTS == 1 ? 2 * 64 + 8 : 1];
   constexpr int TPW = 64 / G;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int ln = lane % G, sub = lane / G;
@@ -255,25 +257,48 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
       const uint32_t o = order_of(is_masked(l[j]) || !a.bias ? l[j] : v[j]);
       rank[j] = mine + place(j) < a.E ? o : 0u;
     }
-    if constexpr (MODE == kGrouped) {
-      const int per = a.E / a.n_group;
+    if constexpr (MODE >= kGrouped) {
+      // Lane g adds up group g's best out of LDS: from the values, or from the
+      // two best of each four.
+      constexpr int Q = MODE == kQuads ? 4 : 1, NQ = V / Q;
+      const int per = a.E / a.n_group / Q;
       float* val = reinterpret_cast<float*>(smem + w * wave_lds) + sub * (a.E + 2 * a.n_group);
       float* strength = val + a.E + a.n_group;
-      int grp[V];
+      int grp[NQ];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int e = mine + place(j);
+      for (int j = 0; j < NQ; ++j) {
+        const int e = (mine + place(j * Q)) / Q;
         grp[j] = (int)(((uint32_t)e * per_mul) >> 20);
-        if (e < a.E) val[e + grp[j]] = is_masked(l[j]) ? -INFINITY : v[j];
+        if constexpr (MODE == kQuads) {
+          float b1 = -INFINITY, b2 = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float x = is_masked(l[4 * j + i]) ? -INFINITY : v[4 * j + i];
+            b2 = __builtin_amdgcn_fmed3f(b2, b1, x);
+            b1 = fmaxf(b1, x);
+          }
+          if (e * 4 < a.E) reinterpret_cast<float2*>(val)[e + grp[j]] = make_float2(b1, b2);
+        } else {
+          if (e < a.E) val[e + grp[j]] = is_masked(l[j]) ? -INFINITY : v[j];
+        }
       }
       wave_lds_order();
       for (int g = ln; g < a.n_group; g += G) {
-        float b1 = -INFINITY, b2 = -INFINITY;
-        const float* q = val + g * (per + 1);
+        float b1 = -INFINITY, b2 = -INFINITY;  // b2 <= b1: med3 is the second of the three
+        if constexpr (MODE == kQuads) {
+          const float2* q = reinterpret_cast<const float2*>(val) + g * (per + 1);
 #pragma unroll 8
-        for (int i = 0; i < per; ++i) {
-          b2 = __builtin_amdgcn_fmed3f(b2, b1, q[i]);  // b2 <= b1: the second largest of the three
-          b1 = fmaxf(b1, q[i]);
+          for (int i = 0; i < per; ++i) {
+            b2 = fmaxf(__builtin_amdgcn_fmed3f(b2, b1, q[i].x), q[i].y);
+            b1 = fmaxf(b1, q[i].x);
+          }
+        } else {
+          const float* q = val + g * (per + 1);
+#pragma unroll 8
+          for (int i = 0; i < per; ++i) {
+            b2 = __builtin_amdgcn_fmed3f(b2, b1, q[i]);
+            b1 = fmaxf(b1, q[i]);
+          }
         }
         strength[g] = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
       }
@@ -298,8 +323,11 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
       next = run_maxf<G>(next);
       near = next > -INFINITY && !(weakest - next > 4e-6f * (1.f + fabsf(next)));
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (!(((grp[j] < 32 ? lo : hi) >> (grp[j] & 31)) & 1)) rank[j] = 0u;
+      for (int j = 0; j < NQ; ++j) {
+        const bool keep = ((grp[j] < 32 ? lo : hi) >> (grp[j] & 31)) & 1;
+#pragma unroll
+        for (int i = 0; i < Q; ++i) rank[Q * j + i] = keep ? rank[Q * j + i] : 0u;
+      }
     }
   }
 
@@ -327,27 +355,40 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
       ROUTE_ROTATE(11) ROUTE_ROTATE(12) ROUTE_ROTATE(13) ROUTE_ROTATE(14) ROUTE_ROTATE(15)
 #undef ROUTE_ROTATE
       const uint32_t T = max(1u, run_minu<G>(above < want ? own : ~0u));
-      uint64_t* list = lists[w] + sub * G;  // (rank, ~expert), larger is earlier
-      int count = 0;
+      // (rank, ~expert) of each candidate, larger is earlier; one slot past the
+      // list takes what is no candidate
+      uint32_t* list = lists[w] + sub * (2 * G + 2);
+      int held = 0;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const bool in = rank[j] >= T;
-        const uint64_t all = __ballot(in);
-        int at;
-        if constexpr (G == 64) {
-          at = count + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0u));
-          count += __popcll(all);
-        } else {
-          const uint32_t mates = (uint32_t)(all >> (16 * sub)) & 0xffffu;
-          at = count + __popc(mates & ((1u << ln) - 1u));
-          count += __popc(mates);
-        }
-        if (in && at < G) list[at] = (uint64_t)rank[j] << 32 | (uint32_t)~(mine + place(j));
+      for (int j = 0; j < V; ++j) held += rank[j] >= T ? 1 : 0;
+      int at = held;  // inclusive sums over the token's lanes
+      at += row_shr<1>(at);
+      at += row_shr<2>(at);
+      at += row_shr<4>(at);
+      at += row_shr<8>(at);
+      int count;
+      if constexpr (G == 64) {
+        int rows[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) rows[r] = __builtin_amdgcn_readlane(at, 16 * r + 15);
+        at += (ln >= 16 ? rows[0] : 0) + (ln >= 32 ? rows[1] : 0) + (ln >= 48 ? rows[2] : 0);
+        count = rows[0] + rows[1] + rows[2] + rows[3];
+      } else {
+        count = run_sumi<G>(held);
       }
       if (!__any(count > G)) {
         done = true;
+        at -= held;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const bool in = rank[j] >= T;
+          const int to = in ? at : G;
+          list[to] = rank[j];
+          list[G + 1 + to] = ~(uint32_t)(mine + place(j));
+          at += in ? 1 : 0;
+        }
         wave_lds_order();
-        const uint64_t cand = ln < count ? list[ln] : 0ull;
+        const uint64_t cand = ln < count ? (uint64_t)list[ln] << 32 | list[G + 1 + ln] : 0ull;
         wave_lds_order();
         int before = 0;
         if constexpr (G == 64) {
@@ -364,16 +405,17 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
           ROUTE_ROTATE(11) ROUTE_ROTATE(12) ROUTE_ROTATE(13) ROUTE_ROTATE(14) ROUTE_ROTATE(15)
 #undef ROUTE_ROTATE
         }
-        if (ln < count) list[before] = cand;
+        const int to = ln < count ? before : G;
+        list[to] = (uint32_t)(cand >> 32);
+        list[G + 1 + to] = (uint32_t)cand;
         wave_lds_order();
-        const uint64_t sel = ln < count ? list[ln] : 0ull;
+        const uint64_t sel = ln < count ? (uint64_t)list[ln] << 32 | list[G + 1 + ln] : 0ull;
         if (ln < a.k) {
           my_i[0] = (int)~(uint32_t)sel;
           my_v[0] = value_of((uint32_t)(sel >> 32));
         }
         if (close) {
-          const uint64_t next = ln + 1 < count ? list[ln + 1] : 0ull;
-          const float x = next ? value_of((uint32_t)(next >> 32)) : -INFINITY;
+          const float x = ln + 1 < count ? value_of(list[ln + 1]) : -INFINITY;
           const bool pair = ln < a.k && x > -INFINITY && !(my_v[0] - x > 2e-6f * (1.f + fabsf(x)));
           near |= run_or<G>(pair ? 1u : 0u) != 0u;
         }
@@ -678,9 +720,10 @@ MOE_API int route_forward(const route_plan_t* plan, const float* logits, const f
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
   const int vec = rows_aligned(P.E, logits, bias);
-  const int mode = P.n_group > 1 ? kGrouped : bias ? kByScore : kByLogit;
-  const int per = P.E / P.n_group;
+  const bool quads = vec && P.E / P.n_group % 4 == 0;
+  const int mode = P.n_group > 1 ? (quads ? kQuads : kGrouped) : bias ? kByScore : kByLogit;
   // e / per as a product: exact for e < 1024, per < 1024
+  const int per = P.E / P.n_group / (mode == kQuads ? 4 : 1);
   const uint32_t per_mul = ((1u << 20) + per - 1) / per;
   with_shape(P.E, P.k, [&](auto g, auto v, auto s) {
     constexpr int G = g.value, V = v.value, S = s.value;
@@ -690,8 +733,10 @@ MOE_API int route_forward(const route_plan_t* plan, const float* logits, const f
       route_forward_kernel<G, V, kByLogit, S><<<grid, kThreads, 0, st>>>(a, vec, per_mul, 0);
     else if (mode == kByScore)
       route_forward_kernel<G, V, kByScore, S><<<grid, kThreads, 0, st>>>(a, vec, per_mul, 0);
-    else
+    else if (mode == kGrouped)
       route_forward_kernel<G, V, kGrouped, S><<<grid, kThreads, kWaves * lds, st>>>(a, vec, per_mul, (int)lds);
+    else
+      route_forward_kernel<G, V, kQuads, S><<<grid, kThreads, kWaves * lds, st>>>(a, 1, per_mul, (int)lds);
   });
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
 }

@@ -26,6 +26,12 @@ __device__ __forceinline__ V row_ror(V v) {
   return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x120 + n, 0xf, 0xf, false));
 }
 
+// v of the lane n places before, 0 before the row's first lane.
+template <int n>
+__device__ __forceinline__ int row_shr(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, 0x110 + n, 0xf, 0xf, false);
+}
+
 // Reductions over aligned runs of G = 16 or 64 lanes; every lane of the run ends
 // with the same bits.  Within a row of 16 by rotations, whose pairs are
 // combined commutatively step by step; the four rows through lanes 0, 16, 32,
@@ -46,6 +52,10 @@ __device__ __forceinline__ V run_reduce(V v, Op op) {
 template <int G>
 __device__ __forceinline__ float run_sum(float v) {
   return run_reduce<G>(v, [](float a, float b) { return a + b; });
+}
+template <int G>
+__device__ __forceinline__ int run_sumi(int v) {
+  return run_reduce<G>(v, [](int a, int b) { return a + b; });
 }
 template <int G>
 __device__ __forceinline__ float run_maxf(float v) {
