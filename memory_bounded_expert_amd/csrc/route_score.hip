@@ -60,6 +60,41 @@ __device__ __forceinline__ float value_of(uint32_t o) {
 
 __device__ __forceinline__ bool is_masked(float l) { return !(l > -INFINITY); }
 
+// The hardware exponential's argument is rounded (a step per unit of it) and
+// its result within a step, as the reciprocal's.
+__device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// A selected expert's score: relative to exp(c), c <= 0 and c = the largest
+// logit if that is below 0, so that the largest neither under- nor overflows
+// (c = 0: the score itself); and 1 - sigmoid.
+__device__ __forceinline__ float sigmoid_rel(float l, float c, float* one_less) {
+  const float r = rcp(1.f + __expf(-fabsf(l)));
+  const float far = __expf(-fabsf(l)) * r;
+  if (one_less) *one_less = l < 0.f ? r : far;
+  return l < 0.f ? __expf(l - c) * r : r;
+}
+
+// How near two scores (group strengths: sums of two) may be for 32 bits to tell
+// them apart.  A sigmoid is off by less than 3e-7 (0.25 of its exponential's
+// relative error of 1.2e-7 + 6e-8 |l|, |l| s (1 - s) <= 0.23; a step each of
+// 1 + x and the reciprocal).  A softmax's own error is no larger, but the sum
+// of up to 1024 terms is off by up to 22 roundings, 1.3e-6, which moves two
+// scores apart by as much of their distance.  Adding the bias rounds by half a step of the result.
+__device__ __forceinline__ float nearness(int sigmoid, float x) {
+  return (sigmoid ? 7e-7f : 2e-6f) * (1.f + fabsf(x));
+}
+
+// Sums exp(l - top) in 64 bits over a token's G lanes.
+template <int G, int V>
+__device__ __forceinline__ double softmax_sum64(const float (&l)[V], float top) {
+  double z = 0.0;
+#pragma unroll
+  for (int j = 0; j < V; ++j) z += is_masked(l[j]) ? 0.0 : exp((double)l[j] - (double)top);
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) z += __shfl_xor(z, o);
+  return z;
+}
+
 // One token's selection in 64 bits by the whole wave (every lane of it calls):
 // lane s returns slot s's expert.  lds: E + n_group doubles of the wave's own.
 template <int V>
@@ -219,16 +254,13 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
   }
 
   uint32_t rank[V];
-  bool near = false;  // two values that decide something are too near for 32 bits
+  bool near = false;  // 32 bits do not tell: select again with route_exact
   if constexpr (MODE == kByLogit) {
 #pragma unroll
     for (int j = 0; j < V; ++j) rank[j] = mine + place(j) < a.E ? order_of(l[j]) : 0u;
   } else {
-    // v_e.  A score is off by less than 5e-7 (its exponential's argument is
-    // rounded, which costs at most max x exp(-x) = 0.37 of a step; a sum of up
-    // to 1024 terms, 22 steps), adding the bias rounds once more.
-    // (Loads and the choice of score stand outside the loops: a branch per
-    // element would wait for each load by itself.)
+    // v_e.  Loads and the choice of score stand outside the loops: a branch per
+    // element would wait for each load by itself.
     float v[V], b[V];
     if (a.sigmoid) {
 #pragma unroll
@@ -283,6 +315,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
         }
       }
       wave_lds_order();
+      float size = 0.f;  // of the values summed
       for (int g = ln; g < a.n_group; g += G) {
         float b1 = -INFINITY, b2 = -INFINITY;  // b2 <= b1: med3 is the second of the three
         if constexpr (MODE == kQuads) {
@@ -301,6 +334,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
           }
         }
         strength[g] = a.group_top == 2 && b2 > -INFINITY ? b1 + b2 : b1;
+        if (b1 > -INFINITY) size = fmaxf(size, fmaxf(fabsf(b1), b2 > -INFINITY ? fabsf(b2) : 0.f));
       }
       wave_lds_order();
       uint32_t lo = 0u, hi = 0u;
@@ -321,7 +355,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
       hi = run_or<G>(hi);
       weakest = run_minf<G>(weakest);
       next = run_maxf<G>(next);
-      near = next > -INFINITY && !(weakest - next > 4e-6f * (1.f + fabsf(next)));
+      near = next > -INFINITY && !(weakest - next > 2.f * nearness(a.sigmoid, run_maxf<G>(size)));
 #pragma unroll
       for (int j = 0; j < NQ; ++j) {
         const bool keep = ((grp[j] < 32 ? lo : hi) >> (grp[j] & 31)) & 1;
@@ -354,27 +388,49 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
       ROUTE_ROTATE(6) ROUTE_ROTATE(7) ROUTE_ROTATE(8) ROUTE_ROTATE(9) ROUTE_ROTATE(10)
       ROUTE_ROTATE(11) ROUTE_ROTATE(12) ROUTE_ROTATE(13) ROUTE_ROTATE(14) ROUTE_ROTATE(15)
 #undef ROUTE_ROTATE
-      const uint32_t T = max(1u, run_minu<G>(above < want ? own : ~0u));
+      // with close, whatever may turn out to be ahead of T belongs to the candidates
+      auto below = [&](uint32_t r) __attribute__((always_inline)) {
+        const float x = value_of(r);
+        return close && r > 1u && x > -INFINITY ? order_of(x - nearness(a.sigmoid, x)) : r;
+      };
+      uint32_t T = below(max(1u, run_minu<G>(above < want ? own : ~0u)));
       // (rank, ~expert) of each candidate, larger is earlier; one slot past the
       // list takes what is no candidate
       uint32_t* list = lists[w] + sub * (2 * G + 2);
       int held = 0;
+      auto count_from = [&](uint32_t from) __attribute__((always_inline)) {
+        held = 0;
 #pragma unroll
-      for (int j = 0; j < V; ++j) held += rank[j] >= T ? 1 : 0;
+        for (int j = 0; j < V; ++j) held += rank[j] >= from ? 1 : 0;
+        return run_sumi<G>(held);
+      };
+      int count = count_from(T);
+      if (__any(count > G)) {
+        // the best sit in few lanes (kept groups do): halve the way from T to
+        // the largest until what is left fits
+        uint32_t low = T, high = run_maxu<G>(own) + 1u;
+        bool open = count > G;
+        for (int i = 0; i < 12 && __any(open); ++i) {
+          const uint32_t mid = low + (high - low) / 2;
+          const int c = count_from(mid);
+          if (open) {
+            if (c >= want * ROWS) low = mid; else high = mid;
+            open = c < want * ROWS || c >= G;
+          }
+        }
+        if (count > G) T = below(low);
+        count = count_from(T);
+      }
       int at = held;  // inclusive sums over the token's lanes
       at += row_shr<1>(at);
       at += row_shr<2>(at);
       at += row_shr<4>(at);
       at += row_shr<8>(at);
-      int count;
       if constexpr (G == 64) {
-        int rows[4];
+        int rows[3];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) rows[r] = __builtin_amdgcn_readlane(at, 16 * r + 15);
+        for (int r = 0; r < 3; ++r) rows[r] = __builtin_amdgcn_readlane(at, 16 * r + 15);
         at += (ln >= 16 ? rows[0] : 0) + (ln >= 32 ? rows[1] : 0) + (ln >= 48 ? rows[2] : 0);
-        count = rows[0] + rows[1] + rows[2] + rows[3];
-      } else {
-        count = run_sumi<G>(held);
       }
       if (!__any(count > G)) {
         done = true;
@@ -405,6 +461,31 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
           ROUTE_ROTATE(11) ROUTE_ROTATE(12) ROUTE_ROTATE(13) ROUTE_ROTATE(14) ROUTE_ROTATE(15)
 #undef ROUTE_ROTATE
         }
+        if (close) {
+          // put in order, are neighbours that matter too near?
+          list[ln < count ? before : G] = (uint32_t)(cand >> 32);
+          wave_lds_order();
+          const float x = ln < count ? value_of(list[ln]) : -INFINITY;
+          const float y = ln + 1 < count ? value_of(list[ln + 1]) : -INFINITY;
+          wave_lds_order();
+          if (__any(ln < a.k && y > -INFINITY && !(x - y > nearness(a.sigmoid, y)))) {
+            // then all candidates rank by their values in 64 bits
+            double z = 1.0;
+            if (!a.sigmoid) z = softmax_sum64<G>(l, top);
+            const int e = ln < count ? (int)~(uint32_t)cand : 0;
+            const float le = row[e];
+            const double s64 = a.sigmoid ? 1.0 / (1.0 + exp(-(double)le)) : exp((double)le - (double)top) / z;
+            const uint64_t o64 = order_of(is_masked(le) ? -(double)INFINITY : s64 + (double)a.bias[e]);
+            const uint32_t id = (uint32_t)cand;
+            before = 0;
+            for (int c = 0; c < G; ++c) {
+              const int from = sub * G + c;
+              const uint64_t o = __shfl(o64, from);
+              const uint32_t oid = __shfl(id, from);
+              before += c < count && (o > o64 || (o == o64 && oid > id)) ? 1 : 0;
+            }
+          }
+        }
         const int to = ln < count ? before : G;
         list[to] = (uint32_t)(cand >> 32);
         list[G + 1 + to] = (uint32_t)cand;
@@ -413,11 +494,6 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
         if (ln < a.k) {
           my_i[0] = (int)~(uint32_t)sel;
           my_v[0] = value_of((uint32_t)(sel >> 32));
-        }
-        if (close) {
-          const float x = ln + 1 < count ? value_of(list[ln + 1]) : -INFINITY;
-          const bool pair = ln < a.k && x > -INFINITY && !(my_v[0] - x > 2e-6f * (1.f + fabsf(x)));
-          near |= run_or<G>(pair ? 1u : 0u) != 0u;
         }
       }
     }
@@ -430,7 +506,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     best = run_maxu<G>(best);
     const float x = best ? value_of(best) : -INFINITY;
     if (close) {
-      near |= x > -INFINITY && !(prev - x > 2e-6f * (1.f + fabsf(x)));
+      near |= x > -INFINITY && !(prev - x > nearness(a.sigmoid, x));
       prev = x;
       if (s == a.k) break;
     }
@@ -484,20 +560,20 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     for (int q = 0; q < SLOTS; ++q) {
       g[q] = 0.f;
       if (ls[q] > -INFINITY)
-        g[q] = !a.sigmoid ? expf(ls[q] - c) : ls[q] < 0.f ? expf(ls[q] - c) / (1.f + expf(ls[q])) : 1.f / (1.f + expf(-ls[q]));
+        g[q] = a.sigmoid ? sigmoid_rel(ls[q], c, nullptr) : __expf(ls[q] - c);
       sum += g[q];
     }
     sum = run_sum<G>(sum);
-    const float f = sum > 0.f ? a.scale / sum : 0.f;
+    const float f = sum > 0.f ? a.scale * rcp(sum) : 0.f;
 #pragma unroll
     for (int q = 0; q < SLOTS; ++q) g[q] *= f;
   } else {
 #pragma unroll
     for (int q = 0; q < SLOTS; ++q) {
       if (a.sigmoid)
-        g[q] = a.scale * (ls[q] < 0.f ? expf(ls[q]) / (1.f + expf(ls[q])) : 1.f / (1.f + expf(-ls[q])));
+        g[q] = a.scale * sigmoid_rel(ls[q], 0.f, nullptr);
       else
-        g[q] = ls[q] > -INFINITY ? a.scale * (expf(ls[q] - top) * inv_z) : 0.f;
+        g[q] = ls[q] > -INFINITY ? a.scale * (__expf(ls[q] - top) * inv_z) : 0.f;
     }
   }
 #pragma unroll
@@ -538,7 +614,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteBwd
   auto place = [&](int j) { return (j / 4) * 4 * G + (j % 4) * step; };
 
   int e[SLOTS];
-  float ls[SLOTS], dg[SLOTS], wgt[SLOTS], m = -INFINITY;
+  float ls[SLOTS], dg[SLOTS], wgt[SLOTS], one_less[SLOTS], m = -INFINITY;
 #pragma unroll
   for (int q = 0; q < SLOTS; ++q) {
     e[q] = -1;
@@ -593,22 +669,21 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteBwd
     float sum = 0.f;
 #pragma unroll
     for (int q = 0; q < SLOTS; ++q) {
-      wgt[q] = 0.f;
-      if (e[q] >= 0)
-        wgt[q] = !a.sigmoid ? expf(ls[q] - c) : ls[q] < 0.f ? expf(ls[q] - c) / (1.f + expf(ls[q])) : 1.f / (1.f + expf(-ls[q]));
+      wgt[q] = a.sigmoid ? sigmoid_rel(ls[q], c, &one_less[q]) : __expf(ls[q] - c);
+      if (e[q] < 0) wgt[q] = 0.f;
       sum += wgt[q];
     }
     sum = run_sum<G>(sum);
-    const float f = sum > 0.f ? 1.f / sum : 0.f;
+    const float f = sum > 0.f ? rcp(sum) : 0.f;
 #pragma unroll
     for (int q = 0; q < SLOTS; ++q) wgt[q] *= f;
   } else {
 #pragma unroll
     for (int q = 0; q < SLOTS; ++q) {
       if (a.sigmoid)
-        wgt[q] = ls[q] < 0.f ? expf(ls[q]) / (1.f + expf(ls[q])) : 1.f / (1.f + expf(-ls[q]));
+        wgt[q] = sigmoid_rel(ls[q], 0.f, &one_less[q]);
       else
-        wgt[q] = e[q] >= 0 ? expf(ls[q] - top) * inv_z : 0.f;
+        wgt[q] = e[q] >= 0 ? __expf(ls[q] - top) * inv_z : 0.f;
     }
   }
   float dot = 0.f;  // sum_j g_j dg_j
@@ -635,8 +710,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteBwd
   for (int q = 0; q < SLOTS; ++q) {
     if (e[q] >= 0) {
       float d = wgt[q] * (a.scale * dg[q] - (dense ? 0.f : dot));
-      if (a.sigmoid)  // 1 - s
-        d *= ls[q] < 0.f ? 1.f / (1.f + expf(ls[q])) : expf(-ls[q]) / (1.f + expf(-ls[q]));
+      if (a.sigmoid) d *= one_less[q];
       out[e[q]] += d;
     }
   }

@@ -127,8 +127,25 @@ def test_near_ties_are_told_apart(score, groups):
     steps = np.random.default_rng(0).permuted(np.tile(np.arange(E), (N, 1)), axis=1)
     l = (base.view(np.int32) + np.where(base < 0, -steps, steps).astype(np.int32)).view(np.float32)
     up = np.ones((N, k), np.float32)
-    for bias in (None, np.zeros(E, np.float32), np.full(E, 3.0, np.float32)):
+    far = np.where(np.arange(E) % 2, 50.0, -49.0).astype(np.float32)  # sums of two, each with its own rounding
+    for bias in (None, np.zeros(E, np.float32), np.full(E, 3.0, np.float32), far):
         check(l, bias, up, k, score, *groups, 2, True, 1.0, ("near", score, bias is None))
+    # a few near pairs among ordinary rows, where the last slot and the next expert are the pair too
+    r = np.random.default_rng(1)
+    l = r.standard_normal((N, E)).astype(np.float32)
+    bias = (0.1 * r.standard_normal(E)).astype(np.float32)
+    for t in range(N):
+        order = oracle.route_select(l[t:t + 1], E // 4, score, bias, *groups, 2)[0]
+        i, j = order[t % 12], order[t % 12 + 1]
+        bias_gap = np.float64(bias[j]) - np.float64(bias[i])
+        if score == "sigmoid":  # j's score made i's less the biases' gap, up to rounding
+            s = 1 / (1 + np.exp(-np.float64(l[t, i]))) - bias_gap
+            if 0 < s < 1:
+                l[t, j] = np.float32(np.log(s / (1 - s)))
+        else:
+            l[t, j] = l[t, i]
+    for renorm in (True, False):
+        check(l, bias, up, k, score, *groups, 2, renorm, 1.0, ("pairs", score))
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
