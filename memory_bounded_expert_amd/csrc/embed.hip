@@ -1,11 +1,17 @@
 // Token embedding with scaling and its gradient (include/embed.h).
 //
-// Forward: a gather of rows, one vector per thread.  Backward: the positions
-// are sorted by id with a stable radix sort, the sorted rows are summed in
-// tiles of kTileRows positions, and runs of one id that cross tiles are
-// joined in order by a last launch.
+// Forward: a gather of rows, one vector per thread, bound by HBM.
+//
+// Backward: what it cannot do without is reading dY and writing dW whole, zeros
+// for the most part.  The positions are sorted by id with a stable radix sort
+// of two or three passes; the sorted rows are summed in tiles of kTileRows
+// positions by blocks of columns, and runs of one id that cross tiles are
+// joined in order by a last launch.  The sort's launches are short and fill few
+// CUs, so each also zeroes a slice of dW on the others; the rest is zeroed in
+// the summing launch, which knows the ids and skips the rows it writes itself.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "device_common.hpp"
 #include "embed.h"
@@ -19,11 +25,15 @@ namespace {
 
 constexpr uint32_t kEmbedMagic = 0x454d4231u;  // "EMB1"
 constexpr int kTileRows = 32;                  // sorted positions per summing tile
-constexpr int kSortTile = 2048;                // keys per work-group of a sort pass
+constexpr int kSortTile = 1024;                // keys per work-group of a sort pass
 constexpr int kSortRounds = kSortTile / kThreads;
 constexpr int kWaves = kThreads / 64;
 constexpr int kMaxDigit = 10;                  // bits of a sort pass's digit
 constexpr int kScanThreads = 1024;
+// Bytes of dW that a sort launch zeroes beside its own work: what the chip
+// writes in the 5 us that such a launch takes.
+constexpr int64_t kSliceBytes = 32 << 20;
+constexpr int64_t kZeroBytes = 1 << 18;        // bytes zeroed by a work-group
 
 // ---- forward
 
@@ -69,7 +79,30 @@ struct SortPass {
   int32_t* hist;        // [bins][tiles]: counts, then first output positions
   int64_t N, V;
   int tiles, shift, bits;
+  // work-groups from `groups` on zero [zero, zero_end)
+  int groups;
+  float* zero;
+  float* zero_end;
 };
+
+// Zeroes kZeroBytes of [p, end) from piece i on, by the whole work-group.
+__device__ __forceinline__ void zero_piece(float* p, float* end, int64_t i) {
+  p += i * (kZeroBytes / 4);
+  const int64_t n = min((int64_t)(end - p), kZeroBytes / 4);
+  if ((uintptr_t)p % 16 == 0) {
+    const int n4 = (int)(n / 4);
+    for (int q = threadIdx.x; q < n4; q += blockDim.x)
+      reinterpret_cast<u32x4_t*>(p)[q] = u32x4_t{0u, 0u, 0u, 0u};
+    for (int q = n4 * 4 + threadIdx.x; q < n; q += blockDim.x) p[q] = 0.f;
+  } else {
+    for (int q = threadIdx.x; q < n; q += blockDim.x) p[q] = 0.f;
+  }
+}
+__device__ __forceinline__ bool zeroes(const SortPass& a) {
+  if ((int)blockIdx.x < a.groups) return false;
+  zero_piece(a.zero, a.zero_end, (int)blockIdx.x - a.groups);
+  return true;
+}
 
 __device__ __forceinline__ uint32_t sort_key(const SortPass& a, int64_t i) {
   if (!a.ids) return a.key[i];
@@ -79,6 +112,7 @@ __device__ __forceinline__ uint32_t sort_key(const SortPass& a, int64_t i) {
 
 __global__ __launch_bounds__(kThreads) void sort_count_kernel(const SortPass a) {
   __shared__ int32_t cnt[1 << kMaxDigit];
+  if (zeroes(a)) return;
   const int bins = 1 << a.bits;
   for (int b = threadIdx.x; b < bins; b += kThreads) cnt[b] = 0;
   __syncthreads();
@@ -91,28 +125,47 @@ __global__ __launch_bounds__(kThreads) void sort_count_kernel(const SortPass a) 
   for (int b = threadIdx.x; b < bins; b += kThreads) a.hist[(int64_t)b * a.tiles + blockIdx.x] = cnt[b];
 }
 
-// Exclusive scan of n counts in place, one work-group.
-__global__ __launch_bounds__(kScanThreads) void sort_scan_kernel(int32_t* __restrict__ v, int n) {
-  __shared__ int32_t sums[kScanThreads / 64];
-  const int per = (n + kScanThreads - 1) / kScanThreads;
-  const int lo = min(n, (int)threadIdx.x * per), hi = min(n, lo + per);
-  int s = 0;
-  for (int i = lo; i < hi; ++i) s += v[i];
-  int inc = s;
+// Exclusive scan of the n counts in place by one work-group: each wave sums a
+// contiguous share (256 counts at a time), the shares are scanned, and each
+// wave scans its share again from its start.
+__global__ __launch_bounds__(kScanThreads) void sort_scan_kernel(const SortPass a, int n) {
+  constexpr int W = kScanThreads / 64;
+  __shared__ int32_t sums[W];
+  if (zeroes(a)) return;
+  int32_t* v = a.hist;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int u = __shfl_up(inc, o);
-    if (lane >= o) inc += u;
+  const int share = (n + W * 256 - 1) / (W * 256) * 256;
+  const int lo = min(n, w * share), hi = min(n, lo + share);
+  auto load = [&](int i) {  // counts i .. i + 3; the array is padded to whole 256
+    return *reinterpret_cast<const int4*>(v + i + 4 * lane);
+  };
+  int s = 0;
+#pragma unroll 4
+  for (int i = lo; i < hi; i += 256) {
+    const int4 c = load(i);
+    s += c.x + c.y + c.z + c.w;
   }
-  if (lane == 63) sums[w] = inc;
+  s = run_sumi<64>(s);
+  if (lane == 0) sums[w] = s;
   __syncthreads();
-  int run = inc - s;
+  int run = 0;
   for (int x = 0; x < w; ++x) run += sums[x];
-  for (int i = lo; i < hi; ++i) {
-    const int c = v[i];
-    v[i] = run;
-    run += c;
+#pragma unroll 4
+  for (int i = lo; i < hi; i += 256) {
+    int4 c = load(i);
+    const int own = c.x + c.y + c.z + c.w;
+    int inc = own;
+    inc += row_shr<1>(inc);
+    inc += row_shr<2>(inc);
+    inc += row_shr<4>(inc);
+    inc += row_shr<8>(inc);
+    const int r0 = __builtin_amdgcn_readlane(inc, 15), r1 = __builtin_amdgcn_readlane(inc, 31),
+              r2 = __builtin_amdgcn_readlane(inc, 47), r3 = __builtin_amdgcn_readlane(inc, 63);
+    inc += (lane >= 16 ? r0 : 0) + (lane >= 32 ? r1 : 0) + (lane >= 48 ? r2 : 0);
+    int at = run + inc - own;
+    const int4 o = make_int4(at, at + c.x, at + c.x + c.y, at + c.x + c.y + c.z);
+    *reinterpret_cast<int4*>(v + i + 4 * lane) = o;
+    run += r0 + r1 + r2 + r3;
   }
 }
 
@@ -120,6 +173,7 @@ __global__ __launch_bounds__(kScanThreads) void sort_scan_kernel(int32_t* __rest
 // keys, equal digits rank by lane (one ballot per digit bit).
 __global__ __launch_bounds__(kThreads) void sort_place_kernel(const SortPass a) {
   __shared__ int32_t next[kWaves][1 << kMaxDigit];
+  if (zeroes(a)) return;
   const int bins = 1 << a.bits;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   for (int b = lane; b < bins; b += 64) next[w][b] = 0;
@@ -176,7 +230,12 @@ struct SumArgs {
   int64_t N, V;
   int H, accumulate;
   float scale;
+  // embed_sum_kernel's work-groups: `groups` for tiles, `blocks` of columns
+  // each; the others zero zero_step rows each, from zero_from on
+  int blocks;
+  int64_t groups, zero_from, zero_step;
 };
+constexpr int kMaxZeroRows = 4096;
 
 template <int EPC>
 __device__ __forceinline__ void store_row(float* p, const float* v) {
@@ -197,65 +256,166 @@ __device__ __forceinline__ void write_dw(const SumArgs& a, uint32_t id, int64_t 
   store_row<EPC>(p, v);
 }
 
-// One tile of sorted positions by a block of columns.
+// First sorted position with key >= id, by the whole wave: 64 probes a step.
+__device__ __forceinline__ int64_t lower_bound(const uint32_t* key, int64_t N, uint32_t id) {
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, hi = N;  // key[lo - 1] < id <= key[hi]
+  while (hi - lo > 0) {
+    const int64_t step = (hi - lo + 63) / 64;
+    const int64_t at = lo + lane * step;
+    const int below = __popcll(__ballot(at < hi && key[min(at, N - 1)] < id));
+    if (below == 0) return lo;
+    lo += (below - 1) * step + 1;
+    hi = min(hi, lo - 1 + step);
+  }
+  return lo;
+}
+
+// Zeroes rows [r0, r1) of dW but those whose ids occur.
+__device__ __forceinline__ void zero_rows(const SumArgs& a, int64_t r0, int64_t r1, uint8_t* occurs) {
+  const int rows = (int)(r1 - r0);
+  for (int r = threadIdx.x; r < rows; r += kThreads) occurs[r] = 0;
+  __syncthreads();
+  for (int64_t i = lower_bound(a.key, a.N, (uint32_t)r0) + threadIdx.x; i < a.N; i += kThreads) {
+    const uint32_t k = a.key[i];
+    if (k >= r1) break;
+    occurs[k - r0] = 1;
+  }
+  __syncthreads();
+  const bool vec = a.H % 4 == 0 && (uintptr_t)a.dW % 16 == 0;
+  for (int r = 0; r < rows; ++r) {
+    if (occurs[r]) continue;
+    float* p = a.dW + (r0 + r) * a.H;
+    if (vec)
+      for (int q = threadIdx.x; q < a.H / 4; q += kThreads)
+        reinterpret_cast<u32x4_t*>(p)[q] = u32x4_t{0u, 0u, 0u, 0u};
+    else
+      for (int q = threadIdx.x; q < a.H; q += kThreads) p[q] = 0.f;
+  }
+}
+
+// Work-groups [0, tiles * blocks): one tile of sorted positions by a block of
+// columns, kAhead rows in flight.  The others zero `zero_rows` rows each.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(const SumArgs a) {
   constexpr int EPC = VEC ? Elem<T>::kPer16B : 1;
-  const int64_t i0 = (int64_t)blockIdx.x * kTileRows, i1 = min(a.N, i0 + kTileRows);
-  const int64_t col = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * EPC;
-  if (col >= a.H) return;
-  uint32_t cur = a.key[i0];
-  bool head = i0 > 0 && a.key[i0 - 1] == cur;
+  constexpr int kAhead = 8;
+  using Raw = std::conditional_t<VEC, u32x4_t, T>;
+  __shared__ uint8_t occurs[kMaxZeroRows];
+  if ((int64_t)blockIdx.x >= a.groups) {
+    const int64_t r0 = a.zero_from + ((int64_t)blockIdx.x - a.groups) * a.zero_step;
+    zero_rows(a, r0, min(a.V, r0 + a.zero_step), occurs);
+    return;
+  }
+  const int64_t tile = blockIdx.x / a.blocks;
+  const int64_t i0 = tile * kTileRows;
+  const int n = (int)min((int64_t)kTileRows, a.N - i0);
+  const int64_t col = ((int64_t)(blockIdx.x - tile * a.blocks) * kThreads + threadIdx.x) * EPC;
+  // lane l holds position i0 + l; lanes n and up repeat the last
+  const int lane = threadIdx.x & 63;
+  const uint32_t my_key = a.key[i0 + min(lane, n - 1)], my_pos = a.pos[i0 + min(lane, n - 1)];
+  uint32_t cur = __builtin_amdgcn_readfirstlane(my_key);
+  const bool starts = i0 == 0 || a.key[i0 - 1] != cur;
+  const uint32_t last = __builtin_amdgcn_readlane(my_key, n - 1);
+  const bool goes_on = i0 + n < a.N && a.key[min(i0 + n, a.N - 1)] == last;
+  const bool in = col < a.H;  // the other lanes stay: their keys are read
+  bool head = !starts;
   float acc[EPC];
 #pragma unroll
   for (int e = 0; e < EPC; ++e) acc[e] = 0.f;
-  auto flush = [&](bool goes_on) {
-    if (cur >= a.V) return;
-    if (head || goes_on)
-      store_row<EPC>(a.part + (blockIdx.x * 2 + (head ? 0 : 1)) * (int64_t)a.H + col, acc);
+  auto flush = [&](bool on) {
+    if (cur >= a.V || !in) return;
+    if (head || on)
+      store_row<EPC>(a.part + (tile * 2 + (head ? 0 : 1)) * (int64_t)a.H + col, acc);
     else
       write_dw<EPC>(a, cur, col, acc);
   };
-  for (int64_t i = i0; i < i1; ++i) {
-    const uint32_t k = a.key[i];
-    if (k != cur) {
-      flush(false);
-      cur = k;
-      head = false;
+  Raw raw[kAhead];
+  auto request = [&](int i, int u) {
+    // padded positions come last and are not read
+    const uint32_t k = __builtin_amdgcn_readlane(my_key, i), p = __builtin_amdgcn_readlane(my_pos, i);
+    if (i < n && k < a.V && in) raw[u] = *reinterpret_cast<const Raw*>(static_cast<const T*>(a.dY) + (int64_t)p * a.H + col);
+  };
 #pragma unroll
-      for (int e = 0; e < EPC; ++e) acc[e] = 0.f;
+  for (int u = 0; u < kAhead; ++u) request(u, u);
+#pragma unroll
+  for (int i0_ = 0; i0_ < kTileRows; i0_ += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0_ + u;
+      if (i < n) {
+        const uint32_t k = __builtin_amdgcn_readlane(my_key, i);
+        if (k != cur) {
+          flush(false);
+          cur = k;
+          head = false;
+#pragma unroll
+          for (int e = 0; e < EPC; ++e) acc[e] = 0.f;
+        }
+        if (k < a.V && in) {
+          float v[EPC];
+          if constexpr (VEC)
+            unpack16(raw[u], v, T());
+          else
+            v[0] = Elem<T>::to_f(raw[u]);
+#pragma unroll
+          for (int e = 0; e < EPC; ++e) acc[e] += v[e];
+        }
+        if (i + kAhead < kTileRows) request(i + kAhead, u);
+      }
     }
-    if (k >= a.V) return;  // the padded positions come last
-    const T* row = static_cast<const T*>(a.dY) + (int64_t)a.pos[i] * a.H + col;
-    float v[EPC];
-    if constexpr (VEC)
-      unpack16(*reinterpret_cast<const u32x4_t*>(row), v, T());
-    else
-      v[0] = Elem<T>::to_f(*row);
-#pragma unroll
-    for (int e = 0; e < EPC; ++e) acc[e] += v[e];
   }
-  flush(i1 < a.N && a.key[i1] == cur);
+  flush(goes_on);
 }
 
-// Joins the run that starts in this tile and goes on past it, tile by tile.
+// Joins the run that starts in tile blockIdx.x and goes on past it: a wave adds
+// a quarter of the tiles' sums, in order, and the waves' sums are added in
+// order.  64 lanes' columns per work-group.
 template <int EPC>
 __global__ __launch_bounds__(kThreads) void embed_join_kernel(const SumArgs a) {
-  const int64_t i0 = (int64_t)blockIdx.x * kTileRows, i1 = i0 + kTileRows;
-  const int64_t col = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * EPC;
-  if (i1 >= a.N || col >= a.H) return;
+  __shared__ float sums[kWaves][64 * EPC];
+  const int64_t tile = blockIdx.x, i0 = tile * kTileRows, i1 = i0 + kTileRows;
+  if (i1 >= a.N) return;
   const uint32_t cur = a.key[i1];
-  if (cur >= a.V || a.key[i1 - 1] != cur) return;             // nothing goes on
-  if (i0 > 0 && a.key[i0 - 1] == cur) return;  // it started earlier
-  float acc[EPC];
-  const float* p = a.part + (blockIdx.x * 2 + 1) * (int64_t)a.H + col;
-#pragma unroll
-  for (int e = 0; e < EPC; ++e) acc[e] = p[e];
-  for (int64_t c = blockIdx.x + 1; c * kTileRows < a.N && a.key[c * kTileRows] == cur; ++c) {
-    const float* q = a.part + c * 2 * (int64_t)a.H + col;
-#pragma unroll
-    for (int e = 0; e < EPC; ++e) acc[e] += q[e];
+  if (cur >= a.V || a.key[i1 - 1] != cur) return;  // nothing goes on
+  if (i0 > 0 && a.key[i0 - 1] == cur) return;      // it started earlier
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  // tiles that the run reaches after its first
+  int64_t more = 0;
+  for (bool full = true; full;) {
+    const int64_t at = (tile + 1 + more + lane) * kTileRows;
+    const int c = __popcll(__ballot(at < a.N && a.key[min(at, a.N - 1)] == cur));
+    more += c;
+    full = c == 64;
   }
+  const int64_t col = ((int64_t)blockIdx.y * 64 + lane) * EPC;
+  const bool in = col < a.H;
+  const int64_t share = (more + 1 + kWaves - 1) / kWaves;
+  const int64_t lo = min(more + 1, w * share), hi = min(more + 1, lo + share);
+  float acc[EPC];
+#pragma unroll
+  for (int e = 0; e < EPC; ++e) acc[e] = 0.f;
+  if (in) {
+    // sum 0 is the first tile's second row, the others the tiles' first rows
+    const float* p = a.part + tile * 2 * (int64_t)a.H + col;
+#pragma unroll 8
+    for (int64_t c = lo; c < hi; ++c) {
+      const float* q = p + (2 * c + (c == 0 ? 1 : 0)) * (int64_t)a.H;
+      float v[EPC];
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) v[e] = q[e];
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) acc[e] += v[e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < EPC; ++e) sums[w][lane * EPC + e] = acc[e];
+  __syncthreads();
+  if (w != 0 || !in) return;
+#pragma unroll
+  for (int v = 1; v < kWaves; ++v)
+#pragma unroll
+    for (int e = 0; e < EPC; ++e) acc[e] += sums[v][lane * EPC + e];
   write_dw<EPC>(a, cur, col, acc);
 }
 
@@ -279,22 +439,27 @@ EmbedLayout embed_layout(int64_t N, int64_t V, int H) {
   L.tiles = (int)ceil_div(N, kSortTile);
   for (int i = 0; i < 2; ++i) L.key[i] = take((size_t)N * 4);
   for (int i = 0; i < 2; ++i) L.pos[i] = take((size_t)N * 4);
-  L.hist = take(((size_t)L.tiles << L.bits) * 4);
+  L.hist = take((((size_t)L.tiles << L.bits) + 255) / 256 * 256 * 4);  // whole 256 for the scan
   L.part = take((size_t)ceil_div(N, kTileRows) * 2 * H * 4);
   L.total = cur;
   return L;
 }
 
 template <typename T>
-hipError_t sum_and_join(const SumArgs& a, bool vec, hipStream_t st) {
+hipError_t sum_and_join(SumArgs a, bool vec, hipStream_t st) {
   const int epc = vec ? Elem<T>::kPer16B : 1;
-  const dim3 grid((unsigned)ceil_div(a.N, kTileRows), (unsigned)ceil_div(a.H, kThreads * epc));
+  const int64_t tiles = ceil_div(a.N, kTileRows);
+  a.blocks = (int)ceil_div(a.H, kThreads * epc);
+  a.groups = tiles * a.blocks;
+  a.zero_step = std::min<int64_t>(std::max<int64_t>(kZeroBytes / 4 / a.H, 1), kMaxZeroRows);
+  const unsigned grid = (unsigned)(a.groups + ceil_div(a.V - a.zero_from, a.zero_step));
+  const dim3 join((unsigned)tiles, (unsigned)ceil_div(a.H, 64 * epc));
   if (vec) {
     embed_sum_kernel<T, true><<<grid, kThreads, 0, st>>>(a);
-    embed_join_kernel<Elem<T>::kPer16B><<<grid, kThreads, 0, st>>>(a);
+    if (a.N > kTileRows) embed_join_kernel<Elem<T>::kPer16B><<<join, kThreads, 0, st>>>(a);
   } else {
     embed_sum_kernel<T, false><<<grid, kThreads, 0, st>>>(a);
-    embed_join_kernel<1><<<grid, kThreads, 0, st>>>(a);
+    if (a.N > kTileRows) embed_join_kernel<1><<<join, kThreads, 0, st>>>(a);
   }
   return hipGetLastError();
 }
@@ -354,11 +519,16 @@ MOE_API int embed_backward(const embed_plan_t* plan, const int32_t* ids, const v
   if (workspace_bytes < (size_t)P.bwd_workspace_bytes) return MOE_EWORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
-  if (!accumulate && launch_fill_zero(dW, (size_t)P.V * P.H * sizeof(float), st) != hipSuccess)
-    return MOE_EHIP;
-  if (P.N == 0) return MOE_OK;
+  const int64_t values = P.V * P.H;
+  if (P.N == 0) {
+    if (!accumulate && launch_fill_zero(dW, (size_t)values * sizeof(float), st) != hipSuccess)
+      return MOE_EHIP;
+    return MOE_OK;
+  }
   const EmbedLayout L = embed_layout(P.N, P.V, P.H);
   char* ws = (char*)workspace;
+  // rows [0, zeroed) of dW are zeroed beside the sort
+  int64_t zeroed = accumulate ? P.V : 0;
   SortPass s{};
   s.ids = ids;
   s.hist = (int32_t*)(ws + L.hist);
@@ -366,19 +536,32 @@ MOE_API int embed_backward(const embed_plan_t* plan, const int32_t* ids, const v
   s.V = P.V;
   s.tiles = L.tiles;
   s.bits = L.bits;
+  // takes the next slice; the launch's work-groups
+  auto grid = [&](int groups) {
+    const int64_t rows = std::min(P.V - zeroed, ceil_div(kSliceBytes / 4, P.H));
+    s.groups = groups;
+    s.zero = dW + zeroed * P.H;
+    s.zero_end = s.zero + rows * P.H;
+    zeroed += rows;
+    return (unsigned)(groups + ceil_div(rows * P.H, kZeroBytes / 4));
+  };
   for (int i = 0; i < L.passes; ++i) {
     s.shift = i * L.bits;
     s.key_out = (uint32_t*)(ws + L.key[i & 1]);
     s.pos_out = (uint32_t*)(ws + L.pos[i & 1]);
-    sort_count_kernel<<<L.tiles, kThreads, 0, st>>>(s);
-    sort_scan_kernel<<<1, kScanThreads, 0, st>>>(s.hist, L.tiles << L.bits);
-    sort_place_kernel<<<L.tiles, kThreads, 0, st>>>(s);
+    unsigned g = grid(L.tiles);
+    sort_count_kernel<<<g, kThreads, 0, st>>>(s);
+    g = grid(1);
+    sort_scan_kernel<<<g, kScanThreads, 0, st>>>(s, L.tiles << L.bits);
+    g = grid(L.tiles);
+    sort_place_kernel<<<g, kThreads, 0, st>>>(s);
     s.ids = nullptr;
     s.key = s.key_out;
     s.pos = s.pos_out;
   }
   if (hipGetLastError() != hipSuccess) return MOE_EHIP;
-  const SumArgs a{s.key, s.pos, dY, dW, (float*)(ws + L.part), P.N, P.V, P.H, accumulate != 0, P.scale};
+  const SumArgs a{s.key, s.pos, dY, dW, (float*)(ws + L.part), P.N, P.V, P.H, accumulate != 0, P.scale,
+                  0,     0,     zeroed, 0};
   const bool vec = P.H % (16 / elem_bytes(P.dtype)) == 0 && aligned16(dY) && aligned16(dW);
   const hipError_t err = P.dtype == MOE_BF16 ? sum_and_join<bf16_t>(a, vec, st) : sum_and_join<float>(a, vec, st);
   return err == hipSuccess ? MOE_OK : MOE_EHIP;
