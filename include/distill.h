@@ -22,9 +22,12 @@
  * The forward pass runs cce_forward's strips on y / T and then forms the list
  * entries' logits as K products of rows, so its cost does not grow with K V.
  * The backward pass recomputes each strip's logits, stores the strip's share
- * of dy in bf16 (N x v_chunk, the only strip-sized buffer), corrects the list
- * entries that fall into the strip, and consumes it in the dX and dW
- * products.  Every output is deterministic, and bitwise independent of
+ * of dy in bf16 (the only strip-sized buffer), corrects the list entries that
+ * fall into the strip, and consumes it in the dX and dW products.  A small
+ * batch would fill few of the GPU's units with one strip of v_chunk entries,
+ * so its strips are as many times v_chunk as fit that buffer into
+ * KD_STRIP_BYTES, and its dX is summed over ranges of the vocabulary that run
+ * side by side.  Every output is deterministic, and bitwise independent of
  * v_chunk as cce.h's are.
  *
  * Conventions: as cce.h.  X [N][H] and W [V][H] are bfloat16; t_idx [N][K]
@@ -43,6 +46,9 @@
 extern "C" {
 #endif
 
+/* Strips wider than v_chunk keep the strip buffer within this. */
+#define KD_STRIP_BYTES (64u << 20)
+
 /* Filled by kd_plan; passed unchanged to the other calls. */
 typedef struct kd_plan {
     uint32_t magic;               /* set by kd_plan                           */
@@ -50,12 +56,15 @@ typedef struct kd_plan {
     int64_t N;                    /* tokens                                   */
     int64_t V;                    /* vocabulary entries                       */
     int32_t H;                    /* hidden width                             */
-    int32_t v_chunk;              /* strip width                              */
+    int32_t v_chunk;              /* least strip width                        */
     int32_t K;                    /* entries of a teacher's list              */
     float temperature;
     int32_t dw_dtype;             /* enum moe_dtype of dW                     */
-    int32_t S;                    /* strips, ceil(V / v_chunk); 0 if N = 0    */
-    int64_t strip_bound_bytes;    /* N * min(v_chunk, V) * 2                  */
+    int32_t S;                    /* strips, ceil(V / strip); 0 if N = 0      */
+    int32_t strip;                /* strip width: v_chunk, or the largest
+                                     multiple within KD_STRIP_BYTES           */
+    int32_t reserved0;
+    int64_t strip_bound_bytes;    /* N * min(strip, V) * 2                    */
     int64_t fwd_workspace_bytes;  /* workspace kd_forward needs               */
     int64_t bwd_workspace_bytes;  /* workspace kd_backward needs              */
 } kd_plan_t;

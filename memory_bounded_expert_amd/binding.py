@@ -99,7 +99,7 @@ class KdPlan(_c.Structure):
         ("magic", _c.c_uint32), ("dtype", _c.c_int32), ("N", _c.c_int64), ("V", _c.c_int64),
         ("H", _c.c_int32), ("v_chunk", _c.c_int32), ("K", _c.c_int32),
         ("temperature", _c.c_float), ("dw_dtype", _c.c_int32), ("S", _c.c_int32),
-        ("strip_bound_bytes", _c.c_int64), ("fwd_workspace_bytes", _c.c_int64),
+        ("strip", _c.c_int32), ("reserved0", _c.c_int32), ("strip_bound_bytes", _c.c_int64), ("fwd_workspace_bytes", _c.c_int64),
         ("bwd_workspace_bytes", _c.c_int64),
     ]
 

@@ -149,11 +149,6 @@ hipError_t launch_cce_fold(const float* pmax, const float* psum, int nslices, in
   return hipGetLastError();
 }
 
-hipError_t launch_cce_round(const float* src, void* dst, int64_t n, hipStream_t st) {
-  cce_round_kernel<<<blocks(n / 4), kCceThreads, 0, st>>>(src, (bf16_t*)dst, n / 4);
-  return hipGetLastError();
-}
-
 }  // namespace moe
 
 using namespace moe;
@@ -252,7 +247,9 @@ MOE_API int cce_backward(const cce_plan_t* plan, const void* X, const void* W,
     CCE_CHECK(gemm_cce_dx(G, cols, Ws, P.N, P.H, w, dx, s == 0, st));
     CCE_CHECK(gemm_cce_dw(G, cols, X, P.N, P.H, w, dW + v0 * P.H, st));
   }
-  CCE_CHECK(launch_cce_round(dx, dX, P.N * P.H, st));
+  const int64_t n4 = P.N * P.H / 4;
+  cce_round_kernel<<<blocks(n4), kCceThreads, 0, st>>>(dx, (bf16_t*)dX, n4);
+  CCE_CHECK(hipGetLastError());
   return MOE_OK;
 }
 

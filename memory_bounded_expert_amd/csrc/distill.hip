@@ -171,13 +171,58 @@ __global__ __launch_bounds__(kThreads) void kd_entries_kernel(
   G[t * ldg + v] = f2bf(dl[t] * (expf(y_top[i] / a.T - a.lse[t]) - p));
 }
 
+// dX [N][H] = bf16 of the slots' sums, added in order; 4 values per thread.
+__global__ __launch_bounds__(kThreads) void kd_fold_dx_kernel(const float* __restrict__ sums,
+                                                              int slots, int64_t n4,
+                                                              bf16_t* __restrict__ dX) {
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n4) return;
+  f32x4_t s = reinterpret_cast<const f32x4_t*>(sums)[i];
+#pragma unroll 8
+  for (int z = 1; z < slots; ++z) s += reinterpret_cast<const f32x4_t*>(sums)[z * n4 + i];
+  reinterpret_cast<ushort4*>(dX)[i] = make_ushort4(f2bf(s[0]), f2bf(s[1]), f2bf(s[2]), f2bf(s[3]));
+}
+
+// The backward pass's strips: v_chunk, times what KD_STRIP_BYTES leaves.
+int strip_of(int64_t N, int64_t V, int H, int v_chunk) {
+  const int64_t most = std::min<int64_t>((int64_t)KD_STRIP_BYTES / 2 / std::max<int64_t>(N, 1),
+                                         (((int64_t)1 << 30) - 1) / H);
+  const int64_t wanted = std::min(most, ceil_div(V, 256) * 256);
+  return (int)(std::max<int64_t>(wanted / v_chunk, 1) * v_chunk);
+}
+
+// The forward pass keeps no logits, so its strips are as many of these as make
+// four rounds of 256 x 256 tiles, one per CU (32-bit offsets into W allowing).
+int forward_strip(int64_t N, int64_t V, int H, int strip) {
+  const int64_t rows = ceil_div(N, 256);
+  const int64_t wanted = std::min(ceil_div(4 * 256, rows) * 256, V);
+  const int64_t most = (((int64_t)1 << 30) - 1) / H / strip;
+  return (int)(std::max<int64_t>(1, std::min(ceil_div(wanted, strip), most)) * strip);
+}
+
+// dX's ranges: with fewer than 256 tiles of dX, as many sums side by side as
+// fill the CUs once, each range at least 512 entries (16 K-tiles).  Depends on
+// N, H and V alone, so dX does not depend on the strips.
+struct DxRanges {
+  int range, slots;
+};
+DxRanges dx_ranges(int64_t N, int64_t V, int H) {
+  const int64_t tiles = ceil_div(N, 256) * (H / (H % 256 == 0 ? 256 : 128));
+  const int64_t want = 256 / tiles;
+  if (want < 2) return {0, 1};
+  const int64_t span = std::min<int64_t>(V, (int64_t)KD_STRIP_BYTES / 2 / N);
+  const int range = (int)std::max<int64_t>(512, ceil_div(ceil_div(span, want), 256) * 256);
+  return {range, (int)std::min(want, ceil_div(V, range))};
+}
+
 struct KdLayout {
   size_t pmax = 0, psum = 0, m = 0, z = 0;      // forward
   size_t g = 0, dx = 0, dl = 0, p = 0;          // backward
   size_t total = 0;
 };
 
-KdLayout kd_layout(int64_t N, int H, int cols, int K, bool backward) {
+// cols: the pass's strip columns (strip_cols).
+KdLayout kd_layout(int64_t N, int64_t V, int H, int cols, int K, bool backward) {
   KdLayout L;
   size_t cur = 0;
   auto take = [&](size_t bytes) {
@@ -194,7 +239,7 @@ KdLayout kd_layout(int64_t N, int H, int cols, int K, bool backward) {
     L.z = take(n * 4);
   } else {
     L.g = take(n * (size_t)cols * 2);
-    L.dx = take(n * (size_t)H * 4);
+    L.dx = take((size_t)dx_ranges(N, V, H).slots * n * (size_t)H * 4);
     L.dl = take(n * 4);
     L.p = take(n * (size_t)K * 4);
   }
@@ -241,11 +286,12 @@ MOE_API int kd_plan(int64_t N, int32_t H, int64_t V, int32_t v_chunk, int32_t K,
   p.K = K;
   p.temperature = temperature;
   p.dw_dtype = dw_dtype;
-  p.S = N == 0 ? 0 : (int32_t)ceil_div(V, v_chunk);
-  p.strip_bound_bytes = N * std::min<int64_t>(v_chunk, V) * 2;
-  const int cols = strip_cols(V, v_chunk);
-  p.fwd_workspace_bytes = N == 0 ? 0 : (int64_t)kd_layout(N, H, cols, K, false).total;
-  p.bwd_workspace_bytes = N == 0 ? 0 : (int64_t)kd_layout(N, H, cols, K, true).total;
+  p.strip = strip_of(N, V, H, v_chunk);
+  p.S = N == 0 ? 0 : (int32_t)ceil_div(V, p.strip);
+  p.strip_bound_bytes = N * std::min<int64_t>(p.strip, V) * 2;
+  const int fcols = strip_cols(V, forward_strip(N, V, H, p.strip)), cols = strip_cols(V, p.strip);
+  p.fwd_workspace_bytes = N == 0 ? 0 : (int64_t)kd_layout(N, V, H, fcols, K, false).total;
+  p.bwd_workspace_bytes = N == 0 ? 0 : (int64_t)kd_layout(N, V, H, cols, K, true).total;
   *out = p;
   return MOE_OK;
 }
@@ -259,20 +305,20 @@ MOE_API int kd_forward(const kd_plan_t* plan, const void* X, const void* W, cons
   if (!X || !W || !t_idx || !t_logit || !loss || !lse || !y_top || !workspace) return MOE_EINVAL;
   if ((uintptr_t)workspace % 256) return MOE_EINVAL;
   if (workspace_bytes < (size_t)P.fwd_workspace_bytes) return MOE_EWORKSPACE;
-  const KdLayout L = kd_layout(P.N, P.H, strip_cols(P.V, P.v_chunk), P.K, false);
+  const int strip = forward_strip(P.N, P.V, P.H, P.strip);
+  const KdLayout L = kd_layout(P.N, P.V, P.H, strip_cols(P.V, strip), P.K, false);
   hipStream_t st = (hipStream_t)stream;
   char* ws = (char*)workspace;
   float* pmax = (float*)(ws + L.pmax);
   float* psum = (float*)(ws + L.psum);
   (void)hipGetLastError();
-  for (int s = 0; s < P.S; ++s) {
-    const int64_t v0 = (int64_t)s * P.v_chunk;
-    const int w = (int)std::min<int64_t>(P.v_chunk, P.V - v0);
+  for (int64_t v0 = 0; v0 < P.V; v0 += strip) {
+    const int w = (int)std::min<int64_t>(strip, P.V - v0);
     KD_CHECK(gemm_kd_logits(false, X, (const bf16_t*)W + v0 * P.H, P.N, P.H, w, 1.f / P.temperature,
                             pmax, psum, nullptr, nullptr, nullptr, 0, st));
     const int nsl = (int)ceil_div(w, 256) * (256 / kCceSlice);
-    KD_CHECK(launch_cce_fold(pmax, psum, nsl, P.N, (float*)(ws + L.m), (float*)(ws + L.z), s == 0,
-                             s == P.S - 1, nullptr, nullptr, P.V, nullptr, lse, st));
+    KD_CHECK(launch_cce_fold(pmax, psum, nsl, P.N, (float*)(ws + L.m), (float*)(ws + L.z), v0 == 0,
+                             v0 + w == P.V, nullptr, nullptr, P.V, nullptr, lse, st));
   }
   kd_loss_kernel<<<(unsigned)P.N, kThreads, 0, st>>>(kd_args(P, X, W, t_idx, t_logit, lse), loss,
                                                      y_top);
@@ -298,8 +344,9 @@ MOE_API int kd_backward(const kd_plan_t* plan, const void* X, const void* W, con
     KD_CHECK(launch_fill_zero(dW, (size_t)P.V * P.H * dwb, st));
     return MOE_OK;
   }
-  const int cols = strip_cols(P.V, P.v_chunk);
-  const KdLayout L = kd_layout(P.N, P.H, cols, P.K, true);
+  const int cols = strip_cols(P.V, P.strip);
+  const KdLayout L = kd_layout(P.N, P.V, P.H, cols, P.K, true);
+  const DxRanges R = dx_ranges(P.N, P.V, P.H);
   char* ws = (char*)workspace;
   bf16_t* G = (bf16_t*)(ws + L.g);
   float* dx = (float*)(ws + L.dx);
@@ -309,20 +356,25 @@ MOE_API int kd_backward(const kd_plan_t* plan, const void* X, const void* W, con
   kd_prep_kernel<<<(unsigned)ceil_div(P.N, kWaves), kThreads, 0, st>>>(a, dloss, dl, psum);
   KD_CHECK(hipGetLastError());
   for (int s = 0; s < P.S; ++s) {
-    const int64_t v0 = (int64_t)s * P.v_chunk;
-    const int w = (int)std::min<int64_t>(P.v_chunk, P.V - v0);
+    const int64_t v0 = (int64_t)s * P.strip;
+    const int w = (int)std::min<int64_t>(P.strip, P.V - v0);
     const bf16_t* Ws = (const bf16_t*)W + v0 * P.H;
     KD_CHECK(gemm_kd_logits(true, X, Ws, P.N, P.H, w, 1.f / P.temperature, nullptr, nullptr, lse,
                             dl, G, cols, st));
     kd_entries_kernel<<<(unsigned)ceil_div(P.N * P.K, kThreads), kThreads, 0, st>>>(
         a, y_top, dl, psum, v0, w, G, cols);
     KD_CHECK(hipGetLastError());
-    KD_CHECK(gemm_cce_dx(G, cols, Ws, P.N, P.H, w, dx, s == 0, st));
+    if (R.slots > 1)
+      KD_CHECK(gemm_kd_dx(G, cols, Ws, P.N, P.H, w, v0, dx, R.range, R.slots, st));
+    else
+      KD_CHECK(gemm_cce_dx(G, cols, Ws, P.N, P.H, w, dx, s == 0, st));
     if (P.dw_dtype == MOE_BF16)
       KD_CHECK(gemm_kd_dw_bf16(G, cols, X, P.N, P.H, w, (bf16_t*)dW + v0 * P.H, st));
     else
       KD_CHECK(gemm_cce_dw(G, cols, X, P.N, P.H, w, (float*)dW + v0 * P.H, st));
   }
-  KD_CHECK(launch_cce_round(dx, dX, P.N * P.H, st));
+  const int64_t n4 = P.N * P.H / 4;
+  kd_fold_dx_kernel<<<(unsigned)ceil_div(n4, kThreads), kThreads, 0, st>>>(dx, R.slots, n4, (bf16_t*)dX);
+  KD_CHECK(hipGetLastError());
   return MOE_OK;
 }

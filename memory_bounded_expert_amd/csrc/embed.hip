@@ -24,7 +24,7 @@ namespace moe {
 namespace {
 
 constexpr uint32_t kEmbedMagic = 0x454d4231u;  // "EMB1"
-constexpr int kTileRows = 32;                  // sorted positions per summing tile
+constexpr int kTileRows = 64;                  // sorted positions per summing tile
 constexpr int kSortTile = 1024;                // keys per work-group of a sort pass
 constexpr int kSortRounds = kSortTile / kThreads;
 constexpr int kWaves = kThreads / 64;
@@ -299,7 +299,7 @@ __device__ __forceinline__ void zero_rows(const SumArgs& a, int64_t r0, int64_t 
 template <typename T, bool VEC>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(const SumArgs a) {
   constexpr int EPC = VEC ? Elem<T>::kPer16B : 1;
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 16;
   using Raw = std::conditional_t<VEC, u32x4_t, T>;
   __shared__ uint8_t occurs[kMaxZeroRows];
   if ((int64_t)blockIdx.x >= a.groups) {

@@ -89,6 +89,34 @@ hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, i
   return launch_lds<Mode::Dense, Logit, false, true, true, false, Epi::KDGrad>(p, grid, st);
 }
 
+hipError_t gemm_kd_dx(const void* G, int ldg, const void* Ws, int64_t N, int H, int w, int64_t v0,
+                      float* sums, int range, int slots, hipStream_t st) {
+  Params p{};
+  p.lda = ldg;
+  p.ldb = H;
+  p.C = sums; p.ldc = H; p.c_estride = N * H;
+  p.M = (int)N; p.N = H;
+  p.range = range;
+  p.range_slots = slots;
+  const int bn = H % 256 == 0 ? 256 : 128;
+  // at most `slots` ranges a launch, so that each has a sum of its own
+  for (int64_t v = v0; v < v0 + w;) {
+    const int64_t first = v / range, end = std::min(v0 + w, (first + slots) * range);
+    p.A = (const bf16_t*)G + (v - v0);
+    p.B = (const bf16_t*)Ws + (v - v0) * H;
+    p.K = (int)(end - v);
+    p.range_first = (int)first;
+    p.range_off = (int)(v - first * range);
+    const dim3 grid((unsigned)ceil_div(N, 256), (unsigned)(H / bn), (unsigned)ceil_div(end - first * range, range));
+    const hipError_t err =
+        bn == 256 ? launch_lds<Mode::Dense, Shape<256, 256, 4, 2, 32, 1>, false, true, false, false, Epi::AccRanges>(p, grid, st)
+                  : launch_lds<Mode::Dense, Shape<256, 128, 4, 2, 32, 1>, false, true, false, false, Epi::AccRanges>(p, grid, st);
+    if (err != hipSuccess) return err;
+    v = end;
+  }
+  return hipSuccess;
+}
+
 hipError_t gemm_kd_dw_bf16(const void* G, int ldg, const void* X, int64_t N, int H, int w,
                            void* dws, hipStream_t st) {
   if (w == 0) return hipSuccess;

@@ -51,9 +51,11 @@ enum class Mode { Rows, Dense, Expert, ExpertIdx, ExpertIdxB };
 // pipeline, Dense mode only).
 // KDStats and KDGrad are their forms for distillation: logits times ce_scale,
 // no targets.
+// AccRanges is AccF32 over ranges of K, each with a sum of its own (LDS
+// pipeline, Dense mode only).
 // SwiGLUBwd is the SwiGLU backward fused into dY W_down^T (LDS pipeline,
 // Rows mode only).
-enum class Epi { Store, SwiGLU, SwiGLUSave, F32, BiasF32, AccF32, CEStats, CEGrad, KDStats, KDGrad, SwiGLUBwd };
+enum class Epi { Store, SwiGLU, SwiGLUSave, F32, BiasF32, AccF32, CEStats, CEGrad, KDStats, KDGrad, AccRanges, SwiGLUBwd };
 
 struct Params {
   const void* A;
@@ -90,6 +92,11 @@ struct Params {
   // accumulators before the K loop and store the result, so that C + A B is
   // one fp32 accumulation chain continuing C's own.
   int acc_chain;
+  // Epi::AccRanges: the K columns start range_off into range range_first of
+  // `range` columns each; blockIdx.z takes the z-th range's part of them onto
+  // the sum in slot (range_first + z) % range_slots (c_estride elements
+  // each), as acc_chain does, from zero where the slot's first range starts.
+  int range, range_off, range_first, range_slots;
   // Epi::CEStats / Epi::CEGrad: the N columns of the tile grid are vocabulary
   // entries ce_col0 + n; ce_targets[row] is the row's target entry.
   const int32_t* ce_targets;

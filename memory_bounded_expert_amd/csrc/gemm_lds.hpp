@@ -257,6 +257,7 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
   constexpr bool KIDX_A = MODE == Mode::ExpertIdx, KIDX_B = MODE == Mode::ExpertIdxB;
   constexpr bool KIDX = KIDX_A || KIDX_B;
   constexpr bool EXPERT = MODE == Mode::Expert || KIDX;
+  constexpr bool ACC = EPI == Epi::AccF32 || EPI == Epi::AccRanges;
   static_assert(!KIDX_A || (!A_K && !KCAT), "row-indexed K needs an M-contiguous A");
   static_assert(!KIDX_B || (!B_K && !DUAL && !KCAT), "row-indexed K needs one N-contiguous B");
   // loads per thread per K-tile (an indexed product adds its index block)
@@ -271,8 +272,9 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
   const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int e = 0, m0 = 0, row_end = 0;
   int n0 = blockIdx.y * BN;
-  int64_t k_begin = 0;
+  int64_t k_begin = 0, kslice = 0;
   int k_len = p.K;
+  bool chain = p.acc_chain && !p.acc_init;  // accumulators continue C's sum
   if constexpr (MODE == Mode::Rows) {
     // XCD-aware renumbering of the 1-D grid (xcd_contiguous), then the
     // expert-local N-major order of rows_tile
@@ -289,6 +291,13 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
     m0 = blockIdx.x * BM;
     row_end = p.M;
     if (gridDim.z > 1) k_len = p.Kseg;
+    if constexpr (EPI == Epi::AccRanges) {
+      const int z = blockIdx.z;
+      kslice = max(0, z * p.range - p.range_off);
+      k_len = min(p.K, (z + 1) * p.range - p.range_off) - (int)kslice;
+      e = (p.range_first + z) % p.range_slots;
+      chain = (z == 0 && p.range_off > 0) || p.range_first + z >= p.range_slots;
+    }
   } else {
     const ExpertTile t = expert_tile(p.tile_group);
     e = t.e;
@@ -307,7 +316,8 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
   k_len = __builtin_amdgcn_readfirstlane(k_len);
   k_begin = (int64_t)__builtin_amdgcn_readfirstlane((int)k_begin);
 
-  const int64_t kslice = (MODE == Mode::Dense && gridDim.z > 1) ? (int64_t)blockIdx.z * p.Kseg : 0;
+  if constexpr (MODE == Mode::Dense && EPI != Epi::AccRanges)
+    kslice = gridDim.z > 1 ? (int64_t)blockIdx.z * p.Kseg : 0;
   const T* Ap = static_cast<const T*>(p.A) + kslice;
   const T* A2p = static_cast<const T*>(p.A2);
   const int64_t boff = (MODE == Mode::Rows) ? (int64_t)e * p.b_estride : kslice * p.ldb;
@@ -541,8 +551,8 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
       for (int j = 0; j < FN; ++j) acc[g][i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
   const int l16 = lane & 15, lg = lane >> 4;  // column/row within a fragment, k-group
-  if constexpr (EPI == Epi::AccF32) {
-    if (p.acc_chain && !p.acc_init) {
+  if constexpr (ACC) {
+    if (chain) {
       // C into the accumulators (rows past row_end as zeros), through this
       // wave's LDS share, before the pipeline takes the stages over
       using AG = AccGeom<S, C>;
@@ -767,7 +777,7 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
   wait_vmcnt<0>();
   }
 
-  if constexpr (EPI == Epi::AccF32) {
+  if constexpr (ACC) {
     // C += tile (fp32 read-modify-write), or C = tile with acc_init or
     // acc_chain (the accumulators then already hold the whole sum).  Each
     // wave moves its own block through its LDS share (AccGeom); the old
@@ -793,7 +803,7 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
       float* Cg = static_cast<float*>(g == 0 ? p.C : p.C2) + (int64_t)e * p.c_estride;
       return reinterpret_cast<f32x4_t*>(Cg + (int64_t)grow(s, u) * p.ldc + cw0 + c4 * 4);
     };
-    const bool accumulate = !p.acc_init && !p.acc_chain;
+    const bool accumulate = EPI == Epi::AccF32 && !p.acc_init && !p.acc_chain;
     constexpr int PD = 3;  // slices of old values requested ahead
     f32x4_t old[PD + 1][AG::PER];
     if (accumulate) {

@@ -388,8 +388,6 @@ hipError_t launch_cce_fold(const float* pmax, const float* psum, int nslices, in
                            float* z, bool first, bool last, const float* ytgt,
                            const int32_t* targets, int64_t V, float* loss, float* lse,
                            hipStream_t st);
-// dst = bf16(src), n a multiple of 4.
-hipError_t launch_cce_round(const float* src, void* dst, int64_t n, hipStream_t st);
 
 // ---- distillation over vocabulary strips (distill.hip, gemm_cce.hip)
 // As gemm_cce_logits on logits times inv_t, without targets: the statistics,
@@ -397,6 +395,12 @@ hipError_t launch_cce_round(const float* src, void* dst, int64_t n, hipStream_t 
 hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, int H, int w,
                           float inv_t, float* pmax, float* psum, const float* lse, const float* dl,
                           void* G, int ldg, hipStream_t st);
+// As gemm_cce_dx for the strip that starts at vocabulary entry v0 (v0, range
+// multiples of 256), with the vocabulary in ranges of `range` entries: range r
+// adds to sum r % slots (sums [slots][N][H] fp32, each one accumulation chain
+// over its ranges in order), so that the ranges of a strip run side by side.
+hipError_t gemm_kd_dx(const void* G, int ldg, const void* Ws, int64_t N, int H, int w, int64_t v0,
+                      float* sums, int range, int slots, hipStream_t st);
 // As gemm_cce_dw, rounded once to bf16.
 hipError_t gemm_kd_dw_bf16(const void* G, int ldg, const void* X, int64_t N, int H, int w,
                            void* dws, hipStream_t st);

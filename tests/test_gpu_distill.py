@@ -131,6 +131,33 @@ def test_ragged_batch_and_strip_width(T):
             assert torch.equal(out[k], other[k]), (vc, k)
 
 
+@pytest.mark.parametrize("H", [256, 384])
+def test_ranges_of_dx_across_strips(H):
+    """Several strips, and dX in ranges that start inside a strip and take turns
+    on their sums; the same bits for every strip width."""
+    require_lib()
+    N, V, K, T = 2000, 60_000, 5, 2.0
+    c = Case(N, H, V, K, seed=H)
+    p = B.kd_plan(N, H, V, 4096, K, T)
+    assert p.S > 2
+    out = run(c, 4096, T)
+    for vc in (256, 1280, 16_640):
+        other = run(c, vc, T)
+        for k in out:
+            assert torch.equal(out[k], other[k]), (vc, k)
+    X, W, idx = c.X.double(), c.W.double(), dev(c.idx).long()
+    y = X @ W.T / T
+    lse = torch.logsumexp(y, 1)
+    assert torch.all((out["lse"].double() - lse).abs() <= 2e-5)
+    p64 = torch.softmax(dev(c.t).double() / T, 1)
+    up = T * dev(c.dloss).double()[:, None]
+    g = torch.exp(y - lse[:, None]).scatter_add_(1, idx, -p64) * up
+    # e of each gradient (and 1e-4 of it for fp32's share), V u of the sum, e of the result
+    dX, dW, aX, aW = g @ W, g.T @ X, X.abs(), W.abs()
+    assert torch.all((out["dX"].double() - dX).abs() <= (E + 1e-4 + V * U) * (g.abs() @ aW) + E * dX.abs())
+    assert torch.all((out["dW"].double() - dW).abs() <= (E + 1e-4 + N * U) * (g.abs().T @ aX) + U * dW.abs())
+
+
 def test_extreme_lists():
     require_lib()
     c = Case(40, 128, 500, 8, seed=4)
