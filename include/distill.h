@@ -61,8 +61,8 @@ typedef struct kd_plan {
     float temperature;
     int32_t dw_dtype;             /* enum moe_dtype of dW                     */
     int32_t S;                    /* strips, ceil(V / strip); 0 if N = 0      */
-    int32_t strip;                /* strip width: v_chunk, or the largest
-                                     multiple within KD_STRIP_BYTES           */
+    int32_t strip;                /* strip width: v_chunk, or a multiple with
+                                     strip_bound_bytes <= KD_STRIP_BYTES      */
     int32_t reserved0;
     int64_t strip_bound_bytes;    /* N * min(strip, V) * 2                    */
     int64_t fwd_workspace_bytes;  /* workspace kd_forward needs               */

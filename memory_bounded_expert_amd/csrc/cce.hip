@@ -36,6 +36,12 @@ struct CceLayout {
   size_t total = 0;
 };
 
+// Columns of the strip buffers: the widest strip rounded up to whole
+// 256-column logit tiles (v_chunk itself unless the vocabulary is narrower).
+int strip_cols(int64_t V, int v_chunk) {
+  return (int)std::min<int64_t>(v_chunk, ceil_div(V, 256) * 256);
+}
+
 CceLayout cce_layout(int64_t N, int H, int cols, bool backward) {
   CceLayout L;
   size_t cur = 0;
@@ -101,7 +107,6 @@ __global__ __launch_bounds__(kFoldThreads) void cce_fold_kernel(
   if (last) {
     const float l = mm + logf(zz);
     lse[t] = l;
-    if (!loss) return;  // only the normaliser is wanted
     const int tg = targets[t];
     loss[t] = (tg >= 0 && (int64_t)tg < V) ? l - ytgt[t] : 0.f;
   } else {
@@ -139,16 +144,6 @@ unsigned blocks(int64_t n) { return (unsigned)ceil_div(n, kCceThreads); }
 bool plan_ok(const cce_plan_t* p) { return p != nullptr && p->magic == kCceMagic; }
 
 }  // namespace
-
-hipError_t launch_cce_fold(const float* pmax, const float* psum, int nslices, int64_t N, float* m,
-                           float* z, bool first, bool last, const float* ytgt,
-                           const int32_t* targets, int64_t V, float* loss, float* lse,
-                           hipStream_t st) {
-  cce_fold_kernel<<<(unsigned)ceil_div(N, kFoldThreads), kFoldThreads, 0, st>>>(
-      pmax, psum, nslices, N, m, z, first, last, ytgt, targets, V, loss, lse);
-  return hipGetLastError();
-}
-
 }  // namespace moe
 
 using namespace moe;
@@ -209,8 +204,9 @@ MOE_API int cce_forward(const cce_plan_t* plan, const void* X, const void* W,
                               nullptr, nullptr, 0, st));
     // slices the GEMM wrote: whole 256-column tiles, two slices each
     const int nsl = (int)ceil_div(w, 256) * (256 / kCceSlice);
-    CCE_CHECK(launch_cce_fold(pmax, psum, nsl, P.N, m, z, s == 0, s == P.S - 1, ytgt, targets, P.V,
-                              loss, lse, st));
+    cce_fold_kernel<<<(unsigned)ceil_div(P.N, kFoldThreads), kFoldThreads, 0, st>>>(
+        pmax, psum, nsl, P.N, m, z, s == 0, s == P.S - 1, ytgt, targets, P.V, loss, lse);
+    CCE_CHECK(hipGetLastError());
   }
   return MOE_OK;
 }
@@ -285,10 +281,11 @@ MOE_API int cce_debug_stage(const cce_plan_t* plan, int32_t stage, int32_t strip
       break;
     case CCE_STAGE_FOLD: {
       const int nsl = (int)ceil_div(w, 256) * (256 / kCceSlice);
-      CCE_CHECK(launch_cce_fold((float*)(ws + L.pmax), (float*)(ws + L.psum), nsl, P.N,
-                                (float*)(ws + L.m), (float*)(ws + L.z), strip == 0,
-                                strip == P.S - 1, (float*)(ws + L.ytgt), targets, P.V, loss, lse,
-                                st));
+      cce_fold_kernel<<<(unsigned)ceil_div(P.N, kFoldThreads), kFoldThreads, 0, st>>>(
+          (float*)(ws + L.pmax), (float*)(ws + L.psum), nsl, P.N, (float*)(ws + L.m),
+          (float*)(ws + L.z), strip == 0, strip == P.S - 1, (float*)(ws + L.ytgt), targets, P.V,
+          loss, lse);
+      CCE_CHECK(hipGetLastError());
       break;
     }
     case CCE_STAGE_GRAD:

@@ -74,6 +74,43 @@ __device__ __forceinline__ bool list_softmax(const KdArgs& a, int64_t t, int lan
   return any;
 }
 
+// Folds a strip's slice pairs into the running maximum m and sum z of
+// exp(y - m), in vocabulary order: the larger maximum stays, the other's sum is
+// rescaled by one exponential.  A slice past the vocabulary has maximum -inf.
+// One thread per token, 64-token blocks; the pairs are loaded kFoldAhead at a
+// time.  The last strip finishes lse.
+constexpr int kFoldThreads = 64, kFoldAhead = 16;
+__global__ __launch_bounds__(kFoldThreads) void kd_fold_kernel(
+    const float* __restrict__ pmax, const float* __restrict__ psum, int nslices, int64_t N,
+    float* __restrict__ m, float* __restrict__ z, int first, int last, float* __restrict__ lse) {
+  const int64_t t = (int64_t)blockIdx.x * kFoldThreads + threadIdx.x;
+  if (t >= N) return;
+  float mm = first ? -INFINITY : m[t];
+  float zz = first ? 0.f : z[t];
+  for (int s0 = 0; s0 < nslices; s0 += kFoldAhead) {
+    float a[kFoldAhead], b[kFoldAhead];
+#pragma unroll
+    for (int u = 0; u < kFoldAhead; ++u) {
+      const int s = min(s0 + u, nslices - 1);
+      a[u] = pmax[(int64_t)s * N + t];
+      b[u] = psum[(int64_t)s * N + t];
+    }
+#pragma unroll
+    for (int u = 0; u < kFoldAhead; ++u) {
+      if (s0 + u >= nslices || a[u] == -INFINITY) continue;
+      const float far = __expf(-fabsf(a[u] - mm));
+      zz = a[u] > mm ? fmaf(zz, far, b[u]) : fmaf(b[u], far, zz);
+      mm = fmaxf(mm, a[u]);
+    }
+  }
+  if (last) {
+    lse[t] = mm + logf(zz);
+  } else {
+    m[t] = mm;
+    z[t] = zz;
+  }
+}
+
 // One work-group per token: the list entries' logits, a wave taking kDots
 // rows of W at a time, then the loss.
 __global__ __launch_bounds__(kThreads) void kd_loss_kernel(const KdArgs a, float* __restrict__ loss,
@@ -183,12 +220,20 @@ __global__ __launch_bounds__(kThreads) void kd_fold_dx_kernel(const float* __res
   reinterpret_cast<ushort4*>(dX)[i] = make_ushort4(f2bf(s[0]), f2bf(s[1]), f2bf(s[2]), f2bf(s[3]));
 }
 
-// The backward pass's strips: v_chunk, times what KD_STRIP_BYTES leaves.
+// Columns of a strip's buffers: whole 256-column logit tiles.
+int strip_cols(int64_t V, int strip) {
+  return (int)std::min<int64_t>(strip, ceil_div(V, 256) * 256);
+}
+
+// The backward pass's strips: v_chunk, times what KD_STRIP_BYTES leaves (and
+// 32-bit offsets into W), evened out over the vocabulary.
 int strip_of(int64_t N, int64_t V, int H, int v_chunk) {
+  const int64_t cols = ceil_div(V, 256) * 256;
   const int64_t most = std::min<int64_t>((int64_t)KD_STRIP_BYTES / 2 / std::max<int64_t>(N, 1),
                                          (((int64_t)1 << 30) - 1) / H);
-  const int64_t wanted = std::min(most, ceil_div(V, 256) * 256);
-  return (int)(std::max<int64_t>(wanted / v_chunk, 1) * v_chunk);
+  if (cols <= most) return (int)(ceil_div(cols, v_chunk) * v_chunk);
+  const int64_t strips = ceil_div(V, std::max<int64_t>(most / v_chunk, 1) * v_chunk);
+  return (int)(ceil_div(ceil_div(V, strips), v_chunk) * v_chunk);
 }
 
 // The forward pass keeps no logits, so its strips are as many of these as make
@@ -317,8 +362,9 @@ MOE_API int kd_forward(const kd_plan_t* plan, const void* X, const void* W, cons
     KD_CHECK(gemm_kd_logits(false, X, (const bf16_t*)W + v0 * P.H, P.N, P.H, w, 1.f / P.temperature,
                             pmax, psum, nullptr, nullptr, nullptr, 0, st));
     const int nsl = (int)ceil_div(w, 256) * (256 / kCceSlice);
-    KD_CHECK(launch_cce_fold(pmax, psum, nsl, P.N, (float*)(ws + L.m), (float*)(ws + L.z), v0 == 0,
-                             v0 + w == P.V, nullptr, nullptr, P.V, nullptr, lse, st));
+    kd_fold_kernel<<<(unsigned)ceil_div(P.N, kFoldThreads), kFoldThreads, 0, st>>>(
+        pmax, psum, nsl, P.N, (float*)(ws + L.m), (float*)(ws + L.z), v0 == 0, v0 + w == P.V, lse);
+    KD_CHECK(hipGetLastError());
   }
   kd_loss_kernel<<<(unsigned)P.N, kThreads, 0, st>>>(kd_args(P, X, W, t_idx, t_logit, lse), loss,
                                                      y_top);

@@ -6,7 +6,8 @@
 // for the most part.  The positions are sorted by id with a stable radix sort
 // of two or three passes; the sorted rows are summed in tiles of kTileRows
 // positions by blocks of columns, and runs of one id that cross tiles are
-// joined in order by a last launch.  The sort's launches are short and fill few
+// joined in order by a last launch.  Up to kSmallSort positions are sorted by
+// one work-group in LDS.  The sort's launches are short and fill few
 // CUs, so each also zeroes a slice of dW on the others; the rest is zeroed in
 // the summing launch, which knows the ids and skips the rows it writes itself.
 #include <algorithm>
@@ -169,8 +170,23 @@ __global__ __launch_bounds__(kScanThreads) void sort_scan_kernel(const SortPass 
   }
 }
 
-// Each wave places its kSortTile / kWaves consecutive keys in order: within 64
-// keys, equal digits rank by lane (one ballot per digit bit).
+// The output place of each lane's digit d: equal digits of a wave rank by lane
+// (one ballot per digit bit); next[d], the wave's own, moves past them.
+__device__ __forceinline__ int place_equal(int32_t* next, uint32_t d, int bits, bool in) {
+  const int lane = threadIdx.x & 63;
+  uint64_t same = __ballot(in);
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t m = __ballot((d >> b) & 1);
+    same &= (d >> b) & 1 ? m : ~m;
+  }
+  const int at = in ? next[d] + __popcll(same & ((1ull << lane) - 1)) : 0;
+  wave_lds_order();  // every lane has read its start
+  if (in && (same >> lane) == 1) next[d] = at + 1;  // the digit's last lane
+  wave_lds_order();
+  return at;
+}
+
+// Each wave places its kSortTile / kWaves consecutive keys in order.
 __global__ __launch_bounds__(kThreads) void sort_place_kernel(const SortPass a) {
   __shared__ int32_t next[kWaves][1 << kMaxDigit];
   if (zeroes(a)) return;
@@ -201,20 +217,93 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(const SortPass a) 
   for (int r = 0; r < kSortRounds; ++r) {
     const int64_t i = base + r * 64 + lane;
     const bool in = i < a.N;
-    const uint32_t d = (key[r] >> a.shift) & (bins - 1);
-    uint64_t same = __ballot(in);
-    for (int b = 0; b < a.bits; ++b) {
-      const uint64_t m = __ballot((d >> b) & 1);
-      same &= (d >> b) & 1 ? m : ~m;
-    }
-    const int before = __popcll(same & ((1ull << lane) - 1));
-    const int at = in ? next[w][d] + before : 0;
-    wave_lds_order();  // every lane has read its start
-    if (in && (same >> lane) == 1) next[w][d] = at + 1;  // the digit's last lane
-    wave_lds_order();
+    const int at = place_equal(next[w], (key[r] >> a.shift) & (bins - 1), a.bits, in);
     if (in) {
       a.key_out[at] = key[r];
       a.pos_out[at] = a.ids ? (uint32_t)i : a.pos[i];
+    }
+  }
+}
+
+// All passes for N <= kSmallSort positions in one work-group: each wave holds
+// consecutive ones in registers, places them in LDS by digits of 8 bits, and
+// takes them up again in order.
+constexpr int kSmallSort = 4096, kSmallThreads = 1024, kSmallBits = 8;
+__global__ __launch_bounds__(kSmallThreads) void sort_small_kernel(const SortPass a) {
+  constexpr int W = kSmallThreads / 64, R = kSmallSort / kSmallThreads, BINS = 1 << kSmallBits;
+  __shared__ uint32_t keys[kSmallSort], poss[kSmallSort];
+  __shared__ int32_t next[W][BINS];
+  __shared__ int32_t sums[BINS / 64];
+  if (zeroes(a)) return;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int N = (int)a.N;
+  const int per = (N + W * 64 - 1) / (W * 64);  // rounds of 64 a wave
+  uint32_t key[R], pos[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = (w * per + r) * 64 + lane;
+    key[r] = 0u;
+    pos[r] = (uint32_t)i;
+    if (r < per && i < N) key[r] = sort_key(a, i);
+  }
+  for (int shift = 0; shift < a.bits; shift += kSmallBits) {
+    for (int b = threadIdx.x; b < W * BINS; b += kSmallThreads) (&next[0][0])[b] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < per && (w * per + r) * 64 + lane < N) atomicAdd(&next[w][(key[r] >> shift) & (BINS - 1)], 1);
+    __syncthreads();
+    // first places: bins in order, a bin's waves in order
+    int total = 0, inc = 0;
+    if (threadIdx.x < BINS) {
+      for (int v = 0; v < W; ++v) total += next[v][threadIdx.x];
+      inc = total;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(inc, o);
+        if (lane >= o) inc += u;
+      }
+      if (lane == 63) sums[w] = inc;
+    }
+    __syncthreads();
+    if (threadIdx.x < BINS) {
+      int run = inc - total;
+      for (int v = 0; v < w; ++v) run += sums[v];
+      for (int v = 0; v < W; ++v) {
+        const int c = next[v][threadIdx.x];
+        next[v][threadIdx.x] = run;
+        run += c;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r < per) {
+        const bool in = (w * per + r) * 64 + lane < N;
+        const int at = place_equal(next[w], (key[r] >> shift) & (BINS - 1), kSmallBits, in);
+        if (in) {
+          keys[at] = key[r];
+          poss[at] = pos[r];
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = (w * per + r) * 64 + lane;
+      if (r < per && i < N) {
+        key[r] = keys[i];
+        pos[r] = poss[i];
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = (w * per + r) * 64 + lane;
+    if (r < per && i < N) {
+      a.key_out[i] = key[r];
+      a.pos_out[i] = pos[r];
     }
   }
 }
@@ -421,7 +510,7 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(const SumArgs a) {
 
 struct EmbedLayout {
   size_t key[2], pos[2], hist, part, total;
-  int tiles, passes, bits;
+  int tiles, passes, bits, key_bits;
 };
 
 EmbedLayout embed_layout(int64_t N, int64_t V, int H) {
@@ -434,6 +523,7 @@ EmbedLayout embed_layout(int64_t N, int64_t V, int H) {
   };
   int bits = 1;
   while (((int64_t)1 << bits) <= V) ++bits;  // keys 0 .. V
+  L.key_bits = bits;
   L.passes = (bits + kMaxDigit - 1) / kMaxDigit;
   L.bits = (bits + L.passes - 1) / L.passes;
   L.tiles = (int)ceil_div(N, kSortTile);
@@ -545,7 +635,16 @@ MOE_API int embed_backward(const embed_plan_t* plan, const int32_t* ids, const v
     zeroed += rows;
     return (unsigned)(groups + ceil_div(rows * P.H, kZeroBytes / 4));
   };
-  for (int i = 0; i < L.passes; ++i) {
+  if (P.N <= kSmallSort) {
+    s.bits = L.key_bits;
+    s.key_out = (uint32_t*)(ws + L.key[0]);
+    s.pos_out = (uint32_t*)(ws + L.pos[0]);
+    const unsigned g = grid(1);
+    sort_small_kernel<<<g, kSmallThreads, 0, st>>>(s);
+    s.key = s.key_out;
+    s.pos = s.pos_out;
+  }
+  for (int i = 0; P.N > kSmallSort && i < L.passes; ++i) {
     s.shift = i * L.bits;
     s.key_out = (uint32_t*)(ws + L.key[i & 1]);
     s.pos_out = (uint32_t*)(ws + L.pos[i & 1]);

@@ -11,7 +11,9 @@ namespace {
 // 256 x 256 tiles of 4 x 2 waves; each wave's 64 x 128 block is one
 // 128-column vocabulary slice of the statistics.
 using Logit = Shape<256, 256, 4, 2, 32, 1>;
+using LogitFew = Shape<128, 256, 2, 2, 32, 2>;
 static_assert(Logit::BN / Logit::WGN == kCceSlice, "statistics slice = one wave's columns");
+static_assert(LogitFew::BN / LogitFew::WGN == kCceSlice, "statistics slice = one wave's columns");
 }  // namespace
 
 hipError_t gemm_cce_logits(bool grad, const void* X, const void* Ws, int64_t N, int H, int w,
@@ -80,13 +82,19 @@ hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, i
   p.M = (int)N; p.N = w; p.K = H;
   p.ce_scale = inv_t;
   const dim3 grid((unsigned)ceil_div(N, Logit::BM), (unsigned)ceil_div(w, Logit::BN));
+  // Less than four rounds of tiles, one per CU: 128-row tiles, two per CU, lose
+  // less in the last round and in a batch of at most 128 tokens.
+  const bool few = (int64_t)grid.x * grid.y < 4 * kCus;
+  const dim3 grid2((unsigned)ceil_div(N, LogitFew::BM), grid.y);
   if (!grad) {
     p.ce_pmax = pmax; p.ce_psum = psum;
-    return launch_lds<Mode::Dense, Logit, false, true, true, false, Epi::KDStats>(p, grid, st);
+    return few ? launch_lds<Mode::Dense, LogitFew, false, true, true, false, Epi::KDStats>(p, grid2, st)
+               : launch_lds<Mode::Dense, Logit, false, true, true, false, Epi::KDStats>(p, grid, st);
   }
   p.ce_lse = lse; p.ce_dl = dl;
   p.C = G; p.ldc = ldg;
-  return launch_lds<Mode::Dense, Logit, false, true, true, false, Epi::KDGrad>(p, grid, st);
+  return few ? launch_lds<Mode::Dense, LogitFew, false, true, true, false, Epi::KDGrad>(p, grid2, st)
+             : launch_lds<Mode::Dense, Logit, false, true, true, false, Epi::KDGrad>(p, grid, st);
 }
 
 hipError_t gemm_kd_dx(const void* G, int ldg, const void* Ws, int64_t N, int H, int w, int64_t v0,

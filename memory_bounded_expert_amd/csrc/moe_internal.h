@@ -6,8 +6,6 @@
 #include <stddef.h>
 #include <stdint.h>
 
-#include <algorithm>
-
 #include "moebound.h"
 
 namespace moe {
@@ -376,18 +374,6 @@ hipError_t gemm_cce_dx(const void* G, int ldg, const void* Ws, int64_t N, int H,
 // dws [w][H] fp32 = G[:, :w]^T X.
 hipError_t gemm_cce_dw(const void* G, int ldg, const void* X, int64_t N, int H, int w, float* dws,
                        hipStream_t st);
-
-// Columns of the strip buffers: the widest strip rounded up to whole
-// 256-column logit tiles (v_chunk itself unless the vocabulary is narrower).
-inline int strip_cols(int64_t V, int v_chunk) {
-  return (int)std::min<int64_t>(v_chunk, ceil_div(V, 256) * 256);
-}
-// Folds a strip's slice pairs into the running state (m, z); with last, lse
-// and, unless loss is nullptr, loss.
-hipError_t launch_cce_fold(const float* pmax, const float* psum, int nslices, int64_t N, float* m,
-                           float* z, bool first, bool last, const float* ytgt,
-                           const int32_t* targets, int64_t V, float* loss, float* lse,
-                           hipStream_t st);
 
 // ---- distillation over vocabulary strips (distill.hip, gemm_cce.hip)
 // As gemm_cce_logits on logits times inv_t, without targets: the statistics,

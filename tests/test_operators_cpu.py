@@ -260,8 +260,9 @@ def test_kd_strips_and_workspace():
     for N, H, V, v_chunk in ((777, 512, 20_000, 4096), (16, 7168, 200_000, 1024), (2000, 1024, 150_000, 256), (1, 128, 10, 256)):
         p = B.kd_plan(N, H, V, v_chunk, 4)
         assert p.strip % v_chunk == 0 and p.S == -(-V // p.strip)
-        assert p.strip == v_chunk or N * p.strip * 2 <= 64 << 20
-        assert p.strip >= min(V, (64 << 20) // (2 * N)) - v_chunk or p.strip * H > (1 << 30) - v_chunk * H
+        assert p.strip == v_chunk or p.strip_bound_bytes <= 64 << 20
+        most = min((64 << 20) // (2 * N), ((1 << 30) - 1) // H)  # columns that fit
+        assert p.S <= -(-V // max(most // v_chunk * v_chunk, v_chunk)) or p.S == 1
 
 
 def test_kd_argument_errors():
