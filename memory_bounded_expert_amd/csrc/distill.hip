@@ -74,35 +74,48 @@ __device__ __forceinline__ bool list_softmax(const KdArgs& a, int64_t t, int lan
   return any;
 }
 
-// Folds a strip's slice pairs into the running maximum m and sum z of
-// exp(y - m), in vocabulary order: the larger maximum stays, the other's sum is
-// rescaled by one exponential.  A slice past the vocabulary has maximum -inf.
-// One thread per token, 64-token blocks; the pairs are loaded kFoldAhead at a
-// time.  The last strip finishes lse.
-constexpr int kFoldThreads = 64, kFoldAhead = 16;
-__global__ __launch_bounds__(kFoldThreads) void kd_fold_kernel(
+// Adds (a, b), b = sum of exp(y - a), to (m, z): the larger maximum stays, the
+// other's sum is rescaled by one exponential.  A slice past the vocabulary has
+// a = -inf.
+__device__ __forceinline__ void fold(float a, float b, float& m, float& z) {
+  if (a == -INFINITY) return;
+  const float far = __expf(-fabsf(a - m));
+  z = a > m ? fmaf(z, far, b) : fmaf(b, far, z);
+  m = fmaxf(m, a);
+}
+
+// Folds a strip's slice pairs into the running state (m, z).  A work-group takes
+// 16 tokens, 16 threads each: every thread folds each 16th slice in order, then
+// one thread a token its state and the 16 results in order.  The last strip
+// finishes lse.
+constexpr int kFoldTokens = 16, kFoldWays = kThreads / kFoldTokens, kFoldAhead = 4;
+__global__ __launch_bounds__(kThreads) void kd_fold_kernel(
     const float* __restrict__ pmax, const float* __restrict__ psum, int nslices, int64_t N,
     float* __restrict__ m, float* __restrict__ z, int first, int last, float* __restrict__ lse) {
-  const int64_t t = (int64_t)blockIdx.x * kFoldThreads + threadIdx.x;
-  if (t >= N) return;
-  float mm = first ? -INFINITY : m[t];
-  float zz = first ? 0.f : z[t];
-  for (int s0 = 0; s0 < nslices; s0 += kFoldAhead) {
+  __shared__ float ms[kFoldWays][kFoldTokens], zs[kFoldWays][kFoldTokens];
+  const int i = threadIdx.x % kFoldTokens, way = threadIdx.x / kFoldTokens;
+  const int64_t t = (int64_t)blockIdx.x * kFoldTokens + i, tc = min(t, N - 1);
+  float mm = -INFINITY, zz = 0.f;
+  for (int s0 = way; s0 < nslices; s0 += kFoldAhead * kFoldWays) {
     float a[kFoldAhead], b[kFoldAhead];
 #pragma unroll
     for (int u = 0; u < kFoldAhead; ++u) {
-      const int s = min(s0 + u, nslices - 1);
-      a[u] = pmax[(int64_t)s * N + t];
-      b[u] = psum[(int64_t)s * N + t];
+      const int s = min(s0 + u * kFoldWays, nslices - 1);
+      a[u] = pmax[(int64_t)s * N + tc];
+      b[u] = psum[(int64_t)s * N + tc];
     }
 #pragma unroll
-    for (int u = 0; u < kFoldAhead; ++u) {
-      if (s0 + u >= nslices || a[u] == -INFINITY) continue;
-      const float far = __expf(-fabsf(a[u] - mm));
-      zz = a[u] > mm ? fmaf(zz, far, b[u]) : fmaf(b[u], far, zz);
-      mm = fmaxf(mm, a[u]);
-    }
+    for (int u = 0; u < kFoldAhead; ++u)
+      if (s0 + u * kFoldWays < nslices) fold(a[u], b[u], mm, zz);
   }
+  ms[way][i] = mm;
+  zs[way][i] = zz;
+  __syncthreads();
+  if (way != 0 || t >= N) return;
+  mm = first ? -INFINITY : m[t];
+  zz = first ? 0.f : z[t];
+#pragma unroll
+  for (int v = 0; v < kFoldWays; ++v) fold(ms[v][i], zs[v][i], mm, zz);
   if (last) {
     lse[t] = mm + logf(zz);
   } else {
@@ -208,15 +221,33 @@ __global__ __launch_bounds__(kThreads) void kd_entries_kernel(
   G[t * ldg + v] = f2bf(dl[t] * (expf(y_top[i] / a.T - a.lse[t]) - p));
 }
 
-// dX [N][H] = bf16 of the slots' sums, added in order; 4 values per thread.
+// dX [N][H] = bf16 of the slots' sums: a wave adds a quarter of the slots in
+// order, then the waves' sums are added in order.  4 values per lane.
 __global__ __launch_bounds__(kThreads) void kd_fold_dx_kernel(const float* __restrict__ sums,
                                                               int slots, int64_t n4,
                                                               bf16_t* __restrict__ dX) {
+  __shared__ f32x4_t part[kWaves][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t i = (int64_t)blockIdx.x * 64 + lane, ic = min(i, n4 - 1);
+  const int share = (slots + kWaves - 1) / kWaves;
+  f32x4_t s{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+  for (int v = w * share; v < min(slots, (w + 1) * share); ++v)
+    s += reinterpret_cast<const f32x4_t*>(sums)[v * n4 + ic];
+  part[w][lane] = s;
+  __syncthreads();
+  if (w != 0 || i >= n4) return;
+#pragma unroll
+  for (int v = 1; v < kWaves; ++v) s += part[v][lane];
+  reinterpret_cast<ushort4*>(dX)[i] = make_ushort4(f2bf(s[0]), f2bf(s[1]), f2bf(s[2]), f2bf(s[3]));
+}
+
+// The same of one sum; 4 values per thread.
+__global__ __launch_bounds__(kThreads) void kd_round_dx_kernel(const float* __restrict__ sum,
+                                                               int64_t n4, bf16_t* __restrict__ dX) {
   const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= n4) return;
-  f32x4_t s = reinterpret_cast<const f32x4_t*>(sums)[i];
-#pragma unroll 8
-  for (int z = 1; z < slots; ++z) s += reinterpret_cast<const f32x4_t*>(sums)[z * n4 + i];
+  const f32x4_t s = reinterpret_cast<const f32x4_t*>(sum)[i];
   reinterpret_cast<ushort4*>(dX)[i] = make_ushort4(f2bf(s[0]), f2bf(s[1]), f2bf(s[2]), f2bf(s[3]));
 }
 
@@ -236,13 +267,13 @@ int strip_of(int64_t N, int64_t V, int H, int v_chunk) {
   return (int)(ceil_div(ceil_div(V, strips), v_chunk) * v_chunk);
 }
 
-// The forward pass keeps no logits, so its strips are as many of these as make
-// four rounds of 256 x 256 tiles, one per CU (32-bit offsets into W allowing).
-int forward_strip(int64_t N, int64_t V, int H, int strip) {
-  const int64_t rows = ceil_div(N, 256);
-  const int64_t wanted = std::min(ceil_div(4 * 256, rows) * 256, V);
-  const int64_t most = (((int64_t)1 << 30) - 1) / H / strip;
-  return (int)(std::max<int64_t>(1, std::min(ceil_div(wanted, strip), most)) * strip);
+// The forward pass keeps no logits: its strips are wide enough for four rounds
+// of 256 x 256 tiles, one per CU (32-bit offsets into W allowing), and so
+// depend on N, V and H alone, as lse then does.
+int forward_strip(int64_t N, int64_t V, int H) {
+  const int64_t wanted = std::min(ceil_div(4 * 256, ceil_div(N, 256)) * 256, ceil_div(V, 256) * 256);
+  const int64_t most = (((int64_t)1 << 30) - 1) / H / 256 * 256;
+  return (int)std::min(wanted, most);
 }
 
 // dX's ranges: with fewer than 256 tiles of dX, as many sums side by side as
@@ -334,7 +365,7 @@ MOE_API int kd_plan(int64_t N, int32_t H, int64_t V, int32_t v_chunk, int32_t K,
   p.strip = strip_of(N, V, H, v_chunk);
   p.S = N == 0 ? 0 : (int32_t)ceil_div(V, p.strip);
   p.strip_bound_bytes = N * std::min<int64_t>(p.strip, V) * 2;
-  const int fcols = strip_cols(V, forward_strip(N, V, H, p.strip)), cols = strip_cols(V, p.strip);
+  const int fcols = strip_cols(V, forward_strip(N, V, H)), cols = strip_cols(V, p.strip);
   p.fwd_workspace_bytes = N == 0 ? 0 : (int64_t)kd_layout(N, V, H, fcols, K, false).total;
   p.bwd_workspace_bytes = N == 0 ? 0 : (int64_t)kd_layout(N, V, H, cols, K, true).total;
   *out = p;
@@ -350,7 +381,7 @@ MOE_API int kd_forward(const kd_plan_t* plan, const void* X, const void* W, cons
   if (!X || !W || !t_idx || !t_logit || !loss || !lse || !y_top || !workspace) return MOE_EINVAL;
   if ((uintptr_t)workspace % 256) return MOE_EINVAL;
   if (workspace_bytes < (size_t)P.fwd_workspace_bytes) return MOE_EWORKSPACE;
-  const int strip = forward_strip(P.N, P.V, P.H, P.strip);
+  const int strip = forward_strip(P.N, P.V, P.H);
   const KdLayout L = kd_layout(P.N, P.V, P.H, strip_cols(P.V, strip), P.K, false);
   hipStream_t st = (hipStream_t)stream;
   char* ws = (char*)workspace;
@@ -362,7 +393,7 @@ MOE_API int kd_forward(const kd_plan_t* plan, const void* X, const void* W, cons
     KD_CHECK(gemm_kd_logits(false, X, (const bf16_t*)W + v0 * P.H, P.N, P.H, w, 1.f / P.temperature,
                             pmax, psum, nullptr, nullptr, nullptr, 0, st));
     const int nsl = (int)ceil_div(w, 256) * (256 / kCceSlice);
-    kd_fold_kernel<<<(unsigned)ceil_div(P.N, kFoldThreads), kFoldThreads, 0, st>>>(
+    kd_fold_kernel<<<(unsigned)ceil_div(P.N, kFoldTokens), kThreads, 0, st>>>(
         pmax, psum, nsl, P.N, (float*)(ws + L.m), (float*)(ws + L.z), v0 == 0, v0 + w == P.V, lse);
     KD_CHECK(hipGetLastError());
   }
@@ -420,7 +451,10 @@ MOE_API int kd_backward(const kd_plan_t* plan, const void* X, const void* W, con
       KD_CHECK(gemm_cce_dw(G, cols, X, P.N, P.H, w, (float*)dW + v0 * P.H, st));
   }
   const int64_t n4 = P.N * P.H / 4;
-  kd_fold_dx_kernel<<<(unsigned)ceil_div(n4, kThreads), kThreads, 0, st>>>(dx, R.slots, n4, (bf16_t*)dX);
+  if (R.slots > 1)
+    kd_fold_dx_kernel<<<(unsigned)ceil_div(n4, 64), kThreads, 0, st>>>(dx, R.slots, n4, (bf16_t*)dX);
+  else
+    kd_round_dx_kernel<<<(unsigned)ceil_div(n4, kThreads), kThreads, 0, st>>>(dx, n4, (bf16_t*)dX);
   KD_CHECK(hipGetLastError());
   return MOE_OK;
 }

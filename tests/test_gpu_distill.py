@@ -3,7 +3,7 @@
 Tolerances, u = 2^-24 and e = 2^-8 (half a step of bf16), elementwise:
   a logit: H products summed in fp32, at most (H + 2) u sum |x w| off, dy.
   lse: dy / T, and relative to its sum: 50 u an exponential, 12 u in a slice,
-    4 u for each of the V / 128 steps of the fold; 4 u of its own size.
+    4 u for each of at most V / 128 steps of the fold; 4 u of its own size.
   p: (80 + 4 R) u relative, R the range of the list's logits over T.
   loss: T^2 times the sum over the list of p's error times |log p - log q|,
     and p times log p's, y's and lse's errors.
