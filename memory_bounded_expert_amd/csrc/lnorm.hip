@@ -2,7 +2,7 @@
 //
 // Both passes move a few bytes per operation and are bound by HBM, so a row is
 // read once and held in registers: W waves per row, C vectors of 16 bytes per
-// lane (single elements where rows do not start on 16-byte steps).  A
+// lane.  A
 // work-group walks over rows with gamma, beta (or the shares of dgamma and
 // dbeta) in registers and the next row's loads in flight.  The backward pass
 // writes each work-group's shares of dgamma and dbeta to the workspace, and a
@@ -41,50 +41,68 @@ __device__ __forceinline__ float group_sum(float v, float* red) {
   return s;
 }
 
-// One lane's part of a row: C vectors of EPC elements, vector c at c * 64 W + its
-// place in the row's lanes.
-template <typename T, int EPC, int W, int C>
-struct RowPart {
-  static constexpr int COLS = EPC * C;
-  using Raw = std::conditional_t<EPC == 1, T, u32x4_t>;
-  Raw raw[C];
+// 16 bytes at an address that need not be a multiple of 16 (rows of any width
+// follow each other; the memory pipeline takes any alignment).
+typedef u32x4_t __attribute__((aligned(2))) u32x4_any_t;
+typedef f32x4_t __attribute__((aligned(4))) f32x4_any_t;
 
-  __device__ __forceinline__ void load(const T* row, int place, int vecs) {
+// One lane's part of a row: C vectors of EPC elements, vector c at c * 64 W + its
+// place in the row's lanes.  TAIL: the row's last vector is short, and the lane
+// that holds it moves its elements one by one.
+template <typename T, int W, int C, bool TAIL>
+struct RowPart {
+  static constexpr int EPC = Elem<T>::kPer16B, COLS = EPC * C;
+  u32x4_t raw[C];
+
+  __device__ __forceinline__ void load(const T* row, int place, int H) {
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      raw[c] = c * 64 * W + place < vecs ? reinterpret_cast<const Raw*>(row)[c * 64 * W + place] : Raw{};
+    for (int c = 0; c < C; ++c) {
+      const int at = (c * 64 * W + place) * EPC;
+      raw[c] = u32x4_t{0u, 0u, 0u, 0u};
+      if (at + EPC <= H) raw[c] = *reinterpret_cast<const u32x4_any_t*>(row + at);
+    }
+    if constexpr (TAIL) {
+      const int last = H / EPC;  // the short vector
+      if (last % (64 * W) == place) {
+        float v[EPC];
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) v[e] = last * EPC + e < H ? Elem<T>::to_f(row[last * EPC + e]) : 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (c == last / (64 * W)) raw[c] = pack16(v, T());
+      }
+    }
   }
-  __device__ __forceinline__ void get(int c, float* v) const {
-    if constexpr (EPC == 1)
-      v[0] = Elem<T>::to_f(raw[c]);
-    else
-      unpack16(raw[c], v, T());
-  }
-  __device__ static __forceinline__ void put(T* row, int at, const float* v) {
-    if constexpr (EPC == 1)
-      row[at] = Elem<T>::from_f(v[0]);
-    else
-      reinterpret_cast<u32x4_t*>(row)[at] = pack16(v, T());
+  __device__ __forceinline__ void get(int c, float* v) const { unpack16(raw[c], v, T()); }
+  __device__ static __forceinline__ void put(T* row, int at, int H, const float* v) {
+    if (at + EPC <= H) {
+      *reinterpret_cast<u32x4_any_t*>(row + at) = pack16(v, T());
+    } else if constexpr (TAIL) {
+#pragma unroll
+      for (int e = 0; e < EPC; ++e)
+        if (at + e < H) row[at + e] = Elem<T>::from_f(v[e]);
+    }
   }
 };
 
 // A lane's columns of gamma or beta; 0 past the row's end and without p.
-// Vectors start on 16-byte steps (checked by the host).
-template <int EPC, int W, int C>
-__device__ __forceinline__ void load_cols(const float* p, int place, int vecs, float* out) {
+template <int EPC, int W, int C, bool TAIL>
+__device__ __forceinline__ void load_cols(const float* p, int place, int H, float* out) {
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int at = c * 64 * W + place;
-    if constexpr (EPC == 1) {
-      out[c] = p && at < vecs ? p[at] : 0.f;
-    } else {
+    const int at = (c * 64 * W + place) * EPC;
 #pragma unroll
-      for (int e = 0; e < EPC; e += 4) {
-        f32x4_t v{0.f, 0.f, 0.f, 0.f};
-        if (p && at < vecs) v = *reinterpret_cast<const f32x4_t*>(p + at * EPC + e);
+    for (int e = 0; e < EPC; e += 4) {
+      f32x4_t v{0.f, 0.f, 0.f, 0.f};
+      if (p && at + e + 4 <= H) {
+        v = *reinterpret_cast<const f32x4_any_t*>(p + at + e);
+      } else if (TAIL && p) {
 #pragma unroll
-        for (int f = 0; f < 4; ++f) out[c * EPC + e + f] = v[f];
+        for (int f = 0; f < 4; ++f)
+          if (at + e + f < H) v[f] = p[at + e + f];
       }
+#pragma unroll
+      for (int f = 0; f < 4; ++f) out[c * EPC + e + f] = v[f];
     }
   }
 }
@@ -117,30 +135,30 @@ constexpr bool kAhead = W < 16;
 template <int W>
 constexpr int kGroup = W == 1 ? kThreads : 64 * W;  // threads of a work-group
 
-template <typename T, int EPC, int W, int C>
+template <typename T, int W, int C, bool TAIL>
 __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_forward_kernel(
     const T* X, const float* __restrict__ gamma, const float* __restrict__ beta, T* Y,
     float* __restrict__ mean, float* __restrict__ rstd, int64_t N, int H, float eps) {
-  using Part = RowPart<T, EPC, W, C>;
+  using Part = RowPart<T, W, C, TAIL>;
+  constexpr int EPC = Part::EPC;
   __shared__ float red[2][1][16];
   constexpr int RPG = kGroup<W> / (64 * W);  // rows of a work-group at a time
   const int place = threadIdx.x % (64 * W);
-  const int vecs = H / EPC;
   const float inv = 1.f / H;
   float ga[Part::COLS], be[Part::COLS];
-  load_cols<EPC, W, C>(gamma, place, vecs, ga);
-  load_cols<EPC, W, C>(beta, place, vecs, be);
+  load_cols<EPC, W, C, TAIL>(gamma, place, H, ga);
+  load_cols<EPC, W, C, TAIL>(beta, place, H, be);
   int half = 0;
   int64_t t = (int64_t)blockIdx.x * RPG + threadIdx.x / (64 * W);
   const int64_t step = (int64_t)gridDim.x * RPG;
   Part cur;
-  if (kAhead<W> && t < N) cur.load(X + t * H, place, vecs);
+  if (kAhead<W> && t < N) cur.load(X + t * H, place, H);
   for (; t < N; t += step) {
     Part next;
     if constexpr (kAhead<W>) {
-      if (t + step < N) next.load(X + (t + step) * H, place, vecs);
+      if (t + step < N) next.load(X + (t + step) * H, place, H);
     } else {
-      cur.load(X + t * H, place, vecs);
+      cur.load(X + t * H, place, H);
     }
     float s[1] = {0.f};
 #pragma unroll
@@ -155,11 +173,13 @@ __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_forward_kernel(
     s[0] = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (c * 64 * W + place < vecs) {
+      const int at = (c * 64 * W + place) * EPC;
+      if (at < H) {
         float v[EPC];
         cur.get(c, v);
 #pragma unroll
-        for (int e = 0; e < EPC; ++e) s[0] = fmaf(v[e] - m, v[e] - m, s[0]);
+        for (int e = 0; e < EPC; ++e)
+          if (!TAIL || at + e < H) s[0] = fmaf(v[e] - m, v[e] - m, s[0]);
       }
     }
     row_sums<W>(s, red, half);
@@ -170,12 +190,13 @@ __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_forward_kernel(
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (c * 64 * W + place < vecs) {
+      const int at = (c * 64 * W + place) * EPC;
+      if (at < H) {
         float v[EPC];
         cur.get(c, v);
 #pragma unroll
         for (int e = 0; e < EPC; ++e) v[e] = fmaf((v[e] - m) * r, ga[c * EPC + e], be[c * EPC + e]);
-        Part::put(Y + t * H, c * 64 * W + place, v);
+        Part::put(Y + t * H, at, H, v);
       }
     }
     if constexpr (kAhead<W>) cur = next;
@@ -183,19 +204,19 @@ __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_forward_kernel(
 }
 
 // part: [work-group][2][H], its rows' shares of dgamma and dbeta.
-template <typename T, int EPC, int W, int C>
+template <typename T, int W, int C, bool TAIL>
 __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_backward_kernel(
     const T* __restrict__ X, const float* __restrict__ gamma, const T* dY,
     const float* __restrict__ mean, const float* __restrict__ rstd, T* dX,
     float* __restrict__ part, int64_t N, int H) {
-  using Part = RowPart<T, EPC, W, C>;
+  using Part = RowPart<T, W, C, TAIL>;
+  constexpr int EPC = Part::EPC;
   constexpr int RPG = kGroup<W> / (64 * W);
   __shared__ float red[2][2][16];
   const int place = threadIdx.x % (64 * W);
-  const int vecs = H / EPC;
   const float inv = 1.f / H;
   float ga[Part::COLS], dg[Part::COLS], db[Part::COLS];
-  load_cols<EPC, W, C>(gamma, place, vecs, ga);
+  load_cols<EPC, W, C, TAIL>(gamma, place, H, ga);
 #pragma unroll
   for (int i = 0; i < Part::COLS; ++i) dg[i] = db[i] = 0.f;
   int half = 0;
@@ -204,8 +225,8 @@ __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_backward_kernel(
   Part x, dy;
   float m = 0.f, r = 0.f;
   auto load = [&](int64_t u, Part& px, Part& pd, float& pm, float& pr) {
-    px.load(X + u * H, place, vecs);
-    pd.load(dY + u * H, place, vecs);
+    px.load(X + u * H, place, H);
+    pd.load(dY + u * H, place, H);
     pm = mean[u];
     pr = rstd[u];
   };
@@ -239,14 +260,15 @@ __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_backward_kernel(
     const float a = s[0] * inv, b = s[1] * inv;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      if (c * 64 * W + place < vecs) {
+      const int at = (c * 64 * W + place) * EPC;
+      if (at < H) {
         float v[EPC], d[EPC];
         x.get(c, v);
         dy.get(c, d);
 #pragma unroll
         for (int e = 0; e < EPC; ++e)
           d[e] = r * (fmaf(d[e], ga[c * EPC + e], -a) - (v[e] - m) * r * b);
-        Part::put(dX + t * H, c * 64 * W + place, d);
+        Part::put(dX + t * H, at, H, d);
       }
     }
     if constexpr (kAhead<W>) {
@@ -260,12 +282,12 @@ __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_backward_kernel(
   if constexpr (RPG == 1) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int at = c * 64 * W + place;
-      if (at < vecs)
+      const int at = (c * 64 * W + place) * EPC;
 #pragma unroll
-        for (int e = 0; e < EPC; ++e) {
-          pg[at * EPC + e] = dg[c * EPC + e];
-          pg[H + at * EPC + e] = db[c * EPC + e];
+      for (int e = 0; e < EPC; ++e)
+        if (at + e < H) {
+          pg[at + e] = dg[c * EPC + e];
+          pg[H + at + e] = db[c * EPC + e];
         }
     }
   } else {
@@ -375,25 +397,19 @@ __global__ __launch_bounds__(64 * kFoldWaves) void lnorm_fold_kernel(const float
     dbeta[c - H] = s;
 }
 
-// How a row is held: EPC elements per vector, W waves, C vectors per lane.  The
-// smallest W, then the smallest C, that hold it; at most four vectors per lane
-// (16 single elements), which with gamma and two sums fills the registers of
-// two waves per SIMD.  W = 0: too wide.
+// How a row is held: W waves, C vectors per lane.  The smallest W, then the
+// smallest C, that hold it; at most four vectors per lane, which with gamma and
+// two sums fills the registers of two waves per SIMD.  W = 0: too wide.
 struct Holding {
-  int epc, W, C;
+  int W, C;
 };
-Holding holding(const lnorm_plan_t& P, bool aligned) {
+Holding holding(const lnorm_plan_t& P) {
   const int epc = 16 / elem_bytes(P.dtype);
-  if (!aligned || P.H % epc) {
-    for (int W : {1, 4, 16})
-      for (int C : {4, 16})
-        if ((W == 1 || C == 16) && P.H <= 64 * W * C) return {1, W, C};
-    return {1, 0, 0};
-  }
+  const int64_t vecs = ceil_div(P.H, epc);
   for (int W : {1, 2, 4, 8, 16})
     for (int C : {1, 2, 4})
-      if ((W == 1 || C == 4) && (W < 16 || epc == 4) && P.H / epc <= 64 * W * C) return {epc, W, C};
-  return {1, 0, 0};
+      if ((W == 1 || C == 4) && (W < 16 || epc == 4) && vecs <= 64 * W * C) return {W, C};
+  return {0, 0};
 }
 int rows_per_group(int W) { return W == 1 ? kThreads / 64 : 1; }
 int waves_per_group(int W) { return W == 1 ? kThreads / 64 : W; }
@@ -404,42 +420,42 @@ int row_groups(int64_t N, int W) {
   return (int)std::min<int64_t>(ceil_div(N, rows_per_group(W)), std::max(256, kRowWaves / waves_per_group(W)));
 }
 
-// Calls f with the holding as template arguments.
+// Calls f with the holding, and whether a row's last vector is short, as
+// template arguments.
 template <typename T, typename F>
-void with_holding(const Holding& h, F f) {
+void with_holding(const Holding& h, int H, F f) {
   constexpr int EPC = Elem<T>::kPer16B;
-  auto is = [&](int epc, int W, int C) { return h.epc == epc && h.W == W && h.C == C; };
+  using std::bool_constant;
   using std::integral_constant;
-#define LNORM_CASE(e, w, c) \
-  if (is(e, w, c)) return f(integral_constant<int, e>(), integral_constant<int, w>(), integral_constant<int, c>());
-  LNORM_CASE(EPC, 1, 1)
-  LNORM_CASE(EPC, 1, 2)
-  LNORM_CASE(EPC, 1, 4)
-  LNORM_CASE(EPC, 2, 4)
-  LNORM_CASE(EPC, 4, 4)
-  LNORM_CASE(EPC, 8, 4)
-  if constexpr (EPC == 4) {
-    LNORM_CASE(EPC, 16, 4)
+#define LNORM_CASE(w, c)                                                                            \
+  if (h.W == w && h.C == c) {                                                                      \
+    if (H % EPC) return f(integral_constant<int, w>(), integral_constant<int, c>(), bool_constant<true>()); \
+    return f(integral_constant<int, w>(), integral_constant<int, c>(), bool_constant<false>());     \
   }
-  LNORM_CASE(1, 1, 4)
-  LNORM_CASE(1, 1, 16)
-  LNORM_CASE(1, 4, 16)
-  LNORM_CASE(1, 16, 16)
+  LNORM_CASE(1, 1)
+  LNORM_CASE(1, 2)
+  LNORM_CASE(1, 4)
+  LNORM_CASE(2, 4)
+  LNORM_CASE(4, 4)
+  LNORM_CASE(8, 4)
+  if constexpr (EPC == 4) {
+    LNORM_CASE(16, 4)
+  }
 #undef LNORM_CASE
 }
 
 template <typename T>
 hipError_t run_forward(const lnorm_plan_t& P, const void* X, const float* gamma, const float* beta,
                        void* Y, float* mean, float* rstd, hipStream_t st) {
-  const Holding h = holding(P, ((uintptr_t)X | (uintptr_t)Y | (uintptr_t)gamma | (uintptr_t)beta) % 16 == 0);
+  const Holding h = holding(P);
   if (h.W == 0) {
     const unsigned grid = (unsigned)std::min<int64_t>(P.N, kMaxRowGrid);
     lnorm_forward_kernel<T><<<grid, kThreads, 0, st>>>((const T*)X, gamma, beta, (T*)Y, mean, rstd,
                                                        P.N, P.H, P.eps);
   } else {
     const int grid = row_groups(P.N, h.W);
-    with_holding<T>(h, [&](auto e, auto w, auto c) {
-      lnorm_rows_forward_kernel<T, e.value, w.value, c.value><<<grid, kGroup<w.value>, 0, st>>>(
+    with_holding<T>(h, P.H, [&](auto w, auto c, auto tail) {
+      lnorm_rows_forward_kernel<T, w.value, c.value, tail.value><<<grid, kGroup<w.value>, 0, st>>>(
           (const T*)X, gamma, beta, (T*)Y, mean, rstd, P.N, P.H, P.eps);
     });
   }
@@ -450,14 +466,14 @@ template <typename T>
 hipError_t run_backward(const lnorm_plan_t& P, const void* X, const float* gamma, const void* dY,
                         const float* mean, const float* rstd, void* dX, float* part, int* slabs,
                         hipStream_t st) {
-  const Holding h = holding(P, ((uintptr_t)X | (uintptr_t)dY | (uintptr_t)dX | (uintptr_t)gamma) % 16 == 0);
+  const Holding h = holding(P);
   const int grid = *slabs = row_groups(P.N, h.W);
   if (h.W == 0) {
     lnorm_backward_kernel<T><<<grid, kThreads, 0, st>>>((const T*)X, gamma, (const T*)dY, mean, rstd,
                                                         (T*)dX, part, P.N, P.H);
   } else {
-    with_holding<T>(h, [&](auto e, auto w, auto c) {
-      lnorm_rows_backward_kernel<T, e.value, w.value, c.value><<<grid, kGroup<w.value>, 0, st>>>(
+    with_holding<T>(h, P.H, [&](auto w, auto c, auto tail) {
+      lnorm_rows_backward_kernel<T, w.value, c.value, tail.value><<<grid, kGroup<w.value>, 0, st>>>(
           (const T*)X, gamma, (const T*)dY, mean, rstd, (T*)dX, part, P.N, P.H);
     });
   }
