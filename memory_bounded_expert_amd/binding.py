@@ -283,6 +283,14 @@ def _on(device, stream):
     return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
+def _out(t, name, shape, dtype, device):
+    """The output tensor given, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _expect(t, name, shape, dtype, device)
+    return t
+
+
 def moe_plan_chunks(N: int, H: int, F: int, E: int, k: int, c: int, K_max: int,
                     dtype: int) -> MoePlan:
     plan = MoePlan()
@@ -551,10 +559,8 @@ def route_forward(plan: RoutePlan, logits, bias=None, topk_idx=None, gates=None,
     if bias is not None:
         _expect(bias, "bias", (E,), torch.float32, dev)
     with _on(dev, stream):
-        topk_idx = torch.empty((N, k), dtype=torch.int32, device=dev) if topk_idx is None else topk_idx
-        gates = torch.empty((N, k), dtype=torch.float32, device=dev) if gates is None else gates
-        _expect(topk_idx, "topk_idx", (N, k), torch.int32, dev)
-        _expect(gates, "gates", (N, k), torch.float32, dev)
+        topk_idx = _out(topk_idx, "topk_idx", (N, k), torch.int32, dev)
+        gates = _out(gates, "gates", (N, k), torch.float32, dev)
         _check(lib().route_forward(ctypes.byref(plan), _ptr(logits), _ptr(bias), _ptr(topk_idx),
                                    _ptr(gates), _stream(dev, None)), "route_forward")
     return topk_idx, gates
@@ -568,8 +574,7 @@ def route_backward(plan: RoutePlan, logits, topk_idx, dgates, dlogits=None, stre
     _expect(topk_idx, "topk_idx", (N, k), torch.int32, dev)
     _expect(dgates, "dgates", (N, k), torch.float32, dev)
     with _on(dev, stream):
-        dlogits = torch.empty((N, E), dtype=torch.float32, device=dev) if dlogits is None else dlogits
-        _expect(dlogits, "dlogits", (N, E), torch.float32, dev)
+        dlogits = _out(dlogits, "dlogits", (N, E), torch.float32, dev)
         _check(lib().route_backward(ctypes.byref(plan), _ptr(logits), _ptr(topk_idx), _ptr(dgates),
                                     _ptr(dlogits), _stream(dev, None)), "route_backward")
     return dlogits
@@ -587,8 +592,7 @@ def moe_routed_forward(plan: MoePlan, X, W_gate, W_up, W_down, topk_idx, gates, 
                        (gates, "gates", (N, k), torch.float32)):
         _expect(t, n, s, d, dev)
     with _on(dev, stream):
-        Y = torch.empty((N, H), dtype=dt, device=dev) if Y is None else Y
-        _expect(Y, "Y", (N, H), dt, dev)
+        Y = _out(Y, "Y", (N, H), dt, dev)
         ws = workspace(plan, "fwd", dev) if ws is None else ws
         st = MoeStats()
         _check(lib().moe_routed_forward(
@@ -611,16 +615,11 @@ def moe_routed_backward(plan: MoePlan, X, W_gate, W_up, W_down, dY, topk_idx, ga
                        (gates, "gates", (N, k), f32)):
         _expect(t, n, s, d, dev)
     with _on(dev, stream):
-        new = lambda shape, d=f32: torch.empty(shape, dtype=d, device=dev)
-        dX = new((N, H), dt) if dX is None else dX
-        dW_gate = new((E, H, F)) if dW_gate is None else dW_gate
-        dW_up = new((E, H, F)) if dW_up is None else dW_up
-        dW_down = new((E, F, H)) if dW_down is None else dW_down
-        dgates = new((N, k)) if dgates is None else dgates
-        for t, n, s, d in ((dX, "dX", (N, H), dt), (dW_gate, "dW_gate", (E, H, F), f32),
-                           (dW_up, "dW_up", (E, H, F), f32), (dW_down, "dW_down", (E, F, H), f32),
-                           (dgates, "dgates", (N, k), f32)):
-            _expect(t, n, s, d, dev)
+        dX = _out(dX, "dX", (N, H), dt, dev)
+        dW_gate = _out(dW_gate, "dW_gate", (E, H, F), f32, dev)
+        dW_up = _out(dW_up, "dW_up", (E, H, F), f32, dev)
+        dW_down = _out(dW_down, "dW_down", (E, F, H), f32, dev)
+        dgates = _out(dgates, "dgates", (N, k), f32, dev)
         ws = workspace(plan, "bwd", dev) if ws is None else ws
         st = MoeStats()
         _check(lib().moe_routed_backward(
@@ -651,12 +650,9 @@ def lnorm_forward(plan: LnormPlan, X, gamma, beta=None, Y=None, mean=None, rstd=
     if beta is not None:
         _expect(beta, "beta", (H,), f32, dev)
     with _on(dev, stream):
-        Y = torch.empty((N, H), dtype=dt, device=dev) if Y is None else Y
-        mean = torch.empty(N, dtype=f32, device=dev) if mean is None else mean
-        rstd = torch.empty(N, dtype=f32, device=dev) if rstd is None else rstd
-        _expect(Y, "Y", (N, H), dt, dev)
-        _expect(mean, "mean", (N,), f32, dev)
-        _expect(rstd, "rstd", (N,), f32, dev)
+        Y = _out(Y, "Y", (N, H), dt, dev)
+        mean = _out(mean, "mean", (N,), f32, dev)
+        rstd = _out(rstd, "rstd", (N,), f32, dev)
         _check(lib().lnorm_forward(ctypes.byref(plan), _ptr(X), _ptr(gamma), _ptr(beta), _ptr(Y),
                                    _ptr(mean), _ptr(rstd), _stream(dev, None)), "lnorm_forward")
     return Y, mean, rstd
@@ -672,14 +668,10 @@ def lnorm_backward(plan: LnormPlan, X, gamma, dY, mean, rstd, dX=None, dgamma=No
                        (mean, "mean", (N,), f32), (rstd, "rstd", (N,), f32)):
         _expect(t, n, s, d, dev)
     with _on(dev, stream):
-        dX = torch.empty((N, H), dtype=dt, device=dev) if dX is None else dX
-        dgamma = torch.empty(H, dtype=f32, device=dev) if dgamma is None else dgamma
-        if dbeta is None and want_dbeta:
-            dbeta = torch.empty(H, dtype=f32, device=dev)
-        _expect(dX, "dX", (N, H), dt, dev)
-        _expect(dgamma, "dgamma", (H,), f32, dev)
-        if dbeta is not None:
-            _expect(dbeta, "dbeta", (H,), f32, dev)
+        dX = _out(dX, "dX", (N, H), dt, dev)
+        dgamma = _out(dgamma, "dgamma", (H,), f32, dev)
+        if dbeta is not None or want_dbeta:
+            dbeta = _out(dbeta, "dbeta", (H,), f32, dev)
         ws = workspace(plan, "bwd", dev) if ws is None else ws
         _check(lib().lnorm_backward(ctypes.byref(plan), _ptr(X), _ptr(gamma), _ptr(dY), _ptr(mean),
                                     _ptr(rstd), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws),
@@ -704,8 +696,7 @@ def embed_forward(plan: EmbedPlan, W, ids, Y=None, stream=None):
     _expect(W, "W", (V, H), dt, dev)
     _expect(ids, "ids", (N,), torch.int32, dev)
     with _on(dev, stream):
-        Y = torch.empty((N, H), dtype=dt, device=dev) if Y is None else Y
-        _expect(Y, "Y", (N, H), dt, dev)
+        Y = _out(Y, "Y", (N, H), dt, dev)
         _check(lib().embed_forward(ctypes.byref(plan), _ptr(W), _ptr(ids), _ptr(Y),
                                    _stream(dev, None)), "embed_forward")
     return Y
@@ -720,8 +711,7 @@ def embed_backward(plan: EmbedPlan, ids, dY, dW=None, accumulate=False, ws=None,
     if accumulate and dW is None:
         raise ValueError("accumulate needs the dW to add to")
     with _on(dev, stream):
-        dW = torch.empty((V, H), dtype=torch.float32, device=dev) if dW is None else dW
-        _expect(dW, "dW", (V, H), torch.float32, dev)
+        dW = _out(dW, "dW", (V, H), torch.float32, dev)
         ws = workspace(plan, "bwd", dev) if ws is None else ws
         _check(lib().embed_backward(ctypes.byref(plan), _ptr(ids), _ptr(dY), _ptr(dW),
                                     int(bool(accumulate)), _ptr(ws), ws.numel(),
@@ -750,12 +740,9 @@ def kd_forward(plan: KdPlan, X, W, t_idx, t_logit, loss=None, lse=None, y_top=No
                        (t_idx, "t_idx", (N, K), torch.int32), (t_logit, "t_logit", (N, K), f32)):
         _expect(t, n, s, d, dev)
     with _on(dev, stream):
-        loss = torch.empty(N, dtype=f32, device=dev) if loss is None else loss
-        lse = torch.empty(N, dtype=f32, device=dev) if lse is None else lse
-        y_top = torch.empty((N, K), dtype=f32, device=dev) if y_top is None else y_top
-        _expect(loss, "loss", (N,), f32, dev)
-        _expect(lse, "lse", (N,), f32, dev)
-        _expect(y_top, "y_top", (N, K), f32, dev)
+        loss = _out(loss, "loss", (N,), f32, dev)
+        lse = _out(lse, "lse", (N,), f32, dev)
+        y_top = _out(y_top, "y_top", (N, K), f32, dev)
         ws = workspace(plan, "fwd", dev) if ws is None else ws
         _check(lib().kd_forward(ctypes.byref(plan), _ptr(X), _ptr(W), _ptr(t_idx), _ptr(t_logit),
                                 _ptr(loss), _ptr(lse), _ptr(y_top), _ptr(ws), ws.numel(),
@@ -775,10 +762,8 @@ def kd_backward(plan: KdPlan, X, W, t_idx, t_logit, lse, y_top, dloss, dX=None, 
                        (dloss, "dloss", (N,), f32)):
         _expect(t, n, s, d, dev)
     with _on(dev, stream):
-        dX = torch.empty((N, H), dtype=bf16, device=dev) if dX is None else dX
-        dW = torch.empty((V, H), dtype=wt, device=dev) if dW is None else dW
-        _expect(dX, "dX", (N, H), bf16, dev)
-        _expect(dW, "dW", (V, H), wt, dev)
+        dX = _out(dX, "dX", (N, H), bf16, dev)
+        dW = _out(dW, "dW", (V, H), wt, dev)
         ws = workspace(plan, "bwd", dev) if ws is None else ws
         _check(lib().kd_backward(ctypes.byref(plan), _ptr(X), _ptr(W), _ptr(t_idx), _ptr(t_logit),
                                  _ptr(lse), _ptr(y_top), _ptr(dloss), _ptr(dX), _ptr(dW), _ptr(ws),
