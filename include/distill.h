@@ -89,7 +89,8 @@ int kd_plan(int64_t N, int32_t H, int64_t V, int32_t v_chunk, int32_t K, float t
  * workspace: at least plan->fwd_workspace_bytes bytes, 256-byte aligned;
  *   contents on entry do not matter.
  * Errors: MOE_EINVAL (plan not from kd_plan, a required pointer NULL with
- *   N > 0, workspace not 256-byte aligned), MOE_EWORKSPACE (too small),
+ *   N > 0, workspace not 256-byte aligned, X or W (kd_backward: dX or dW) not
+ *   16-byte aligned), MOE_EWORKSPACE (too small),
  *   MOE_EHIP (enqueue failed).  Nothing is enqueued on the first two.
  */
 int kd_forward(const kd_plan_t* plan, const void* X, const void* W, const int32_t* t_idx,

@@ -283,6 +283,15 @@ def _on(device, stream):
     return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
+def _workspace(ws, plan, kind, device):
+    """(workspace, its bytes): the one given, on the device and in one piece, or a new one."""
+    if ws is None:
+        ws = workspace(plan, kind, device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    return ws, ws.numel() * ws.element_size()
+
+
 def _out(t, name, shape, dtype, device):
     """The output tensor given, checked, or a new one."""
     if t is None:
@@ -593,11 +602,11 @@ def moe_routed_forward(plan: MoePlan, X, W_gate, W_up, W_down, topk_idx, gates, 
         _expect(t, n, s, d, dev)
     with _on(dev, stream):
         Y = _out(Y, "Y", (N, H), dt, dev)
-        ws = workspace(plan, "fwd", dev) if ws is None else ws
+        ws, ws_bytes = _workspace(ws, plan, "fwd", dev)
         st = MoeStats()
         _check(lib().moe_routed_forward(
             ctypes.byref(plan), _ptr(X), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(topk_idx),
-            _ptr(gates), _ptr(Y), _ptr(ws), ws.numel(), _stream(dev, None), ctypes.byref(st)),
+            _ptr(gates), _ptr(Y), _ptr(ws), ws_bytes, _stream(dev, None), ctypes.byref(st)),
             "moe_routed_forward")
     return Y, st.as_dict()
 
@@ -620,12 +629,12 @@ def moe_routed_backward(plan: MoePlan, X, W_gate, W_up, W_down, dY, topk_idx, ga
         dW_up = _out(dW_up, "dW_up", (E, H, F), f32, dev)
         dW_down = _out(dW_down, "dW_down", (E, F, H), f32, dev)
         dgates = _out(dgates, "dgates", (N, k), f32, dev)
-        ws = workspace(plan, "bwd", dev) if ws is None else ws
+        ws, ws_bytes = _workspace(ws, plan, "bwd", dev)
         st = MoeStats()
         _check(lib().moe_routed_backward(
             ctypes.byref(plan), _ptr(X), _ptr(W_gate), _ptr(W_up), _ptr(W_down), _ptr(dY),
             _ptr(topk_idx), _ptr(gates), _ptr(dX), _ptr(dW_gate), _ptr(dW_up), _ptr(dW_down),
-            _ptr(dgates), _ptr(ws), ws.numel(), _stream(dev, None), ctypes.byref(st)),
+            _ptr(dgates), _ptr(ws), ws_bytes, _stream(dev, None), ctypes.byref(st)),
             "moe_routed_backward")
     return dict(dX=dX, dW_gate=dW_gate, dW_up=dW_up, dW_down=dW_down, dgates=dgates,
                 stats=st.as_dict())
@@ -672,10 +681,10 @@ def lnorm_backward(plan: LnormPlan, X, gamma, dY, mean, rstd, dX=None, dgamma=No
         dgamma = _out(dgamma, "dgamma", (H,), f32, dev)
         if dbeta is not None or want_dbeta:
             dbeta = _out(dbeta, "dbeta", (H,), f32, dev)
-        ws = workspace(plan, "bwd", dev) if ws is None else ws
+        ws, ws_bytes = _workspace(ws, plan, "bwd", dev)
         _check(lib().lnorm_backward(ctypes.byref(plan), _ptr(X), _ptr(gamma), _ptr(dY), _ptr(mean),
                                     _ptr(rstd), _ptr(dX), _ptr(dgamma), _ptr(dbeta), _ptr(ws),
-                                    ws.numel(), _stream(dev, None)), "lnorm_backward")
+                                    ws_bytes, _stream(dev, None)), "lnorm_backward")
     return dX, dgamma, dbeta
 
 
@@ -712,9 +721,9 @@ def embed_backward(plan: EmbedPlan, ids, dY, dW=None, accumulate=False, ws=None,
         raise ValueError("accumulate needs the dW to add to")
     with _on(dev, stream):
         dW = _out(dW, "dW", (V, H), torch.float32, dev)
-        ws = workspace(plan, "bwd", dev) if ws is None else ws
+        ws, ws_bytes = _workspace(ws, plan, "bwd", dev)
         _check(lib().embed_backward(ctypes.byref(plan), _ptr(ids), _ptr(dY), _ptr(dW),
-                                    int(bool(accumulate)), _ptr(ws), ws.numel(),
+                                    int(bool(accumulate)), _ptr(ws), ws_bytes,
                                     _stream(dev, None)), "embed_backward")
     return dW
 
@@ -743,9 +752,9 @@ def kd_forward(plan: KdPlan, X, W, t_idx, t_logit, loss=None, lse=None, y_top=No
         loss = _out(loss, "loss", (N,), f32, dev)
         lse = _out(lse, "lse", (N,), f32, dev)
         y_top = _out(y_top, "y_top", (N, K), f32, dev)
-        ws = workspace(plan, "fwd", dev) if ws is None else ws
+        ws, ws_bytes = _workspace(ws, plan, "fwd", dev)
         _check(lib().kd_forward(ctypes.byref(plan), _ptr(X), _ptr(W), _ptr(t_idx), _ptr(t_logit),
-                                _ptr(loss), _ptr(lse), _ptr(y_top), _ptr(ws), ws.numel(),
+                                _ptr(loss), _ptr(lse), _ptr(y_top), _ptr(ws), ws_bytes,
                                 _stream(dev, None)), "kd_forward")
     return loss, lse, y_top
 
@@ -764,8 +773,8 @@ def kd_backward(plan: KdPlan, X, W, t_idx, t_logit, lse, y_top, dloss, dX=None, 
     with _on(dev, stream):
         dX = _out(dX, "dX", (N, H), bf16, dev)
         dW = _out(dW, "dW", (V, H), wt, dev)
-        ws = workspace(plan, "bwd", dev) if ws is None else ws
+        ws, ws_bytes = _workspace(ws, plan, "bwd", dev)
         _check(lib().kd_backward(ctypes.byref(plan), _ptr(X), _ptr(W), _ptr(t_idx), _ptr(t_logit),
                                  _ptr(lse), _ptr(y_top), _ptr(dloss), _ptr(dX), _ptr(dW), _ptr(ws),
-                                 ws.numel(), _stream(dev, None)), "kd_backward")
+                                 ws_bytes, _stream(dev, None)), "kd_backward")
     return dX, dW

@@ -13,6 +13,11 @@ typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 // stay in registers (HIP's uint4 is a struct and copies of it go through memory).
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
 
+// The same at an address that need not be a multiple of 16 (rows of any width
+// that follow each other; the memory pipeline takes any alignment).
+typedef u32x4_t __attribute__((aligned(2))) u32x4_any_t;
+typedef f32x4_t __attribute__((aligned(4))) f32x4_any_t;
+
 constexpr int kThreads = 256;  // work-group size of every kernel but the planner's
 
 __device__ __forceinline__ float bf2f(bf16_t v) { return __uint_as_float(((uint32_t)v) << 16); }

@@ -325,6 +325,9 @@ KdLayout kd_layout(int64_t N, int64_t V, int H, int cols, int K, bool backward) 
 
 bool plan_ok(const kd_plan_t* p) { return p != nullptr && p->magic == kKdMagic; }
 
+// The matrices move in vectors of 16 bytes.
+bool off16(const void* a, const void* b) { return ((uintptr_t)a | (uintptr_t)b) % 16 != 0; }
+
 KdArgs kd_args(const kd_plan_t& P, const void* X, const void* W, const int32_t* t_idx,
                const float* t_logit, const float* lse) {
   return KdArgs{(const bf16_t*)X, (const bf16_t*)W, t_idx, t_logit, lse, P.N, P.V, P.H, P.K,
@@ -379,7 +382,7 @@ MOE_API int kd_forward(const kd_plan_t* plan, const void* X, const void* W, cons
   const kd_plan_t& P = *plan;
   if (P.N == 0) return MOE_OK;
   if (!X || !W || !t_idx || !t_logit || !loss || !lse || !y_top || !workspace) return MOE_EINVAL;
-  if ((uintptr_t)workspace % 256) return MOE_EINVAL;
+  if ((uintptr_t)workspace % 256 || off16(X, W)) return MOE_EINVAL;
   if (workspace_bytes < (size_t)P.fwd_workspace_bytes) return MOE_EWORKSPACE;
   const int strip = forward_strip(P.N, P.V, P.H);
   const KdLayout L = kd_layout(P.N, P.V, P.H, strip_cols(P.V, strip), P.K, false);
@@ -412,7 +415,7 @@ MOE_API int kd_backward(const kd_plan_t* plan, const void* X, const void* W, con
   if (!dW) return MOE_EINVAL;
   if (P.N > 0 && (!X || !W || !t_idx || !t_logit || !lse || !y_top || !dloss || !dX || !workspace))
     return MOE_EINVAL;
-  if (P.N > 0 && (uintptr_t)workspace % 256) return MOE_EINVAL;
+  if (P.N > 0 && ((uintptr_t)workspace % 256 || off16(X, W) || off16(dX, dW))) return MOE_EINVAL;
   if (workspace_bytes < (size_t)P.bwd_workspace_bytes) return MOE_EWORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   const size_t dwb = P.dw_dtype == MOE_BF16 ? 2 : 4;

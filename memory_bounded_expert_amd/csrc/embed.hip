@@ -12,7 +12,6 @@
 // the summing launch, which knows the ids and skips the rows it writes itself.
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "device_common.hpp"
 #include "embed.h"
@@ -40,36 +39,90 @@ constexpr int kScanThreads = 1024;
 constexpr int64_t kSliceBytes = 32 << 20;
 constexpr int64_t kZeroBytes = 1 << 18;        // bytes zeroed by a work-group
 
+// ---- one lane's vector of a row: elements col .. col + EPC - 1, the row's last
+// one short where TAIL (its elements then move one by one)
+
+template <typename T, bool TAIL>
+__device__ __forceinline__ u32x4_t load_vec(const T* row, int col, int H) {
+  constexpr int EPC = Elem<T>::kPer16B;
+  if (!TAIL || col + EPC <= H) return *reinterpret_cast<const u32x4_any_t*>(row + col);
+  float v[EPC];
+#pragma unroll
+  for (int e = 0; e < EPC; ++e) v[e] = col + e < H ? Elem<T>::to_f(row[col + e]) : 0.f;
+  return pack16(v, T());
+}
+template <typename T, bool TAIL>
+__device__ __forceinline__ void store_vec(T* row, int col, int H, const float* v) {
+  constexpr int EPC = Elem<T>::kPer16B;
+  if (!TAIL || col + EPC <= H) {
+    *reinterpret_cast<u32x4_any_t*>(row + col) = pack16(v, T());
+  } else {
+#pragma unroll
+    for (int e = 0; e < EPC; ++e)
+      if (col + e < H) row[col + e] = Elem<T>::from_f(v[e]);
+  }
+}
+// The same of fp32 rows, EPC elements (4 or 8).
+template <int EPC, bool TAIL>
+__device__ __forceinline__ void load_sum(const float* row, int col, int H, float* v) {
+#pragma unroll
+  for (int e = 0; e < EPC; e += 4) {
+    f32x4_t q{0.f, 0.f, 0.f, 0.f};
+    if (!TAIL || col + e + 4 <= H) {
+      q = *reinterpret_cast<const f32x4_any_t*>(row + col + e);
+    } else {
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        if (col + e + f < H) q[f] = row[col + e + f];
+    }
+#pragma unroll
+    for (int f = 0; f < 4; ++f) v[e + f] = q[f];
+  }
+}
+template <int EPC, bool TAIL>
+__device__ __forceinline__ void store_sum(float* row, int col, int H, const float* v) {
+#pragma unroll
+  for (int e = 0; e < EPC; e += 4) {
+    if (!TAIL || col + e + 4 <= H) {
+      *reinterpret_cast<f32x4_any_t*>(row + col + e) = f32x4_t{v[e], v[e + 1], v[e + 2], v[e + 3]};
+    } else {
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        if (col + e + f < H) row[col + e + f] = v[e + f];
+    }
+  }
+}
+// Zeroes n values from p on by the whole work-group.
+__device__ __forceinline__ void zero_values(float* p, int n) {
+  for (int q = threadIdx.x; q < n / 4; q += blockDim.x)
+    *reinterpret_cast<u32x4_any_t*>(p + 4 * q) = u32x4_t{0u, 0u, 0u, 0u};
+  if ((int)threadIdx.x < n % 4) p[n - 1 - threadIdx.x] = 0.f;
+}
+
 // ---- forward
 
-// VEC: one 16-byte vector per thread, else one element.
-template <typename T, bool VEC>
+template <typename T, bool TAIL>
 __global__ __launch_bounds__(kThreads) void embed_forward_kernel(const T* __restrict__ W,
                                                                  const int32_t* __restrict__ ids,
                                                                  T* __restrict__ Y, int64_t N,
                                                                  int64_t V, int H, float scale) {
-  constexpr int EPC = VEC ? Elem<T>::kPer16B : 1;
-  const int cpr = H / EPC;
+  constexpr int EPC = Elem<T>::kPer16B;
+  const int cpr = (H + EPC - 1) / EPC;
   const int64_t total = N * cpr;
   for (int64_t q = (int64_t)blockIdx.x * kThreads + threadIdx.x; q < total;
        q += (int64_t)gridDim.x * kThreads) {
     const int64_t t = q / cpr;
-    const int c = (int)(q - t * cpr);
+    const int col = (int)(q - t * cpr) * EPC;
     const int64_t id = ids[t];
-    const bool real = id >= 0 && id < V;
-    if constexpr (VEC) {
-      u32x4_t raw{0u, 0u, 0u, 0u};
-      if (real) {
-        float v[EPC];
-        unpack16(reinterpret_cast<const u32x4_t*>(W + id * H)[c], v, T());
+    float v[EPC];
 #pragma unroll
-        for (int e = 0; e < EPC; ++e) v[e] *= scale;
-        raw = pack16(v, T());
-      }
-      reinterpret_cast<u32x4_t*>(Y + t * H)[c] = raw;
-    } else {
-      Y[t * H + c] = real ? Elem<T>::from_f(Elem<T>::to_f(W[id * H + c]) * scale) : Elem<T>::from_f(0.f);
+    for (int e = 0; e < EPC; ++e) v[e] = 0.f;
+    if (id >= 0 && id < V) {
+      unpack16(load_vec<T, TAIL>(W + id * H, col, H), v, T());
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) v[e] *= scale;
     }
+    store_vec<T, TAIL>(Y + t * H, col, H, v);
   }
 }
 
@@ -93,15 +146,7 @@ struct SortPass {
 // Zeroes kZeroBytes of [p, end) from piece i on, by the whole work-group.
 __device__ __forceinline__ void zero_piece(float* p, float* end, int64_t i) {
   p += i * (kZeroBytes / 4);
-  const int64_t n = min((int64_t)(end - p), kZeroBytes / 4);
-  if ((uintptr_t)p % 16 == 0) {
-    const int n4 = (int)(n / 4);
-    for (int q = threadIdx.x; q < n4; q += blockDim.x)
-      reinterpret_cast<u32x4_t*>(p)[q] = u32x4_t{0u, 0u, 0u, 0u};
-    for (int q = n4 * 4 + threadIdx.x; q < n; q += blockDim.x) p[q] = 0.f;
-  } else {
-    for (int q = threadIdx.x; q < n; q += blockDim.x) p[q] = 0.f;
-  }
+  zero_values(p, (int)min((int64_t)(end - p), kZeroBytes / 4));
 }
 __device__ __forceinline__ bool zeroes(const SortPass& a) {
   if ((int)blockIdx.x < a.groups) return false;
@@ -331,23 +376,19 @@ struct SumArgs {
 };
 constexpr int kMaxZeroRows = 4096;
 
-template <int EPC>
-__device__ __forceinline__ void store_row(float* p, const float* v) {
-  if constexpr (EPC == 1) {
-    *p = v[0];
-  } else {
-#pragma unroll
-    for (int e = 0; e < EPC; e += 4)
-      *reinterpret_cast<f32x4_t*>(p + e) = f32x4_t{v[e], v[e + 1], v[e + 2], v[e + 3]};
-  }
-}
-template <int EPC>
-__device__ __forceinline__ void write_dw(const SumArgs& a, uint32_t id, int64_t col, const float* acc) {
-  float* p = a.dW + (int64_t)id * a.H + col;
+template <int EPC, bool TAIL>
+__device__ __forceinline__ void write_dw(const SumArgs& a, uint32_t id, int col, const float* acc) {
+  float* row = a.dW + (int64_t)id * a.H;
   float v[EPC];
 #pragma unroll
-  for (int e = 0; e < EPC; ++e) v[e] = a.accumulate ? p[e] + a.scale * acc[e] : a.scale * acc[e];
-  store_row<EPC>(p, v);
+  for (int e = 0; e < EPC; ++e) v[e] = a.scale * acc[e];
+  if (a.accumulate) {
+    float old[EPC];
+    load_sum<EPC, TAIL>(row, col, a.H, old);
+#pragma unroll
+    for (int e = 0; e < EPC; ++e) v[e] += old[e];
+  }
+  store_sum<EPC, TAIL>(row, col, a.H, v);
 }
 
 // First sorted position with key >= id, by the whole wave: 64 probes a step.
@@ -376,25 +417,16 @@ __device__ __forceinline__ void zero_rows(const SumArgs& a, int64_t r0, int64_t 
     occurs[k - r0] = 1;
   }
   __syncthreads();
-  const bool vec = a.H % 4 == 0 && (uintptr_t)a.dW % 16 == 0;
-  for (int r = 0; r < rows; ++r) {
-    if (occurs[r]) continue;
-    float* p = a.dW + (r0 + r) * a.H;
-    if (vec)
-      for (int q = threadIdx.x; q < a.H / 4; q += kThreads)
-        reinterpret_cast<u32x4_t*>(p)[q] = u32x4_t{0u, 0u, 0u, 0u};
-    else
-      for (int q = threadIdx.x; q < a.H; q += kThreads) p[q] = 0.f;
-  }
+  for (int r = 0; r < rows; ++r)
+    if (!occurs[r]) zero_values(a.dW + (r0 + r) * a.H, a.H);
 }
 
 // Work-groups [0, tiles * blocks): one tile of sorted positions by a block of
 // columns, kAhead rows in flight.  The others zero `zero_rows` rows each.
-template <typename T, bool VEC>
+template <typename T, bool TAIL>
 __global__ __launch_bounds__(kThreads) void embed_sum_kernel(const SumArgs a) {
-  constexpr int EPC = VEC ? Elem<T>::kPer16B : 1;
+  constexpr int EPC = Elem<T>::kPer16B;
   constexpr int kAhead = 16;
-  using Raw = std::conditional_t<VEC, u32x4_t, T>;
   __shared__ uint8_t occurs[kMaxZeroRows];
   if ((int64_t)blockIdx.x >= a.groups) {
     const int64_t r0 = a.zero_from + ((int64_t)blockIdx.x - a.groups) * a.zero_step;
@@ -404,7 +436,7 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(const SumArgs a) {
   const int64_t tile = blockIdx.x / a.blocks;
   const int64_t i0 = tile * a.rows;
   const int n = (int)min((int64_t)a.rows, a.N - i0);
-  const int64_t col = ((int64_t)(blockIdx.x - tile * a.blocks) * kThreads + threadIdx.x) * EPC;
+  const int col = ((int)(blockIdx.x - tile * a.blocks) * kThreads + (int)threadIdx.x) * EPC;
   // lane l holds position i0 + l; lanes n and up repeat the last
   const int lane = threadIdx.x & 63;
   const uint32_t my_key = a.key[i0 + min(lane, n - 1)], my_pos = a.pos[i0 + min(lane, n - 1)];
@@ -420,20 +452,21 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(const SumArgs a) {
   auto flush = [&](bool on) {
     if (cur >= a.V || !in) return;
     if (head || on)
-      store_row<EPC>(a.part + (tile * 2 + (head ? 0 : 1)) * (int64_t)a.H + col, acc);
+      store_sum<EPC, TAIL>(a.part + (tile * 2 + (head ? 0 : 1)) * (int64_t)a.H, col, a.H, acc);
     else
-      write_dw<EPC>(a, cur, col, acc);
+      write_dw<EPC, TAIL>(a, cur, col, acc);
   };
   // The rows of a batch are requested together, without a branch: a store in
   // between would make the next row's wait cover it.  Padded positions are read
   // for nothing; lanes past the row read its start.
-  const T* from = static_cast<const T*>(a.dY) + (in ? col : 0);
+  const T* dY = static_cast<const T*>(a.dY);
+  const int from = in ? col : 0;
   for (int b0 = 0; b0 < n; b0 += kAhead) {
-    Raw raw[kAhead];
+    u32x4_t raw[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const uint32_t p = __builtin_amdgcn_readlane(my_pos, min(b0 + u, n - 1));
-      raw[u] = *reinterpret_cast<const Raw*>(from + (int64_t)p * a.H);
+      raw[u] = load_vec<T, TAIL>(dY + (int64_t)p * a.H, from, a.H);
     }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
@@ -447,10 +480,7 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(const SumArgs a) {
           for (int e = 0; e < EPC; ++e) acc[e] = 0.f;
         }
         float v[EPC];
-        if constexpr (VEC)
-          unpack16(raw[u], v, T());
-        else
-          v[0] = Elem<T>::to_f(raw[u]);
+        unpack16(raw[u], v, T());
 #pragma unroll
         for (int e = 0; e < EPC; ++e) acc[e] += v[e];
       }
@@ -462,7 +492,7 @@ __global__ __launch_bounds__(kThreads) void embed_sum_kernel(const SumArgs a) {
 // Joins the run that starts in tile blockIdx.x and goes on past it: a wave adds
 // a quarter of the tiles' sums, in order, and the waves' sums are added in
 // order.  64 lanes' columns per work-group.
-template <int EPC>
+template <int EPC, bool TAIL>
 __global__ __launch_bounds__(kThreads) void embed_join_kernel(const SumArgs a) {
   __shared__ float sums[kWaves][64 * EPC];
   const int64_t tile = blockIdx.x, i0 = tile * a.rows, i1 = i0 + a.rows;
@@ -479,7 +509,7 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(const SumArgs a) {
     more += c;
     full = c == 64;
   }
-  const int64_t col = ((int64_t)blockIdx.y * 64 + lane) * EPC;
+  const int col = ((int)blockIdx.y * 64 + lane) * EPC;
   const bool in = col < a.H;
   const int64_t share = (more + 1 + kWaves - 1) / kWaves;
   const int64_t lo = min(more + 1, w * share), hi = min(more + 1, lo + share);
@@ -488,13 +518,11 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(const SumArgs a) {
   for (int e = 0; e < EPC; ++e) acc[e] = 0.f;
   if (in) {
     // sum 0 is the first tile's second row, the others the tiles' first rows
-    const float* p = a.part + tile * 2 * (int64_t)a.H + col;
+    const float* p = a.part + tile * 2 * (int64_t)a.H;
 #pragma unroll 8
     for (int64_t c = lo; c < hi; ++c) {
-      const float* q = p + (2 * c + (c == 0 ? 1 : 0)) * (int64_t)a.H;
       float v[EPC];
-#pragma unroll
-      for (int e = 0; e < EPC; ++e) v[e] = q[e];
+      load_sum<EPC, TAIL>(p + (2 * c + (c == 0 ? 1 : 0)) * (int64_t)a.H, col, a.H, v);
 #pragma unroll
       for (int e = 0; e < EPC; ++e) acc[e] += v[e];
     }
@@ -507,7 +535,7 @@ __global__ __launch_bounds__(kThreads) void embed_join_kernel(const SumArgs a) {
   for (int v = 1; v < kWaves; ++v)
 #pragma unroll
     for (int e = 0; e < EPC; ++e) acc[e] += sums[v][lane * EPC + e];
-  write_dw<EPC>(a, cur, col, acc);
+  write_dw<EPC, TAIL>(a, cur, col, acc);
 }
 
 struct EmbedLayout {
@@ -543,26 +571,19 @@ EmbedLayout embed_layout(int64_t N, int64_t V, int H, int dtype) {
   return L;
 }
 
-template <typename T>
-hipError_t sum_and_join(SumArgs a, bool vec, hipStream_t st) {
-  const int epc = vec ? Elem<T>::kPer16B : 1;
+template <typename T, bool TAIL>
+hipError_t sum_and_join(SumArgs a, hipStream_t st) {
+  constexpr int EPC = Elem<T>::kPer16B;
   const int64_t tiles = ceil_div(a.N, a.rows);
-  a.blocks = (int)ceil_div(a.H, kThreads * epc);
+  a.blocks = (int)ceil_div(a.H, kThreads * EPC);
   a.groups = tiles * a.blocks;
   a.zero_step = std::min<int64_t>(std::max<int64_t>(kZeroBytes / 4 / a.H, 1), kMaxZeroRows);
   const unsigned grid = (unsigned)(a.groups + ceil_div(a.V - a.zero_from, a.zero_step));
-  const dim3 join((unsigned)tiles, (unsigned)ceil_div(a.H, 64 * epc));
-  if (vec) {
-    embed_sum_kernel<T, true><<<grid, kThreads, 0, st>>>(a);
-    if (a.N > a.rows) embed_join_kernel<Elem<T>::kPer16B><<<join, kThreads, 0, st>>>(a);
-  } else {
-    embed_sum_kernel<T, false><<<grid, kThreads, 0, st>>>(a);
-    if (a.N > a.rows) embed_join_kernel<1><<<join, kThreads, 0, st>>>(a);
-  }
+  embed_sum_kernel<T, TAIL><<<grid, kThreads, 0, st>>>(a);
+  const dim3 join((unsigned)tiles, (unsigned)ceil_div(a.H, 64 * EPC));
+  if (a.N > a.rows) embed_join_kernel<EPC, TAIL><<<join, kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
-
-bool aligned16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
 bool plan_ok(const embed_plan_t* p) { return p != nullptr && p->magic == kEmbedMagic; }
 
@@ -597,13 +618,13 @@ MOE_API int embed_forward(const embed_plan_t* plan, const void* W, const int32_t
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
   const int epc = 16 / elem_bytes(P.dtype);
-  const bool vec = P.H % epc == 0 && aligned16(W) && aligned16(Y);
-  const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(P.N * (P.H / (vec ? epc : 1)), kThreads), 1 << 20);
+  const bool tail = P.H % epc != 0;
+  const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(P.N * ceil_div(P.H, epc), kThreads), 1 << 20);
   auto run = [&](auto kern, auto* w, auto* y) { kern<<<grid, kThreads, 0, st>>>(w, ids, y, P.N, P.V, P.H, P.scale); };
   if (P.dtype == MOE_BF16)
-    run(vec ? embed_forward_kernel<bf16_t, true> : embed_forward_kernel<bf16_t, false>, (const bf16_t*)W, (bf16_t*)Y);
+    run(tail ? embed_forward_kernel<bf16_t, true> : embed_forward_kernel<bf16_t, false>, (const bf16_t*)W, (bf16_t*)Y);
   else
-    run(vec ? embed_forward_kernel<float, true> : embed_forward_kernel<float, false>, (const float*)W, (float*)Y);
+    run(tail ? embed_forward_kernel<float, true> : embed_forward_kernel<float, false>, (const float*)W, (float*)Y);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
 }
 
@@ -669,7 +690,9 @@ MOE_API int embed_backward(const embed_plan_t* plan, const int32_t* ids, const v
   if (hipGetLastError() != hipSuccess) return MOE_EHIP;
   const SumArgs a{s.key, s.pos, dY, dW, (float*)(ws + L.part), P.N, P.V, P.H, accumulate != 0, P.scale,
                   tile_rows(P.N, P.H, P.dtype), 0, 0, zeroed, 0};
-  const bool vec = P.H % (16 / elem_bytes(P.dtype)) == 0 && aligned16(dY) && aligned16(dW);
-  const hipError_t err = P.dtype == MOE_BF16 ? sum_and_join<bf16_t>(a, vec, st) : sum_and_join<float>(a, vec, st);
+  const bool tail = P.H % (16 / elem_bytes(P.dtype)) != 0;
+  const hipError_t err = P.dtype == MOE_BF16
+                             ? (tail ? sum_and_join<bf16_t, true>(a, st) : sum_and_join<bf16_t, false>(a, st))
+                             : (tail ? sum_and_join<float, true>(a, st) : sum_and_join<float, false>(a, st));
   return err == hipSuccess ? MOE_OK : MOE_EHIP;
 }

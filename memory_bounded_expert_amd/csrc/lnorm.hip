@@ -41,11 +41,6 @@ __device__ __forceinline__ float group_sum(float v, float* red) {
   return s;
 }
 
-// 16 bytes at an address that need not be a multiple of 16 (rows of any width
-// follow each other; the memory pipeline takes any alignment).
-typedef u32x4_t __attribute__((aligned(2))) u32x4_any_t;
-typedef f32x4_t __attribute__((aligned(4))) f32x4_any_t;
-
 // One lane's part of a row: C vectors of EPC elements, vector c at c * 64 W + its
 // place in the row's lanes.  TAIL: the row's last vector is short, and the lane
 // that holds it moves its elements one by one.

@@ -277,6 +277,15 @@ def test_kd_argument_errors():
             args[i] = None
             assert f(ref(p), *args, big, None) == B.MOE_EINVAL
         assert f(ref(p), *[FAKE] * (n - 1), ctypes.c_void_p(0x100080), big, None) == B.MOE_EINVAL
+    off = ctypes.c_void_p(0x100008)
+    for i in (0, 1):
+        args = [FAKE] * 8
+        args[i] = off
+        assert L.kd_forward(ref(p), *args, big, None) == B.MOE_EINVAL
+    for i in (0, 1, 7, 8):
+        args = [FAKE] * 10
+        args[i] = off
+        assert L.kd_backward(ref(p), *args, big, None) == B.MOE_EINVAL
     assert L.kd_forward(ref(p), *[FAKE] * 8, p.fwd_workspace_bytes - 1, None) == B.MOE_EWORKSPACE
     assert L.kd_backward(ref(p), *[FAKE] * 10, p.bwd_workspace_bytes - 1, None) == B.MOE_EWORKSPACE
     p0 = B.kd_plan(**{**KD_OK, "N": 0})
@@ -292,3 +301,10 @@ def test_kd_binding_refuses_wrong_tensors():
                    dict(t_logit=ok["t_logit"][:, :8]), dict()):  # the last: not on a GPU
         with pytest.raises(ValueError):
             B.kd_forward(p, **{**ok, **change})
+
+
+def test_binding_refuses_a_workspace_elsewhere():
+    with pytest.raises(ValueError):
+        B._workspace(torch.empty(1 << 20, dtype=torch.uint8), B.lnorm_plan(4, 64, B.MOE_F32), "bwd", torch.device("cuda:0"))
+    with pytest.raises(ValueError):
+        B._workspace(torch.empty((64, 64), dtype=torch.uint8)[:, ::2], B.lnorm_plan(4, 64, B.MOE_F32), "bwd", torch.device("cpu"))
