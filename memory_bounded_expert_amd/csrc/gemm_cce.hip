@@ -14,6 +14,20 @@ using Logit = Shape<256, 256, 4, 2, 32, 1>;
 using LogitFew = Shape<128, 256, 2, 2, 32, 2>;
 static_assert(Logit::BN / Logit::WGN == kCceSlice, "statistics slice = one wave's columns");
 static_assert(LogitFew::BN / LogitFew::WGN == kCceSlice, "statistics slice = one wave's columns");
+
+// Whether 128-row tiles, two per CU, finish before 256-row tiles, one per CU:
+// in rounds of the chip, where a CU left with one 128-row tile needs half of
+// one, and the smaller tiles take a tenth longer for the same products.  They
+// win where a last round of 256-row tiles is mostly empty, and for batches of
+// up to 128 tokens: whole passes of 777 x 512 x 20,000 take 167 us so and 175
+// us with 256-row tiles, of 16 x 4096 x 100,000 802 and 839 us, but of 1000 x
+// 4096 x 30,000 (1.8 full rounds) 1,106 and 1,021 us.
+bool few_tiles(int64_t t256, int64_t t128) {
+  if (t256 >= 4 * kCus) return false;
+  const int64_t rest = t128 % (2 * kCus);
+  const double half_rounds = 2.0 * (double)(t128 / (2 * kCus)) + (rest == 0 ? 0 : rest <= kCus ? 1 : 2);
+  return 1.1 * half_rounds < 2.0 * (double)ceil_div(t256, kCus);
+}
 }  // namespace
 
 hipError_t gemm_cce_logits(bool grad, const void* X, const void* Ws, int64_t N, int H, int w,
@@ -82,10 +96,8 @@ hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, i
   p.M = (int)N; p.N = w; p.K = H;
   p.ce_scale = inv_t;
   const dim3 grid((unsigned)ceil_div(N, Logit::BM), (unsigned)ceil_div(w, Logit::BN));
-  // Less than four rounds of tiles, one per CU: 128-row tiles, two per CU, lose
-  // less in the last round and in a batch of at most 128 tokens.
-  const bool few = (int64_t)grid.x * grid.y < 4 * kCus;
   const dim3 grid2((unsigned)ceil_div(N, LogitFew::BM), grid.y);
+  const bool few = few_tiles((int64_t)grid.x * grid.y, (int64_t)grid2.x * grid2.y);
   if (!grad) {
     p.ce_pmax = pmax; p.ce_psum = psum;
     return few ? launch_lds<Mode::Dense, LogitFew, false, true, true, false, Epi::KDStats>(p, grid2, st)
