@@ -87,7 +87,8 @@ __device__ __forceinline__ void fold(float a, float b, float& m, float& z) {
 // Folds a strip's slice pairs into the running state (m, z).  A work-group takes
 // 16 tokens, 16 threads each: every thread folds each 16th slice in order, then
 // one thread a token its state and the 16 results in order.  The last strip
-// finishes lse.
+// finishes lse.  Latency bounds it: 64 slices of 8192 tokens 5.1 us, 158 of 777
+// tokens 5.6 us (16.5 with one thread a token).
 constexpr int kFoldTokens = 16, kFoldWays = kThreads / kFoldTokens, kFoldAhead = 4;
 __global__ __launch_bounds__(kThreads) void kd_fold_kernel(
     const float* __restrict__ pmax, const float* __restrict__ psum, int nslices, int64_t N,
@@ -124,8 +125,10 @@ __global__ __launch_bounds__(kThreads) void kd_fold_kernel(
   }
 }
 
-// One work-group per token: the list entries' logits, a wave taking kDots
-// rows of W at a time, then the loss.
+// One work-group per token: the list entries' logits, a wave taking kDots rows
+// of W at a time, then the loss.  Bound by the gathered rows: 8192 tokens, 32
+// entries of 7168, 590 us for 3.8 GB (6.4 TB/s, partly from cache), 0.8% of the
+// pass.
 __global__ __launch_bounds__(kThreads) void kd_loss_kernel(const KdArgs a, float* __restrict__ loss,
                                                            float* __restrict__ y_top) {
   __shared__ float ys[kMaxList];
@@ -206,7 +209,7 @@ __global__ __launch_bounds__(kThreads) void kd_prep_kernel(const KdArgs a,
   if (lane == 0) dl[t] = any ? dloss[t] * a.T : 0.f;
 }
 
-// The strip's list entries: G[t][i - v0] = dl (q - p), from the entries' own
+// The strip's list entries (latency, 5 us): G[t][i - v0] = dl (q - p), from the entries' own
 // logits (entries of one index write the same value).
 __global__ __launch_bounds__(kThreads) void kd_entries_kernel(
     const KdArgs a, const float* __restrict__ y_top, const float* __restrict__ dl,
@@ -257,7 +260,9 @@ int strip_cols(int64_t V, int strip) {
 }
 
 // The backward pass's strips: v_chunk, times what KD_STRIP_BYTES leaves (and
-// 32-bit offsets into W), evened out over the vocabulary.
+// 32-bit offsets into W), evened out over the vocabulary.  777 x 512 x 20,000 at
+// v_chunk 4096 takes 167 us so and 348 with strips of v_chunk, 100 x 2048 x 50,000
+// 260 and 1,101, 2000 x 2048 x 50,000 1,770 and 2,329.
 int strip_of(int64_t N, int64_t V, int H, int v_chunk) {
   const int64_t cols = ceil_div(V, 256) * 256;
   const int64_t most = std::min<int64_t>((int64_t)KD_STRIP_BYTES / 2 / std::max<int64_t>(N, 1),
@@ -278,7 +283,8 @@ int forward_strip(int64_t N, int64_t V, int H) {
 
 // dX's ranges: with fewer than 256 tiles of dX, as many sums side by side as
 // fill the CUs once, each range at least 512 entries (16 K-tiles).  Depends on
-// N, H and V alone, so dX does not depend on the strips.
+// N, H and V alone, so dX does not depend on the strips.  The passes above take
+// 488, 775 and 2,238 us with one sum.
 struct DxRanges {
   int range, slots;
 };

