@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "device_common.hpp"
+#include "wave_ops.hpp"
 #include "gemm_kernel.hpp"  // Mode, Epi, Params, make_rsrc, wave_uniform
 #include "moe_internal.h"
 
@@ -841,7 +842,7 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
     return;
   }
 
-  if constexpr (EPI == Epi::CEStats || EPI == Epi::KDStats) {
+  if constexpr (EPI == Epi::CEStats) {
     // Vocabulary-strip cross-entropy, forward: the tile's logits stay on
     // chip.  Per row, each wave reduces its WN-column slice (columns past N,
     // the ragged end of the strip, excluded) to the slice's max m and
@@ -850,12 +851,7 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
     // (commutative pairwise steps, so every lane ends with the same bits).
     // Slice s of the strip covers columns [s WN, (s + 1) WN), the same
     // vocabulary columns whatever the strip width.  The lane holding the
-    // row's target column also writes that logit.  KDStats: the same of the
-    // logits times ce_scale, without targets.
-    constexpr bool KD = EPI == Epi::KDStats;
-    auto logit = [&](int i, int j, int q) __attribute__((always_inline)) {
-      return KD ? acc[0][i][j][q] * p.ce_scale : acc[0][i][j][q];
-    };
+    // row's target column also writes that logit.
     const int col0 = n0 + wn * WN;
     const int slice = col0 / WN;
     const int64_t M = p.M;
@@ -867,13 +863,13 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
         float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-          if (col0 + j * 16 + l16 < p.N) mx = fmaxf(mx, logit(i, j, q));
+          if (col0 + j * 16 + l16 < p.N) mx = fmaxf(mx, acc[0][i][j][q]);
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor(mx, o));
         float sm = 0.f;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
-          if (col0 + j * 16 + l16 < p.N) sm += __expf(logit(i, j, q) - mx);
+          if (col0 + j * 16 + l16 < p.N) sm += __expf(acc[0][i][j][q] - mx);
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) sm += __shfl_xor(sm, o);
         if (row < row_end) {
@@ -881,18 +877,58 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
             p.ce_pmax[slice * M + row] = mx;
             p.ce_psum[slice * M + row] = sm;
           }
-          if constexpr (!KD) {
-            const int64_t rel = (int64_t)p.ce_targets[row] - p.ce_col0 - col0;
-            if (rel >= 0 && rel < WN && (int)(rel & 15) == l16) {
-              float v = 0.f;
+          const int64_t rel = (int64_t)p.ce_targets[row] - p.ce_col0 - col0;
+          if (rel >= 0 && rel < WN && (int)(rel & 15) == l16) {
+            float v = 0.f;
 #pragma unroll
-              for (int j = 0; j < FN; ++j)
-                if ((int)(rel >> 4) == j) v = acc[0][i][j][q];
-              p.ce_ytgt[row] = v;
-            }
+            for (int j = 0; j < FN; ++j)
+              if ((int)(rel >> 4) == j) v = acc[0][i][j][q];
+            p.ce_ytgt[row] = v;
           }
         }
       }
+    return;
+  }
+
+  if constexpr (EPI == Epi::KDStats) {
+    // Distillation, forward: the slice statistics of the logits times ce_scale,
+    // per row over the wave's WN columns as CEStats takes them, without targets.
+    // The maximum is taken before scaling (ce_scale > 0), an exponential is one
+    // fused multiply-add and the hardware's base-2 exponential, and the row's 16
+    // lanes reduce by rotations in DPP operands: with shuffles through LDS and
+    // masks throughout, the epilogue was a third of a 512-wide product's time.
+    const int col0 = n0 + wn * WN;
+    const int slice = col0 / WN;
+    const int64_t M = p.M;
+    const float c = p.ce_scale * 1.44269504f;
+    auto stats = [&](auto whole) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = m0 + wm * WM + i * 16 + 4 * lg + q;
+          float mx = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            if (whole.value || col0 + j * 16 + l16 < p.N) mx = fmaxf(mx, acc[0][i][j][q]);
+          mx = run_maxf<16>(mx);
+          const float top = mx * c;
+          float sm = 0.f;
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            if (whole.value || col0 + j * 16 + l16 < p.N)
+              sm += __builtin_amdgcn_exp2f(fmaf(acc[0][i][j][q], c, -top));
+          sm = run_sum<16>(sm);
+          if (row < row_end && l16 == 0) {
+            p.ce_pmax[slice * M + row] = mx * p.ce_scale;
+            p.ce_psum[slice * M + row] = sm;
+          }
+        }
+    };
+    if (col0 + WN <= p.N)
+      stats(std::true_type());
+    else
+      stats(std::false_type());
     return;
   }
 
@@ -1077,13 +1113,19 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int row = min(m0 + wm * WM + i * 16 + 4 * lg + q, row_end - 1);
-          rlse[i][q] = p.ce_lse[row];
+          rlse[i][q] = p.ce_lse[row] * 1.44269504f;
           rdl[i][q] = p.ce_dl[row];
         }
-      stage_store(static_cast<T*>(p.C), [&](int i, int j, int q) {
-        const float gv = rdl[i][q] * __expf(fmaf(acc[0][i][j][q], p.ce_scale, -rlse[i][q]));
-        return f2bf(n0 + wn * WN + j * 16 + l16 < p.N ? gv : 0.f);
-      });
+      const float c = p.ce_scale * 1.44269504f;
+      if (n0 + BN <= p.N)  // the same way for every wave: stage_store has barriers
+        stage_store(static_cast<T*>(p.C), [&](int i, int j, int q) {
+          return f2bf(rdl[i][q] * __builtin_amdgcn_exp2f(fmaf(acc[0][i][j][q], c, -rlse[i][q])));
+        });
+      else
+        stage_store(static_cast<T*>(p.C), [&](int i, int j, int q) {
+          const float gv = rdl[i][q] * __builtin_amdgcn_exp2f(fmaf(acc[0][i][j][q], c, -rlse[i][q]));
+          return f2bf(n0 + wn * WN + j * 16 + l16 < p.N ? gv : 0.f);
+        });
     } else if constexpr (EPI == Epi::CEGrad) {
       // Vocabulary-strip cross-entropy, backward: the strip's logit gradient
       // dl_row (exp(logit - lse_row) - [column == target_row]), bf16;
