@@ -7,8 +7,9 @@
 // lanes past 256 experts), so that a wave selects for four tokens at once and
 // every reduction stays inside a row of lanes, in DPP operands.  The selection
 // runs k rounds: the largest remaining rank, then the lowest expert that holds
-// it.  Ranks are unsigned integers that order as the values do (0: not to be
-// selected), so any input, NaN included, gives k distinct experts.
+// it.  Ranks are the values, -inf for a masked expert and NaN for what is not to
+// be selected, which no maximum and no comparison takes: any input gives k
+// distinct experts.
 //
 // Logits rank exactly as they are.  Scores with a bias, and group strengths,
 // are formed in 32 bits first; a token where two values that decide something
@@ -84,12 +85,13 @@ __device__ __forceinline__ float nearness(int sigmoid, float x) {
   return (sigmoid ? 7e-7f : 2e-6f) * (1.f + fabsf(x));
 }
 
-// Sums exp(l - top) in 64 bits over a token's G lanes.
-template <int G, int V>
-__device__ __forceinline__ double softmax_sum64(const float (&l)[V], float top) {
+// The sum of exp(l - top) in 64 bits over a row, G lanes taking every G-th expert
+// from `first` on.  (A loop: unrolled, its registers would halve the waves.)
+template <int G>
+__device__ __forceinline__ double softmax_sum64(const float* row, int E, int first, float top) {
   double z = 0.0;
-#pragma unroll
-  for (int j = 0; j < V; ++j) z += is_masked(l[j]) ? 0.0 : exp((double)l[j] - (double)top);
+#pragma unroll 2
+  for (int e = first; e < E; e += G) z += is_masked(row[e]) ? 0.0 : exp((double)row[e] - (double)top);
 #pragma unroll
   for (int o = 1; o < G; o <<= 1) z += __shfl_xor(z, o);
   return z;
@@ -97,52 +99,36 @@ __device__ __forceinline__ double softmax_sum64(const float (&l)[V], float top) 
 
 // One token's selection in 64 bits by the whole wave (every lane of it calls):
 // lane s returns slot s's expert.  lds: E + n_group doubles of the wave's own.
-template <int V>
+// The values stay there, not in registers: few tokens come here, and the kernel
+// around it is to keep its waves (E > 512 with a bias: 2 a SIMD with registers).
 __device__ __forceinline__ int route_exact(const RouteArgs& a, int64_t t, double* lds) {
   const int lane = threadIdx.x & 63;
   const float* row = a.logits + t * a.E;
-  const int per = a.E / a.n_group;
-  float l[V], top = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = lane + 64 * j;
-    l[j] = e < a.E ? row[e] : -INFINITY;
-    if (is_masked(l[j])) l[j] = -INFINITY;
-    top = fmaxf(top, l[j]);
+  float top = -INFINITY;
+  double inv = 0.0;
+  if (!a.sigmoid) {
+    for (int e = lane; e < a.E; e += 64) top = fmaxf(top, row[e]);
+    top = run_maxf<64>(top);
+    const double z = softmax_sum64<64>(row, a.E, lane, top);
+    inv = z > 0.0 ? 1.0 / z : 0.0;
   }
-  top = run_maxf<64>(top);
-  double v[V];
-  if (a.sigmoid) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] = 1.0 / (1.0 + exp(-(double)l[j]));
-  } else {
-    double z = 0.0;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      v[j] = is_masked(l[j]) ? 0.0 : exp((double)l[j] - (double)top);
-      z += v[j];
+  wave_lds_order();  // earlier uses of the wave's LDS are done
+#pragma unroll 1
+  for (int e = lane; e < a.E; e += 64) {
+    const float l = row[e];
+    double v = -INFINITY;
+    if (!is_masked(l)) {
+      v = exp(a.sigmoid ? -(double)l : (double)l - (double)top);
+      v = a.sigmoid ? 1.0 / (1.0 + v) : v * inv;
+      if (a.bias) v += (double)a.bias[e];
     }
-    z = wave_sum(z);
-    const double inv = z > 0.0 ? 1.0 / z : 0.0;
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] *= inv;
+    lds[e] = v;
   }
-  uint64_t rank[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int e = lane + 64 * j;
-    if (a.bias && e < a.E) v[j] += (double)a.bias[e];
-    rank[j] = e >= a.E            ? 0ull
-              : is_masked(l[j])   ? order_of(-(double)INFINITY)
-                                  : order_of(a.bias ? v[j] : (double)l[j]);
-  }
+  const int per = a.E / a.n_group;
+  uint64_t kept = ~0ull;
   if (a.n_group > 1) {
-    // group strengths: lane g sums group g's best values out of LDS
+    // group strengths: lane g sums group g's best values
     double* strength = lds + a.E;
-    wave_lds_order();  // earlier uses of the wave's LDS are done
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (lane + 64 * j < a.E) lds[lane + 64 * j] = is_masked(l[j]) ? -INFINITY : v[j];
     wave_lds_order();
     double mine = -INFINITY;
     if (lane < a.n_group) {
@@ -160,32 +146,54 @@ __device__ __forceinline__ int route_exact(const RouteArgs& a, int64_t t, double
     int before = 0;
     for (int h = 0; h < a.n_group; ++h)
       before += strength[h] > mine || (strength[h] == mine && h < lane) ? 1 : 0;
-    const uint64_t kept = __ballot(lane < a.n_group && before < a.topk_group);
-    wave_lds_order();
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (lane + 64 * j < a.E && !((kept >> ((lane + 64 * j) / per)) & 1)) rank[j] = 0ull;
+    kept = __ballot(lane < a.n_group && before < a.topk_group);
+  }
+  // a lane's experts from here on are its own: ranks in the values' place, and
+  // the largest, at the lowest expert, in registers
+  uint64_t* rank = reinterpret_cast<uint64_t*>(lds);
+  uint64_t own = 0ull;
+  int own_e = 0;
+  for (int e = lane; e < a.E; e += 64) {
+    const double x = lds[e];
+    const bool in = a.n_group == 1 || (kept >> (e / per)) & 1;
+    const uint64_t r = in ? order_of(a.bias || x == -INFINITY ? x : (double)row[e]) : 0ull;
+    rank[e] = r;
+    if (r > own) own = r, own_e = e;
   }
   int my_i = 0;
   for (int s = 0; s < a.k; ++s) {
-    uint64_t own = 0ull;
-#pragma unroll
-    for (int j = 0; j < V; ++j) own = rank[j] > own ? rank[j] : own;
     // the largest over the wave, its high half first
     const uint32_t hi = run_maxu<64>((uint32_t)(own >> 32));
     const uint32_t lo = run_maxu<64>((uint32_t)(own >> 32) == hi ? (uint32_t)own : 0u);
-    const uint64_t best = (uint64_t)hi << 32 | lo;
-    uint32_t at = ~0u;
-#pragma unroll
-    for (int j = V - 1; j >= 0; --j)
-      if (rank[j] == best) at = lane + 64 * j;
-    at = run_minu<64>(at);
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-      if ((int)at == lane + 64 * j) rank[j] = 0ull;
+    const bool holds = own == ((uint64_t)hi << 32 | lo);
+    const uint32_t at = run_minu<64>(holds ? (uint32_t)own_e : ~0u);
     if (lane == s) my_i = (int)at;
+    if ((int)(at % 64) == lane) {
+      rank[at] = 0ull;
+      own = 0ull;
+#pragma unroll 8
+      for (int e = lane; e < a.E; e += 64) {
+        const uint64_t r = rank[e];
+        own_e = r > own ? e : own_e;
+        own = r > own ? r : own;
+      }
+    }
   }
   return my_i;
+}
+
+// How many lanes of the lane's row of 16 hold more than it (below 2^31): the
+// signs of the differences, shifted together.  (A sum with the negative: as a
+// subtraction with a DPP operand the compiler's code had the other sign here.)
+__device__ __forceinline__ int lanes_above(uint32_t v) {
+  uint32_t signs = 0u;
+  const uint32_t less = 0u - v;
+#define ROUTE_ROTATE(n) signs = __builtin_amdgcn_alignbit(signs, v + row_ror<n>(less), 31);
+  ROUTE_ROTATE(1) ROUTE_ROTATE(2) ROUTE_ROTATE(3) ROUTE_ROTATE(4) ROUTE_ROTATE(5)
+  ROUTE_ROTATE(6) ROUTE_ROTATE(7) ROUTE_ROTATE(8) ROUTE_ROTATE(9) ROUTE_ROTATE(10)
+  ROUTE_ROTATE(11) ROUTE_ROTATE(12) ROUTE_ROTATE(13) ROUTE_ROTATE(14) ROUTE_ROTATE(15)
+#undef ROUTE_ROTATE
+  return __popc(signs);
 }
 
 // kByScore: with a bias.  kQuads: groups, and every four experts that a lane
@@ -197,7 +205,6 @@ enum RouteMode { kByLogit, kByScore, kGrouped, kQuads };
 // route_exact's doubles.
 template <int G>
 size_t route_lds(int E, int n_group) {
-  if (n_group == 1) return 0;
   const size_t fast = (64 / G) * (size_t)(E + 2 * n_group) * sizeof(float);
   const size_t exact = (size_t)(E + n_group) * sizeof(double);
   return (std::max(fast, exact) + 15) / 16 * 16;
@@ -216,8 +223,9 @@ template <int G, int V, int MODE, int SLOTS>
 __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs a, int vec,
                                                                  uint32_t per_mul, int wave_lds) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  __shared__ uint32_t lists[kWaves][SLOTS == 1 ? 2 * 64 + 8 : 1];
+  __shared__ __attribute__((aligned(16))) uint2 lists[kWaves][SLOTS == 1 ? 64 + 8 : 1];
   constexpr int TPW = 64 / G;
+  const float kNone = __builtin_nanf("");  // a rank that nothing takes
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int ln = lane % G, sub = lane / G;
   const int64_t t0 = ((int64_t)blockIdx.x * kWaves + w) * TPW;
@@ -228,42 +236,38 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
   const int mine = vec ? 4 * ln : ln, step = vec ? 1 : G;
   auto place = [&](int j) { return (j / 4) * 4 * G + (j % 4) * step; };  // expert j's index, less `mine`
 
-  float l[V];
+  float l[V];  // -inf: masked, NaN: past the last expert
   if (vec) {
 #pragma unroll
     for (int j = 0; j < V; j += 4) {
       const f32x4_t q = *reinterpret_cast<const f32x4_t*>(row + min(mine + place(j), a.E - 4));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) l[j + i] = mine + place(j) < a.E ? q[i] : -INFINITY;
+      for (int i = 0; i < 4; ++i) l[j + i] = mine + place(j) < a.E ? fmaxf(q[i], -INFINITY) : kNone;
     }
   } else {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       l[j] = row[min(mine + place(j), a.E - 1)];
-      l[j] = mine + place(j) < a.E ? l[j] : -INFINITY;
+      l[j] = mine + place(j) < a.E ? fmaxf(l[j], -INFINITY) : kNone;
     }
   }
-  float top = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    if (is_masked(l[j])) l[j] = -INFINITY;  // NaN
-    top = fmaxf(top, l[j]);
-  }
-  float inv_z = 0.f;
+  float top = -INFINITY, inv_z = 0.f;
   if (!a.sigmoid && (MODE != kByLogit || !a.renorm)) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) top = fmaxf(top, l[j]);
     top = run_maxf<G>(top);
     float z = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) z += is_masked(l[j]) ? 0.f : __expf(l[j] - top);
+    for (int j = 0; j < V; ++j) z += fmaxf(__expf(l[j] - top), 0.f);  // 0 of NaN
     z = run_sum<G>(z);
     inv_z = z > 0.f ? 1.f / z : 0.f;
   }
 
-  uint32_t rank[V];
+  float rank[V];
   bool near = false;  // 32 bits do not tell: select again with route_exact
   if constexpr (MODE == kByLogit) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) rank[j] = mine + place(j) < a.E ? order_of(l[j]) : 0u;
+    for (int j = 0; j < V; ++j) rank[j] = l[j];
   } else {
     // v_e.  Loads and the choice of score stand outside the loops: a branch per
     // element would wait for each load by itself.
@@ -273,7 +277,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
       for (int j = 0; j < V; ++j) v[j] = logistic(l[j]);
     } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = is_masked(l[j]) ? 0.f : __expf(l[j] - top) * inv_z;
+      for (int j = 0; j < V; ++j) v[j] = fmaxf(__expf(l[j] - top) * inv_z, 0.f);
     }
     if (a.bias) {
       if (vec) {
@@ -292,8 +296,8 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const uint32_t o = order_of(is_masked(l[j]) || !a.bias ? l[j] : v[j]);
-      rank[j] = mine + place(j) < a.E ? o : 0u;
+      v[j] = l[j] > -INFINITY ? v[j] : l[j];
+      rank[j] = a.bias ? v[j] : l[j];
     }
     if constexpr (MODE >= kGrouped) {
       // Lane g adds up group g's best out of LDS: from the values, or from the
@@ -308,16 +312,16 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
         const int e = (mine + place(j * Q)) / Q;
         grp[j] = (int)(((uint32_t)e * per_mul) >> 20);
         if constexpr (MODE == kQuads) {
-          float b1 = -INFINITY, b2 = -INFINITY;
+          const float* x = v + 4 * j;
+          float b1 = fmaxf(x[0], x[1]), b2 = fminf(x[0], x[1]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float x = is_masked(l[4 * j + i]) ? -INFINITY : v[4 * j + i];
-            b2 = __builtin_amdgcn_fmed3f(b2, b1, x);
-            b1 = fmaxf(b1, x);
+          for (int i = 2; i < 4; ++i) {
+            b2 = __builtin_amdgcn_fmed3f(b2, b1, x[i]);
+            b1 = fmaxf(b1, x[i]);
           }
           if (e * 4 < a.E) reinterpret_cast<float2*>(val)[e + grp[j]] = make_float2(b1, b2);
         } else {
-          if (e < a.E) val[e + grp[j]] = is_masked(l[j]) ? -INFINITY : v[j];
+          if (e < a.E) val[e + grp[j]] = v[j];
         }
       }
       wave_lds_order();
@@ -366,7 +370,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
       for (int j = 0; j < NQ; ++j) {
         const bool keep = ((grp[j] < 32 ? lo : hi) >> (grp[j] & 31)) & 1;
 #pragma unroll
-        for (int i = 0; i < Q; ++i) rank[Q * j + i] = keep ? rank[Q * j + i] : 0u;
+        for (int i = 0; i < Q; ++i) rank[Q * j + i] = keep ? rank[Q * j + i] : kNone;
       }
     }
   }
@@ -385,26 +389,21 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     constexpr int ROWS = G / 16;
     const int want = (a.k + (close ? 1 : 0) + ROWS - 1) / ROWS;
     if (want <= 16) {
-      uint32_t own = 0u;
+      float best = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < V; ++j) own = max(own, rank[j]);
-      int above = 0;
-#define ROUTE_ROTATE(n) above += row_ror<n>(own) > own ? 1 : 0;
-      ROUTE_ROTATE(1) ROUTE_ROTATE(2) ROUTE_ROTATE(3) ROUTE_ROTATE(4) ROUTE_ROTATE(5)
-      ROUTE_ROTATE(6) ROUTE_ROTATE(7) ROUTE_ROTATE(8) ROUTE_ROTATE(9) ROUTE_ROTATE(10)
-      ROUTE_ROTATE(11) ROUTE_ROTATE(12) ROUTE_ROTATE(13) ROUTE_ROTATE(14) ROUTE_ROTATE(15)
-#undef ROUTE_ROTATE
+      for (int j = 0; j < V; ++j) best = fmaxf(best, rank[j]);
+      // how many of the row's lanes have more: signs of differences, the lowest
+      // bit left out (a lane too many with that much is as good)
+      const int above = lanes_above(order_of(best) >> 1);
       // with close, whatever may turn out to be ahead of T belongs to the candidates
-      auto below = [&](uint32_t r) __attribute__((always_inline)) {
-        const float x = value_of(r);
-        return close && r > 1u && x > -INFINITY ? order_of(x - nearness(a.sigmoid, x)) : r;
+      auto below = [&](float x) __attribute__((always_inline)) {
+        return close && x > -INFINITY ? x - nearness(a.sigmoid, x) : x;
       };
-      uint32_t T = below(max(1u, run_minu<G>(above < want ? own : ~0u)));
-      // (rank, ~expert) of each candidate, larger is earlier; one slot past the
-      // list takes what is no candidate
-      uint32_t* list = lists[w] + sub * (2 * G + 2);
+      float T = below(run_minf<G>(above < want ? best : INFINITY));
+      // (value, ~expert) of each candidate; larger is earlier
+      uint2* list = lists[w] + sub * (G + 2);
       int held = 0;
-      auto count_from = [&](uint32_t from) __attribute__((always_inline)) {
+      auto count_from = [&](float from) __attribute__((always_inline)) {
         held = 0;
 #pragma unroll
         for (int j = 0; j < V; ++j) held += rank[j] >= from ? 1 : 0;
@@ -413,18 +412,22 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
       int count = count_from(T);
       if (__any(count > G)) {
         // the best sit in few lanes (kept groups do): halve the way from T to
-        // the largest until what is left fits
-        uint32_t low = T, high = run_maxu<G>(own) + 1u;
+        // the largest until what is left fits, from the lowest lane's largest if
+        // that will do (-inf is many halvings away)
+        const float some = run_minf<G>(best > -INFINITY ? best : INFINITY);
+        const int with_some = count_from(some);
+        const bool enough = T == -INFINITY && with_some >= want * ROWS;
+        uint32_t low = order_of(enough ? some : T), high = order_of(run_maxf<G>(best)) + 1u;
         bool open = count > G;
         for (int i = 0; i < 12 && __any(open); ++i) {
           const uint32_t mid = low + (high - low) / 2;
-          const int c = count_from(mid);
+          const int c = count_from(value_of(mid));
           if (open) {
             if (c >= want * ROWS) low = mid; else high = mid;
             open = c < want * ROWS || c >= G;
           }
         }
-        if (count > G) T = below(low);
+        if (count > G) T = below(value_of(low));
         count = count_from(T);
       }
       int at = held;  // inclusive sums over the token's lanes
@@ -440,77 +443,91 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
       }
       if (!__any(count > G)) {
         done = true;
-        at -= held;
+        uint2* to = list + (at - held);
+        const uint32_t last = ~(uint32_t)mine;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const bool in = rank[j] >= T;
-          const int to = in ? at : G;
-          list[to] = rank[j];
-          list[G + 1 + to] = ~(uint32_t)(mine + place(j));
-          at += in ? 1 : 0;
-        }
+        for (int j = 0; j < V; ++j)
+          if (rank[j] >= T) *to++ = make_uint2(__float_as_uint(rank[j]), last - place(j));
+        if (G == 64 && ln < 8) list[count + ln].x = __float_as_uint(kNone);  // read by eights
         wave_lds_order();
-        const uint64_t cand = ln < count ? (uint64_t)list[ln] << 32 | list[G + 1 + ln] : 0ull;
-        wave_lds_order();
+        const bool in = ln < count;
+        const uint2 c0 = list[ln];
+        const float x0 = in ? __uint_as_float(c0.x) : -INFINITY;
         int before = 0;
         if constexpr (G == 64) {
-          for (int c = 0; c < count; ++c) {
-            const uint64_t o = (uint64_t)__builtin_amdgcn_readlane((int)(cand >> 32), c) << 32 |
-                               (uint32_t)__builtin_amdgcn_readlane((int)cand, c);
-            before += o > cand ? 1 : 0;
-          }
+          const int n = __builtin_amdgcn_readfirstlane(count);
+          for (int c = 0; c < n; c += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint4 q = reinterpret_cast<const uint4*>(list + c)[u];
+              before += __uint_as_float(q.x) > x0 ? 1 : 0;
+              before += __uint_as_float(q.z) > x0 ? 1 : 0;
+            }
         } else {
+          before = lanes_above(in ? order_of(x0) >> 1 : 0u);
+        }
+        if (__any(run_sumi<G>(in ? before : 0) != count * (count - 1) / 2)) {
+          // equal values (or a lowest bit apart): by value, then expert
+          const uint64_t cand = in ? (uint64_t)order_of(x0) << 32 | c0.y : 0ull;
+          before = 0;
+          if constexpr (G == 64) {
+            const int n = __builtin_amdgcn_readfirstlane(count);
+            for (int c = 0; c < n; ++c) {
+              const uint64_t o = (uint64_t)__builtin_amdgcn_readlane((int)(cand >> 32), c) << 32 |
+                                 (uint32_t)__builtin_amdgcn_readlane((int)cand, c);
+              before += o > cand ? 1 : 0;
+            }
+          } else {
 #define ROUTE_ROTATE(n)                                                                       \
   before += ((uint64_t)row_ror<n>((uint32_t)(cand >> 32)) << 32 | row_ror<n>((uint32_t)cand)) > cand ? 1 : 0;
-          ROUTE_ROTATE(1) ROUTE_ROTATE(2) ROUTE_ROTATE(3) ROUTE_ROTATE(4) ROUTE_ROTATE(5)
-          ROUTE_ROTATE(6) ROUTE_ROTATE(7) ROUTE_ROTATE(8) ROUTE_ROTATE(9) ROUTE_ROTATE(10)
-          ROUTE_ROTATE(11) ROUTE_ROTATE(12) ROUTE_ROTATE(13) ROUTE_ROTATE(14) ROUTE_ROTATE(15)
+            ROUTE_ROTATE(1) ROUTE_ROTATE(2) ROUTE_ROTATE(3) ROUTE_ROTATE(4) ROUTE_ROTATE(5)
+            ROUTE_ROTATE(6) ROUTE_ROTATE(7) ROUTE_ROTATE(8) ROUTE_ROTATE(9) ROUTE_ROTATE(10)
+            ROUTE_ROTATE(11) ROUTE_ROTATE(12) ROUTE_ROTATE(13) ROUTE_ROTATE(14) ROUTE_ROTATE(15)
 #undef ROUTE_ROTATE
+          }
         }
+        wave_lds_order();
+        if (in) list[before] = c0;
+        wave_lds_order();
+        uint2 sel = list[ln];
         if (close) {
-          // put in order, are neighbours that matter too near?
-          list[ln < count ? before : G] = (uint32_t)(cand >> 32);
-          wave_lds_order();
-          const float x = ln < count ? value_of(list[ln]) : -INFINITY;
-          const float y = ln + 1 < count ? value_of(list[ln + 1]) : -INFINITY;
-          wave_lds_order();
+          // in order now: are neighbours that matter too near?
+          const float x = in ? __uint_as_float(sel.x) : -INFINITY;
+          const float y = ln + 1 < count ? __uint_as_float(list[ln + 1].x) : -INFINITY;
           if (__any(ln < a.k && y > -INFINITY && !(x - y > nearness(a.sigmoid, y)))) {
             // then all candidates rank by their values in 64 bits
             double z = 1.0;
-            if (!a.sigmoid) z = softmax_sum64<G>(l, top);
-            const int e = ln < count ? (int)~(uint32_t)cand : 0;
+            if (!a.sigmoid) z = softmax_sum64<G>(row, a.E, ln, top);
+            const int e = in ? (int)~c0.y : 0;
             const float le = row[e];
             const double s64 = a.sigmoid ? 1.0 / (1.0 + exp(-(double)le)) : exp((double)le - (double)top) / z;
             const uint64_t o64 = order_of(is_masked(le) ? -(double)INFINITY : s64 + (double)a.bias[e]);
-            const uint32_t id = (uint32_t)cand;
             before = 0;
             for (int c = 0; c < G; ++c) {
               const int from = sub * G + c;
               const uint64_t o = __shfl(o64, from);
-              const uint32_t oid = __shfl(id, from);
-              before += c < count && (o > o64 || (o == o64 && oid > id)) ? 1 : 0;
+              const uint32_t oid = __shfl(c0.y, from);
+              before += c < count && (o > o64 || (o == o64 && oid > c0.y)) ? 1 : 0;
             }
+            wave_lds_order();
+            if (in) list[before] = c0;
+            wave_lds_order();
+            sel = list[ln];
           }
         }
-        const int to = ln < count ? before : G;
-        list[to] = (uint32_t)(cand >> 32);
-        list[G + 1 + to] = (uint32_t)cand;
-        wave_lds_order();
-        const uint64_t sel = ln < count ? (uint64_t)list[ln] << 32 | list[G + 1 + ln] : 0ull;
         if (ln < a.k) {
-          my_i[0] = (int)~(uint32_t)sel;
-          my_v[0] = value_of((uint32_t)(sel >> 32));
+          my_i[0] = (int)~sel.y;
+          my_v[0] = __uint_as_float(sel.x);
         }
       }
     }
   }
   float prev = INFINITY;
   for (int s = 0; !done && s < a.k + (close ? 1 : 0); ++s) {
-    uint32_t best = 0u;
+    float x = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < V; ++j) best = max(best, rank[j]);
-    best = run_maxu<G>(best);
-    const float x = best ? value_of(best) : -INFINITY;
+    for (int j = 0; j < V; ++j) x = fmaxf(x, rank[j]);
+    x = run_maxf<G>(x);
     if (close) {
       near |= x > -INFINITY && !(prev - x > nearness(a.sigmoid, x));
       prev = x;
@@ -519,12 +536,12 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     uint32_t at = ~0u;
 #pragma unroll
     for (int j = V - 1; j >= 0; --j)
-      if (rank[j] == best) at = place(j);
+      if (rank[j] == x) at = place(j);
     at = run_minu<G>(at == ~0u ? at : at + mine);
     const uint32_t mine_at = at - mine;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if ((int)mine_at == place(j)) rank[j] = 0u;
+      if ((int)mine_at == place(j)) rank[j] = kNone;
 #pragma unroll
     for (int q = 0; q < SLOTS; ++q)
       if (ln + G * q == s) my_i[q] = (int)at, my_v[q] = x;
@@ -535,8 +552,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     while (again) {
       const int first = __builtin_ctzll(again);
       again &= again - 1;
-      const int at = route_exact<(G * V + 63) / 64>(a, t0 + first / G,
-                                                    reinterpret_cast<double*>(smem + w * wave_lds));
+      const int at = route_exact(a, t0 + first / G, reinterpret_cast<double*>(smem + w * wave_lds));
 #pragma unroll
       for (int q = 0; q < SLOTS; ++q) {
         const int x = __shfl(at, (ln + G * q) & 63);
@@ -818,7 +834,7 @@ MOE_API int route_forward(const route_plan_t* plan, const float* logits, const f
     if (mode == kByLogit)
       route_forward_kernel<G, V, kByLogit, S><<<grid, kThreads, 0, st>>>(a, vec, per_mul, 0);
     else if (mode == kByScore)
-      route_forward_kernel<G, V, kByScore, S><<<grid, kThreads, 0, st>>>(a, vec, per_mul, 0);
+      route_forward_kernel<G, V, kByScore, S><<<grid, kThreads, kWaves * lds, st>>>(a, vec, per_mul, (int)lds);
     else if (mode == kGrouped)
       route_forward_kernel<G, V, kGrouped, S><<<grid, kThreads, kWaves * lds, st>>>(a, vec, per_mul, (int)lds);
     else
