@@ -210,20 +210,21 @@ size_t route_lds(int E, int n_group) {
   return (std::max(fast, exact) + 15) / 16 * 16;
 }
 
-// G lanes per token, V experts per lane, up to SLOTS slots per lane.
+// G lanes per token, V experts and at most one slot per lane.
 // Measured (logits read once; the copy rate would take 4, 4 and 6 us): 65,536 x
-// 64, k 8: 11.2 us, 420 vector instructions per wave of four tokens, which alone
-// take 11 us; 16,384 x 256 in groups, k 8, biased: 18.3 us, of which one wave's
-// own latency is 5.4; 8192 x 896, k 16: 16.3 us.  Against a wave per token with
-// 64-bit ranks throughout: 120, 50 and 60 us.  k rounds over all experts in the
-// place of candidates: 14.7, 32.8 and 31.2 us.  Lane ln
+// 64, k 8: 9.7 us, 257 vector instructions per wave of four tokens, which alone
+// take 6.7 us; 16,384 x 256 in groups, k 8, biased: 13.2 us, 1,020 a wave, 6.8
+// us, after one wave's own latency of 2 and the loads'; 8192 x 896, k 16: 11.7
+// us, 549 a wave of one token, 7.2 us.  Against a wave per token with 64-bit
+// ranks throughout: 120, 50 and 60 us.  k rounds over all experts in the place
+// of candidates: 14.7, 32.8 and 31.2 us.  Lane ln
 // holds expert (j / 4) 4 G + (vec ? 4 ln + j % 4 : ln + (j % 4) G) as its j-th:
 // ascending in j, and 16 bytes at a time where rows start on 16-byte steps.
-template <int G, int V, int MODE, int SLOTS>
+template <int G, int V, int MODE>
 __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs a, int vec,
                                                                  uint32_t per_mul, int wave_lds) {
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-  __shared__ __attribute__((aligned(16))) uint2 lists[kWaves][SLOTS == 1 ? 64 + 8 : 1];
+  __shared__ __attribute__((aligned(16))) uint2 lists[kWaves][64 + 8];
   constexpr int TPW = 64 / G;
   const float kNone = __builtin_nanf("");  // a rank that nothing takes
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -375,150 +376,146 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     }
   }
 
-  int my_i[SLOTS];
-  float my_v[SLOTS];  // the values they rank by
-#pragma unroll
-  for (int q = 0; q < SLOTS; ++q) my_i[q] = 0, my_v[q] = -INFINITY;
+  int my_i = 0;
+  float my_v = -INFINITY;  // the value it ranks by
   const bool close = MODE != kByLogit && a.bias;  // ranks are scores, not exact
   bool done = false;
-  if constexpr (SLOTS == 1) {
-    // The wanted ranks are among few candidates: with `want` of the lanes'
-    // largest at or above T, so are the `want` largest of all.  T is taken per
-    // row of 16 lanes, from how many of the row's lanes have a larger largest.
-    // The candidates, one a lane, then count those before them.
-    constexpr int ROWS = G / 16;
-    const int want = (a.k + (close ? 1 : 0) + ROWS - 1) / ROWS;
-    if (want <= 16) {
-      float best = -INFINITY;
+  // The wanted ranks are among few candidates: with `want` of the lanes'
+  // largest at or above T, so are the `want` largest of all.  T is taken per
+  // row of 16 lanes, from how many of the row's lanes have a larger largest.
+  // The candidates, one a lane, then count those before them.
+  constexpr int ROWS = G / 16;
+  const int want = (a.k + (close ? 1 : 0) + ROWS - 1) / ROWS;
+  if (want <= 16) {
+    float best = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < V; ++j) best = fmaxf(best, rank[j]);
-      // how many of the row's lanes have more: signs of differences, the lowest
-      // bit left out (a lane too many with that much is as good)
-      const int above = lanes_above(order_of(best) >> 1);
-      // with close, whatever may turn out to be ahead of T belongs to the candidates
-      auto below = [&](float x) __attribute__((always_inline)) {
-        return close && x > -INFINITY ? x - nearness(a.sigmoid, x) : x;
-      };
-      float T = below(run_minf<G>(above < want ? best : INFINITY));
-      // (value, ~expert) of each candidate; larger is earlier
-      uint2* list = lists[w] + sub * (G + 2);
-      int held = 0;
-      auto count_from = [&](float from) __attribute__((always_inline)) {
-        held = 0;
+    for (int j = 0; j < V; ++j) best = fmaxf(best, rank[j]);
+    // how many of the row's lanes have more: signs of differences, the lowest
+    // bit left out (a lane too many with that much is as good)
+    const int above = lanes_above(order_of(best) >> 1);
+    // with close, whatever may turn out to be ahead of T belongs to the candidates
+    auto below = [&](float x) __attribute__((always_inline)) {
+      return close && x > -INFINITY ? x - nearness(a.sigmoid, x) : x;
+    };
+    float T = below(run_minf<G>(above < want ? best : INFINITY));
+    // (value, ~expert) of each candidate; larger is earlier
+    uint2* list = lists[w] + sub * (G + 2);
+    int held = 0;
+    auto count_from = [&](float from) __attribute__((always_inline)) {
+      held = 0;
 #pragma unroll
-        for (int j = 0; j < V; ++j) held += rank[j] >= from ? 1 : 0;
-        return run_sumi<G>(held);
-      };
-      int count = count_from(T);
-      if (__any(count > G)) {
-        // the best sit in few lanes (kept groups do): halve the way from T to
-        // the largest until what is left fits, from the lowest lane's largest if
-        // that will do (-inf is many halvings away)
-        const float some = run_minf<G>(best > -INFINITY ? best : INFINITY);
-        const int with_some = count_from(some);
-        const bool enough = T == -INFINITY && with_some >= want * ROWS;
-        uint32_t low = order_of(enough ? some : T), high = order_of(run_maxf<G>(best)) + 1u;
-        bool open = count > G;
-        for (int i = 0; i < 12 && __any(open); ++i) {
-          const uint32_t mid = low + (high - low) / 2;
-          const int c = count_from(value_of(mid));
-          if (open) {
-            if (c >= want * ROWS) low = mid; else high = mid;
-            open = c < want * ROWS || c >= G;
-          }
+      for (int j = 0; j < V; ++j) held += rank[j] >= from ? 1 : 0;
+      return run_sumi<G>(held);
+    };
+    int count = count_from(T);
+    if (__any(count > G)) {
+      // the best sit in few lanes (kept groups do): halve the way from T to
+      // the largest until what is left fits, from the lowest lane's largest if
+      // that will do (-inf is many halvings away)
+      const float some = run_minf<G>(best > -INFINITY ? best : INFINITY);
+      const int with_some = count_from(some);
+      const bool enough = T == -INFINITY && with_some >= want * ROWS;
+      uint32_t low = order_of(enough ? some : T), high = order_of(run_maxf<G>(best)) + 1u;
+      bool open = count > G;
+      for (int i = 0; i < 12 && __any(open); ++i) {
+        const uint32_t mid = low + (high - low) / 2;
+        const int c = count_from(value_of(mid));
+        if (open) {
+          if (c >= want * ROWS) low = mid; else high = mid;
+          open = c < want * ROWS || c >= G;
         }
-        if (count > G) T = below(value_of(low));
-        count = count_from(T);
       }
-      int at = held;  // inclusive sums over the token's lanes
-      at += row_shr<1>(at);
-      at += row_shr<2>(at);
-      at += row_shr<4>(at);
-      at += row_shr<8>(at);
+      if (count > G) T = below(value_of(low));
+      count = count_from(T);
+    }
+    int at = held;  // inclusive sums over the token's lanes
+    at += row_shr<1>(at);
+    at += row_shr<2>(at);
+    at += row_shr<4>(at);
+    at += row_shr<8>(at);
+    if constexpr (G == 64) {
+      int rows[3];
+#pragma unroll
+      for (int r = 0; r < 3; ++r) rows[r] = __builtin_amdgcn_readlane(at, 16 * r + 15);
+      at += (ln >= 16 ? rows[0] : 0) + (ln >= 32 ? rows[1] : 0) + (ln >= 48 ? rows[2] : 0);
+    }
+    if (!__any(count > G)) {
+      done = true;
+      uint2* to = list + (at - held);
+      const uint32_t last = ~(uint32_t)mine;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if (rank[j] >= T) *to++ = make_uint2(__float_as_uint(rank[j]), last - place(j));
+      if (G == 64 && ln < 8) list[count + ln].x = __float_as_uint(kNone);  // read by eights
+      wave_lds_order();
+      const bool in = ln < count;
+      const uint2 c0 = list[ln];
+      const float x0 = in ? __uint_as_float(c0.x) : -INFINITY;
+      int before = 0;
       if constexpr (G == 64) {
-        int rows[3];
+        const int n = __builtin_amdgcn_readfirstlane(count);
+        for (int c = 0; c < n; c += 8)
 #pragma unroll
-        for (int r = 0; r < 3; ++r) rows[r] = __builtin_amdgcn_readlane(at, 16 * r + 15);
-        at += (ln >= 16 ? rows[0] : 0) + (ln >= 32 ? rows[1] : 0) + (ln >= 48 ? rows[2] : 0);
+          for (int u = 0; u < 4; ++u) {
+            const uint4 q = reinterpret_cast<const uint4*>(list + c)[u];
+            before += __uint_as_float(q.x) > x0 ? 1 : 0;
+            before += __uint_as_float(q.z) > x0 ? 1 : 0;
+          }
+      } else {
+        before = lanes_above(in ? order_of(x0) >> 1 : 0u);
       }
-      if (!__any(count > G)) {
-        done = true;
-        uint2* to = list + (at - held);
-        const uint32_t last = ~(uint32_t)mine;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          if (rank[j] >= T) *to++ = make_uint2(__float_as_uint(rank[j]), last - place(j));
-        if (G == 64 && ln < 8) list[count + ln].x = __float_as_uint(kNone);  // read by eights
-        wave_lds_order();
-        const bool in = ln < count;
-        const uint2 c0 = list[ln];
-        const float x0 = in ? __uint_as_float(c0.x) : -INFINITY;
-        int before = 0;
+      if (__any(run_sumi<G>(in ? before : 0) != count * (count - 1) / 2)) {
+        // equal values (or a lowest bit apart): by value, then expert
+        const uint64_t cand = in ? (uint64_t)order_of(x0) << 32 | c0.y : 0ull;
+        before = 0;
         if constexpr (G == 64) {
           const int n = __builtin_amdgcn_readfirstlane(count);
-          for (int c = 0; c < n; c += 8)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const uint4 q = reinterpret_cast<const uint4*>(list + c)[u];
-              before += __uint_as_float(q.x) > x0 ? 1 : 0;
-              before += __uint_as_float(q.z) > x0 ? 1 : 0;
-            }
+          for (int c = 0; c < n; ++c) {
+            const uint64_t o = (uint64_t)__builtin_amdgcn_readlane((int)(cand >> 32), c) << 32 |
+                               (uint32_t)__builtin_amdgcn_readlane((int)cand, c);
+            before += o > cand ? 1 : 0;
+          }
         } else {
-          before = lanes_above(in ? order_of(x0) >> 1 : 0u);
-        }
-        if (__any(run_sumi<G>(in ? before : 0) != count * (count - 1) / 2)) {
-          // equal values (or a lowest bit apart): by value, then expert
-          const uint64_t cand = in ? (uint64_t)order_of(x0) << 32 | c0.y : 0ull;
-          before = 0;
-          if constexpr (G == 64) {
-            const int n = __builtin_amdgcn_readfirstlane(count);
-            for (int c = 0; c < n; ++c) {
-              const uint64_t o = (uint64_t)__builtin_amdgcn_readlane((int)(cand >> 32), c) << 32 |
-                                 (uint32_t)__builtin_amdgcn_readlane((int)cand, c);
-              before += o > cand ? 1 : 0;
-            }
-          } else {
 #define ROUTE_ROTATE(n)                                                                       \
   before += ((uint64_t)row_ror<n>((uint32_t)(cand >> 32)) << 32 | row_ror<n>((uint32_t)cand)) > cand ? 1 : 0;
-            ROUTE_ROTATE(1) ROUTE_ROTATE(2) ROUTE_ROTATE(3) ROUTE_ROTATE(4) ROUTE_ROTATE(5)
-            ROUTE_ROTATE(6) ROUTE_ROTATE(7) ROUTE_ROTATE(8) ROUTE_ROTATE(9) ROUTE_ROTATE(10)
-            ROUTE_ROTATE(11) ROUTE_ROTATE(12) ROUTE_ROTATE(13) ROUTE_ROTATE(14) ROUTE_ROTATE(15)
+          ROUTE_ROTATE(1) ROUTE_ROTATE(2) ROUTE_ROTATE(3) ROUTE_ROTATE(4) ROUTE_ROTATE(5)
+          ROUTE_ROTATE(6) ROUTE_ROTATE(7) ROUTE_ROTATE(8) ROUTE_ROTATE(9) ROUTE_ROTATE(10)
+          ROUTE_ROTATE(11) ROUTE_ROTATE(12) ROUTE_ROTATE(13) ROUTE_ROTATE(14) ROUTE_ROTATE(15)
 #undef ROUTE_ROTATE
+        }
+      }
+      wave_lds_order();
+      if (in) list[before] = c0;
+      wave_lds_order();
+      uint2 sel = list[ln];
+      if (close) {
+        // in order now: are neighbours that matter too near?
+        const float x = in ? __uint_as_float(sel.x) : -INFINITY;
+        const float y = ln + 1 < count ? __uint_as_float(list[ln + 1].x) : -INFINITY;
+        if (__any(ln < a.k && y > -INFINITY && !(x - y > nearness(a.sigmoid, y)))) {
+          // then all candidates rank by their values in 64 bits
+          double z = 1.0;
+          if (!a.sigmoid) z = softmax_sum64<G>(row, a.E, ln, top);
+          const int e = in ? (int)~c0.y : 0;
+          const float le = row[e];
+          const double s64 = a.sigmoid ? 1.0 / (1.0 + exp(-(double)le)) : exp((double)le - (double)top) / z;
+          const uint64_t o64 = order_of(is_masked(le) ? -(double)INFINITY : s64 + (double)a.bias[e]);
+          before = 0;
+          for (int c = 0; c < G; ++c) {
+            const int from = sub * G + c;
+            const uint64_t o = __shfl(o64, from);
+            const uint32_t oid = __shfl(c0.y, from);
+            before += c < count && (o > o64 || (o == o64 && oid > c0.y)) ? 1 : 0;
           }
+          wave_lds_order();
+          if (in) list[before] = c0;
+          wave_lds_order();
+          sel = list[ln];
         }
-        wave_lds_order();
-        if (in) list[before] = c0;
-        wave_lds_order();
-        uint2 sel = list[ln];
-        if (close) {
-          // in order now: are neighbours that matter too near?
-          const float x = in ? __uint_as_float(sel.x) : -INFINITY;
-          const float y = ln + 1 < count ? __uint_as_float(list[ln + 1].x) : -INFINITY;
-          if (__any(ln < a.k && y > -INFINITY && !(x - y > nearness(a.sigmoid, y)))) {
-            // then all candidates rank by their values in 64 bits
-            double z = 1.0;
-            if (!a.sigmoid) z = softmax_sum64<G>(row, a.E, ln, top);
-            const int e = in ? (int)~c0.y : 0;
-            const float le = row[e];
-            const double s64 = a.sigmoid ? 1.0 / (1.0 + exp(-(double)le)) : exp((double)le - (double)top) / z;
-            const uint64_t o64 = order_of(is_masked(le) ? -(double)INFINITY : s64 + (double)a.bias[e]);
-            before = 0;
-            for (int c = 0; c < G; ++c) {
-              const int from = sub * G + c;
-              const uint64_t o = __shfl(o64, from);
-              const uint32_t oid = __shfl(c0.y, from);
-              before += c < count && (o > o64 || (o == o64 && oid > c0.y)) ? 1 : 0;
-            }
-            wave_lds_order();
-            if (in) list[before] = c0;
-            wave_lds_order();
-            sel = list[ln];
-          }
-        }
-        if (ln < a.k) {
-          my_i[0] = (int)~sel.y;
-          my_v[0] = __uint_as_float(sel.x);
-        }
+      }
+      if (ln < a.k) {
+        my_i = (int)~sel.y;
+        my_v = __uint_as_float(sel.x);
       }
     }
   }
@@ -542,9 +539,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
 #pragma unroll
     for (int j = 0; j < V; ++j)
       if ((int)mine_at == place(j)) rank[j] = kNone;
-#pragma unroll
-    for (int q = 0; q < SLOTS; ++q)
-      if (ln + G * q == s) my_i[q] = (int)at, my_v[q] = x;
+    if (ln == s) my_i = (int)at, my_v = x;
   }
   bool by_logit = MODE == kByLogit || !a.bias;  // my_v holds logits
   if constexpr (MODE != kByLogit) {
@@ -553,57 +548,32 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
       const int first = __builtin_ctzll(again);
       again &= again - 1;
       const int at = route_exact(a, t0 + first / G, reinterpret_cast<double*>(smem + w * wave_lds));
-#pragma unroll
-      for (int q = 0; q < SLOTS; ++q) {
-        const int x = __shfl(at, (ln + G * q) & 63);
-        if (sub == first / G) my_i[q] = x;
-      }
+      const int mine_at = __shfl(at, ln);
+      if (sub == first / G) my_i = mine_at;
       by_logit = false;
     }
   }
 
-  // gates, lane ln for slots ln + G q
-  float ls[SLOTS], g[SLOTS], m = -INFINITY;
-#pragma unroll
-  for (int q = 0; q < SLOTS; ++q) {
-    ls[q] = -INFINITY;
-    if (ln + G * q < a.k) {
-      ls[q] = by_logit ? my_v[q] : row[my_i[q]];
-      if (is_masked(ls[q])) ls[q] = -INFINITY;
-    }
-    m = fmaxf(m, ls[q]);
-  }
+  // gates, lane ln for slot ln
+  const bool slot = ln < a.k;
+  const float ls = !slot ? -INFINITY : fmaxf(by_logit ? my_v : row[my_i], -INFINITY);
+  float g;
   if (a.renorm) {
     // scores relative to the largest one selected: no sum underflows
-    m = run_maxf<G>(m);
+    const float m = run_maxf<G>(ls);
     const float c = a.sigmoid ? fminf(m, 0.f) : m;
-    float sum = 0.f;
-#pragma unroll
-    for (int q = 0; q < SLOTS; ++q) {
-      g[q] = 0.f;
-      if (ls[q] > -INFINITY)
-        g[q] = a.sigmoid ? sigmoid_rel(ls[q], c, nullptr) : __expf(ls[q] - c);
-      sum += g[q];
-    }
-    sum = run_sum<G>(sum);
-    const float f = sum > 0.f ? a.scale * rcp(sum) : 0.f;
-#pragma unroll
-    for (int q = 0; q < SLOTS; ++q) g[q] *= f;
+    g = 0.f;
+    if (ls > -INFINITY) g = a.sigmoid ? sigmoid_rel(ls, c, nullptr) : __expf(ls - c);
+    const float sum = run_sum<G>(g);
+    g *= sum > 0.f ? a.scale * rcp(sum) : 0.f;
+  } else if (a.sigmoid) {
+    g = a.scale * sigmoid_rel(ls, 0.f, nullptr);
   } else {
-#pragma unroll
-    for (int q = 0; q < SLOTS; ++q) {
-      if (a.sigmoid)
-        g[q] = a.scale * sigmoid_rel(ls[q], 0.f, nullptr);
-      else
-        g[q] = ls[q] > -INFINITY ? a.scale * (__expf(ls[q] - top) * inv_z) : 0.f;
-    }
+    g = ls > -INFINITY ? a.scale * (__expf(ls - top) * inv_z) : 0.f;
   }
-#pragma unroll
-  for (int q = 0; q < SLOTS; ++q) {
-    if (valid && ln + G * q < a.k) {
-      a.idx[t * a.k + ln + G * q] = my_i[q];
-      a.gates[t * a.k + ln + G * q] = g[q];
-    }
+  if (valid && slot) {
+    a.idx[t * a.k + ln] = my_i;
+    a.gates[t * a.k + ln] = g;
   }
 }
 
@@ -620,10 +590,9 @@ struct RouteBwdArgs {
 // Writing the row of dlogits bounds it: 65,536 x 64 takes 6.9 us (2.4 TB/s
 // written), 16,384 x 256 5.6 us (3.0), 8192 x 896 with the dense part 9.0 us
 // (3.3, as much read).  G lanes per token as in the forward pass: lane ln works
-// out the shares of
-// slots ln + G q, the row goes through LDS (zeros or the softmax's dense part,
-// then the selected experts' shares added) and out.
-template <int G, int V, int SLOTS>
+// out slot ln's share, the row goes through LDS (zeros or the softmax's dense
+// part, then the selected experts' shares added) and out.
+template <int G, int V>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteBwdArgs a, int vec) {
   constexpr int TPW = 64 / G;
   __shared__ __attribute__((aligned(16))) float rows[kWaves * TPW][G * V];
@@ -638,24 +607,16 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteBwd
   const int mine = vec ? 4 * ln : ln, step = vec ? 1 : G;
   auto place = [&](int j) { return (j / 4) * 4 * G + (j % 4) * step; };
 
-  int e[SLOTS];
-  float ls[SLOTS], dg[SLOTS], wgt[SLOTS], one_less[SLOTS], m = -INFINITY;
-#pragma unroll
-  for (int q = 0; q < SLOTS; ++q) {
-    e[q] = -1;
-    ls[q] = -INFINITY;
-    dg[q] = 0.f;
-    if (ln + G * q < a.k) {
-      e[q] = a.idx[t * a.k + ln + G * q];
-      dg[q] = a.dgates[t * a.k + ln + G * q];
-      if ((unsigned)e[q] < (unsigned)a.E) ls[q] = row[e[q]];
-      if (is_masked(ls[q])) {  // a gate fixed at 0
-        ls[q] = -INFINITY;
-        e[q] = -1;
-        dg[q] = 0.f;
-      }
+  int e = -1;
+  float ls = -INFINITY, dg = 0.f;
+  if (ln < a.k) {
+    const int at = a.idx[t * a.k + ln];
+    const float up = a.dgates[t * a.k + ln];
+    if ((unsigned)at < (unsigned)a.E) ls = fmaxf(row[at], -INFINITY);
+    if (ls > -INFINITY) {  // else a gate fixed at 0
+      e = at;
+      dg = up;
     }
-    m = fmaxf(m, ls[q]);
   }
   const bool dense = !a.sigmoid && !a.renorm;
   float l[V], top = -INFINITY, inv_z = 0.f;
@@ -687,36 +648,21 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteBwd
     z = run_sum<G>(z);
     inv_z = z > 0.f ? 1.f / z : 0.f;
   }
-  // w_s = g_s / scale
+  float w_s, one_less = 0.f;  // g_s / scale, 1 - s
   if (a.renorm) {
-    m = run_maxf<G>(m);
+    const float m = run_maxf<G>(ls);
     const float c = a.sigmoid ? fminf(m, 0.f) : m;
-    float sum = 0.f;
-#pragma unroll
-    for (int q = 0; q < SLOTS; ++q) {
-      wgt[q] = a.sigmoid ? sigmoid_rel(ls[q], c, &one_less[q]) : __expf(ls[q] - c);
-      if (e[q] < 0) wgt[q] = 0.f;
-      sum += wgt[q];
-    }
-    sum = run_sum<G>(sum);
-    const float f = sum > 0.f ? rcp(sum) : 0.f;
-#pragma unroll
-    for (int q = 0; q < SLOTS; ++q) wgt[q] *= f;
+    w_s = a.sigmoid ? sigmoid_rel(ls, c, &one_less) : __expf(ls - c);
+    if (e < 0) w_s = 0.f;
+    const float sum = run_sum<G>(w_s);
+    w_s *= sum > 0.f ? rcp(sum) : 0.f;
+  } else if (a.sigmoid) {
+    w_s = sigmoid_rel(ls, 0.f, &one_less);
   } else {
-#pragma unroll
-    for (int q = 0; q < SLOTS; ++q) {
-      if (a.sigmoid)
-        wgt[q] = sigmoid_rel(ls[q], 0.f, &one_less[q]);
-      else
-        wgt[q] = e[q] >= 0 ? __expf(ls[q] - top) * inv_z : 0.f;
-    }
+    w_s = e >= 0 ? __expf(ls - top) * inv_z : 0.f;
   }
   float dot = 0.f;  // sum_j g_j dg_j
-  if (!a.sigmoid || a.renorm) {
-#pragma unroll
-    for (int q = 0; q < SLOTS; ++q) dot = fmaf(wgt[q], dg[q], dot);
-    dot = a.scale * run_sum<G>(dot);
-  }
+  if (!a.sigmoid || a.renorm) dot = a.scale * run_sum<G>(w_s * dg);
 #pragma unroll
   for (int j = 0; j < V; j += 4) {
     f32x4_t q{0.f, 0.f, 0.f, 0.f};
@@ -731,13 +677,10 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteBwd
     }
   }
   wave_lds_order();
-#pragma unroll
-  for (int q = 0; q < SLOTS; ++q) {
-    if (e[q] >= 0) {
-      float d = wgt[q] * (a.scale * dg[q] - (dense ? 0.f : dot));
-      if (a.sigmoid) d *= one_less[q];
-      out[e[q]] += d;
-    }
+  if (e >= 0) {
+    float d = w_s * (a.scale * dg - (dense ? 0.f : dot));
+    if (a.sigmoid) d *= one_less;
+    out[e] += d;
   }
   wave_lds_order();
   if (!valid) return;
@@ -754,22 +697,21 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const RouteBwd
   }
 }
 
-// Calls f with lanes per token, experts per lane and slots per lane: the fewest
-// lanes that hold the experts, 16 each at most (what keeps the registers of a
-// lane to half a SIMD's), and slots for k.
+// Calls f with lanes per token and experts per lane, for a selection among the
+// `wanted` largest.  A row of 16 lanes while 16 experts each (what keeps a lane
+// to a fifth of a SIMD's registers) and one slot each do; a wave past that:
+// 20,000 x 250, k 32 takes 16.4 us so and took 35.6 with four slots a lane in k
+// rounds, k 16 with a bias 25 and 42.
 template <typename F>
-void with_shape(int E, int k, F f) {
+void with_shape(int E, int wanted, F f) {
   using std::integral_constant;
-#define ROUTE_SHAPE(g, v, s) f(integral_constant<int, g>(), integral_constant<int, v>(), integral_constant<int, s>())
-  if (E > 512) return ROUTE_SHAPE(64, 16, 1);
-  if (E > 256) return ROUTE_SHAPE(64, 8, 1);
-  if (k > 16) {
-    if (E > 64) return ROUTE_SHAPE(16, 16, 4);
-    return ROUTE_SHAPE(16, 4, 4);
-  }
-  if (E > 128) return ROUTE_SHAPE(16, 16, 1);
-  if (E > 64) return ROUTE_SHAPE(16, 8, 1);
-  return ROUTE_SHAPE(16, 4, 1);
+#define ROUTE_SHAPE(g, v) f(integral_constant<int, g>(), integral_constant<int, v>())
+  if (E > 512) return ROUTE_SHAPE(64, 16);
+  if (E > 256) return ROUTE_SHAPE(64, 8);
+  if (wanted > 16) return ROUTE_SHAPE(64, 4);
+  if (E > 128) return ROUTE_SHAPE(16, 16);
+  if (E > 64) return ROUTE_SHAPE(16, 8);
+  return ROUTE_SHAPE(16, 4);
 #undef ROUTE_SHAPE
 }
 
@@ -827,18 +769,18 @@ MOE_API int route_forward(const route_plan_t* plan, const float* logits, const f
   // e / per as a product: exact for e < 1024, per < 1024
   const int per = P.E / P.n_group / (mode == kQuads ? 4 : 1);
   const uint32_t per_mul = ((1u << 20) + per - 1) / per;
-  with_shape(P.E, P.k, [&](auto g, auto v, auto s) {
-    constexpr int G = g.value, V = v.value, S = s.value;
+  with_shape(P.E, P.k + (bias ? 1 : 0), [&](auto g, auto v) {
+    constexpr int G = g.value, V = v.value;
     const unsigned grid = (unsigned)ceil_div(P.N, kWaves * (64 / G));
     const size_t lds = route_lds<G>(P.E, P.n_group);
     if (mode == kByLogit)
-      route_forward_kernel<G, V, kByLogit, S><<<grid, kThreads, 0, st>>>(a, vec, per_mul, 0);
+      route_forward_kernel<G, V, kByLogit><<<grid, kThreads, 0, st>>>(a, vec, per_mul, 0);
     else if (mode == kByScore)
-      route_forward_kernel<G, V, kByScore, S><<<grid, kThreads, kWaves * lds, st>>>(a, vec, per_mul, (int)lds);
+      route_forward_kernel<G, V, kByScore><<<grid, kThreads, kWaves * lds, st>>>(a, vec, per_mul, (int)lds);
     else if (mode == kGrouped)
-      route_forward_kernel<G, V, kGrouped, S><<<grid, kThreads, kWaves * lds, st>>>(a, vec, per_mul, (int)lds);
+      route_forward_kernel<G, V, kGrouped><<<grid, kThreads, kWaves * lds, st>>>(a, vec, per_mul, (int)lds);
     else
-      route_forward_kernel<G, V, kQuads, S><<<grid, kThreads, kWaves * lds, st>>>(a, 1, per_mul, (int)lds);
+      route_forward_kernel<G, V, kQuads><<<grid, kThreads, kWaves * lds, st>>>(a, 1, per_mul, (int)lds);
   });
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
 }
@@ -853,10 +795,10 @@ MOE_API int route_backward(const route_plan_t* plan, const float* logits, const 
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
   const int vec = rows_aligned(P.E, logits, dlogits);
-  with_shape(P.E, P.k, [&](auto g, auto v, auto s) {
-    constexpr int G = g.value, V = v.value, S = s.value;
+  with_shape(P.E, P.k, [&](auto g, auto v) {
+    constexpr int G = g.value, V = v.value;
     const unsigned grid = (unsigned)ceil_div(P.N, kWaves * (64 / G));
-    route_backward_kernel<G, V, S><<<grid, kThreads, 0, st>>>(a, vec);
+    route_backward_kernel<G, V><<<grid, kThreads, 0, st>>>(a, vec);
   });
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
 }

@@ -27,7 +27,8 @@ SHAPES = [
     (64, 64, 64, 1, 1, 1), (333, 256, 8, 8, 4, 2), (130, 1000, 32, 8, 3, 2),
     (77, 1024, 64, 64, 16, 2), (257, 896, 16, 1, 1, 1), (100, 72, 3, 24, 5, 1),
     (50, 16, 3, 16, 4, 2), (1001, 128, 8, 1, 1, 1), (19, 320, 5, 2, 1, 2), (21, 513, 4, 3, 2, 2),
-    (37, 260, 17, 1, 1, 1),
+    (37, 260, 17, 1, 1, 1), (90, 250, 32, 1, 1, 1), (33, 100, 40, 1, 1, 1), (41, 40, 33, 1, 1, 1),
+    (29, 256, 48, 8, 4, 2), (23, 192, 64, 6, 3, 2), (31, 128, 16, 1, 1, 1), (35, 128, 17, 1, 1, 1),
 ]
 
 
