@@ -261,8 +261,8 @@ int strip_cols(int64_t V, int strip) {
 
 // The backward pass's strips: v_chunk, times what KD_STRIP_BYTES leaves (and
 // 32-bit offsets into W), evened out over the vocabulary.  777 x 512 x 20,000 at
-// v_chunk 4096 takes 167 us so and 348 with strips of v_chunk, 100 x 2048 x 50,000
-// 260 and 1,101, 2000 x 2048 x 50,000 1,770 and 2,329.
+// v_chunk 4096 takes 159 us so and 342 with strips of v_chunk, 100 x 2048 x 50,000
+// 256 and 1,075, 2000 x 2048 x 50,000 1,731 and 2,296.
 int strip_of(int64_t N, int64_t V, int H, int v_chunk) {
   const int64_t cols = ceil_div(V, 256) * 256;
   const int64_t most = std::min<int64_t>((int64_t)KD_STRIP_BYTES / 2 / std::max<int64_t>(N, 1),
@@ -284,7 +284,7 @@ int forward_strip(int64_t N, int64_t V, int H) {
 // dX's ranges: with fewer than 256 tiles of dX, as many sums side by side as
 // fill the CUs once, each range at least 512 entries (16 K-tiles).  Depends on
 // N, H and V alone, so dX does not depend on the strips.  The passes above take
-// 488, 775 and 2,238 us with one sum.
+// 481, 776 and 2,176 us with one sum.
 struct DxRanges {
   int range, slots;
 };

@@ -12,16 +12,22 @@ namespace {
 // 128-column vocabulary slice of the statistics.
 using Logit = Shape<256, 256, 4, 2, 32, 1>;
 using LogitFew = Shape<128, 256, 2, 2, 32, 2>;
+// For up to 64 tokens, where reading W bounds the product and half the columns
+// a tile keep twice the CUs busy: whole passes of 47 x 3456 x 8123 take 97 us so
+// and 147 us with LogitFew, of 16 x 4096 x 100,000 772 and 795 us (100 x 2048 x
+// 50,000: 284 and 256 us).
+using LogitThin = Shape<64, 128, 4, 1, 64, 2>;
 static_assert(Logit::BN / Logit::WGN == kCceSlice, "statistics slice = one wave's columns");
 static_assert(LogitFew::BN / LogitFew::WGN == kCceSlice, "statistics slice = one wave's columns");
+static_assert(LogitThin::BN / LogitThin::WGN == kCceSlice, "statistics slice = one wave's columns");
 
 // Whether 128-row tiles, two per CU, finish before 256-row tiles, one per CU:
 // in rounds of the chip, where a CU left with one 128-row tile needs half of
 // one, and the smaller tiles take a tenth longer for the same products.  They
 // win where a last round of 256-row tiles is mostly empty, and for batches of
-// up to 128 tokens: whole passes of 777 x 512 x 20,000 take 167 us so and 175
-// us with 256-row tiles, of 16 x 4096 x 100,000 802 and 839 us, but of 1000 x
-// 4096 x 30,000 (1.8 full rounds) 1,106 and 1,021 us.
+// up to 128 tokens: whole passes of 777 x 512 x 20,000 take 158 us so and 168
+// us with 256-row tiles, of 2000 x 2048 x 50,000 (forward strips) 1,731 and
+// 1,753 us, but of 1000 x 4096 x 30,000 (1.8 full rounds) 1,098 and 1,004 us.
 bool few_tiles(int64_t t256, int64_t t128) {
   if (t256 >= 4 * kCus) return false;
   const int64_t rest = t128 % (2 * kCus);
@@ -95,18 +101,23 @@ hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, i
   p.B = Ws; p.ldb = H;
   p.M = (int)N; p.N = w; p.K = H;
   p.ce_scale = inv_t;
-  const dim3 grid((unsigned)ceil_div(N, Logit::BM), (unsigned)ceil_div(w, Logit::BN));
-  const dim3 grid2((unsigned)ceil_div(N, LogitFew::BM), grid.y);
-  const bool few = few_tiles((int64_t)grid.x * grid.y, (int64_t)grid2.x * grid2.y);
   if (!grad) {
     p.ce_pmax = pmax; p.ce_psum = psum;
-    return few ? launch_lds<Mode::Dense, LogitFew, false, true, true, false, Epi::KDStats>(p, grid2, st)
-               : launch_lds<Mode::Dense, Logit, false, true, true, false, Epi::KDStats>(p, grid, st);
+  } else {
+    p.ce_lse = lse; p.ce_dl = dl;
+    p.C = G; p.ldc = ldg;
   }
-  p.ce_lse = lse; p.ce_dl = dl;
-  p.C = G; p.ldc = ldg;
-  return few ? launch_lds<Mode::Dense, LogitFew, false, true, true, false, Epi::KDGrad>(p, grid2, st)
-             : launch_lds<Mode::Dense, Logit, false, true, true, false, Epi::KDGrad>(p, grid, st);
+  const unsigned cols = (unsigned)ceil_div(w, 256);  // the statistics and G go to whole 256 columns
+  const dim3 grid((unsigned)ceil_div(N, Logit::BM), cols), few((unsigned)ceil_div(N, LogitFew::BM), cols);
+  const dim3 thin((unsigned)ceil_div(N, LogitThin::BM), 2 * cols);
+  auto run = [&](auto shape, dim3 g) {
+    using S = decltype(shape);
+    return grad ? launch_lds<Mode::Dense, S, false, true, true, false, Epi::KDGrad>(p, g, st)
+                : launch_lds<Mode::Dense, S, false, true, true, false, Epi::KDStats>(p, g, st);
+  };
+  if (N <= LogitThin::BM) return run(LogitThin(), thin);
+  if (few_tiles((int64_t)grid.x * grid.y, (int64_t)few.x * few.y)) return run(LogitFew(), few);
+  return run(Logit(), grid);
 }
 
 hipError_t gemm_kd_dx(const void* G, int ldg, const void* Ws, int64_t N, int H, int w, int64_t v0,
@@ -146,11 +157,17 @@ hipError_t gemm_kd_dw_bf16(const void* G, int ldg, const void* X, int64_t N, int
   p.C = dws; p.ldc = H;
   p.M = w; p.N = H; p.K = (int)N;
   p.tile_group = kCceDwGroup;  // as gemm_cce_dw
-  const int bn = H % 256 == 0 ? 256 : 128;
+  // Few tokens: writing dW bounds it, and three small work-groups a CU write
+  // more steadily (whole passes of 16 x 4096 x 100,000 755 and 774 us, 333 x
+  // 2048 x 50,000 448 and 454, but 1000 x 4096 x 30,000 1,016 and 1,001).  Where H
+  // is no multiple of 256 they do for any number (one 512-thread work-group a CU
+  // instead: 16 x 4224 x 100,000 726 and 915 us, 4000 x 4224 x 20,000 2,736 and
+  // 2,896).
+  const int bn = H % 256 == 0 && N > 512 ? 256 : 128;
   const dim3 grid((unsigned)ceil_div(w, 128), (unsigned)(H / bn), 1u);
   if (bn == 256)
     return launch_lds<Mode::Expert, Shape<128, 256, 2, 2, 32, 2>, false, false, false, false, Epi::Store>(p, grid, st);
-  return launch_lds<Mode::Expert, Shape<128, 128, 2, 4, 64, 1>, false, false, false, false, Epi::Store>(p, grid, st);
+  return launch_lds<Mode::Expert, Shape<128, 128, 2, 2, 32, 3>, false, false, false, false, Epi::Store>(p, grid, st);
 }
 
 }  // namespace moe

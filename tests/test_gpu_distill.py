@@ -95,7 +95,8 @@ def check(c, v_chunk, T, name=""):
 
 # N, H, V, v_chunk, K, T
 SIZES = [(1, 128, 100, 256, 1, 1.0), (300, 256, 257, 256, 4, 2.0), (64, 384, 3000, 512, 64, 0.5),
-         (17, 128, 300, 256, 256, 4.0), (5, 128, 1, 256, 2, 1.0), (257, 640, 1000, 1024, 70, 1.0)]
+         (17, 128, 300, 256, 256, 4.0), (5, 128, 1, 256, 2, 1.0), (257, 640, 1000, 1024, 70, 1.0),
+         (65, 256, 1300, 512, 9, 1.5), (512, 256, 700, 256, 3, 1.0), (513, 512, 900, 512, 8, 1.0)]
 
 
 @pytest.mark.parametrize("size", SIZES, ids=lambda s: "x".join(map(str, s)))
