@@ -85,14 +85,17 @@ __device__ __forceinline__ void fold(float a, float b, float& m, float& z) {
 }
 
 // Folds a strip's slice pairs into the running state (m, z).  A work-group takes
-// 16 tokens, 16 threads each: every thread folds each 16th slice in order, then
-// one thread a token its state and the 16 results in order.  The last strip
-// finishes lse.  Latency bounds it: 64 slices of 8192 tokens 5.1 us, 158 of 777
-// tokens 5.6 us (16.5 with one thread a token).
-constexpr int kFoldTokens = 16, kFoldWays = kThreads / kFoldTokens, kFoldAhead = 4;
+// 16 tokens (4 of up to kFoldFew), the threads of a token each fold every so
+// many-th slice in order, then one thread a token its state and their results
+// in order.  The last strip finishes lse.  Latency bounds it: 64 slices of 8192
+// tokens 5.1 us, 158 of 777 tokens 5.6 us (16.5 with one thread a token), 1168
+// of 21 tokens 10.6 us (16.4 by 16).
+constexpr int kFoldAhead = 4, kFoldFew = 256;
+template <int kFoldTokens>
 __global__ __launch_bounds__(kThreads) void kd_fold_kernel(
     const float* __restrict__ pmax, const float* __restrict__ psum, int nslices, int64_t N,
     float* __restrict__ m, float* __restrict__ z, int first, int last, float* __restrict__ lse) {
+  constexpr int kFoldWays = kThreads / kFoldTokens;
   __shared__ float ms[kFoldWays][kFoldTokens], zs[kFoldWays][kFoldTokens];
   const int i = threadIdx.x % kFoldTokens, way = threadIdx.x / kFoldTokens;
   const int64_t t = (int64_t)blockIdx.x * kFoldTokens + i, tc = min(t, N - 1);
@@ -115,7 +118,7 @@ __global__ __launch_bounds__(kThreads) void kd_fold_kernel(
   if (way != 0 || t >= N) return;
   mm = first ? -INFINITY : m[t];
   zz = first ? 0.f : z[t];
-#pragma unroll
+#pragma unroll 16
   for (int v = 0; v < kFoldWays; ++v) fold(ms[v][i], zs[v][i], mm, zz);
   if (last) {
     lse[t] = mm + logf(zz);
@@ -402,8 +405,11 @@ MOE_API int kd_forward(const kd_plan_t* plan, const void* X, const void* W, cons
     KD_CHECK(gemm_kd_logits(false, X, (const bf16_t*)W + v0 * P.H, P.N, P.H, w, 1.f / P.temperature,
                             pmax, psum, nullptr, nullptr, nullptr, 0, st));
     const int nsl = (int)ceil_div(w, 256) * (256 / kCceSlice);
-    kd_fold_kernel<<<(unsigned)ceil_div(P.N, kFoldTokens), kThreads, 0, st>>>(
-        pmax, psum, nsl, P.N, (float*)(ws + L.m), (float*)(ws + L.z), v0 == 0, v0 + w == P.V, lse);
+    auto fold = [&](auto kern, int tokens) {
+      kern<<<(unsigned)ceil_div(P.N, tokens), kThreads, 0, st>>>(pmax, psum, nsl, P.N, (float*)(ws + L.m),
+                                                                 (float*)(ws + L.z), v0 == 0, v0 + w == P.V, lse);
+    };
+    P.N <= kFoldFew ? fold(kd_fold_kernel<4>, 4) : fold(kd_fold_kernel<16>, 16);
     KD_CHECK(hipGetLastError());
   }
   kd_loss_kernel<<<(unsigned)P.N, kThreads, 0, st>>>(kd_args(P, X, W, t_idx, t_logit, lse), loss,

@@ -12,10 +12,11 @@ namespace {
 // 128-column vocabulary slice of the statistics.
 using Logit = Shape<256, 256, 4, 2, 32, 1>;
 using LogitFew = Shape<128, 256, 2, 2, 32, 2>;
-// For up to 64 tokens, where reading W bounds the product and half the columns
-// a tile keep twice the CUs busy: whole passes of 47 x 3456 x 8123 take 97 us so
-// and 147 us with LogitFew, of 16 x 4096 x 100,000 772 and 795 us (100 x 2048 x
-// 50,000: 284 and 256 us).
+// For up to 64 tokens, where reading W bounds the product, and where the whole
+// product is one round of it, two a CU, whose steps along K take half as long:
+// whole passes of 47 x 3456 x 8123 take 97 us so and 147 us with LogitFew, of 16
+// x 4096 x 100,000 772 and 795 us, of 500 x 2048 x 2000 77 and 114 us, but of
+// 100 x 2048 x 50,000 (1.5 rounds) 284 and 256 us.
 using LogitThin = Shape<64, 128, 4, 1, 64, 2>;
 static_assert(Logit::BN / Logit::WGN == kCceSlice, "statistics slice = one wave's columns");
 static_assert(LogitFew::BN / LogitFew::WGN == kCceSlice, "statistics slice = one wave's columns");
@@ -115,7 +116,7 @@ hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, i
     return grad ? launch_lds<Mode::Dense, S, false, true, true, false, Epi::KDGrad>(p, g, st)
                 : launch_lds<Mode::Dense, S, false, true, true, false, Epi::KDStats>(p, g, st);
   };
-  if (N <= LogitThin::BM) return run(LogitThin(), thin);
+  if (N <= LogitThin::BM || (int64_t)thin.x * thin.y <= 2 * kCus) return run(LogitThin(), thin);
   if (few_tiles((int64_t)grid.x * grid.y, (int64_t)few.x * few.y)) return run(LogitFew(), few);
   return run(Logit(), grid);
 }
