@@ -202,14 +202,20 @@ __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_forward_kernel(
   }
 }
 
-// part: [work-group][2][H], its rows' shares of dgamma and dbeta.  Measured:
+// Where work-group g's rows' shares of dgamma and dbeta go: g 2H floats past
+// these.  One work-group writes dgamma and dbeta themselves.
+struct Slabs {
+  float *dgamma, *dbeta;
+};
+
+// Measured:
 // 65,536 x 2048 bf16 160 us, 5.0 TB/s (the copy rate); 8192 x 7168 86 us, 4.1
 // TB/s, 16 rows a work-group, two work-groups a CU and a barrier a row.
 template <typename T, int W, int C, bool TAIL>
 __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_backward_kernel(
     const T* __restrict__ X, const float* __restrict__ gamma, const T* dY,
     const float* __restrict__ mean, const float* __restrict__ rstd, T* dX,
-    float* __restrict__ part, int64_t N, int H) {
+    const Slabs part, int64_t N, int H) {
   using Part = RowPart<T, W, C, TAIL>;
   constexpr int EPC = Part::EPC;
   constexpr int RPG = kGroup<W> / (64 * W);
@@ -279,7 +285,8 @@ __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_backward_kernel(
       r = r2;
     }
   }
-  float* pg = part + (int64_t)blockIdx.x * 2 * H;
+  float* pg = part.dgamma + (int64_t)blockIdx.x * 2 * H;
+  float* pb = part.dbeta + (int64_t)blockIdx.x * 2 * H;
   if constexpr (RPG == 1) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -288,7 +295,7 @@ __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_backward_kernel(
       for (int e = 0; e < EPC; ++e)
         if (at + e < H) {
           pg[at + e] = dg[c * EPC + e];
-          pg[H + at + e] = db[c * EPC + e];
+          pb[at + e] = db[c * EPC + e];
         }
     }
   } else {
@@ -308,7 +315,7 @@ __global__ __launch_bounds__(kGroup<W>) void lnorm_rows_backward_kernel(
     }
     for (int h = threadIdx.x; h < H; h += kThreads) {
       pg[h] = sum[0][h];
-      pg[H + h] = sum[1][h];
+      pb[h] = sum[1][h];
     }
   }
 }
@@ -338,15 +345,14 @@ __global__ __launch_bounds__(kThreads) void lnorm_forward_kernel(
   }
 }
 
-// part: [slab][2][H], this slab's shares of dgamma and dbeta.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void lnorm_backward_kernel(
     const T* __restrict__ X, const float* __restrict__ gamma, const T* dY,
     const float* __restrict__ mean, const float* __restrict__ rstd, T* dX,
-    float* __restrict__ part, int64_t N, int H) {
+    const Slabs part, int64_t N, int H) {
   __shared__ float red[kThreads / 64];
-  float* pg = part + (int64_t)blockIdx.x * 2 * H;
-  float* pb = pg + H;
+  float* pg = part.dgamma + (int64_t)blockIdx.x * 2 * H;
+  float* pb = part.dbeta + (int64_t)blockIdx.x * 2 * H;
   for (int h = threadIdx.x; h < H; h += kThreads) pg[h] = pb[h] = 0.f;
   for (int64_t t = blockIdx.x; t < N; t += gridDim.x) {
     const T* x = X + t * H;
@@ -418,10 +424,21 @@ Holding holding(const lnorm_plan_t& P) {
 int rows_per_group(int W) { return W == 1 ? kThreads / 64 : 1; }
 int waves_per_group(int W) { return W == 1 ? kThreads / 64 : W; }
 
-// Work-groups of a pass over the rows (the backward pass's slabs).
+// Work-groups of a pass over the rows.
 int row_groups(int64_t N, int W) {
   if (W == 0) return (int)std::min<int64_t>(N, 512);
   return (int)std::min<int64_t>(ceil_div(N, rows_per_group(W)), std::max(256, kRowWaves / waves_per_group(W)));
+}
+
+// The backward pass's work-groups.  Up to kAloneRounds rows a wave (a work-group
+// of several waves a row) stay with one: another round costs it less than the
+// fold's launch (calls on 16 x 512 fp32 13.7 us so and 16.3 with the fold, on 4
+// x 4096 bf16 13.7 and 16.8; 8 rounds take longer than it at 8 x 4096, 17.5 and
+// 16.3).
+constexpr int kAloneRounds = 4;
+int slab_count(int64_t N, int W) {
+  if (W != 0 && N <= kAloneRounds * rows_per_group(W)) return 1;
+  return row_groups(N, W);
 }
 
 // Calls f with the holding, and whether a row's last vector is short, as
@@ -468,10 +485,10 @@ hipError_t run_forward(const lnorm_plan_t& P, const void* X, const float* gamma,
 
 template <typename T>
 hipError_t run_backward(const lnorm_plan_t& P, const void* X, const float* gamma, const void* dY,
-                        const float* mean, const float* rstd, void* dX, float* part, int* slabs,
+                        const float* mean, const float* rstd, void* dX, Slabs part, int slabs,
                         hipStream_t st) {
   const Holding h = holding(P);
-  const int grid = *slabs = row_groups(P.N, h.W);
+  const int grid = slabs;
   if (h.W == 0) {
     lnorm_backward_kernel<T><<<grid, kThreads, 0, st>>>((const T*)X, gamma, (const T*)dY, mean, rstd,
                                                         (T*)dX, part, P.N, P.H);
@@ -532,14 +549,16 @@ MOE_API int lnorm_backward(const lnorm_plan_t* plan, const void* X, const float*
   if (workspace_bytes < (size_t)P.bwd_workspace_bytes) return MOE_EWORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
-  int slabs = 0;
+  const int slabs = P.N > 0 ? slab_count(P.N, holding(P).W) : 0;
   float* part = (float*)workspace;
   if (P.N > 0) {
+    const Slabs to = slabs == 1 ? Slabs{dgamma, dbeta ? dbeta : part} : Slabs{part, part + P.H};
     const hipError_t err =
         P.dtype == MOE_BF16
-            ? run_backward<bf16_t>(P, X, gamma, dY, mean, rstd, dX, part, &slabs, st)
-            : run_backward<float>(P, X, gamma, dY, mean, rstd, dX, part, &slabs, st);
+            ? run_backward<bf16_t>(P, X, gamma, dY, mean, rstd, dX, to, slabs, st)
+            : run_backward<float>(P, X, gamma, dY, mean, rstd, dX, to, slabs, st);
     if (err != hipSuccess) return MOE_EHIP;
+    if (slabs == 1) return MOE_OK;
   }
   lnorm_fold_kernel<<<(unsigned)ceil_div(2 * (int64_t)P.H, 64), 64 * kFoldWaves, 0, st>>>(
       part, slabs, P.H, dgamma, dbeta);
