@@ -85,17 +85,13 @@ __device__ __forceinline__ void fold(float a, float b, float& m, float& z) {
 }
 
 // Folds a strip's slice pairs into the running state (m, z).  A work-group takes
-// 16 tokens (4 of up to kFoldFew), the threads of a token each fold every so
-// many-th slice in order, then one thread a token its state and their results
-// in order.  The last strip finishes lse.  Latency bounds it: 64 slices of 8192
-// tokens 5.1 us, 158 of 777 tokens 5.6 us (16.5 with one thread a token), 1168
-// of 21 tokens 10.6 us (16.4 by 16).
-constexpr int kFoldAhead = 4, kFoldFew = 256;
-template <int kFoldTokens>
+// 16 tokens, 16 threads each: every thread folds each 16th slice in order, then
+// one thread a token its state and the 16 results in order.  The last strip's are
+// folded by kd_loss_kernel.  Latency bounds it: 64 slices of 8192 tokens 5.1 us.
+constexpr int kFoldTokens = 16, kFoldWays = kThreads / kFoldTokens, kFoldAhead = 4;
 __global__ __launch_bounds__(kThreads) void kd_fold_kernel(
     const float* __restrict__ pmax, const float* __restrict__ psum, int nslices, int64_t N,
-    float* __restrict__ m, float* __restrict__ z, int first, int last, float* __restrict__ lse) {
-  constexpr int kFoldWays = kThreads / kFoldTokens;
+    float* __restrict__ m, float* __restrict__ z, int first) {
   __shared__ float ms[kFoldWays][kFoldTokens], zs[kFoldWays][kFoldTokens];
   const int i = threadIdx.x % kFoldTokens, way = threadIdx.x / kFoldTokens;
   const int64_t t = (int64_t)blockIdx.x * kFoldTokens + i, tc = min(t, N - 1);
@@ -118,25 +114,35 @@ __global__ __launch_bounds__(kThreads) void kd_fold_kernel(
   if (way != 0 || t >= N) return;
   mm = first ? -INFINITY : m[t];
   zz = first ? 0.f : z[t];
-#pragma unroll 16
+#pragma unroll
   for (int v = 0; v < kFoldWays; ++v) fold(ms[v][i], zs[v][i], mm, zz);
-  if (last) {
-    lse[t] = mm + logf(zz);
-  } else {
-    m[t] = mm;
-    z[t] = zz;
-  }
+  m[t] = mm;
+  z[t] = zz;
 }
 
-// One work-group per token: the list entries' logits, a wave taking kDots rows
-// of W at a time, then the loss.  Bound by the gathered rows: 8192 tokens, 32
+// One work-group per token: the last strip's slices folded in, which gives lse,
+// the list entries' logits, a wave taking kDots rows of W at a time, then the
+// loss.  (With a fold of its own launch 777 x 512 x 20,000 takes 157 us instead of
+// 153, 25 x 256 x 43,363 59 and 53.)  Bound by the gathered rows: 8192 tokens, 32
 // entries of 7168, 590 us for 3.8 GB (6.4 TB/s, partly from cache), 0.8% of the
 // pass.
-__global__ __launch_bounds__(kThreads) void kd_loss_kernel(const KdArgs a, float* __restrict__ loss,
-                                                           float* __restrict__ y_top) {
-  __shared__ float ys[kMaxList];
+__global__ __launch_bounds__(kThreads) void kd_loss_kernel(
+    const KdArgs a, const float* __restrict__ pmax, const float* __restrict__ psum, int nslices,
+    const float* __restrict__ m, const float* __restrict__ z, int first, float* __restrict__ lse,
+    float* __restrict__ loss, float* __restrict__ y_top) {
+  __shared__ float ys[kMaxList], ms[kWaves], zs[kWaves];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t t = blockIdx.x;
+  float mm = -INFINITY, zz = 0.f;
+  for (int s = threadIdx.x; s < nslices; s += kThreads)
+    fold(pmax[(int64_t)s * a.N + t], psum[(int64_t)s * a.N + t], mm, zz);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {  // the same way round for both lanes of a pair
+    const float m2 = __shfl_xor(mm, o), z2 = __shfl_xor(zz, o);
+    fold(m2, z2, mm, zz);
+  }
+  ms[w] = mm;
+  zs[w] = zz;
   const u32x4_t* x = reinterpret_cast<const u32x4_t*>(a.X + t * a.H);
   for (int j0 = w * kDots; j0 < a.K; j0 += kWaves * kDots) {
     const u32x4_t* row[kDots];
@@ -173,13 +179,19 @@ __global__ __launch_bounds__(kThreads) void kd_loss_kernel(const KdArgs a, float
   }
   __syncthreads();
   if (w != 0) return;
+  mm = first ? -INFINITY : m[t];
+  zz = first ? 0.f : z[t];
+#pragma unroll
+  for (int v = 0; v < kWaves; ++v) fold(ms[v], zs[v], mm, zz);
+  const float lse_t = mm + logf(zz);
+  if (lane == 0) lse[t] = lse_t;
   int32_t id[kPer];
   float p[kPer], logp[kPer];
   const bool any = list_softmax(a, t, lane, id, p, logp);
   float s = 0.f;
 #pragma unroll
   for (int q = 0; q < kPer; ++q)
-    if (p[q] > 0.f) s = fmaf(p[q], logp[q] - (ys[lane + 64 * q] / a.T - a.lse[t]), s);
+    if (p[q] > 0.f) s = fmaf(p[q], logp[q] - (ys[lane + 64 * q] / a.T - lse_t), s);
   s = run_sum<64>(s);
   if (lane == 0) loss[t] = any ? a.T * a.T * s : 0.f;
 }
@@ -405,16 +417,14 @@ MOE_API int kd_forward(const kd_plan_t* plan, const void* X, const void* W, cons
     KD_CHECK(gemm_kd_logits(false, X, (const bf16_t*)W + v0 * P.H, P.N, P.H, w, 1.f / P.temperature,
                             pmax, psum, nullptr, nullptr, nullptr, 0, st));
     const int nsl = (int)ceil_div(w, 256) * (256 / kCceSlice);
-    auto fold = [&](auto kern, int tokens) {
-      kern<<<(unsigned)ceil_div(P.N, tokens), kThreads, 0, st>>>(pmax, psum, nsl, P.N, (float*)(ws + L.m),
-                                                                 (float*)(ws + L.z), v0 == 0, v0 + w == P.V, lse);
-    };
-    P.N <= kFoldFew ? fold(kd_fold_kernel<4>, 4) : fold(kd_fold_kernel<16>, 16);
+    float *m = (float*)(ws + L.m), *z = (float*)(ws + L.z);
+    if (v0 + w < P.V)
+      kd_fold_kernel<<<(unsigned)ceil_div(P.N, kFoldTokens), kThreads, 0, st>>>(pmax, psum, nsl, P.N, m, z, v0 == 0);
+    else
+      kd_loss_kernel<<<(unsigned)P.N, kThreads, 0, st>>>(kd_args(P, X, W, t_idx, t_logit, nullptr), pmax, psum, nsl,
+                                                         m, z, v0 == 0, lse, loss, y_top);
     KD_CHECK(hipGetLastError());
   }
-  kd_loss_kernel<<<(unsigned)P.N, kThreads, 0, st>>>(kd_args(P, X, W, t_idx, t_logit, lse), loss,
-                                                     y_top);
-  KD_CHECK(hipGetLastError());
   return MOE_OK;
 }
 
