@@ -297,7 +297,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      v[j] = l[j] > -INFINITY ? v[j] : l[j];
+      v[j] = l[j] > -INFINITY ? fmaxf(v[j], -INFINITY) : l[j];  // a NaN bias masks its expert
       rank[j] = a.bias ? v[j] : l[j];
     }
     if constexpr (MODE >= kGrouped) {
@@ -395,7 +395,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
     const int above = lanes_above(order_of(best) >> 1);
     // with close, whatever may turn out to be ahead of T belongs to the candidates
     auto below = [&](float x) __attribute__((always_inline)) {
-      return close && x > -INFINITY ? x - nearness(a.sigmoid, x) : x;
+      return close && fabsf(x) < INFINITY ? x - nearness(a.sigmoid, x) : x;
     };
     float T = below(run_minf<G>(above < want ? best : INFINITY));
     // (value, ~expert) of each candidate; larger is earlier

@@ -166,6 +166,20 @@ def test_infinite_logits_still_give_distinct_experts(E, groups, score):
             assert i.min() >= 0 and i.max() < E and all(len(set(r)) == 7 for r in i.tolist())
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups", [(64, 7, (1, 1)), (64, 7, (8, 2)), (512, 9, (16, 3)), (96, 40, (1, 1))])
+def test_bias_that_is_not_finite_still_gives_distinct_experts(E, k, groups, score):
+    require_lib()
+    l = torch.randn(64, E, device=DEV)
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        for share in (0.05, 0.5, 1.0):
+            bias = torch.randn(E, device=DEV)
+            bias[torch.rand(E, device=DEV) < share] = bad
+            idx, _ = B.route_forward(B.route_plan(64, E, k, score, *groups, 2), l, bias)
+            i = idx.cpu().numpy()
+            assert i.min() >= 0 and i.max() < E and all(len(set(r)) == k for r in i.tolist()), (bad, share)
+
+
 def test_unaligned_rows_other_stream_and_untouched_neighbours():
     require_lib()
     rng = np.random.default_rng(9)
