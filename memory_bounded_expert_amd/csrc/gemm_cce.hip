@@ -12,6 +12,11 @@ namespace {
 // 128-column vocabulary slice of the statistics.
 using Logit = Shape<256, 256, 4, 2, 32, 1>;
 using LogitFew = Shape<128, 256, 2, 2, 32, 2>;
+// LogitFew's work for rows of up to 512, where a tile's first loads and its
+// epilogue take as long as its products and a third work-group a CU hides them:
+// 777 x 512 x 20,000 takes 148 us so and 154 with LogitFew, 600 x 256 x 60,000
+// 196 and 201, but 300 x 4096 x 100,000 1,630 and 1,563.
+using LogitShort = Shape<128, 128, 4, 1, 32, 3>;
 // For up to 64 tokens, where reading W bounds the product, and where the whole
 // product is one round of it, two a CU, whose steps along K take half as long:
 // whole passes of 47 x 3456 x 8123 take 97 us so and 147 us with LogitFew, of 16
@@ -20,6 +25,7 @@ using LogitFew = Shape<128, 256, 2, 2, 32, 2>;
 using LogitThin = Shape<64, 128, 4, 1, 64, 2>;
 static_assert(Logit::BN / Logit::WGN == kCceSlice, "statistics slice = one wave's columns");
 static_assert(LogitFew::BN / LogitFew::WGN == kCceSlice, "statistics slice = one wave's columns");
+static_assert(LogitShort::BN / LogitShort::WGN == kCceSlice, "statistics slice = one wave's columns");
 static_assert(LogitThin::BN / LogitThin::WGN == kCceSlice, "statistics slice = one wave's columns");
 
 // Whether 128-row tiles, two per CU, finish before 256-row tiles, one per CU:
@@ -117,7 +123,8 @@ hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, i
                 : launch_lds<Mode::Dense, S, false, true, true, false, Epi::KDStats>(p, g, st);
   };
   if (N <= LogitThin::BM || (int64_t)thin.x * thin.y <= 2 * kCus) return run(LogitThin(), thin);
-  if (few_tiles((int64_t)grid.x * grid.y, (int64_t)few.x * few.y)) return run(LogitFew(), few);
+  if (few_tiles((int64_t)grid.x * grid.y, (int64_t)few.x * few.y))
+    return H <= 512 ? run(LogitShort(), dim3(few.x, 2 * cols)) : run(LogitFew(), few);
   return run(Logit(), grid);
 }
 
