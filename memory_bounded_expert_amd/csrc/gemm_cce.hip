@@ -119,6 +119,15 @@ hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, i
   const dim3 thin((unsigned)ceil_div(N, LogitThin::BM), 2 * cols);
   auto run = [&](auto shape, dim3 g) {
     using S = decltype(shape);
+    // Few row tiles: those of a column tile on one XCD, whose L2 then reads W
+    // once.  In the plain order each is on another: 777 x 512 x 20,000 takes 148
+    // us so and 140 in this order, 500 x 4096 x 30,000 558 and 525, 1000 x 4096 x
+    // 30,000 1,002 and 940, 2000 x 2048 x 50,000 1,720 and 1,690; of 16 tiles the
+    // rows themselves no longer fit beside W (4000 x 4096 x 20,000 2,295 and 2,308).
+    if (g.x > 1 && g.x <= 8) {
+      p.tile_group = (int)g.y;
+      g.y = (g.y + 7) / 8 * 8;
+    }
     return grad ? launch_lds<Mode::Dense, S, false, true, true, false, Epi::KDGrad>(p, g, st)
                 : launch_lds<Mode::Dense, S, false, true, true, false, Epi::KDStats>(p, g, st);
   };

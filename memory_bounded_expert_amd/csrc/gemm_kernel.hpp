@@ -75,6 +75,8 @@ struct Params {
   int M, N, K, Kseg;
   int ntiles;  // Rows mode: N-tiles per M-tile (N / BN)
   int tile_group;  // Expert mode: M-tiles per dispatch group (0 or 1: N-tile fastest)
+                   // KDStats, KDGrad: if not 0, the column tiles of a grid of whole eights,
+                   // whose M-tiles then share an XCD
   const int2* tiles;
   const int32_t* tile_count;
   const int32_t* offsets;  // Rows: expert row offsets; Expert: segment rows (or null: one of K)

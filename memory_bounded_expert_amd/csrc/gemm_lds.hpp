@@ -291,6 +291,16 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
     // [z * Kseg, (z + 1) * Kseg) and writes the z-th partial output)
     m0 = blockIdx.x * BM;
     row_end = p.M;
+    if constexpr (EPI == Epi::KDStats || EPI == Epi::KDGrad) {
+      if (p.tile_group) {
+        // the M-tiles of a column tile on one XCD, one after the other
+        const int id = blockIdx.x + blockIdx.y * gridDim.x, at = id / 8;
+        const int y = id % 8 + 8 * (at / (int)gridDim.x);
+        if (y >= p.tile_group) return;
+        m0 = (at % (int)gridDim.x) * BM;
+        n0 = y * BN;
+      }
+    }
     if (gridDim.z > 1) k_len = p.Kseg;
     if constexpr (EPI == Epi::AccRanges) {
       const int z = blockIdx.z;
