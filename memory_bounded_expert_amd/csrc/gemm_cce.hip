@@ -100,18 +100,18 @@ hipError_t gemm_cce_dw(const void* G, int ldg, const void* X, int64_t N, int H, 
 }
 
 hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, int H, int w,
-                          float inv_t, float* pmax, float* psum, const float* lse, const float* dl,
+                          float T, float* pmax, float* psum, const float* lse, const float* dloss,
                           void* G, int ldg, hipStream_t st) {
   if (N == 0 || w == 0) return hipSuccess;
   Params p{};
   p.A = X; p.lda = H;
   p.B = Ws; p.ldb = H;
   p.M = (int)N; p.N = w; p.K = H;
-  p.ce_scale = inv_t;
+  p.ce_scale = 1.f / T;
   if (!grad) {
     p.ce_pmax = pmax; p.ce_psum = psum;
   } else {
-    p.ce_lse = lse; p.ce_dl = dl;
+    p.ce_lse = lse; p.ce_dl = dloss; p.ce_up = T;
     p.C = G; p.ldc = ldg;
   }
   const unsigned cols = (unsigned)ceil_div(w, 256);  // the statistics and G go to whole 256 columns

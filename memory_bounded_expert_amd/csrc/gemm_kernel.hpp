@@ -109,6 +109,7 @@ struct Params {
   const float* ce_lse;     // CEGrad: [M] log-normaliser
   const float* ce_dl;      // CEGrad: [M] upstream gradient, 0 for ignored rows
   float ce_scale;          // KDStats, KDGrad: factor on the logits, 1 / temperature
+  float ce_up;             // KDGrad: factor on ce_dl, the temperature
   // Epi::SwiGLUBwd: C = h (then g h), C2 = a (then da), C3 = u (then du),
   // row r's pair sw_perm[r] (< sw_nk) and its gate; sw_dgp[n-tile][row]
   // (row stride sw_rows) receives the tile's share of sum_f dh' h.

@@ -1115,8 +1115,9 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
         for (int q = 0; q < 4; ++q) rg[i][q] = __shfl(row_scale_lane, i * 16 + 4 * lg + q, 64);
       stage_store(static_cast<T*>(p.C), [&](int i, int j, int q) { return f2bf(acc[0][i][j][q] * rg[i][q]); });
     } else if constexpr (EPI == Epi::KDGrad) {
-      // Distillation, backward: dl_row exp(ce_scale logit - lse_row), bf16 (the
-      // teacher's entries are corrected afterwards); zeros as for CEGrad.
+      // Distillation, backward: dl_row ce_up exp(ce_scale logit - lse_row), bf16
+      // (the teacher's entries, and tokens without any, are corrected
+      // afterwards); zeros past the vocabulary.
       float rlse[FM][4], rdl[FM][4];
 #pragma unroll
       for (int i = 0; i < FM; ++i)
@@ -1124,7 +1125,7 @@ __device__ __forceinline__ void gemm_lds_body(const Params& p, int bid) {
         for (int q = 0; q < 4; ++q) {
           const int row = min(m0 + wm * WM + i * 16 + 4 * lg + q, row_end - 1);
           rlse[i][q] = p.ce_lse[row] * 1.44269504f;
-          rdl[i][q] = p.ce_dl[row];
+          rdl[i][q] = p.ce_dl[row] * p.ce_up;
         }
       const float c = p.ce_scale * 1.44269504f;
       if (n0 + BN <= p.N)  // the same way for every wave: stage_store has barriers

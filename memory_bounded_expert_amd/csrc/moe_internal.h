@@ -376,10 +376,10 @@ hipError_t gemm_cce_dw(const void* G, int ldg, const void* X, int64_t N, int H, 
                        hipStream_t st);
 
 // ---- distillation over vocabulary strips (distill.hip, gemm_cce.hip)
-// As gemm_cce_logits on logits times inv_t, without targets: the statistics,
-// or G = dl exp(inv_t logit - lse).
+// As gemm_cce_logits on logits / T, without targets: the statistics, or G =
+// dloss T exp(logit / T - lse).
 hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, int H, int w,
-                          float inv_t, float* pmax, float* psum, const float* lse, const float* dl,
+                          float T, float* pmax, float* psum, const float* lse, const float* dloss,
                           void* G, int ldg, hipStream_t st);
 // As gemm_cce_dx for the strip that starts at vocabulary entry v0 (v0, range
 // multiples of 256), with the vocabulary in ranges of `range` entries: range r
