@@ -490,7 +490,7 @@ hipError_t launch_exact_wgrad(const int8_t* a_hi, const int8_t* a_lo, const int8
                               const int32_t* offpad, uint32_t* c_lo, int32_t* c_hi, int E, int M,
                               int N, bool init, hipStream_t st) {
   if (M % kXBM || N % kXBN) return hipErrorInvalidValue;
-  static bool attr = false;
+  static uint64_t attr = 0;
   if (hipError_t err = gemm::set_lds_attr(exact_wgrad_kernel, kXNS * kXStage, attr);
       err != hipSuccess)
     return err;

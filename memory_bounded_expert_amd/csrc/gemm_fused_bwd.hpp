@@ -525,7 +525,7 @@ hipError_t launch_fused_bwd(const FusedBwdParams& p, dim3 grid, hipStream_t st) 
   if (p.H % (S::BK * C::NS) != 0 || p.F % S::BN != 0) return hipErrorInvalidValue;
   auto kern = fused_bwd_kernel<S>;
   constexpr int lds = kLdsBytes;
-  static bool attr_set = false;
+  static uint64_t attr_set = 0;
   if (hipError_t err = set_lds_attr(kern, lds, attr_set); err != hipSuccess) return err;
   kern<<<grid, C::THREADS, lds, st>>>(p);
   return hipGetLastError();

@@ -1279,11 +1279,16 @@ __attribute__((amdgpu_waves_per_eu(G1::S::WG_PER_CU * G1::C::WAVES / 4))) void g
     G2::run(p2, L);
 }
 
+// Allows the kernel `lds` bytes on the current device; `done` holds a bit per device
+// that has them (a function's attributes are each device's own).
 template <class KERN>
-hipError_t set_lds_attr(KERN kern, int lds, bool& done) {
-  if (done) return hipSuccess;  // per instantiation; benign race (idempotent)
+hipError_t set_lds_attr(KERN kern, int lds, uint64_t& done) {
+  int dev = 0;
+  if (hipError_t err = hipGetDevice(&dev); err != hipSuccess) return err;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done & bit) return hipSuccess;  // per instantiation; benign race (idempotent)
   hipError_t err = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (err == hipSuccess) done = true;
+  if (err == hipSuccess) done |= bit;
   return err;
 }
 
@@ -1292,7 +1297,7 @@ hipError_t launch_lds(const Params& p, dim3 grid, hipStream_t st) {
   using C = LdsCfg<S, DUAL, mode_kidx(MODE)>;
   auto kern = gemm_lds_kernel<MODE, S, DUAL, A_K, B_K, KCAT, EPI>;
   constexpr int lds = lds_bytes<MODE, S, DUAL>();
-  static bool attr_set = false;
+  static uint64_t attr_set = 0;
   if (hipError_t err = set_lds_attr(kern, lds, attr_set); err != hipSuccess) return err;
   kern<<<grid, C::THREADS, lds, st>>>(p);
   return hipGetLastError();
@@ -1307,7 +1312,7 @@ hipError_t launch_lds_pair(const Params& p1, int n1, const Params& p2, int n2, h
   auto kern = gemm_lds_pair_kernel<G1, G2, ALT>;
   constexpr int l1 = G1::C::NS * G1::C::STAGE, l2 = G2::C::NS * G2::C::STAGE;
   constexpr int lds = l1 > l2 ? l1 : l2;
-  static bool attr_set = false;
+  static uint64_t attr_set = 0;
   if (hipError_t err = set_lds_attr(kern, lds, attr_set); err != hipSuccess) return err;
   // n1, n2: each list's largest possible number of work-groups; every XCD
   // then gets at least as many ids as its tiles of both lists (the kernel
