@@ -430,15 +430,15 @@ int row_groups(int64_t N, int W) {
   return (int)std::min<int64_t>(ceil_div(N, rows_per_group(W)), std::max(256, kRowWaves / waves_per_group(W)));
 }
 
-// The backward pass's work-groups.  Up to kAloneRounds rows a wave (a work-group
-// of several waves a row) stay with one: another round costs it less than the
-// fold's launch (calls on 16 x 512 fp32 13.7 us so and 16.3 with the fold, on 4
-// x 4096 bf16 13.7 and 16.8; 8 rounds take longer than it at 8 x 4096, 17.5 and
-// 16.3).
-constexpr int kAloneRounds = 4;
+// The backward pass's work-groups: each takes kSlabRounds rows a wave (a
+// work-group of several waves a row) at least, since a slab of its own costs as
+// much to write and fold as the rows to read: 794 x 7808 bf16 26 us with 4 rounds,
+// 35 with 1, 30 with 8.  With one slab there is no fold's launch: calls on 16 x
+// 512 fp32 13.7 us and 16.3 with one, on 4 x 4096 bf16 13.7 and 16.8.
+constexpr int kSlabRounds = 4;
 int slab_count(int64_t N, int W) {
-  if (W != 0 && N <= kAloneRounds * rows_per_group(W)) return 1;
-  return row_groups(N, W);
+  const int most = row_groups(N, W);
+  return W == 0 ? most : (int)std::min<int64_t>(most, ceil_div(N, kSlabRounds * rows_per_group(W)));
 }
 
 // Calls f with the holding, and whether a row's last vector is short, as
