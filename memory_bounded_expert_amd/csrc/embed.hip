@@ -44,6 +44,10 @@ constexpr int kScanThreads = 1024;
 // 411 without, 415 with 96 MB; 1024 positions of 1024 into 5000 rows 16.7 and
 // 20.4 us.
 constexpr int64_t kSliceBytes = 32 << 20;
+// The same beside sort_small_kernel, which takes 8 to 20 us on one CU: calls on
+// 4000 x 512 into 100,000 rows 38.5 us so and 50 with 32 MB, 8 x 512 30 and 34,
+// 1861 x 320 into 123,874 29 and 37, 44 x 128 into 132,469 17.9 and 18.6.
+constexpr int64_t kSmallSlice = 128 << 20;
 constexpr int64_t kZeroBytes = 1 << 18;        // bytes zeroed by a work-group
 
 // ---- one lane's vector of a row: elements col .. col + EPC - 1, the row's last
@@ -673,8 +677,8 @@ MOE_API int embed_backward(const embed_plan_t* plan, const int32_t* ids, const v
   s.tiles = L.tiles;
   s.bits = L.bits;
   // takes the next slice; the launch's work-groups
-  auto grid = [&](int groups) {
-    const int64_t rows = std::min(P.V - zeroed, ceil_div(kSliceBytes / 4, P.H));
+  auto grid = [&](int groups, int64_t slice) {
+    const int64_t rows = std::min(P.V - zeroed, ceil_div(slice / 4, P.H));
     s.groups = groups;
     s.zero = dW + zeroed * P.H;
     s.zero_end = s.zero + rows * P.H;
@@ -685,7 +689,7 @@ MOE_API int embed_backward(const embed_plan_t* plan, const int32_t* ids, const v
     s.bits = L.key_bits;
     s.key_out = (uint32_t*)(ws + L.key[0]);
     s.pos_out = (uint32_t*)(ws + L.pos[0]);
-    const unsigned g = grid(1);
+    const unsigned g = grid(1, kSmallSlice);
     sort_small_kernel<<<g, kSmallThreads, 0, st>>>(s);
     s.key = s.key_out;
     s.pos = s.pos_out;
@@ -694,11 +698,11 @@ MOE_API int embed_backward(const embed_plan_t* plan, const int32_t* ids, const v
     s.shift = i * L.bits;
     s.key_out = (uint32_t*)(ws + L.key[i & 1]);
     s.pos_out = (uint32_t*)(ws + L.pos[i & 1]);
-    unsigned g = grid(L.tiles);
+    unsigned g = grid(L.tiles, kSliceBytes);
     sort_count_kernel<<<g, kThreads, 0, st>>>(s);
-    g = grid(1);
+    g = grid(1, kSliceBytes);
     sort_scan_kernel<<<g, kScanThreads, 0, st>>>(s, L.tiles << L.bits);
-    g = grid(L.tiles);
+    g = grid(L.tiles, kSliceBytes);
     sort_place_kernel<<<g, kThreads, 0, st>>>(s);
     s.ids = nullptr;
     s.key = s.key_out;
