@@ -3,18 +3,20 @@
 // gradient of the logits.
 //
 // The bytes are few (a row of logits in, k pairs out), so the selection's
-// instructions decide.  A token takes 16 lanes of up to 16 experts each (64
-// lanes past 256 experts), so that a wave selects for four tokens at once and
-// every reduction stays inside a row of lanes, in DPP operands.  The selection
-// runs k rounds: the largest remaining rank, then the lowest expert that holds
-// it.  Ranks are the values, -inf for a masked expert and NaN for what is not to
-// be selected, which no maximum and no comparison takes: any input gives k
-// distinct experts.
+// instructions decide.  A token takes 16 lanes of up to 16 experts each (a wave
+// past 256 experts or 16 slots), so that a wave selects for four tokens at once
+// and every reduction stays inside a row of lanes, in DPP operands.  The lanes'
+// largest ranks give a threshold that few experts pass; those, one a lane, count
+// the ones before them.  Where more pass than there are lanes (many equal ones,
+// or more slots than a row's lanes) the selection runs k rounds: the largest
+// remaining rank, then the lowest expert that holds it.
 //
-// Logits rank exactly as they are.  Scores with a bias, and group strengths,
-// are formed in 32 bits first; a token where two values that decide something
-// are nearer than their error bound is selected again in 64 bits by its whole
-// wave (route_exact).
+// Ranks are the values, -inf for a masked expert and NaN for what is not to be
+// selected, which no maximum and no comparison takes: any input gives k
+// distinct experts.  Logits rank exactly as they are.  Scores with a bias, and
+// group strengths, are formed in 32 bits first; where two values that decide
+// something are nearer than their error bound, the candidates, or the token by
+// its whole wave (route_exact), are ranked again in 64 bits.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -78,11 +78,4 @@ __device__ __forceinline__ uint32_t run_or(uint32_t v) {
   return run_reduce<G>(v, [](uint32_t a, uint32_t b) { return a | b; });
 }
 
-// Sum over a wave by xor butterflies; every lane ends with the same bits.
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
-  return v;
-}
-
 }  // namespace moe
