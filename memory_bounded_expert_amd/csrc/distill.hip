@@ -481,10 +481,7 @@ MOE_API int kd_backward(const kd_plan_t* plan, const void* X, const void* W, con
       KD_CHECK(gemm_kd_dx(G, cols, Ws, P.N, P.H, w, v0, dx, R.range, R.slots, st));
     else
       KD_CHECK(gemm_cce_dx(G, cols, Ws, P.N, P.H, w, dx, s == 0, st));
-    if (P.dw_dtype == MOE_BF16)
-      KD_CHECK(gemm_kd_dw_bf16(G, cols, X, P.N, P.H, w, (bf16_t*)dW + v0 * P.H, st));
-    else
-      KD_CHECK(gemm_cce_dw(G, cols, X, P.N, P.H, w, (float*)dW + v0 * P.H, st));
+    KD_CHECK(gemm_kd_dw(P.dw_dtype == MOE_BF16, G, cols, X, P.N, P.H, w, (char*)dW + v0 * P.H * dwb, st));
   }
   const int64_t n4 = P.N * P.H / 4;
   if (R.slots > 1)

@@ -165,26 +165,31 @@ hipError_t gemm_kd_dx(const void* G, int ldg, const void* Ws, int64_t N, int H, 
   return hipSuccess;
 }
 
-hipError_t gemm_kd_dw_bf16(const void* G, int ldg, const void* X, int64_t N, int H, int w,
-                           void* dws, hipStream_t st) {
+hipError_t gemm_kd_dw(bool bf16, const void* G, int ldg, const void* X, int64_t N, int H, int w,
+                      void* dws, hipStream_t st) {
   if (w == 0) return hipSuccess;
   Params p{};
   p.A = G; p.lda = ldg;
   p.B = X; p.ldb = H;
   p.C = dws; p.ldc = H;
   p.M = w; p.N = H; p.K = (int)N;
+  p.acc_init = 1;
   p.tile_group = kCceDwGroup;  // as gemm_cce_dw
   // Few tokens: writing dW bounds it, and three small work-groups a CU write
   // more steadily (whole passes of 16 x 4096 x 100,000 755 and 774 us, 333 x
-  // 2048 x 50,000 448 and 454, but 1000 x 4096 x 30,000 1,016 and 1,001).  Where H
-  // is no multiple of 256 they do for any number (one 512-thread work-group a CU
-  // instead: 16 x 4224 x 100,000 726 and 915 us, 4000 x 4224 x 20,000 2,736 and
-  // 2,896).
-  const int bn = H % 256 == 0 && N > 512 ? 256 : 128;
-  const dim3 grid((unsigned)ceil_div(w, 128), (unsigned)(H / bn), 1u);
-  if (bn == 256)
-    return launch_lds<Mode::Expert, Shape<128, 256, 2, 2, 32, 2>, false, false, false, false, Epi::Store>(p, grid, st);
-  return launch_lds<Mode::Expert, Shape<128, 128, 2, 2, 32, 3>, false, false, false, false, Epi::Store>(p, grid, st);
+  // 2048 x 50,000 448 and 454, but 1000 x 4096 x 30,000 1,016 and 1,001).  So
+  // too where the wide tiles do not fill the chip (8000 x 512 x 20,000, 66 a
+  // strip, 1,077 and 1,263, 7778 x 256 x 1813 165 and 203), and where H is no
+  // multiple of 256 (16 x 4224 x 100,000 726 and 915 with one 512-thread
+  // work-group a CU, 4000 x 4224 x 20,000 2,736 and 2,896).
+  const bool wide = H % 256 == 0 && N > 512 && ceil_div(w, 128) * (H / 256) >= 2 * kCus;
+  auto run = [&](auto shape) {
+    using S = decltype(shape);
+    const dim3 grid((unsigned)ceil_div(w, S::BM), (unsigned)(H / S::BN), 1u);
+    return bf16 ? launch_lds<Mode::Expert, S, false, false, false, false, Epi::Store>(p, grid, st)
+                : launch_lds<Mode::Expert, S, false, false, false, false, Epi::AccF32>(p, grid, st);
+  };
+  return wide ? run(Shape<128, 256, 2, 2, 32, 2>()) : run(Shape<128, 128, 2, 2, 32, 3>());
 }
 
 }  // namespace moe

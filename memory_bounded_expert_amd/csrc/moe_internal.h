@@ -387,8 +387,8 @@ hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, i
 // over its ranges in order), so that the ranges of a strip run side by side.
 hipError_t gemm_kd_dx(const void* G, int ldg, const void* Ws, int64_t N, int H, int w, int64_t v0,
                       float* sums, int range, int slots, hipStream_t st);
-// As gemm_cce_dw, rounded once to bf16.
-hipError_t gemm_kd_dw_bf16(const void* G, int ldg, const void* X, int64_t N, int H, int w,
-                           void* dws, hipStream_t st);
+// As gemm_cce_dw, in fp32 or rounded once to bf16.
+hipError_t gemm_kd_dw(bool bf16, const void* G, int ldg, const void* X, int64_t N, int H, int w,
+                      void* dws, hipStream_t st);
 
 }  // namespace moe
