@@ -400,9 +400,11 @@ MOE_API int kd_plan(int64_t N, int32_t H, int64_t V, int32_t v_chunk, int32_t K,
   p.strip = strip_of(N, V, H, v_chunk);
   p.S = N == 0 ? 0 : (int32_t)ceil_div(V, p.strip);
   p.strip_bound_bytes = N * std::min<int64_t>(p.strip, V) * 2;
-  const int fcols = strip_cols(V, forward_strip(N, V, H)), cols = strip_cols(V, p.strip);
-  p.fwd_workspace_bytes = N == 0 ? 0 : (int64_t)kd_layout(N, V, H, fcols, false).total;
-  p.bwd_workspace_bytes = N == 0 ? 0 : (int64_t)kd_layout(N, V, H, cols, true).total;
+  if (N > 0) {  // without tokens there are no tiles to count, and no workspaces
+    const int fcols = strip_cols(V, forward_strip(N, V, H)), cols = strip_cols(V, p.strip);
+    p.fwd_workspace_bytes = (int64_t)kd_layout(N, V, H, fcols, false).total;
+    p.bwd_workspace_bytes = (int64_t)kd_layout(N, V, H, cols, true).total;
+  }
   *out = p;
   return MOE_OK;
 }
