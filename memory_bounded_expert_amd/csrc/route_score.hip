@@ -122,7 +122,7 @@ __device__ __forceinline__ int route_exact(const RouteArgs& a, int64_t t, double
     if (!is_masked(l)) {
       v = exp(a.sigmoid ? -(double)l : (double)l - (double)top);
       v = a.sigmoid ? 1.0 / (1.0 + v) : v * inv;
-      if (a.bias) v += (double)a.bias[e];
+      if (a.bias) v = fmax(v + (double)a.bias[e], -INFINITY);  // a NaN bias masks, as in 32 bits
     }
     lds[e] = v;
   }
@@ -501,7 +501,7 @@ __global__ __launch_bounds__(kThreads) void route_forward_kernel(const RouteArgs
           const int e = in ? (int)~c0.y : 0;
           const float le = row[e];
           const double s64 = a.sigmoid ? 1.0 / (1.0 + exp(-(double)le)) : exp((double)le - (double)top) / z;
-          const uint64_t o64 = order_of(is_masked(le) ? -(double)INFINITY : s64 + (double)a.bias[e]);
+          const uint64_t o64 = order_of(is_masked(le) ? -(double)INFINITY : fmax(s64 + (double)a.bias[e], -INFINITY));
           before = 0;
           for (int c = 0; c < G; ++c) {
             const int from = sub * G + c;

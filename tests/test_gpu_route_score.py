@@ -269,3 +269,28 @@ def test_graph_replays(score):
     torch.cuda.synchronize()
     refs = {k: t.clone() for k, t in outs.items()}
     replay_and_check("route " + score, capture(call), outs, refs)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups", [(64, 8, (1, 1)), (64, 5, (8, 3)), (256, 8, (8, 4)), (512, 9, (16, 3)),
+                                        (96, 20, (1, 1)), (24, 3, (1, 1))])
+def test_nan_bias_masks_its_expert_among_near_ties(E, k, groups, score):
+    """Few distinct logits and biases, so that equal and nearly equal scores are
+    told apart in 64 bits; every group keeps experts enough.  A NaN bias then
+    ranks as a bias far below all others, and its expert is never selected."""
+    require_lib()
+    rng = np.random.default_rng(E + k)
+    l = (np.round(rng.standard_normal((200, E)) * 2) / 2).astype(np.float32)
+    l = np.where(rng.random(l.shape) < 0.3, np.nextafter(l, np.float32(9)), l)
+    bias = (0.125 * rng.integers(-1, 2, E)).astype(np.float32)
+    for first, step in ((0, 2), (1, 2), (0, 4), (3, 8)):
+        gone = np.zeros(E, bool)
+        gone[first::step] = True
+        per = E // groups[0]
+        assert (~gone).reshape(-1, per).sum(1).min() >= 2 and (~gone).sum() * groups[1] // groups[0] >= k
+        plan = B.route_plan(200, E, k, score, *groups, 2)
+        idx, _ = B.route_forward(plan, dev(l), dev(np.where(gone, np.float32("nan"), bias)))
+        want = oracle.route_select(l, k, score, np.where(gone, -1e30, bias), *groups, 2)
+        got = idx.cpu().numpy()
+        assert not gone[got].any(), (first, step)
+        assert np.array_equal(got, want), (first, step)
