@@ -37,7 +37,8 @@ struct KdArgs {
 };
 
 // The teacher's probabilities of token t's list: lane l holds entries l + 64 q,
-// q < kPer (K <= 64 kPer).
+// q < kPer (K <= 64 kPer).  Differences to the largest logit are divided by T,
+// not the logits: a quotient of a finite logit may overflow where T < 1.
 // p is -1 for an entry that is no part of the list; returns whether any is.
 template <int kPer>
 __device__ __forceinline__ bool list_softmax(const KdArgs& a, int64_t t, int lane, int32_t (&id)[kPer],
@@ -50,7 +51,7 @@ __device__ __forceinline__ bool list_softmax(const KdArgs& a, int64_t t, int lan
     logp[q] = -INFINITY;
     if (j < a.K) {
       const int32_t v = a.t_idx[t * a.K + j];
-      const float l = a.t_logit[t * a.K + j] / a.T;
+      const float l = a.t_logit[t * a.K + j];
       if (v >= 0 && v < a.V && l > -INFINITY) {
         id[q] = v;
         logp[q] = l;
@@ -63,7 +64,8 @@ __device__ __forceinline__ bool list_softmax(const KdArgs& a, int64_t t, int lan
   float z = 0.f;
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
-    p[q] = id[q] >= 0 ? expf(logp[q] - top) : 0.f;
+    logp[q] = (logp[q] - top) / a.T;
+    p[q] = id[q] >= 0 ? expf(logp[q]) : 0.f;
     z += p[q];
   }
   z = run_sum<64>(z);
@@ -71,7 +73,7 @@ __device__ __forceinline__ bool list_softmax(const KdArgs& a, int64_t t, int lan
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
     p[q] = id[q] >= 0 ? p[q] / z : -1.f;
-    logp[q] = logp[q] - top - logz;
+    logp[q] -= logz;
   }
   return any;
 }
@@ -154,7 +156,7 @@ __global__ __launch_bounds__(kThreads) void kd_loss_kernel(
 #pragma unroll
     for (int u = 0; u < kDots; ++u) {
       const int32_t v = j0 + u < a.K ? a.t_idx[t * a.K + j0 + u] : -1;
-      real[u] = v >= 0 && v < a.V && a.t_logit[t * a.K + j0 + u] / a.T > -INFINITY;
+      real[u] = v >= 0 && v < a.V && a.t_logit[t * a.K + j0 + u] > -INFINITY;
       row[u] = reinterpret_cast<const u32x4_t*>(a.W + (int64_t)(real[u] ? v : 0) * a.H);
       acc[u] = 0.f;
     }

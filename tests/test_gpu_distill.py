@@ -252,3 +252,24 @@ def test_graph_replays():
         B.kd_backward(plan, c.X, c.W, idx, t, outs["lse"], outs["y_top"], dl, outs["dX"], outs["dW"], ws=ws)
 
     replay_and_check("distill", capture(call), outs, ref)
+
+
+@pytest.mark.parametrize("T", [0.5, 0.25, 0.3])
+def test_finite_logits_whose_quotients_overflow(T):
+    """An entry is part of the list by its logit, not by logit / T; the softmax
+    is of the differences."""
+    require_lib()
+    c = Case(40, 128, 500, 8, seed=5)
+    lo, hi = np.finfo(np.float32).min, np.finfo(np.float32).max
+    c.t[0] = lo                # all equal, each 1 / 8
+    c.t[1] = hi
+    c.t[2, 1:] = lo            # one real entry beside the lowest value
+    c.t[3, ::2] = lo
+    c.t[4, ::2] = hi
+    c.t[5] = [hi, lo] * 4
+    c.t[6, :3] = -np.inf
+    c.t[6, 3:] = lo
+    c.t[7] = np.nan
+    c.t[8] = hi * (1 - 2.0 ** -20 * np.arange(8))
+    out = check(c, 256, T)
+    assert not out["loss"][7] and bool((out["loss"][:7] > 0).all())
