@@ -30,6 +30,9 @@
  * side by side.  Every output is deterministic, and bitwise independent of
  * v_chunk as cce.h's are.
  *
+ * lse is fp32 and y / T is formed in fp32, so q is off by up to |y / T| 2^-22
+ * of itself: temperatures that take y / T towards 2^22 leave nothing of it.
+ *
  * Conventions: as cce.h.  X [N][H] and W [V][H] are bfloat16; t_idx [N][K]
  * int32, t_logit [N][K] fp32; loss, lse, dloss [N] and y_top [N][K] fp32; dX
  * [N][H] bfloat16; dW [V][H] fp32 or bfloat16, as the plan says.
@@ -73,7 +76,8 @@ typedef struct kd_plan {
  * kd_plan -- strip plan and workspace sizing.  Host only, pure.  N = 0 is
  * valid (S = 0; the calls are no-ops, except that kd_backward zeroes dW).
  * Errors: MOE_EINVAL if out is NULL, N < 0, V < 1, H < 1, v_chunk < 1, K < 1,
- *   temperature not a finite number above 0, or a dtype unknown.
+ *   temperature not a finite number above 0 with a finite fp32 reciprocal, or a
+ *   dtype unknown.
  *   MOE_EUNSUPPORTED if dtype is not MOE_BF16, H is not a multiple of 128,
  *   v_chunk is not a multiple of 256, N*H, N*v_chunk or v_chunk*H reach 2^30,
  *   V >= 2^31, or K > 256.

@@ -381,7 +381,7 @@ using namespace moe;
 MOE_API int kd_plan(int64_t N, int32_t H, int64_t V, int32_t v_chunk, int32_t K, float temperature,
                     int32_t dtype, int32_t dw_dtype, kd_plan_t* out) {
   if (!out || N < 0 || V < 1 || H < 1 || v_chunk < 1 || K < 1) return MOE_EINVAL;
-  if (!(temperature > 0.f) || !std::isfinite(temperature)) return MOE_EINVAL;
+  if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature)) return MOE_EINVAL;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EINVAL;
   if (dw_dtype != MOE_F32 && dw_dtype != MOE_BF16) return MOE_EINVAL;
   if (dtype != MOE_BF16 || H % 128 != 0 || v_chunk % 256 != 0 || K > kMaxList) return MOE_EUNSUPPORTED;

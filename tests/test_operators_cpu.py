@@ -249,6 +249,11 @@ def test_kd_plan_errors(change, status):
     assert B.lib().kd_plan(*{**KD_OK, **change}.values(), ctypes.byref(B.KdPlan())) == status
 
 
+def test_kd_temperatures_without_a_reciprocal():
+    for T, status in ((1e-39, B.MOE_EINVAL), (1e-38, B.MOE_OK), (3e38, B.MOE_OK)):
+        assert B.lib().kd_plan(*{**KD_OK, "temperature": T}.values(), ctypes.byref(B.KdPlan())) == status
+
+
 def test_kd_strips_and_workspace():
     p = B.kd_plan(8192, 7168, 200_000, 8192, 32)
     c = B.cce_plan(8192, 7168, 200_000, 8192)
