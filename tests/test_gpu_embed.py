@@ -163,3 +163,42 @@ def test_graph_replays():
         B.embed_backward(plan, ids, dY, outs["dW"], ws=ws)
 
     replay_and_check("embed", capture(call), outs, {"Y": Y, "dW": dW})
+
+
+# Gradients larger than what is zeroed beside the sort (128 MB with up to 4096
+# positions, 32 MB a launch with more), so that the summing launch zeroes the
+# rest around the rows it writes: narrow and odd rows, pieces of 4096 rows.
+PAST = [(3000, 1_200_000, 37, "bf16"), (5000, 700_000, 101, "f32"), (5000, 700_000, 101, "bf16"),
+        (2000, 16_000_000, 3, "f32"), (4096, 140_000, 513, "bf16"), (20_000, 900_000, 72, "bf16")]
+
+
+@pytest.mark.parametrize("size", PAST, ids=lambda s: "x".join(map(str, s)))
+def test_rows_zeroed_around_those_that_occur(size):
+    require_lib()
+    N, V, H, dtype = size
+    dt = TYPES[dtype]
+    r = np.random.default_rng(V)
+    ids = r.integers(0, V, N)
+    ids[: N // 4] = V - 1 - r.integers(0, 300, N // 4)   # many near the end, some of them often
+    ids[N // 4: N // 2] = V // 2 + np.arange(N // 2 - N // 4) % 977
+    ids[-1], ids[-2], ids[-3] = V - 1, 0, -1
+    di = torch.from_numpy(ids.astype(np.int32)).to(DEV)
+    dY = torch.randn(N, H, generator=torch.Generator().manual_seed(N)).to(dt).to(DEV)
+    plan = B.embed_plan(N, V, H, B.moe_dtype(dt), 0.5)
+    dW = torch.full((V, H), float("nan"), device=DEV)
+    B.embed_backward(plan, di, dY, dW=dW)
+    ok = di >= 0
+    rows, at, n = torch.unique(di[ok].long(), return_inverse=True, return_counts=True)
+    dy = 0.5 * dY[ok].double()
+    ref = torch.zeros((len(rows), H), dtype=torch.float64, device=DEV).index_add_(0, at, dy)
+    size = torch.zeros_like(ref).index_add_(0, at, dy.abs())
+    assert torch.all((dW[rows].double() - ref).abs() <= (64 + n[:, None] / 16 + 16) * U * size)
+    sums = dW[rows]
+    dW[rows] = 0
+    assert not dW.any()  # NaN counts as something
+    # onto ones: one rounding of the sum
+    acc = torch.ones((V, H), device=DEV)
+    B.embed_backward(plan, di, dY, dW=acc, accumulate=True)
+    assert torch.all((acc[rows].double() - 1 - ref).abs() <= (64 + n[:, None] / 16 + 16) * U * size + 2 * U * (1 + ref.abs()))
+    acc[rows] = 1
+    assert bool((acc == 1).all()) and bool(torch.isfinite(sums).all())
