@@ -12,6 +12,7 @@
 
 #include "device_common.hpp"
 #include "distill.h"
+#include "kd_shapes.hpp"
 #include "moe_internal.h"
 #include "wave_ops.hpp"
 
@@ -302,15 +303,6 @@ int strip_of(int64_t N, int64_t V, int H, int v_chunk) {
   return (int)(ceil_div(ceil_div(V, strips), v_chunk) * v_chunk);
 }
 
-// The forward pass keeps no logits: its strips are wide enough for four rounds
-// of 256 x 256 tiles, one per CU (32-bit offsets into W allowing), and so
-// depend on N, V and H alone, as lse then does.
-int forward_strip(int64_t N, int64_t V, int H) {
-  const int64_t wanted = std::min(ceil_div(4 * 256, ceil_div(N, 256)) * 256, ceil_div(V, 256) * 256);
-  const int64_t most = (((int64_t)1 << 30) - 1) / H / 256 * 256;
-  return (int)std::min(wanted, most);
-}
-
 // dX's ranges: with fewer than 256 tiles of dX, as many sums side by side as
 // fill the CUs once, each range at least 512 entries (16 K-tiles).  Depends on
 // N, H and V alone, so dX does not depend on the strips.  The passes above take
@@ -403,7 +395,7 @@ MOE_API int kd_plan(int64_t N, int32_t H, int64_t V, int32_t v_chunk, int32_t K,
   p.S = N == 0 ? 0 : (int32_t)ceil_div(V, p.strip);
   p.strip_bound_bytes = N * std::min<int64_t>(p.strip, V) * 2;
   if (N > 0) {  // without tokens there are no tiles to count, and no workspaces
-    const int fcols = strip_cols(V, forward_strip(N, V, H)), cols = strip_cols(V, p.strip);
+    const int fcols = strip_cols(V, kd_forward_strip(N, V, H)), cols = strip_cols(V, p.strip);
     p.fwd_workspace_bytes = (int64_t)kd_layout(N, V, H, fcols, false).total;
     p.bwd_workspace_bytes = (int64_t)kd_layout(N, V, H, cols, true).total;
   }
@@ -420,7 +412,7 @@ MOE_API int kd_forward(const kd_plan_t* plan, const void* X, const void* W, cons
   if (!X || !W || !t_idx || !t_logit || !loss || !lse || !y_top || !workspace) return MOE_EINVAL;
   if ((uintptr_t)workspace % 256 || off16(X, W)) return MOE_EINVAL;
   if (workspace_bytes < (size_t)P.fwd_workspace_bytes) return MOE_EWORKSPACE;
-  const int strip = forward_strip(P.N, P.V, P.H);
+  const int strip = kd_forward_strip(P.N, P.V, P.H);
   const KdLayout L = kd_layout(P.N, P.V, P.H, strip_cols(P.V, strip), false);
   hipStream_t st = (hipStream_t)stream;
   char* ws = (char*)workspace;

@@ -3,6 +3,7 @@
 // running sum dX += G W_s, and the strip's weight gradient dW_s = G^T X.
 #include "gemm_kernel.hpp"
 #include "gemm_lds.hpp"
+#include "kd_shapes.hpp"
 
 namespace moe {
 using namespace gemm;
@@ -11,36 +12,15 @@ namespace {
 // 256 x 256 tiles of 4 x 2 waves; each wave's 64 x 128 block is one
 // 128-column vocabulary slice of the statistics.
 using Logit = Shape<256, 256, 4, 2, 32, 1>;
+// Distillation's smaller tiles (kd_shapes.hpp says which when).
 using LogitFew = Shape<128, 256, 2, 2, 32, 2>;
-// LogitFew's work for rows of up to 512, where a tile's first loads and its
-// epilogue take as long as its products and a third work-group a CU hides them:
-// 777 x 512 x 20,000 takes 148 us so and 154 with LogitFew, 600 x 256 x 60,000
-// 196 and 201, but 300 x 4096 x 100,000 1,630 and 1,563.
 using LogitShort = Shape<128, 128, 4, 1, 32, 3>;
-// For up to 64 tokens, where reading W bounds the product, and where the whole
-// product is one round of it, two a CU, whose steps along K take half as long:
-// whole passes of 47 x 3456 x 8123 take 97 us so and 147 us with LogitFew, of 16
-// x 4096 x 100,000 772 and 795 us, of 500 x 2048 x 2000 77 and 114 us, but of
-// 100 x 2048 x 50,000 (1.5 rounds) 284 and 256 us.
 using LogitThin = Shape<64, 128, 4, 1, 64, 2>;
+static_assert(kKdCus == kCus, "one chip");
 static_assert(Logit::BN / Logit::WGN == kCceSlice, "statistics slice = one wave's columns");
 static_assert(LogitFew::BN / LogitFew::WGN == kCceSlice, "statistics slice = one wave's columns");
 static_assert(LogitShort::BN / LogitShort::WGN == kCceSlice, "statistics slice = one wave's columns");
 static_assert(LogitThin::BN / LogitThin::WGN == kCceSlice, "statistics slice = one wave's columns");
-
-// Whether 128-row tiles, two per CU, finish before 256-row tiles, one per CU:
-// in rounds of the chip, where a CU left with one 128-row tile needs half of
-// one, and the smaller tiles take a tenth longer for the same products.  They
-// win where a last round of 256-row tiles is mostly empty, and for batches of
-// up to 128 tokens: whole passes of 777 x 512 x 20,000 take 158 us so and 168
-// us with 256-row tiles, of 2000 x 2048 x 50,000 (forward strips) 1,731 and
-// 1,753 us, but of 1000 x 4096 x 30,000 (1.8 full rounds) 1,098 and 1,004 us.
-bool few_tiles(int64_t t256, int64_t t128) {
-  if (t256 >= 4 * kCus) return false;
-  const int64_t rest = t128 % (2 * kCus);
-  const double half_rounds = 2.0 * (double)(t128 / (2 * kCus)) + (rest == 0 ? 0 : rest <= kCus ? 1 : 2);
-  return 1.1 * half_rounds < 2.0 * (double)ceil_div(t256, kCus);
-}
 }  // namespace
 
 hipError_t gemm_cce_logits(bool grad, const void* X, const void* Ws, int64_t N, int H, int w,
@@ -115,10 +95,9 @@ hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, i
     p.C = G; p.ldc = ldg;
   }
   const unsigned cols = (unsigned)ceil_div(w, 256);  // the statistics and G go to whole 256 columns
-  const dim3 grid((unsigned)ceil_div(N, Logit::BM), cols), few((unsigned)ceil_div(N, LogitFew::BM), cols);
-  const dim3 thin((unsigned)ceil_div(N, LogitThin::BM), 2 * cols);
-  auto run = [&](auto shape, dim3 g) {
+  auto run = [&](auto shape) {
     using S = decltype(shape);
+    dim3 g((unsigned)ceil_div(N, S::BM), cols * (256 / S::BN));
     // Few row tiles: those of a column tile on one XCD, whose L2 then reads W
     // once.  In the plain order each is on another: 777 x 512 x 20,000 takes 148
     // us so and 140 in this order, 500 x 4096 x 30,000 558 and 525, 1000 x 4096 x
@@ -131,10 +110,12 @@ hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, i
     return grad ? launch_lds<Mode::Dense, S, false, true, true, false, Epi::KDGrad>(p, g, st)
                 : launch_lds<Mode::Dense, S, false, true, true, false, Epi::KDStats>(p, g, st);
   };
-  if (N <= LogitThin::BM || (int64_t)thin.x * thin.y <= 2 * kCus) return run(LogitThin(), thin);
-  if (few_tiles((int64_t)grid.x * grid.y, (int64_t)few.x * few.y))
-    return H <= 512 ? run(LogitShort(), dim3(few.x, 2 * cols)) : run(LogitFew(), few);
-  return run(Logit(), grid);
+  switch (kd_logit_tile(N, H, w)) {
+    case kKdThin: return run(LogitThin());
+    case kKdShort: return run(LogitShort());
+    case kKdFew: return run(LogitFew());
+    default: return run(Logit());
+  }
 }
 
 hipError_t gemm_kd_dx(const void* G, int ldg, const void* Ws, int64_t N, int H, int w, int64_t v0,

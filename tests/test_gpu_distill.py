@@ -273,3 +273,55 @@ def test_finite_logits_whose_quotients_overflow(T):
     c.t[8] = hi * (1 - 2.0 ** -20 * np.arange(8))
     out = check(c, 256, T)
     assert not out["loss"][7] and bool((out["loss"][:7] > 0).all())
+
+
+# N, H, V, v_chunk, K, T: 128 x 256 logit tiles in both passes, ragged in rows and columns
+FEW = [(100, 640, 40_001, 1024, 5, 1.0), (129, 768, 22_100, 256, 9, 2.0), (65, 1024, 33_000, 4096, 70, 1.0)]
+
+
+@pytest.mark.parametrize("size", FEW, ids=lambda s: "x".join(map(str, s)))
+def test_long_rows_of_few_tokens(size):
+    require_lib()
+    N, H, V, v_chunk, K, T = size
+    c = Case(N, H, V, K, seed=H, w_std=0.02)
+    c.idx[:, 0] = [(V - 1, 0, 255, 256, V - V % 256, V - V % 256 - 1)[i % 6] for i in range(N)]
+    c.idx[5] = -1
+    c.idx[N - 1, 1:] = c.idx[N - 1, 0]
+    check(c, v_chunk, T, size)
+
+
+# N, H, V, and widths for which the strips differ; of the second, dX is one sum
+WIDTHS = [(777, 512, 60_000, (4096, 256, 20_224)), (8200, 640, 10_001, (1024, 4096, 2048))]
+
+
+@pytest.mark.parametrize("size", WIDTHS, ids=lambda s: "x".join(map(str, s[:3])))
+def test_same_bits_for_strips_that_differ(size):
+    require_lib()
+    N, H, V, widths = size
+    K, T = 6, 2.0
+    strips = [B.kd_plan(N, H, V, vc, K, T).strip for vc in widths]
+    assert len(set(strips)) == len(widths) and all(s < V and V % s for s in strips), strips
+    c = Case(N, H, V, K, seed=H, w_std=0.03)
+    c.idx[:6, 0] = [v - d for v in strips for d in (0, 1)]  # either side of the first edges
+    c.idx[9] = -1
+    out = run(c, widths[0], T)
+    for vc in widths[1:]:
+        other = run(c, vc, T)
+        for k in out:
+            assert torch.equal(out[k], other[k]), (vc, k)
+    half = run(c, widths[1], T, B.MOE_BF16)
+    assert torch.equal(half["dW"], out["dW"].bfloat16()) and torch.equal(half["dX"], out["dX"])
+    X, W, idx = c.X.double(), c.W.double(), dev(c.idx).long()
+    y = X @ W.T / T
+    lse = torch.logsumexp(y, 1)
+    # y's sum of H products, the exponentials' and the fold's roundings, at most
+    assert torch.all((out["lse"].double() - lse).abs() <= (H + 2) * U * (X.abs() @ W.abs().T).amax(1) / T + (62 + V / 32) * U + 4 * U * lse.abs())
+    ok = idx >= 0
+    p64 = torch.where(ok, torch.softmax(dev(c.t).double() / T, 1), 0.0)
+    up = torch.where(ok.any(1), T * dev(c.dloss).double(), 0.0)[:, None]
+    g = torch.exp(y - lse[:, None]).scatter_add_(1, idx.clamp_min(0), -p64) * up
+    # e of each gradient (and 1e-4 of it for fp32's share), V u (N u) of the sum, e (u) of the result
+    dX, dW, aX, aW = g @ W, g.T @ X, X.abs(), W.abs()
+    assert torch.all((out["dX"].double() - dX).abs() <= (E + 1e-4 + V * U) * (g.abs() @ aW) + E * dX.abs())
+    assert torch.all((out["dW"].double() - dW).abs() <= (E + 1e-4 + N * U) * (g.abs().T @ aX) + U * dW.abs())
+    assert not out["dX"][9].any() and not out["loss"][9]
