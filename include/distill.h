@@ -19,16 +19,19 @@
  * that occurs twice counts twice, each entry by itself.  The teacher gets no
  * gradient.
  *
- * The forward pass runs cce_forward's strips on y / T and then forms the list
- * entries' logits as K products of rows, so its cost does not grow with K V.
+ * The forward pass takes the logits' statistics as cce_forward does, over
+ * strips of its own that depend on N, V and H alone (it keeps no logits, and
+ * v_chunk does not bear on it), and then forms the list entries' logits as K
+ * products of rows, so its cost does not grow with K V.
  * The backward pass recomputes each strip's logits, stores the strip's share
  * of dy in bf16 (the only strip-sized buffer), corrects the list entries that
- * fall into the strip, and consumes it in the dX and dW products.  A small
- * batch would fill few of the GPU's units with one strip of v_chunk entries,
- * so its strips are as many times v_chunk as fit that buffer into
- * KD_STRIP_BYTES, and its dX is summed over ranges of the vocabulary that run
- * side by side.  Every output is deterministic, and bitwise independent of
- * v_chunk as cce.h's are.
+ * fall into the strip, and consumes it in the dX and dW products.  That
+ * rounding, up to 2^-8 of an entry of dy, limits dX and dW, also where dW is
+ * fp32.  A small batch would fill few of the GPU's units with one strip of
+ * v_chunk entries, so its strips are as many times v_chunk as fit that buffer
+ * into KD_STRIP_BYTES, and its dX is summed over ranges of the vocabulary that
+ * run side by side, in at most 64 MiB of sums (one sum: 4 N H bytes).  Every
+ * output is deterministic, and bitwise independent of v_chunk as cce.h's are.
  *
  * lse is fp32 and y / T is formed in fp32, so q is off by up to |y / T| 2^-22
  * of itself: temperatures that take y / T towards 2^22 leave nothing of it.

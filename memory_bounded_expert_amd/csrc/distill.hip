@@ -1,11 +1,13 @@
 // Distillation from a teacher's top logits through the vocabulary projection
 // (include/distill.h).
 //
-// The strips and their GEMMs are the cross-entropy's (cce.hip, gemm_cce.hip)
-// on logits scaled by 1 / T.  What the teacher's list adds is sparse, K of V
-// entries per token: the forward pass takes their logits as dot products of
-// gathered rows of W, and the backward pass overwrites their values in the
-// strip's logit gradient from those logits, in fp32 before the one rounding.
+// The scheme is the cross-entropy's (cce.hip, gemm_cce.hip): strips of logits,
+// here scaled by 1 / T, formed twice and never kept.  Strips, tiles and the
+// order of dX's sums have rules of their own (kd_shapes.hpp, strip_of,
+// dx_ranges).  What the teacher's list adds is sparse, K of V entries per token:
+// the forward pass takes their logits as dot products of gathered rows of W, and
+// the backward pass overwrites their values in the strip's logit gradient from
+// those logits, in fp32 before the one rounding.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -127,8 +129,8 @@ __global__ __launch_bounds__(kThreads) void kd_fold_kernel(
 
 // One work-group per token: the last strip's slices folded in, which gives lse,
 // the list entries' logits, a wave taking kDots rows of W at a time, then the
-// loss.  (With a fold of its own launch 777 x 512 x 20,000 takes 157 us instead of
-// 153, 25 x 256 x 43,363 59 and 53.)  Bound by the gathered rows: 8192 tokens, 32
+// loss.  (With a fold of its own launch 777 x 512 x 20,000 takes 142 us instead of
+// 136, 25 x 256 x 43,363 56 and 50.)  Bound by the gathered rows: 8192 tokens, 32
 // entries of 7168, 590 us for 3.8 GB (6.4 TB/s, partly from cache), 0.8% of the
 // pass.
 template <int kPer>
@@ -292,8 +294,8 @@ int strip_cols(int64_t V, int strip) {
 
 // The backward pass's strips: v_chunk, times what KD_STRIP_BYTES leaves (and
 // 32-bit offsets into W), evened out over the vocabulary.  777 x 512 x 20,000 at
-// v_chunk 4096 takes 159 us so and 342 with strips of v_chunk, 100 x 2048 x 50,000
-// 256 and 1,075, 2000 x 2048 x 50,000 1,731 and 2,296.
+// v_chunk 4096 takes 136 us so and 281 with strips of v_chunk, at 8192 100 x 2048
+// x 50,000 225 and 484, 2000 x 2048 x 50,000 1,671 and 1,838.
 int strip_of(int64_t N, int64_t V, int H, int v_chunk) {
   const int64_t cols = ceil_div(V, 256) * 256;
   const int64_t most = std::min<int64_t>((int64_t)KD_STRIP_BYTES / 2 / std::max<int64_t>(N, 1),
@@ -306,7 +308,7 @@ int strip_of(int64_t N, int64_t V, int H, int v_chunk) {
 // dX's ranges: with fewer than 256 tiles of dX, as many sums side by side as
 // fill the CUs once, each range at least 512 entries (16 K-tiles).  Depends on
 // N, H and V alone, so dX does not depend on the strips.  The passes above take
-// 481, 776 and 2,176 us with one sum.
+// 460, 742 and 2,114 us with one sum.
 struct DxRanges {
   int range, slots;
 };

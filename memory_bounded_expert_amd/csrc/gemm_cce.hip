@@ -99,10 +99,10 @@ hipError_t gemm_kd_logits(bool grad, const void* X, const void* Ws, int64_t N, i
     using S = decltype(shape);
     dim3 g((unsigned)ceil_div(N, S::BM), cols * (256 / S::BN));
     // Few row tiles: those of a column tile on one XCD, whose L2 then reads W
-    // once.  In the plain order each is on another: 777 x 512 x 20,000 takes 148
-    // us so and 140 in this order, 500 x 4096 x 30,000 558 and 525, 1000 x 4096 x
-    // 30,000 1,002 and 940, 2000 x 2048 x 50,000 1,720 and 1,690; of 16 tiles the
-    // rows themselves no longer fit beside W (4000 x 4096 x 20,000 2,295 and 2,308).
+    // once.  In the plain order each is on another: 777 x 512 x 20,000 takes 142
+    // us so and 136 in this order, 500 x 4096 x 30,000 528 and 518, 1000 x 4096 x
+    // 30,000 938 and 917, 2000 x 2048 x 50,000 1,688 and 1,671; of 16 tiles the
+    // rows themselves no longer fit beside W (4000 x 4096 x 20,000 2,271 and 2,291).
     if (g.x > 1 && g.x <= 8) {
       p.tile_group = (int)g.y;
       g.y = (g.y + 7) / 8 * 8;
@@ -157,12 +157,13 @@ hipError_t gemm_kd_dw(bool bf16, const void* G, int ldg, const void* X, int64_t 
   p.acc_init = 1;
   p.tile_group = kCceDwGroup;  // as gemm_cce_dw
   // Few tokens: writing dW bounds it, and three small work-groups a CU write
-  // more steadily (whole passes of 16 x 4096 x 100,000 755 and 774 us, 333 x
-  // 2048 x 50,000 448 and 454, but 1000 x 4096 x 30,000 1,016 and 1,001).  So
-  // too where the wide tiles do not fill the chip (8000 x 512 x 20,000, 66 a
-  // strip, 1,077 and 1,263, 7778 x 256 x 1813 165 and 203), and where H is no
-  // multiple of 256 (16 x 4224 x 100,000 726 and 915 with one 512-thread
-  // work-group a CU, 4000 x 4224 x 20,000 2,736 and 2,896).
+  // more steadily (16 x 4096 x 100,000 727 us so and 746 with the wide tiles,
+  // 333 x 2048 x 50,000 395 and 398, but 1000 x 4096 x 30,000 932 and 917; nothing
+  // between 333 and 777 tokens was timed).  So too where the wide tiles do not
+  // fill the chip (8000 x 512 x 20,000, 66 a strip, 1,093 and 1,263, 7778 x 256 x
+  // 1813 153 and 189), and where H is no multiple of 256 (16 x 4224 x 100,000 714
+  // and 904 with one 512-thread work-group a CU, 4000 x 4224 x 20,000 2,680 and
+  // 2,855).
   const bool wide = H % 256 == 0 && N > 512 && ceil_div(w, 128) * (H / 256) >= 2 * kCus;
   auto run = [&](auto shape) {
     using S = decltype(shape);

@@ -249,6 +249,23 @@ def test_kd_plan_errors(change, status):
     assert B.lib().kd_plan(*{**KD_OK, **change}.values(), ctypes.byref(B.KdPlan())) == status
 
 
+def test_kd_workspaces_hold_the_strip_and_the_sums_alone():
+    pad = lambda n: -(-n // 256) * 256
+    for N, H, V, v_chunk in ((8192, 7168, 200_000, 8192), (8200, 640, 10_001, 1024), (777, 512, 20_000, 4096),
+                             (1, 128, 10, 256), (16, 4096, 100_000, 1024), (2000, 1024, 150_000, 256)):
+        p = B.kd_plan(N, H, V, v_chunk, 32)
+        strip = pad(N * min(p.strip, -(-V // 256) * 256) * 2)
+        tiles = -(-N // 256) * (H // (256 if H % 256 == 0 else 128))
+        sums = p.bwd_workspace_bytes - strip  # whole sums of dX; one, or what fills the chip once
+        if tiles > 128:
+            assert sums == pad(4 * N * H)
+        else:
+            assert pad(4 * N * H) <= sums <= pad(4 * N * H * (256 // tiles)) <= 64 << 20
+    # the forward pass: two statistics for each 128 columns of its strip, and two a token
+    p, q = (B.kd_plan(8192, 7168, 200_000, c, 32) for c in (8192, 16_384))
+    assert p.fwd_workspace_bytes == q.fwd_workspace_bytes == 2 * (8192 // 128) * 8192 * 4 + 2 * 8192 * 4
+
+
 def test_kd_temperatures_without_a_reciprocal():
     for T, status in ((1e-39, B.MOE_EINVAL), (1e-38, B.MOE_OK), (3e38, B.MOE_OK)):
         assert B.lib().kd_plan(*{**KD_OK, "temperature": T}.values(), ctypes.byref(B.KdPlan())) == status
