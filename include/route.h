@@ -110,7 +110,8 @@ int route_backward(const route_plan_t* plan, const float* logits, const int32_t*
  * distinct within a row; gates [N][k] fp32 may be any finite values.  Same
  * chunk schedule, buffers, workspace size, numerics and stats as
  * moe_bounded_forward; with that call's topk_idx and gates, Y is bitwise its Y.
- * Errors: as moe_bounded_forward.
+ * Errors: as moe_bounded_forward; MOE_EINVAL also where N > 0 and X, a weight
+ *   matrix or Y is not 16-byte aligned.
  */
 int moe_routed_forward(const moe_plan_t* plan, const void* X, const void* W_gate,
                        const void* W_up, const void* W_down, const int32_t* topk_idx,
@@ -123,7 +124,8 @@ int moe_routed_forward(const moe_plan_t* plan, const void* X, const void* W_gate
  * dX [N][H] through the experts only (the caller adds its router's share);
  * dW_gate, dW_up, dW_down fp32 and dgates [N][k] fp32, bitwise
  * moe_bounded_backward's.  MOE_PLAN_EXACT_DW plans are served.
- * Errors: as moe_bounded_backward.
+ * Errors: as moe_bounded_backward; MOE_EINVAL also where N > 0 and X, dY, dX, a
+ *   weight matrix or its gradient is not 16-byte aligned.
  */
 int moe_routed_backward(const moe_plan_t* plan, const void* X, const void* W_gate,
                         const void* W_up, const void* W_down, const void* dY,

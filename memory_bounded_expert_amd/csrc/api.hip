@@ -14,6 +14,7 @@
 // from the caller's workspace and every kernel goes on the caller's stream.
 #include <algorithm>
 #include <cstring>
+#include <initializer_list>
 
 #include "moe_internal.h"
 #include "route.h"
@@ -323,6 +324,14 @@ MOE_API int moe_bounded_forward(const moe_plan_t* plan, const void* X, const voi
                       workspace, (hipStream_t)stream, stats);
 }
 
+// Whether any of the matrices starts off a 16-byte step: they move in vectors of
+// 16 bytes, and straight into LDS.
+static bool off16(std::initializer_list<const void*> matrices) {
+  uintptr_t bits = 0;
+  for (const void* p : matrices) bits |= (uintptr_t)p;
+  return bits % 16 != 0;
+}
+
 MOE_API int moe_routed_forward(const moe_plan_t* plan, const void* X, const void* W_gate,
                                const void* W_up, const void* W_down, const int32_t* topk_idx,
                                const float* gates, void* Y, void* workspace,
@@ -334,7 +343,7 @@ MOE_API int moe_routed_forward(const moe_plan_t* plan, const void* X, const void
     return MOE_OK;
   }
   if (!workspace) return MOE_EINVAL;
-  if ((uintptr_t)workspace % 256) return MOE_EINVAL;
+  if ((uintptr_t)workspace % 256 || off16({X, W_gate, W_up, W_down, Y})) return MOE_EINVAL;
   if (workspace_bytes < (size_t)P.fwd_workspace_bytes) return MOE_EWORKSPACE;
   (void)hipGetLastError();
   const Layout L = make_layout(P, Pass::Forward, false, false);
@@ -653,7 +662,9 @@ MOE_API int moe_routed_backward(const moe_plan_t* plan, const void* X, const voi
   if (P.N > 0 && (!X || !W_gate || !W_up || !W_down || !dY || !topk_idx || !gates || !dX ||
                   !dgates || !workspace))
     return MOE_EINVAL;
-  if (P.N > 0 && (uintptr_t)workspace % 256) return MOE_EINVAL;
+  if (P.N > 0 && ((uintptr_t)workspace % 256 ||
+                  off16({X, W_gate, W_up, W_down, dY, dX, dW_gate, dW_up, dW_down})))
+    return MOE_EINVAL;
   if (workspace_bytes < (size_t)P.bwd_workspace_bytes) return MOE_EWORKSPACE;
   const BwdCall c = bwd_call(P, X, nullptr, W_gate, W_up, W_down, dY, topk_idx, gates, dX, dW_gate,
                              dW_up, dW_down, nullptr, dgates, nullptr, workspace,

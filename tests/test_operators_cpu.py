@@ -125,6 +125,21 @@ def test_routed_layer_argument_errors():
     assert st.launches == 0
 
 
+def test_routed_layer_refuses_matrices_off_a_16_byte_step():
+    L, ref = B.lib(), ctypes.byref
+    for dtype, by in ((B.MOE_F32, 4), (B.MOE_BF16, 2), (B.MOE_BF16, 8)):
+        p = B.moe_plan_chunks(256, 64, 128, 8, 2, 64, 8, dtype)
+        off = ctypes.c_void_p(0x100000 + by)
+        for i in (0, 1, 2, 3, 6):
+            args = [FAKE] * 7
+            args[i] = off
+            assert L.moe_routed_forward(ref(p), *args, FAKE, 1 << 30, None, None) == B.MOE_EINVAL
+        for i in (0, 1, 2, 3, 4, 7, 8, 9, 10):
+            args = [FAKE] * 12
+            args[i] = off
+            assert L.moe_routed_backward(ref(p), *args, FAKE, 1 << 30, None, None) == B.MOE_EINVAL
+
+
 def test_binding_refuses_wrong_tensors():
     p = B.route_plan(4, 8, 2)
     l = torch.zeros(4, 8)
