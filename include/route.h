@@ -24,9 +24,9 @@
  *           s_e is 0
  * Every order is by value descending, then index ascending.  Scores that
  * decide an order are compared in 64 bits wherever 32 bits could get it wrong,
- * so topk_idx is the definition's wherever fp64 tells the values apart (of two
- * different logits or biases whose values fp64 rounds together, either may come
- * first).  The bias has no gradient.
+ * so topk_idx is the definition's wherever fp64 tells the values apart: values
+ * of different logits or biases, and sums of two, that are equal but for fp64's
+ * rounding may come in either order.  The bias has no gradient.
  *
  * For an upstream gradient dg_s of the gates, with w_s = g_s / scale:
  *   sigmoid:            dl_e = w_s (1 - s_e) (scale dg_s - [renorm] sum_j g_j dg_j)
