@@ -2,7 +2,7 @@
 
 Every HIP source is compiled to an object under ``_build/`` in parallel and
 linked into ``memory_bounded_expert_amd/libmoebound.so``.  Host-side
-symbols are hidden except the C ABI declared in ``include/moebound.h``.
+symbols are hidden except the C ABI declared in ``include/``.
 """
 
 from __future__ import annotations
