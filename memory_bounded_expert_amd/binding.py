@@ -25,6 +25,8 @@ HEADERS = (os.path.join(INCLUDE, "moebound.h"), os.path.join(INCLUDE, "cce.h"))
 # the operators around the layer
 OPERATOR_HEADERS = tuple(os.path.join(INCLUDE, n) for n in
                          ("route.h", "lnorm.h", "embed.h", "distill.h"))
+# the 8-bit path of an expert layer
+EXPERT_HEADERS = tuple(os.path.join(INCLUDE, n) for n in ("rms.h", "q8.h", "gmm.h"))
 
 MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EWORKSPACE, MOE_EHIP = 0, 1, 2, 3, 4
 STAGES = {"router": 0, "topk": 1, "plan": 2, "gather": 3, "gemm_up": 4, "gemm_down": 5,
@@ -32,6 +34,7 @@ STAGES = {"router": 0, "topk": 1, "plan": 2, "gather": 3, "gemm_up": 4, "gemm_do
 BSTAGES = {"zero": 0, "transpose": 1, "plan": 2, "recompute": 3, "dh": 4, "wgrad_down": 5,
            "wgrad_gate_up": 6, "dx": 7, "combine_bwd": 8, "dwr": 9}
 MOE_F32, MOE_BF16 = 0, 1
+GMM_BF16, GMM_Q8 = 0, 1
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 CCE_STAGES = {"logits": 0, "fold": 1, "grad": 2, "dx": 3, "dw": 4}
 
@@ -101,6 +104,29 @@ class KdPlan(_c.Structure):
         ("temperature", _c.c_float), ("dw_dtype", _c.c_int32), ("S", _c.c_int32),
         ("strip", _c.c_int32), ("reserved0", _c.c_int32), ("strip_bound_bytes", _c.c_int64), ("fwd_workspace_bytes", _c.c_int64),
         ("bwd_workspace_bytes", _c.c_int64),
+    ]
+
+
+class RmsPlan(_c.Structure):
+    _fields_ = [
+        ("magic", _c.c_uint32), ("dtype", _c.c_int32), ("N", _c.c_int64), ("H", _c.c_int32),
+        ("eps", _c.c_float), ("row_pitch", _c.c_int32), ("scale_pitch", _c.c_int32),
+        ("bwd_workspace_bytes", _c.c_int64),
+    ]
+
+
+class Q8Plan(_c.Structure):
+    _fields_ = [
+        ("magic", _c.c_uint32), ("dtype", _c.c_int32), ("N", _c.c_int64), ("H", _c.c_int32),
+        ("row_pitch", _c.c_int32), ("scale_pitch", _c.c_int32), ("reserved0", _c.c_int32),
+    ]
+
+
+class GmmPlan(_c.Structure):
+    _fields_ = [
+        ("magic", _c.c_uint32), ("operands", _c.c_int32), ("R", _c.c_int64), ("K", _c.c_int32),
+        ("N", _c.c_int32), ("E", _c.c_int32), ("row_pitch", _c.c_int32),
+        ("fwd_workspace_bytes", _c.c_int64), ("bwd_workspace_bytes", _c.c_int64),
     ]
 
 
@@ -191,6 +217,37 @@ def lib() -> ctypes.CDLL:
     L.kd_forward.argtypes = [_c.POINTER(KdPlan)] + [_vp] * 8 + [_c.c_size_t, _vp]
     L.kd_backward.restype = _c.c_int
     L.kd_backward.argtypes = [_c.POINTER(KdPlan)] + [_vp] * 10 + [_c.c_size_t, _vp]
+    L.rms_plan.restype = _c.c_int
+    L.rms_plan.argtypes = [_c.c_int64, _c.c_int32, _c.c_int32, _c.c_float, _c.POINTER(RmsPlan)]
+    L.rms_forward.restype = _c.c_int
+    L.rms_forward.argtypes = [_c.POINTER(RmsPlan)] + [_vp] * 7
+    L.rms_forward_q8.restype = _c.c_int
+    L.rms_forward_q8.argtypes = [_c.POINTER(RmsPlan)] + [_vp] * 8
+    L.rms_backward.restype = _c.c_int
+    L.rms_backward.argtypes = [_c.POINTER(RmsPlan)] + [_vp] * 8 + [_c.c_size_t, _vp]
+    L.q8_plan.restype = _c.c_int
+    L.q8_plan.argtypes = [_c.c_int64, _c.c_int32, _c.c_int32, _c.POINTER(Q8Plan)]
+    L.q8_pack.restype = _c.c_int
+    L.q8_pack.argtypes = [_c.POINTER(Q8Plan)] + [_vp] * 4
+    L.q8_unpack.restype = _c.c_int
+    L.q8_unpack.argtypes = [_c.POINTER(Q8Plan)] + [_vp] * 4
+    L.q8_pack_weights.restype = _c.c_int
+    L.q8_pack_weights.argtypes = [_c.c_int32] * 4 + [_vp] * 6
+    L.q8_swiglu_forward.restype = _c.c_int
+    L.q8_swiglu_forward.argtypes = [_c.POINTER(Q8Plan)] + [_vp] * 9
+    L.q8_swiglu_backward.restype = _c.c_int
+    L.q8_swiglu_backward.argtypes = [_c.POINTER(Q8Plan)] + [_vp] * 8
+    L.gmm_plan.restype = _c.c_int
+    L.gmm_plan.argtypes = [_c.c_int64] + [_c.c_int32] * 4 + [_c.POINTER(GmmPlan)]
+    for f in (L.gmm_forward, L.gmm_backward_dx):
+        f.restype = _c.c_int
+        f.argtypes = [_c.POINTER(GmmPlan)] + [_vp] * 5 + [_c.c_size_t, _vp]
+    L.gmm_backward_dw.restype = _c.c_int
+    L.gmm_backward_dw.argtypes = [_c.POINTER(GmmPlan)] + [_vp] * 4 + [_c.c_int32, _vp, _c.c_size_t, _vp]
+    L.gmm8_forward.restype = _c.c_int
+    L.gmm8_forward.argtypes = [_c.POINTER(GmmPlan)] + [_vp] * 7 + [_c.c_size_t, _vp]
+    L.gmm8_backward_dw.restype = _c.c_int
+    L.gmm8_backward_dw.argtypes = [_c.POINTER(GmmPlan)] + [_vp] * 5 + [_c.c_int32, _vp, _c.c_size_t, _vp]
     _LIB = L
     return L
 
@@ -205,11 +262,16 @@ def declared_operators() -> list:
     return _declared(OPERATOR_HEADERS, "moe|route|lnorm|embed|kd")
 
 
+def declared_expert_operators() -> list:
+    """Function names declared in the headers of the 8-bit path of an expert layer."""
+    return _declared(EXPERT_HEADERS, "rms|q8|gmm8?")
+
+
 def _declared(headers, prefixes) -> list:
     names = set()
     for h in headers:
         text = re.sub(r"/\*.*?\*/", "", open(h).read(), flags=re.S)
-        names |= set(re.findall(r"\b((?:%s)_[a-z_]+)\s*\(" % prefixes, text))
+        names |= set(re.findall(r"\b((?:%s)_[a-z0-9_]+)\s*\(" % prefixes, text))
     return sorted(names)
 
 
@@ -321,8 +383,9 @@ def moe_plan_set_flags(plan: MoePlan, flags: int) -> MoePlan:
 
 
 def workspace(plan, kind: str, device) -> torch.Tensor:
-    """Workspace of a MoePlan ("fwd", "bwd", "debug"), CcePlan or KdPlan ("fwd", "bwd"),
-    LnormPlan or EmbedPlan ("bwd"); "both" is large enough for "fwd" and "bwd"."""
+    """Workspace of a MoePlan ("fwd", "bwd", "debug"), CcePlan, KdPlan or GmmPlan ("fwd",
+    "bwd"), LnormPlan, EmbedPlan or RmsPlan ("bwd"); "both" is large enough for "fwd" and
+    "bwd"."""
     if kind == "both":
         n = max(plan.fwd_workspace_bytes, plan.bwd_workspace_bytes)
     else:
@@ -780,3 +843,275 @@ def kd_backward(plan: KdPlan, X, W, t_idx, t_logit, lse, y_top, dloss, dX=None, 
                                  _ptr(lse), _ptr(y_top), _ptr(dloss), _ptr(dX), _ptr(dW), _ptr(ws),
                                  ws_bytes, _stream(dev, None)), "kd_backward")
     return dX, dW
+
+
+# ---- root-mean-square norm with the residual's addition
+
+E4M3, E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def rms_plan(N: int, H: int, dtype: int = MOE_BF16, eps: float = 1e-6) -> RmsPlan:
+    plan = RmsPlan()
+    _check(lib().rms_plan(N, H, dtype, eps, ctypes.byref(plan)), "rms_plan")
+    return plan
+
+
+def _rms_inputs(plan, X, gamma, residual, S):
+    dev, dt = X.device, torch_dtype(plan.dtype)
+    N, H = plan.N, plan.H
+    _expect(X, "X", (N, H), dt, dev)
+    _expect(gamma, "gamma", (H,), torch.float32, dev)
+    if residual is not None:
+        _expect(residual, "residual", (N, H), dt, dev)
+    elif S is not None:
+        raise ValueError("S is X itself without a residual")
+    return dev, dt, N, H
+
+
+def rms_forward(plan: RmsPlan, X, gamma, residual=None, S=None, Y=None, rstd=None, stream=None):
+    """Returns (Y [N, H], S = X + residual [N, H], rstd [N]); S is X itself without a residual."""
+    dev, dt, N, H = _rms_inputs(plan, X, gamma, residual, S)
+    with _on(dev, stream):
+        if residual is not None:
+            S = _out(S, "S", (N, H), dt, dev)
+        Y = _out(Y, "Y", (N, H), dt, dev)
+        rstd = _out(rstd, "rstd", (N,), torch.float32, dev)
+        _check(lib().rms_forward(ctypes.byref(plan), _ptr(X), _ptr(residual), _ptr(gamma), _ptr(S),
+                                 _ptr(Y), _ptr(rstd), _stream(dev, None)), "rms_forward")
+    return Y, X if S is None else S, rstd
+
+
+def rms_forward_q8(plan: RmsPlan, X, gamma, residual=None, S=None, Yq=None, Ys=None, rstd=None,
+                   stream=None):
+    """Returns (Yq, Ys, S, rstd): Y as rows of 8 bits (see q8_pack), the rest as rms_forward."""
+    dev, dt, N, H = _rms_inputs(plan, X, gamma, residual, S)
+    with _on(dev, stream):
+        if residual is not None:
+            S = _out(S, "S", (N, H), dt, dev)
+        Yq = _out(Yq, "Yq", (N, plan.row_pitch), E4M3, dev)
+        Ys = _out(Ys, "Ys", (N, plan.scale_pitch), E8M0, dev)
+        rstd = _out(rstd, "rstd", (N,), torch.float32, dev)
+        _check(lib().rms_forward_q8(ctypes.byref(plan), _ptr(X), _ptr(residual), _ptr(gamma),
+                                    _ptr(S), _ptr(Yq), _ptr(Ys), _ptr(rstd), _stream(dev, None)),
+               "rms_forward_q8")
+    return Yq, Ys, X if S is None else S, rstd
+
+
+def rms_backward(plan: RmsPlan, S, gamma, dY, rstd, dS=None, dX=None, dgamma=None, ws=None,
+                 stream=None):
+    """Returns (dX [N, H], the gradient of X and of the residual alike, dgamma [H])."""
+    dev = S.device
+    dt, f32 = torch_dtype(plan.dtype), torch.float32
+    N, H = plan.N, plan.H
+    for t, n, s, d in ((S, "S", (N, H), dt), (gamma, "gamma", (H,), f32), (dY, "dY", (N, H), dt),
+                       (rstd, "rstd", (N,), f32)):
+        _expect(t, n, s, d, dev)
+    if dS is not None:
+        _expect(dS, "dS", (N, H), dt, dev)
+    with _on(dev, stream):
+        dX = _out(dX, "dX", (N, H), dt, dev)
+        dgamma = _out(dgamma, "dgamma", (H,), f32, dev)
+        ws, ws_bytes = _workspace(ws, plan, "bwd", dev)
+        _check(lib().rms_backward(ctypes.byref(plan), _ptr(S), _ptr(gamma), _ptr(dY), _ptr(rstd),
+                                  _ptr(dS), _ptr(dX), _ptr(dgamma), _ptr(ws), ws_bytes,
+                                  _stream(dev, None)), "rms_backward")
+    return dX, dgamma
+
+
+# ---- rows in 8 bits, SwiGLU with checkpoints in 8 bits
+
+
+def q8_plan(N: int, H: int, dtype: int = MOE_BF16) -> Q8Plan:
+    plan = Q8Plan()
+    _check(lib().q8_plan(N, H, dtype, ctypes.byref(plan)), "q8_plan")
+    return plan
+
+
+def _expect_q8(plan, q, s, name, dev):
+    _expect(q, name + "q", (plan.N, plan.row_pitch), E4M3, dev)
+    _expect(s, name + "s", (plan.N, plan.scale_pitch), E8M0, dev)
+
+
+def _out_q8(plan, q, s, name, dev):
+    return (_out(q, name + "q", (plan.N, plan.row_pitch), E4M3, dev),
+            _out(s, name + "s", (plan.N, plan.scale_pitch), E8M0, dev))
+
+
+def q8_pack(plan: Q8Plan, X, q=None, s=None, stream=None):
+    """Returns (q [N, row_pitch] float8_e4m3fn, s [N, scale_pitch] float8_e8m0fnu)."""
+    dev = X.device
+    _expect(X, "X", (plan.N, plan.H), torch_dtype(plan.dtype), dev)
+    with _on(dev, stream):
+        q, s = _out_q8(plan, q, s, "", dev)
+        _check(lib().q8_pack(ctypes.byref(plan), _ptr(X), _ptr(q), _ptr(s), _stream(dev, None)),
+               "q8_pack")
+    return q, s
+
+
+def q8_unpack(plan: Q8Plan, q, s, X=None, stream=None):
+    """Returns the values X [N, H]."""
+    dev = q.device
+    _expect_q8(plan, q, s, "", dev)
+    with _on(dev, stream):
+        X = _out(X, "X", (plan.N, plan.H), torch_dtype(plan.dtype), dev)
+        _check(lib().q8_unpack(ctypes.byref(plan), _ptr(q), _ptr(s), _ptr(X), _stream(dev, None)),
+               "q8_unpack")
+    return X
+
+
+def q8_pack_weights(W, along="both", stream=None):
+    """E matrices W [E, K, N] in 8 bits with a scale per 128 x 128: along "K" (qt [E, N, K to 128],
+    st), for products that sum over K; along "N" (q [E, K, N to 128], s), for those that sum over N;
+    or "both" (qt, st, q, s)."""
+    if along not in ("K", "N", "both"):
+        raise ValueError(f"along: {along!r}")
+    if W.dim() != 3:
+        raise ValueError(f"W: {W.dim()} dimensions, 3 are wanted")
+    dev, dtype = W.device, moe_dtype(W.dtype)
+    E, K, N = W.shape
+    _expect(W, "W", (E, K, N), W.dtype, dev)
+    kb, nb = -(-K // 128), -(-N // 128)
+    with _on(dev, stream):
+        qt = st = q = s = None
+        if along != "N":
+            qt = torch.empty((E, N, kb * 128), dtype=E4M3, device=dev)
+            st = torch.empty((E, nb, -(-kb // 4) * 4), dtype=E8M0, device=dev)
+        if along != "K":
+            q = torch.empty((E, K, nb * 128), dtype=E4M3, device=dev)
+            s = torch.empty((E, kb, -(-nb // 4) * 4), dtype=E8M0, device=dev)
+        _check(lib().q8_pack_weights(E, K, N, dtype, _ptr(W), _ptr(q), _ptr(s), _ptr(qt), _ptr(st),
+                                     _stream(dev, None)), "q8_pack_weights")
+    return {"K": (qt, st), "N": (q, s), "both": (qt, st, q, s)}[along]
+
+
+def q8_swiglu_forward(plan: Q8Plan, A, U, keep=True, H=None, kept=None, stream=None):
+    """Returns (Hq, Hs, kept): silu(A) U in 8 bits, and the checkpoint (Aq, As, Uq, Us) of A and U
+    that q8_swiglu_backward reads (None with keep=False).  H: a pair (Hq, Hs) to write."""
+    dev, dt = A.device, torch_dtype(plan.dtype)
+    _expect(A, "A", (plan.N, plan.H), dt, dev)
+    _expect(U, "U", (plan.N, plan.H), dt, dev)
+    with _on(dev, stream):
+        Hq, Hs = _out_q8(plan, *(H or (None, None)), "H", dev)
+        if keep or kept is not None:
+            kept = kept or (None,) * 4
+            kept = _out_q8(plan, *kept[:2], "A", dev) + _out_q8(plan, *kept[2:], "U", dev)
+        _check(lib().q8_swiglu_forward(ctypes.byref(plan), _ptr(A), _ptr(U), _ptr(Hq), _ptr(Hs),
+                                       *(map(_ptr, kept or (None,) * 4)), _stream(dev, None)),
+               "q8_swiglu_forward")
+    return Hq, Hs, kept
+
+
+def q8_swiglu_backward(plan: Q8Plan, kept, dH, dA=None, dU=None, stream=None):
+    """Returns (dA, dU) [N, H] at the checkpoint's values."""
+    dev, dt = dH.device, torch_dtype(plan.dtype)
+    Aq, As, Uq, Us = kept
+    _expect_q8(plan, Aq, As, "A", dev)
+    _expect_q8(plan, Uq, Us, "U", dev)
+    _expect(dH, "dH", (plan.N, plan.H), dt, dev)
+    with _on(dev, stream):
+        dA = _out(dA, "dA", (plan.N, plan.H), dt, dev)
+        dU = _out(dU, "dU", (plan.N, plan.H), dt, dev)
+        _check(lib().q8_swiglu_backward(ctypes.byref(plan), _ptr(Aq), _ptr(As), _ptr(Uq), _ptr(Us),
+                                        _ptr(dH), _ptr(dA), _ptr(dU), _stream(dev, None)),
+               "q8_swiglu_backward")
+    return dA, dU
+
+
+# ---- products grouped by expert
+
+
+def gmm_plan(R: int, K: int, N: int, E: int, operands: int = GMM_BF16) -> GmmPlan:
+    plan = GmmPlan()
+    _check(lib().gmm_plan(R, K, N, E, operands, ctypes.byref(plan)), "gmm_plan")
+    return plan
+
+
+def _gmm_offsets(plan, offsets, dev):
+    if offsets is None:
+        if plan.E != 1:
+            raise ValueError("offsets are required where there is more than one expert")
+    else:
+        _expect(offsets, "offsets", (plan.E + 1,), torch.int32, dev)
+
+
+def _gmm_call(name, plan, kind, tensors, offsets, out, more, ws, dev):
+    needed = plan.fwd_workspace_bytes if kind == "fwd" else plan.bwd_workspace_bytes
+    ws, ws_bytes = _workspace(ws, plan, kind, dev) if needed or ws is not None else (None, 0)
+    _check(getattr(lib(), name)(ctypes.byref(plan), *map(_ptr, tensors), _ptr(offsets), _ptr(out),
+                                *more, _ptr(ws), ws_bytes, _stream(dev, None)), name)
+    return out
+
+
+def gmm_forward(plan: GmmPlan, X, W, offsets=None, Y=None, ws=None, stream=None):
+    """Returns Y [R, N]: rows offsets[e] to offsets[e + 1] of X [R, K] times W[e] [K, N] (rows of no
+    expert are left as they are).  offsets None, with one expert: all rows."""
+    dev, bf = X.device, torch.bfloat16
+    R, K, N, E = plan.R, plan.K, plan.N, plan.E
+    _expect(X, "X", (R, K), bf, dev)
+    _expect(W, "W", (E, K, N), bf, dev)
+    _gmm_offsets(plan, offsets, dev)
+    with _on(dev, stream):
+        Y = _out(Y, "Y", (R, N), bf, dev)
+        return _gmm_call("gmm_forward", plan, "fwd", (X, W), offsets, Y, (), ws, dev)
+
+
+def gmm_backward_dx(plan: GmmPlan, dY, W, offsets=None, dX=None, ws=None, stream=None):
+    """Returns dX [R, K] = dY [R, N] W[e]^T."""
+    dev, bf = dY.device, torch.bfloat16
+    R, K, N, E = plan.R, plan.K, plan.N, plan.E
+    _expect(dY, "dY", (R, N), bf, dev)
+    _expect(W, "W", (E, K, N), bf, dev)
+    _gmm_offsets(plan, offsets, dev)
+    with _on(dev, stream):
+        dX = _out(dX, "dX", (R, K), bf, dev)
+        return _gmm_call("gmm_backward_dx", plan, "fwd", (dY, W), offsets, dX, (), ws, dev)
+
+
+def gmm_backward_dw(plan: GmmPlan, X, dY, offsets=None, dW=None, accumulate=False, ws=None,
+                    stream=None):
+    """Returns dW [E, K, N] fp32 = X_e^T dY_e, added to the dW given with accumulate."""
+    dev, bf = X.device, torch.bfloat16
+    R, K, N, E = plan.R, plan.K, plan.N, plan.E
+    _expect(X, "X", (R, K), bf, dev)
+    _expect(dY, "dY", (R, N), bf, dev)
+    _gmm_offsets(plan, offsets, dev)
+    if accumulate and dW is None:
+        raise ValueError("accumulate needs the dW to add to")
+    with _on(dev, stream):
+        dW = _out(dW, "dW", (E, K, N), torch.float32, dev)
+        return _gmm_call("gmm_backward_dw", plan, "bwd", (X, dY), offsets, dW, (int(accumulate),), ws, dev)
+
+
+def _expect_gmm8_rows(plan, Xq, Xs, dev):
+    _expect(Xq, "Xq", (plan.R, plan.row_pitch), E4M3, dev)
+    _expect(Xs, "Xs", (plan.R, -(-plan.K // 512) * 4), E8M0, dev)
+
+
+def gmm8_forward(plan: GmmPlan, Xq, Xs, Wq, Ws, offsets=None, Y=None, ws=None, stream=None):
+    """Returns Y [R, N] bfloat16 from rows in 8 bits (q8_pack) and weights in 8 bits along K
+    (q8_pack_weights(W, "K"))."""
+    dev = Xq.device
+    R, K, N, E = plan.R, plan.K, plan.N, plan.E
+    _expect_gmm8_rows(plan, Xq, Xs, dev)
+    _expect(Wq, "Wq", (E, N, plan.row_pitch), E4M3, dev)
+    _expect(Ws, "Ws", (E, -(-N // 128), -(-K // 512) * 4), E8M0, dev)
+    _gmm_offsets(plan, offsets, dev)
+    with _on(dev, stream):
+        Y = _out(Y, "Y", (R, N), torch.bfloat16, dev)
+        return _gmm_call("gmm8_forward", plan, "fwd", (Xq, Xs, Wq, Ws), offsets, Y, (), ws, dev)
+
+
+def gmm8_backward_dw(plan: GmmPlan, Xq, Xs, dY, offsets=None, dW=None, accumulate=False, ws=None,
+                     stream=None):
+    """Returns dW [E, K, N] fp32 from X in 8 bits and dY bfloat16, added to the dW given with
+    accumulate."""
+    dev = Xq.device
+    R, K, N, E = plan.R, plan.K, plan.N, plan.E
+    _expect_gmm8_rows(plan, Xq, Xs, dev)
+    _expect(dY, "dY", (R, N), torch.bfloat16, dev)
+    _gmm_offsets(plan, offsets, dev)
+    if accumulate and dW is None:
+        raise ValueError("accumulate needs the dW to add to")
+    with _on(dev, stream):
+        dW = _out(dW, "dW", (E, K, N), torch.float32, dev)
+        return _gmm_call("gmm8_backward_dw", plan, "bwd", (Xq, Xs, dY), offsets, dW, (int(accumulate),), ws, dev)

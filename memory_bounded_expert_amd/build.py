@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "libmoebound.so")
 
 SOURCES = ["api.hip", "route.hip", "plan.hip", "dispatch.hip", "gemm_fwd.hip", "gemm_bwd.hip",
            "cce.hip", "gemm_cce.hip", "noalloc.hip", "exact_dw.hip", "route_score.hip",
-           "lnorm.hip", "embed.hip", "distill.hip"]
+           "lnorm.hip", "embed.hip", "distill.hip", "rms.hip", "q8.hip", "gmm.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

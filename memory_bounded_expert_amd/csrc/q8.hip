@@ -1,0 +1,348 @@
+// Rows in 8 bits, and SwiGLU with activation checkpoints in 8 bits (include/q8.h).
+//
+// All of it moves a few bytes per operation and is bound by HBM.  A block of 128
+// columns is 16 lanes with eight columns each, so its scale is a reduction over a
+// row of lanes; every value is read once.
+#include <algorithm>
+
+#include "device_common.hpp"
+#include "moe_internal.h"
+#include "q8.h"
+#include "q8_ops.hpp"
+#include "wave_ops.hpp"
+
+#define MOE_API extern "C" __attribute__((visibility("default")))
+
+namespace moe {
+namespace {
+
+constexpr uint32_t kQ8Magic = 0x51385031u;  // "Q8P1"
+constexpr unsigned kMaxGroups = 1u << 16;
+
+// Eight values at p, of which n (maybe none) are there; the rest 0.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, float* v) {
+  constexpr int EPC = Elem<T>::kPer16B;
+#pragma unroll
+  for (int c = 0; c < 8; c += EPC) {
+    if (n >= c + EPC) {
+      unpack16(*reinterpret_cast<const u32x4_any_t*>(p + c), v + c, T());
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) v[c + e] = c + e < n ? Elem<T>::to_f(p[c + e]) : 0.f;
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int n, const float* v) {
+  constexpr int EPC = Elem<T>::kPer16B;
+#pragma unroll
+  for (int c = 0; c < 8; c += EPC) {
+    if (n >= c + EPC) {
+      *reinterpret_cast<u32x4_any_t*>(p + c) = pack16(v + c, T());
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPC; ++e)
+        if (c + e < n) p[c + e] = Elem<T>::from_f(v[c + e]);
+    }
+  }
+}
+
+// Where a row of lanes' block goes.
+struct Packed {
+  uint8_t *q, *s;
+};
+struct Shape8 {
+  int64_t units;  // rows times blocks
+  int H, blocks, row_pitch, scale_pitch;
+};
+
+// Writes a lane's eight values of block b of row r, with the block's scale; the
+// row's last block writes the scales' padding too.
+__device__ __forceinline__ void put8(const Packed& to, const Shape8& sh, int64_t r, int b, int lane,
+                                     const float* v) {
+  float amax = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, q8_magnitude(v[e]));
+  const uint32_t byte = q8_scale_byte(run_maxf<16>(amax));
+  const float inv = q8_inverse(byte);
+  *reinterpret_cast<uint2*>(to.q + r * sh.row_pitch + b * kQBlock + lane * 8) =
+      make_uint2(q8_round4(v, inv), q8_round4(v + 4, inv));
+  uint8_t* s = to.s + r * sh.scale_pitch;
+  if (lane == 0) s[b] = (uint8_t)byte;
+  if (b == sh.blocks - 1 && lane < sh.scale_pitch - sh.blocks) s[sh.blocks + lane] = kQOne;
+}
+__device__ __forceinline__ void get8(const uint8_t* q, const uint8_t* s, const Shape8& sh, int64_t r,
+                                     int b, int lane, float* v) {
+  const float scale = q8_scale(s[r * sh.scale_pitch + b]);
+  const uint2 w = *reinterpret_cast<const uint2*>(q + r * sh.row_pitch + b * kQBlock + lane * 8);
+  q8_values4(w.x, scale, v);
+  q8_values4(w.y, scale, v + 4);
+}
+
+// Calls f(row, block, lane of the block, column, columns there) for this thread's
+// share of all blocks.
+template <typename F>
+__device__ __forceinline__ void each_block(const Shape8& sh, F f) {
+  const int lane = threadIdx.x & 15;
+  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4); u < sh.units;
+       u += (int64_t)gridDim.x * (kThreads / 16)) {
+    const int64_t r = u / sh.blocks;
+    const int b = (int)(u - r * sh.blocks), col = b * kQBlock + lane * 8;
+    f(r, b, lane, col, sh.H - col);
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void pack_kernel(const T* __restrict__ X, const Packed to, const Shape8 sh) {
+  each_block(sh, [&](int64_t r, int b, int lane, int col, int n) {
+    float v[8];
+    load8(X + r * sh.H + col, n, v);
+    put8(to, sh, r, b, lane, v);
+  });
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void unpack_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
+                                                          T* __restrict__ X, const Shape8 sh) {
+  each_block(sh, [&](int64_t r, int b, int lane, int col, int n) {
+    float v[8];
+    get8(q, s, sh, r, b, lane, v);
+    store8(X + r * sh.H + col, n, v);
+  });
+}
+
+template <typename T, bool KEEP>
+__global__ __launch_bounds__(kThreads) void swiglu_forward_kernel(const T* __restrict__ A, const T* __restrict__ U,
+                                                                  const Packed h, const Packed ka,
+                                                                  const Packed ku, const Shape8 sh) {
+  each_block(sh, [&](int64_t r, int b, int lane, int col, int n) {
+    float a[8], u[8], v[8];
+    load8(A + r * sh.H + col, n, a);
+    load8(U + r * sh.H + col, n, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = a[e] / (1.f + expf(-a[e])) * u[e];
+    put8(h, sh, r, b, lane, v);
+    if constexpr (KEEP) {
+      put8(ka, sh, r, b, lane, a);
+      put8(ku, sh, r, b, lane, u);
+    }
+  });
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
+    const uint8_t* __restrict__ Aq, const uint8_t* __restrict__ As, const uint8_t* __restrict__ Uq,
+    const uint8_t* __restrict__ Us, const T* dH, T* dA, T* __restrict__ dU, const Shape8 sh) {
+  each_block(sh, [&](int64_t r, int b, int lane, int col, int n) {
+    float a[8], u[8], d[8];
+    get8(Aq, As, sh, r, b, lane, a);
+    get8(Uq, Us, sh, r, b, lane, u);
+    load8(dH + r * sh.H + col, n, d);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float g = 1.f / (1.f + expf(-a[e]));
+      u[e] = d[e] * u[e] * g * fmaf(a[e], 1.f - g, 1.f);
+      d[e] = d[e] * a[e] * g;
+    }
+    store8(dA + r * sh.H + col, n, u);
+    store8(dU + r * sh.H + col, n, d);
+  });
+}
+
+// A 128 x 128 block of one matrix per work-group: read once into registers, its
+// scale by a reduction over the work-group, written along both axes (the second
+// through LDS).  Run once for weights that stay.
+constexpr int kTrPitch = kQBlock + 4;
+template <typename T>
+__global__ __launch_bounds__(kThreads) void pack_weights_kernel(
+    const T* __restrict__ W, int K, int N, uint8_t* __restrict__ q, uint8_t* __restrict__ s,
+    uint8_t* __restrict__ qt, uint8_t* __restrict__ st) {
+  __shared__ float red[kThreads / 64];
+  __shared__ __attribute__((aligned(16))) uint8_t tile[kQBlock * kTrPitch];
+  const int kb = blockIdx.x, nb = blockIdx.y, e = blockIdx.z;
+  const int lane = threadIdx.x & 15, row = threadIdx.x >> 4;
+  const int kblocks = q8_blocks(K), nblocks = q8_blocks(N);
+  const T* w = W + (int64_t)e * K * N;
+  const int col = nb * kQBlock + lane * 8;
+  float v[8][8], amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int k = kb * kQBlock + i * 16 + row;
+    load8(w + (int64_t)min(k, K - 1) * N + min(col, N), k < K ? N - col : 0, v[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, q8_magnitude(v[i][j]));
+  }
+  amax = run_maxf<64>(amax);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
+  __syncthreads();
+  amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const uint32_t byte = q8_scale_byte(amax);
+  const float inv = q8_inverse(byte);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int k = kb * kQBlock + i * 16 + row;
+    const uint2 p = make_uint2(q8_round4(v[i], inv), q8_round4(v[i] + 4, inv));
+    if (q && k < K)
+      *reinterpret_cast<uint2*>(q + ((int64_t)e * K + k) * (nblocks * kQBlock) + col) = p;
+    *reinterpret_cast<uint32_t*>(tile + (i * 16 + row) * kTrPitch + lane * 8) = p.x;
+    *reinterpret_cast<uint32_t*>(tile + (i * 16 + row) * kTrPitch + lane * 8 + 4) = p.y;
+  }
+  if (s && threadIdx.x == 0) {
+    uint8_t* to = s + ((int64_t)e * kblocks + kb) * q8_scale_pitch(N);
+    to[nb] = (uint8_t)byte;
+    if (nb == nblocks - 1)
+      for (int b = nblocks; b < q8_scale_pitch(N); ++b) to[b] = kQOne;
+  }
+  if (st && threadIdx.x == 0) {
+    uint8_t* to = st + ((int64_t)e * nblocks + nb) * q8_scale_pitch(K);
+    to[kb] = (uint8_t)byte;
+    if (kb == kblocks - 1)
+      for (int b = kblocks; b < q8_scale_pitch(K); ++b) to[b] = kQOne;
+  }
+  if (!qt) return;
+  __syncthreads();
+  // thread t: column t / 2 of the block, one half of its 128 rows
+  const int n = threadIdx.x >> 1, k0 = (threadIdx.x & 1) * 64;
+  if (nb * kQBlock + n >= N) return;
+  uint8_t* to = qt + ((int64_t)e * N + nb * kQBlock + n) * (kblocks * kQBlock) + kb * kQBlock + k0;
+#pragma unroll
+  for (int c = 0; c < 64; c += 16) {
+    uint32_t word[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint8_t* from = tile + (k0 + c + i * 4) * kTrPitch + n;
+      word[i] = (uint32_t)from[0] | (uint32_t)from[kTrPitch] << 8 | (uint32_t)from[2 * kTrPitch] << 16 |
+                (uint32_t)from[3 * kTrPitch] << 24;
+    }
+    *reinterpret_cast<u32x4_t*>(to + c) = u32x4_t{word[0], word[1], word[2], word[3]};
+  }
+}
+
+Shape8 shape_of(const q8_plan_t& P) {
+  const int blocks = q8_blocks(P.H);
+  return Shape8{P.N * blocks, P.H, blocks, P.row_pitch, P.scale_pitch};
+}
+unsigned groups_of(const Shape8& sh) {
+  return (unsigned)std::min<int64_t>(ceil_div(sh.units, kThreads / 16), kMaxGroups);
+}
+bool plan_ok(const q8_plan_t* p) { return p != nullptr && p->magic == kQ8Magic; }
+// q on a 16-byte step, s on a 4-byte step, both there
+bool pair_ok(const void* q, const void* s) {
+  return q && s && (uintptr_t)q % 16 == 0 && (uintptr_t)s % 4 == 0;
+}
+bool elem_ok(const q8_plan_t& P, const void* p) { return p && (uintptr_t)p % elem_bytes(P.dtype) == 0; }
+Packed packed(void* q, void* s) { return Packed{(uint8_t*)q, (uint8_t*)s}; }
+int launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API int q8_plan(int64_t N, int32_t H, int32_t dtype, q8_plan_t* out) {
+  if (!out || N < 0 || H < 1) return MOE_EINVAL;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EINVAL;
+  if (H > 65536 || N >= ((int64_t)1 << 31)) return MOE_EUNSUPPORTED;
+  q8_plan_t p{};
+  p.magic = kQ8Magic;
+  p.dtype = dtype;
+  p.N = N;
+  p.H = H;
+  p.row_pitch = q8_row_pitch(H);
+  p.scale_pitch = q8_scale_pitch(H);
+  *out = p;
+  return MOE_OK;
+}
+
+MOE_API int q8_pack(const q8_plan_t* plan, const void* X, void* q, void* s, void* stream) {
+  if (!plan_ok(plan)) return MOE_EINVAL;
+  if (plan->N == 0) return MOE_OK;
+  if (!elem_ok(*plan, X) || !pair_ok(q, s)) return MOE_EINVAL;
+  const Shape8 sh = shape_of(*plan);
+  (void)hipGetLastError();
+  if (plan->dtype == MOE_BF16)
+    pack_kernel<bf16_t><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>((const bf16_t*)X, packed(q, s), sh);
+  else
+    pack_kernel<float><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>((const float*)X, packed(q, s), sh);
+  return launched();
+}
+
+MOE_API int q8_unpack(const q8_plan_t* plan, const void* q, const void* s, void* X, void* stream) {
+  if (!plan_ok(plan)) return MOE_EINVAL;
+  if (plan->N == 0) return MOE_OK;
+  if (!elem_ok(*plan, X) || !pair_ok(q, s)) return MOE_EINVAL;
+  const Shape8 sh = shape_of(*plan);
+  (void)hipGetLastError();
+  if (plan->dtype == MOE_BF16)
+    unpack_kernel<bf16_t><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>((const uint8_t*)q, (const uint8_t*)s, (bf16_t*)X, sh);
+  else
+    unpack_kernel<float><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>((const uint8_t*)q, (const uint8_t*)s, (float*)X, sh);
+  return launched();
+}
+
+MOE_API int q8_pack_weights(int32_t E, int32_t K, int32_t N, int32_t dtype, const void* W, void* q,
+                            void* s, void* qt, void* st, void* stream) {
+  if (E < 0 || K < 1 || N < 1 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_EINVAL;
+  if (K > 65536 || N > 65536 || E > 65535) return MOE_EUNSUPPORTED;
+  if (E == 0) return MOE_OK;
+  if (!W || (uintptr_t)W % elem_bytes(dtype) || (!q && !qt)) return MOE_EINVAL;
+  if ((q || s) && !pair_ok(q, s)) return MOE_EINVAL;
+  if ((qt || st) && !pair_ok(qt, st)) return MOE_EINVAL;
+  const dim3 grid(q8_blocks(K), q8_blocks(N), E);
+  (void)hipGetLastError();
+  if (dtype == MOE_BF16)
+    pack_weights_kernel<bf16_t><<<grid, kThreads, 0, (hipStream_t)stream>>>(
+        (const bf16_t*)W, K, N, (uint8_t*)q, (uint8_t*)s, (uint8_t*)qt, (uint8_t*)st);
+  else
+    pack_weights_kernel<float><<<grid, kThreads, 0, (hipStream_t)stream>>>(
+        (const float*)W, K, N, (uint8_t*)q, (uint8_t*)s, (uint8_t*)qt, (uint8_t*)st);
+  return launched();
+}
+
+namespace {
+template <typename T>
+int swiglu_forward(const q8_plan_t& P, const void* A, const void* U, const Packed& h, const Packed& ka,
+                   const Packed& ku, void* stream) {
+  const Shape8 sh = shape_of(P);
+  (void)hipGetLastError();
+  if (ka.q)
+    swiglu_forward_kernel<T, true><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>((const T*)A, (const T*)U, h, ka, ku, sh);
+  else
+    swiglu_forward_kernel<T, false><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>((const T*)A, (const T*)U, h, ka, ku, sh);
+  return launched();
+}
+template <typename T>
+int swiglu_backward(const q8_plan_t& P, const void* Aq, const void* As, const void* Uq, const void* Us,
+                    const void* dH, void* dA, void* dU, void* stream) {
+  const Shape8 sh = shape_of(P);
+  (void)hipGetLastError();
+  swiglu_backward_kernel<T><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>(
+      (const uint8_t*)Aq, (const uint8_t*)As, (const uint8_t*)Uq, (const uint8_t*)Us, (const T*)dH,
+      (T*)dA, (T*)dU, sh);
+  return launched();
+}
+}  // namespace
+
+MOE_API int q8_swiglu_forward(const q8_plan_t* plan, const void* A, const void* U, void* Hq, void* Hs,
+                              void* Aq, void* As, void* Uq, void* Us, void* stream) {
+  if (!plan_ok(plan)) return MOE_EINVAL;
+  const q8_plan_t& P = *plan;
+  if (P.N == 0) return MOE_OK;
+  if (!elem_ok(P, A) || !elem_ok(P, U) || !pair_ok(Hq, Hs)) return MOE_EINVAL;
+  if ((Aq || As || Uq || Us) && (!pair_ok(Aq, As) || !pair_ok(Uq, Us))) return MOE_EINVAL;
+  const Packed h = packed(Hq, Hs), ka = packed(Aq, As), ku = packed(Uq, Us);
+  return P.dtype == MOE_BF16 ? swiglu_forward<bf16_t>(P, A, U, h, ka, ku, stream)
+                             : swiglu_forward<float>(P, A, U, h, ka, ku, stream);
+}
+
+MOE_API int q8_swiglu_backward(const q8_plan_t* plan, const void* Aq, const void* As, const void* Uq,
+                               const void* Us, const void* dH, void* dA, void* dU, void* stream) {
+  if (!plan_ok(plan)) return MOE_EINVAL;
+  const q8_plan_t& P = *plan;
+  if (P.N == 0) return MOE_OK;
+  if (!pair_ok(Aq, As) || !pair_ok(Uq, Us) || !elem_ok(P, dH) || !elem_ok(P, dA) || !elem_ok(P, dU))
+    return MOE_EINVAL;
+  return P.dtype == MOE_BF16 ? swiglu_backward<bf16_t>(P, Aq, As, Uq, Us, dH, dA, dU, stream)
+                             : swiglu_backward<float>(P, Aq, As, Uq, Us, dH, dA, dU, stream);
+}

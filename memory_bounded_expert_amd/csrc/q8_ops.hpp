@@ -1,0 +1,53 @@
+// Rows in 8 bits on the device (include/q8.h): the scale of a block, rounding to
+// e4m3 and back.
+#pragma once
+
+#include "device_common.hpp"
+#include "wave_ops.hpp"
+
+namespace moe {
+
+constexpr int kQBlock = 128;  // columns that share a scale
+constexpr uint32_t kQOne = 127;  // the scale byte of 2^0, which the padding holds
+// bytes of a row of H numbers, and of its scales
+constexpr int q8_row_pitch(int H) { return (H + kQBlock - 1) / kQBlock * kQBlock; }
+constexpr int q8_blocks(int H) { return (H + kQBlock - 1) / kQBlock; }
+constexpr int q8_scale_pitch(int H) { return (q8_blocks(H) + 3) / 4 * 4; }
+
+// |v|, or 0 where v is not finite: what counts for a block's scale
+__device__ __forceinline__ float q8_magnitude(float v) {
+  return __builtin_isfinite(v) ? fabsf(v) : 0.f;
+}
+
+// The byte of the smallest power of two 2^e, e >= -110, with amax / 2^e <= 448 =
+// 1.75 * 2^8: with amax = 1.f * 2^x, e = x - 8, and one more where 1.f > 1.75.
+__device__ __forceinline__ uint32_t q8_scale_byte(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int byte = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return (uint32_t)max(byte, 17);
+}
+// 1 / scale, of a byte that q8_scale_byte gave (17 to 247: a normal number)
+__device__ __forceinline__ float q8_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// the scale of any byte: 2^-127 is subnormal in fp32, 255 is NaN
+__device__ __forceinline__ float q8_scale(uint32_t byte) {
+  return byte == 0 ? __uint_as_float(0x00400000u) : byte == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
+}
+
+// Four values as e4m3 (v_cvt_pk_fp8_f32: to nearest, ties to even).  The scale
+// leaves no finite quotient above 448; v - v is 0, or NaN where v is not finite.
+__device__ __forceinline__ uint32_t q8_round4(const float* v, float inv) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(fmaf(v[0], inv, v[0] - v[0]), fmaf(v[1], inv, v[1] - v[1]), 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(fmaf(v[2], inv, v[2] - v[2]), fmaf(v[3], inv, v[3] - v[3]), w, true);
+  return (uint32_t)w;
+}
+// Four numbers of a word times the scale
+__device__ __forceinline__ void q8_values4(uint32_t w, float scale, float* v) {
+  const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+  const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+  v[0] = lo[0] * scale;
+  v[1] = lo[1] * scale;
+  v[2] = hi[0] * scale;
+  v[3] = hi[1] * scale;
+}
+
+}  // namespace moe

@@ -1,0 +1,421 @@
+// Root-mean-square norm with the residual's addition, and its gradient
+// (include/rms.h).
+//
+// As layer norm's (lnorm.hip), both passes are bound by HBM: a row is read once
+// and held in registers by W waves, C vectors of 16 bytes per lane, the next row's
+// loads in flight.  A block of 128 columns lies in 16 lanes (bf16) or 32 (fp32),
+// so an 8-bit output takes its scale from a reduction within the wave and costs no
+// pass of its own.  The backward pass needs one sum per row; shares of dgamma go
+// to slabs that a second launch adds up in order.  Rows wider than the registers
+// hold go through kernels that read the row again for each step.
+#include <algorithm>
+#include <cmath>
+
+#include "device_common.hpp"
+#include "moe_internal.h"
+#include "q8_ops.hpp"
+#include "rms.h"
+#include "row_ops.hpp"
+
+#define MOE_API extern "C" __attribute__((visibility("default")))
+
+namespace moe {
+namespace {
+
+constexpr uint32_t kRmsMagic = 0x524d5331u;  // "RMS1"
+
+// Where a row's output goes: Y of the rows' type, or q and s of 8 bits.
+struct RowsOut {
+  void *y, *q, *s;
+  int row_pitch, scale_pitch;
+};
+
+template <typename T, int W, int C, bool TAIL, bool Q8>
+__global__ __launch_bounds__(kGroup<W>) void rms_rows_forward_kernel(
+    const T* X, const T* residual, const float* __restrict__ gamma, T* S, const RowsOut out,
+    float* __restrict__ rstd, int64_t N, int H, float eps) {
+  using Part = RowPart<T, W, C, TAIL>;
+  constexpr int EPC = Part::EPC;
+  __shared__ float red[2][1][16];
+  constexpr int RPG = kGroup<W> / (64 * W);  // rows of a work-group at a time
+  const int place = threadIdx.x % (64 * W);
+  const float inv = 1.f / H;
+  float ga[Part::COLS];
+  load_cols<EPC, W, C, TAIL>(gamma, place, H, ga);
+  int half = 0;
+  int64_t t = (int64_t)blockIdx.x * RPG + threadIdx.x / (64 * W);
+  const int64_t step = (int64_t)gridDim.x * RPG;
+  Part cur, res;
+  auto load = [&](int64_t u, Part& x, Part& r) {
+    x.load(X + u * H, place, H);
+    if (residual) r.load(residual + u * H, place, H);
+  };
+  if (kAhead<W> && t < N) load(t, cur, res);
+  for (; t < N; t += step) {
+    Part next, nres;
+    if constexpr (kAhead<W>) {
+      if (t + step < N) load(t + step, next, nres);
+    } else {
+      load(t, cur, res);
+    }
+    float s[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float v[EPC];
+      cur.get(c, v);
+      if (residual) {
+        // the sum as the rows' type holds it: what is written, normed and read back
+        float r[EPC];
+        res.get(c, r);
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) v[e] += r[e];
+        cur.raw[c] = pack16(v, T());
+        cur.get(c, v);
+        Part::put(S + t * H, (c * 64 * W + place) * EPC, H, v);
+      }
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) s[0] = fmaf(v[e], v[e], s[0]);
+    }
+    row_sums<W>(s, red, half);
+    const float r = 1.f / sqrtf(s[0] * inv + eps);
+    if (place == 0) rstd[t] = r;
+    if constexpr (Q8) {
+      uint8_t* q = (uint8_t*)out.q + t * out.row_pitch;
+      uint8_t* sc = (uint8_t*)out.s + t * out.scale_pitch;
+      const int blocks = q8_blocks(H);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int at = (c * 64 * W + place) * EPC;
+        float v[EPC], amax = 0.f;
+        cur.get(c, v);
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) {
+          v[e] = v[e] * r * ga[c * EPC + e];
+          // past the row's end x and gamma are 0, but r may be NaN
+          if (at + e >= H) v[e] = 0.f;
+          amax = fmaxf(amax, q8_magnitude(v[e]));
+        }
+        amax = run_maxf<16>(amax);
+        if constexpr (EPC == 4) amax = fmaxf(amax, __shfl_xor(amax, 16));
+        const uint32_t byte = q8_scale_byte(amax);
+        const float qi = q8_inverse(byte);
+        if (at < out.row_pitch) {
+          if constexpr (EPC == 8)
+            *reinterpret_cast<uint2*>(q + at) = make_uint2(q8_round4(v, qi), q8_round4(v + 4, qi));
+          else
+            *reinterpret_cast<uint32_t*>(q + at) = q8_round4(v, qi);
+          if (at % kQBlock == 0) sc[at / kQBlock] = (uint8_t)byte;
+        }
+      }
+      if (place < out.scale_pitch - blocks) sc[blocks + place] = kQOne;
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int at = (c * 64 * W + place) * EPC;
+        if (at < H) {
+          float v[EPC];
+          cur.get(c, v);
+#pragma unroll
+          for (int e = 0; e < EPC; ++e) v[e] = v[e] * r * ga[c * EPC + e];
+          Part::put((T*)out.y + t * H, at, H, v);
+        }
+      }
+    }
+    if constexpr (kAhead<W>) {
+      cur = next;
+      res = nres;
+    }
+  }
+}
+
+template <typename T, int W, int C, bool TAIL>
+__global__ __launch_bounds__(kGroup<W>) void rms_rows_backward_kernel(
+    const T* __restrict__ S, const float* __restrict__ gamma, const T* dY,
+    const float* __restrict__ rstd, const T* dS, T* dX, float* __restrict__ part, int64_t N, int H) {
+  using Part = RowPart<T, W, C, TAIL>;
+  constexpr int EPC = Part::EPC;
+  constexpr int RPG = kGroup<W> / (64 * W);
+  __shared__ float red[2][1][16];
+  const int place = threadIdx.x % (64 * W);
+  const float inv = 1.f / H;
+  float ga[Part::COLS], dg[Part::COLS];
+  load_cols<EPC, W, C, TAIL>(gamma, place, H, ga);
+#pragma unroll
+  for (int i = 0; i < Part::COLS; ++i) dg[i] = 0.f;
+  int half = 0;
+  int64_t t = (int64_t)blockIdx.x * RPG + threadIdx.x / (64 * W);
+  const int64_t step = (int64_t)gridDim.x * RPG;
+  Part x, dy, ds;
+  float r = 0.f;
+  auto load = [&](int64_t u, Part& px, Part& pd, Part& ps, float& pr) {
+    px.load(S + u * H, place, H);
+    pd.load(dY + u * H, place, H);
+    if (dS) ps.load(dS + u * H, place, H);
+    pr = rstd[u];
+  };
+  if (kAhead<W> && t < N) load(t, x, dy, ds, r);
+  for (; t < N; t += step) {
+    Part x2, dy2, ds2;
+    float r2 = 0.f;
+    if constexpr (kAhead<W>) {
+      if (t + step < N) load(t + step, x2, dy2, ds2, r2);
+    } else {
+      load(t, x, dy, ds, r);
+    }
+    float s[1] = {0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      // lanes past the row's end hold x = dy = gamma = 0
+      float v[EPC], d[EPC];
+      x.get(c, v);
+      dy.get(c, d);
+#pragma unroll
+      for (int e = 0; e < EPC; ++e) {
+        const int i = c * EPC + e;
+        const float xh = v[e] * r;
+        s[0] = fmaf(d[e] * ga[i], xh, s[0]);
+        dg[i] = fmaf(d[e], xh, dg[i]);
+      }
+    }
+    row_sums<W>(s, red, half);
+    const float b = s[0] * inv;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int at = (c * 64 * W + place) * EPC;
+      if (at < H) {
+        float v[EPC], d[EPC];
+        x.get(c, v);
+        dy.get(c, d);
+#pragma unroll
+        for (int e = 0; e < EPC; ++e) d[e] = r * fmaf(d[e], ga[c * EPC + e], -(v[e] * r * b));
+        if (dS) {
+          ds.get(c, v);
+#pragma unroll
+          for (int e = 0; e < EPC; ++e) d[e] += v[e];
+        }
+        Part::put(dX + t * H, at, H, d);
+      }
+    }
+    if constexpr (kAhead<W>) {
+      x = x2;
+      dy = dy2;
+      ds = ds2;
+      r = r2;
+    }
+  }
+  float* pg = part + (int64_t)blockIdx.x * H;
+  if constexpr (RPG == 1) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int at = (c * 64 * W + place) * EPC;
+#pragma unroll
+      for (int e = 0; e < EPC; ++e)
+        if (at + e < H) pg[at + e] = dg[c * EPC + e];
+    }
+  } else {
+    // the work-group's waves add their shares up in order
+    __shared__ float sum[64 * C * EPC];
+    for (int w = 0; w < RPG; ++w) {
+      if ((int)threadIdx.x >> 6 == w) {
+#pragma unroll
+        for (int i = 0; i < Part::COLS; ++i) {
+          const int at = (i / EPC * 64 + place) * EPC + i % EPC;  // column of this lane's element i
+          sum[at] = w == 0 ? dg[i] : sum[at] + dg[i];
+        }
+      }
+      __syncthreads();
+    }
+    for (int h = threadIdx.x; h < H; h += kThreads) pg[h] = sum[h];
+  }
+}
+
+template <typename T, bool Q8>
+__global__ __launch_bounds__(kThreads) void rms_forward_kernel(
+    const T* X, const T* residual, const float* __restrict__ gamma, T* S, const RowsOut out,
+    float* __restrict__ rstd, int64_t N, int H, float eps) {
+  __shared__ float red[kThreads / 64];
+  for (int64_t t = blockIdx.x; t < N; t += gridDim.x) {
+    const T* x = X + t * H;
+    float q = 0.f;
+    for (int h = threadIdx.x; h < H; h += kThreads) {
+      float v = Elem<T>::to_f(x[h]);
+      if (residual) {
+        const T sum = Elem<T>::from_f(v + Elem<T>::to_f(residual[t * H + h]));
+        S[t * H + h] = sum;
+        v = Elem<T>::to_f(sum);
+      }
+      q = fmaf(v, v, q);
+    }
+    if (residual) x = S + t * H;  // each thread reads back what it wrote
+    const float r = 1.f / sqrtf(group_sum(q, red) / H + eps);
+    if (threadIdx.x == 0) rstd[t] = r;
+    if constexpr (Q8) {
+      // a block of 128 columns in 32 lanes, four columns each; the sum's rows are
+      // read by other threads than wrote them
+      __syncthreads();
+      uint8_t* qo = (uint8_t*)out.q + t * out.row_pitch;
+      uint8_t* sc = (uint8_t*)out.s + t * out.scale_pitch;
+      const int blocks = q8_blocks(H);
+      for (int b = threadIdx.x / 32; b < blocks; b += kThreads / 32) {
+        const int at = b * kQBlock + (threadIdx.x & 31) * 4;
+        float v[4], amax = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = at + e < H ? Elem<T>::to_f(x[at + e]) * r * gamma[at + e] : 0.f;
+          amax = fmaxf(amax, q8_magnitude(v[e]));
+        }
+        amax = run_maxf<16>(amax);
+        amax = fmaxf(amax, __shfl_xor(amax, 16));
+        const uint32_t byte = q8_scale_byte(amax);
+        *reinterpret_cast<uint32_t*>(qo + at) = q8_round4(v, q8_inverse(byte));
+        if ((threadIdx.x & 31) == 0) sc[b] = (uint8_t)byte;
+      }
+      if ((int)threadIdx.x < out.scale_pitch - blocks) sc[blocks + threadIdx.x] = kQOne;
+    } else {
+      T* y = (T*)out.y;
+      for (int h = threadIdx.x; h < H; h += kThreads)
+        y[t * H + h] = Elem<T>::from_f(Elem<T>::to_f(x[h]) * r * gamma[h]);
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void rms_backward_kernel(
+    const T* __restrict__ S, const float* __restrict__ gamma, const T* dY,
+    const float* __restrict__ rstd, const T* dS, T* dX, float* __restrict__ part, int64_t N, int H) {
+  __shared__ float red[kThreads / 64];
+  float* pg = part + (int64_t)blockIdx.x * H;
+  for (int h = threadIdx.x; h < H; h += kThreads) pg[h] = 0.f;
+  for (int64_t t = blockIdx.x; t < N; t += gridDim.x) {
+    const T* x = S + t * H;
+    const T* dy = dY + t * H;
+    const float r = rstd[t];
+    float b = 0.f;
+    for (int h = threadIdx.x; h < H; h += kThreads) {
+      const float d = Elem<T>::to_f(dy[h]), xh = Elem<T>::to_f(x[h]) * r;
+      b = fmaf(d * gamma[h], xh, b);
+      pg[h] = fmaf(d, xh, pg[h]);
+    }
+    b = group_sum(b, red) / H;
+    for (int h = threadIdx.x; h < H; h += kThreads) {
+      float d = r * fmaf(Elem<T>::to_f(dy[h]), gamma[h], -(Elem<T>::to_f(x[h]) * r * b));
+      if (dS) d += Elem<T>::to_f(dS[t * H + h]);
+      dX[t * H + h] = Elem<T>::from_f(d);
+    }
+  }
+}
+
+template <typename T, bool Q8>
+hipError_t run_forward(const rms_plan_t& P, const void* X, const void* residual, const float* gamma,
+                       void* S, const RowsOut& out, float* rstd, hipStream_t st) {
+  const Holding h = holding(P.H, P.dtype);
+  if (h.W == 0) {
+    const unsigned grid = (unsigned)std::min<int64_t>(P.N, kMaxRowGrid);
+    rms_forward_kernel<T, Q8><<<grid, kThreads, 0, st>>>((const T*)X, (const T*)residual, gamma, (T*)S,
+                                                         out, rstd, P.N, P.H, P.eps);
+  } else {
+    const int grid = row_groups(P.N, h.W);
+    with_holding<T>(h, P.H, [&](auto w, auto c, auto tail) {
+      rms_rows_forward_kernel<T, w.value, c.value, tail.value, Q8><<<grid, kGroup<w.value>, 0, st>>>(
+          (const T*)X, (const T*)residual, gamma, (T*)S, out, rstd, P.N, P.H, P.eps);
+    });
+  }
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run_backward(const rms_plan_t& P, const void* S, const float* gamma, const void* dY,
+                        const float* rstd, const void* dS, void* dX, float* part, int slabs,
+                        hipStream_t st) {
+  const Holding h = holding(P.H, P.dtype);
+  if (h.W == 0) {
+    rms_backward_kernel<T><<<slabs, kThreads, 0, st>>>((const T*)S, gamma, (const T*)dY, rstd,
+                                                       (const T*)dS, (T*)dX, part, P.N, P.H);
+  } else {
+    with_holding<T>(h, P.H, [&](auto w, auto c, auto tail) {
+      rms_rows_backward_kernel<T, w.value, c.value, tail.value><<<slabs, kGroup<w.value>, 0, st>>>(
+          (const T*)S, gamma, (const T*)dY, rstd, (const T*)dS, (T*)dX, part, P.N, P.H);
+    });
+  }
+  return hipGetLastError();
+}
+
+bool plan_ok(const rms_plan_t* p) { return p != nullptr && p->magic == kRmsMagic; }
+
+template <bool Q8>
+int forward(const rms_plan_t* plan, const void* X, const void* residual, const float* gamma, void* S,
+            const RowsOut& out, float* rstd, void* stream) {
+  const rms_plan_t& P = *plan;
+  if (P.N == 0) return MOE_OK;
+  if (!X || !gamma || !rstd || (Q8 ? !out.q || !out.s : !out.y)) return MOE_EINVAL;
+  if ((residual == nullptr) != (S == nullptr)) return MOE_EINVAL;
+  if (Q8 && ((uintptr_t)out.q % 16 || (uintptr_t)out.s % 4)) return MOE_EINVAL;
+  hipStream_t st = (hipStream_t)stream;
+  (void)hipGetLastError();
+  const hipError_t err = P.dtype == MOE_BF16
+                             ? run_forward<bf16_t, Q8>(P, X, residual, gamma, S, out, rstd, st)
+                             : run_forward<float, Q8>(P, X, residual, gamma, S, out, rstd, st);
+  return err == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+MOE_API int rms_plan(int64_t N, int32_t H, int32_t dtype, float eps, rms_plan_t* out) {
+  if (!out || N < 0 || H < 1 || !(eps > 0.f) || !std::isfinite(eps)) return MOE_EINVAL;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_EINVAL;
+  if (H > 65536 || N >= ((int64_t)1 << 31)) return MOE_EUNSUPPORTED;
+  rms_plan_t p{};
+  p.magic = kRmsMagic;
+  p.dtype = dtype;
+  p.N = N;
+  p.H = H;
+  p.eps = eps;
+  p.row_pitch = q8_row_pitch(H);
+  p.scale_pitch = q8_scale_pitch(H);
+  p.bwd_workspace_bytes = std::min<int64_t>(N, kMaxSlabs) * H * sizeof(float);
+  *out = p;
+  return MOE_OK;
+}
+
+MOE_API int rms_forward(const rms_plan_t* plan, const void* X, const void* residual,
+                        const float* gamma, void* S, void* Y, float* rstd, void* stream) {
+  if (!plan_ok(plan)) return MOE_EINVAL;
+  return forward<false>(plan, X, residual, gamma, S, RowsOut{Y, nullptr, nullptr, 0, 0}, rstd, stream);
+}
+
+MOE_API int rms_forward_q8(const rms_plan_t* plan, const void* X, const void* residual,
+                           const float* gamma, void* S, void* Yq, void* Ys, float* rstd,
+                           void* stream) {
+  if (!plan_ok(plan)) return MOE_EINVAL;
+  return forward<true>(plan, X, residual, gamma, S,
+                       RowsOut{nullptr, Yq, Ys, plan->row_pitch, plan->scale_pitch}, rstd, stream);
+}
+
+MOE_API int rms_backward(const rms_plan_t* plan, const void* S, const float* gamma, const void* dY,
+                         const float* rstd, const void* dS, void* dX, float* dgamma,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+  if (!plan_ok(plan)) return MOE_EINVAL;
+  const rms_plan_t& P = *plan;
+  if (!dgamma) return MOE_EINVAL;
+  if (P.N > 0 && (!S || !gamma || !dY || !rstd || !dX || !workspace)) return MOE_EINVAL;
+  if (P.N > 0 && (uintptr_t)workspace % 256) return MOE_EINVAL;
+  if (workspace_bytes < (size_t)P.bwd_workspace_bytes) return MOE_EWORKSPACE;
+  hipStream_t st = (hipStream_t)stream;
+  (void)hipGetLastError();
+  const int slabs = P.N > 0 ? slab_count(P.N, holding(P.H, P.dtype).W) : 0;
+  if (P.N > 0) {
+    // one work-group writes dgamma itself
+    float* part = slabs == 1 ? dgamma : (float*)workspace;
+    const hipError_t err = P.dtype == MOE_BF16
+                               ? run_backward<bf16_t>(P, S, gamma, dY, rstd, dS, dX, part, slabs, st)
+                               : run_backward<float>(P, S, gamma, dY, rstd, dS, dX, part, slabs, st);
+    if (err != hipSuccess) return MOE_EHIP;
+    if (slabs == 1) return MOE_OK;
+  }
+  slab_fold_kernel<<<(unsigned)ceil_div(P.H, 64), 64 * kFoldWaves, 0, st>>>(
+      (const float*)workspace, slabs, P.H, P.H, dgamma, nullptr);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
+}

@@ -1,0 +1,305 @@
+"""Products grouped by expert on the GPU against fp64 on the same inputs.
+
+A sum of n products in fp32 is off by at most 2 u per addition of the sum of its terms' sizes, u = 2^-24 (a whole step,
+since the matrix unit need not round its inner additions to nearest): 2 u n S.  The products of bfloat16 numbers, and
+those of e4m3 numbers times powers of two, are exact.  Y and dX are rounded once: 2^-8.  With accumulate, one more
+addition: u of the result."""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import DEV, B, needs_gpu, require_lib
+from oracle import q8_oracle as Q
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+U, E16 = 2.0 ** -24, 2.0 ** -8
+
+
+def ragged(R, E, seed, skew=0.7):
+    g = torch.Generator().manual_seed(seed)
+    share = torch.arange(1, E + 1).double().pow(-skew)[torch.randperm(E, generator=g)]
+    return torch.bincount(torch.multinomial(share, R, True, generator=g), minlength=E).tolist() if R else [0] * E
+
+
+def offsets_of(sizes, start=0):
+    return torch.tensor([start] + (start + np.cumsum(sizes)).tolist(), dtype=torch.int32, device=DEV)
+
+
+def normal(g, *shape, std=1.0):
+    return (torch.randn(*shape, generator=g) * std).bfloat16().to(DEV)
+
+
+def by_expert(offsets):
+    o = offsets.tolist()
+    return [(e, slice(o[e], o[e + 1])) for e in range(len(o) - 1)]
+
+
+def close(got, ref, size, n, e, what):
+    got = got.double()
+    bad = (got - ref).abs() > 2 * U * max(n, 1) * size * (1 + e) + e * ref.abs()
+    assert not bad.any(), (what, int(bad.sum()), float((got - ref).abs().max()))
+
+
+def check_bf16(R, K, N, sizes, seed=0, start=0, after=0, offsets="given"):
+    """Forward, dX, dW with `start` rows before the first expert's and `after` rows behind the last's."""
+    g = torch.Generator().manual_seed(seed)
+    E, R = len(sizes), sum(sizes) + start + after
+    X, dY, W = normal(g, R, K), normal(g, R, N), normal(g, E, K, N, std=0.05)
+    off = offsets_of(sizes, start) if offsets == "given" else None
+    plan = B.gmm_plan(R, K, N, E)
+    sentinel = lambda *s: torch.full(s, 77.0, dtype=torch.bfloat16, device=DEV)
+    Y = B.gmm_forward(plan, X, W, off, Y=sentinel(R, N))
+    dX = B.gmm_backward_dx(plan, dY, W, off, dX=sentinel(R, K))
+    dW = B.gmm_backward_dw(plan, X, dY, off, dW=torch.full((E, K, N), float("nan"), device=DEV))
+    old = torch.randn(E, K, N, generator=g).to(DEV)
+    more = B.gmm_backward_dw(plan, X, dY, off, dW=old.clone(), accumulate=True)
+    torch.cuda.synchronize()
+    for e, r in by_expert(off if off is not None else offsets_of(sizes)):
+        x, d, w = X[r].double(), dY[r].double(), W[e].double()
+        close(Y[r], x @ w, x.abs() @ w.abs(), K, E16, ("Y", e))
+        close(dX[r], d @ w.T.contiguous(), d.abs() @ w.abs().T.contiguous(), N, E16, ("dX", e))
+        xt = x.T.contiguous()
+        ref, size, n = xt @ d, xt.abs() @ d.abs(), r.stop - r.start
+        close(dW[e], ref, size, n, 0, ("dW", e))
+        o = old[e].double()
+        bad = (more[e].double() - o - ref).abs() > 2 * U * n * size + U * ((o + ref).abs() + 2 * U * n * size)
+        assert not bad.any(), ("accumulate", e)
+        if n == 0:
+            assert not dW[e].any() and torch.equal(more[e], old[e])
+    for t in (Y, dX):
+        assert bool((t[:start] == 77).all()) and bool((t[R - after:] == 77).all() if after else True)
+
+
+def rows8(g, R, K):
+    """8-bit rows of their own scales: bytes as q8_pack writes them, and their values in fp64."""
+    x = torch.randn(R, K, generator=g) * torch.exp(torch.randn(R, 1, generator=g))
+    plan = B.q8_plan(R, K, B.MOE_F32)
+    q, s = B.q8_pack(plan, x.to(DEV))
+    return q, s, B.q8_unpack(plan, q, s).double()
+
+
+def check_q8(R, K, N, sizes, seed=0, start=0, after=0):
+    g = torch.Generator().manual_seed(seed)
+    E, R = len(sizes), sum(sizes) + start + after
+    Xq, Xs, X = rows8(g, R, K)
+    W = (torch.randn(E, K, N, generator=g) * 0.05 * torch.exp(torch.randn(1, 1, N, generator=g))).to(DEV)
+    Wq, Ws = B.q8_pack_weights(W, "K")
+    # the packed weights' values
+    nb, kb = -(-N // 128), -(-K // 128)
+    s = torch.exp2(Ws.view(torch.uint8)[:, :, :kb].double() - 127)
+    Wv = Wq[:, :, :K].double() * s.repeat_interleave(128, 1)[:, :N].repeat_interleave(128, 2)[:, :, :K]
+    off = offsets_of(sizes, start)
+    dY = normal(g, R, N)
+    plan = B.gmm_plan(R, K, N, E, B.GMM_Q8)
+    Y = B.gmm8_forward(plan, Xq, Xs, Wq, Ws, off, Y=torch.full((R, N), 77.0, dtype=torch.bfloat16, device=DEV))
+    dW = B.gmm8_backward_dw(plan, Xq, Xs, dY, off, dW=torch.full((E, K, N), float("nan"), device=DEV))
+    old = torch.randn(E, K, N, generator=g).to(DEV)
+    more = B.gmm8_backward_dw(plan, Xq, Xs, dY, off, dW=old.clone(), accumulate=True)
+    torch.cuda.synchronize()
+    assert nb == Ws.shape[1]
+    for e, r in by_expert(off):
+        x, d, w = X[r], dY[r].double(), Wv[e].T.contiguous()
+        close(Y[r], x @ w, x.abs() @ w.abs(), K, E16, ("Y", e))
+        xt = x.T.contiguous()
+        ref, size, n = xt @ d, xt.abs() @ d.abs(), r.stop - r.start
+        close(dW[e], ref, size, n, 0, ("dW", e))
+        o = old[e].double()
+        bad = (more[e].double() - o - ref).abs() > 2 * U * n * size + U * ((o + ref).abs() + 2 * U * n * size)
+        assert not bad.any(), ("accumulate", e)
+    assert bool((Y[:start] == 77).all()) and bool((Y[R - after:] == 77).all() if after else True)
+
+
+# (K, N, rows of each expert): one row, one expert, empty ones first, last and between, tiles' borders, odd sizes
+CASES = [
+    (8, 8, [1]), (64, 64, [64]), (128, 128, [128, 0, 256]), (520, 264, ragged(1000, 7, 3, 1.5)), (72, 200, [0, 3, 0, 0, 129, 1, 0]),
+    (256, 512, [257, 255, 1]), (1024, 136, [16]), (2048, 1408, [2, 0, 1, 3, 1, 0, 0, 4]), (264, 1000, [33, 31, 32, 64, 65, 63]),
+    (4096, 256, [5]), (16, 2048, [300]), (8, 520, [1, 1, 1, 1]), (640, 8, [77, 500]), (136, 72, ragged(3000, 70, 4)), (384, 384, ragged(700, 130, 5)),
+    (1408, 512, [1000, 24]), (512, 768, [513, 511]), (96, 96, [2000]), (7168, 256, [3]), (256, 7168, [2, 2]),
+]
+
+
+@pytest.mark.parametrize("K,N,sizes", CASES, ids=lambda v: str(v) if isinstance(v, int) else "E%d_R%d" % (len(v), sum(v)))
+def test_bf16(K, N, sizes):
+    require_lib()
+    check_bf16(0, K, N, sizes)
+
+
+@pytest.mark.parametrize("K,N,sizes", [(K - d, N, s) for (K, N, s), d in zip(CASES, [0, 1, 0, 7, 3, 0, 127, 0, 100, 0, 15, 7, 0, 5, 1, 0, 0, 1, 0, 0])],
+                         ids=lambda v: str(v) if isinstance(v, int) else "E%d_R%d" % (len(v), sum(v)))
+def test_q8(K, N, sizes):
+    require_lib()
+    check_q8(0, K, N, sizes)
+
+
+@pytest.mark.parametrize("check", [check_bf16, check_q8])
+def test_rows_of_no_expert_are_left(check):
+    check(0, 136, 136, [40, 0, 100, 7], start=13, after=200)
+    check(0, 136, 264, [0, 0, 0], start=5, after=9)
+    check(0, 264, 136, [300], start=1, after=1)
+
+
+def test_without_offsets():
+    check_bf16(0, 264, 392, [530], offsets="none")
+    g = torch.Generator().manual_seed(1)
+    q, s, _ = rows8(g, 530, 300)
+    Wq, Ws = B.q8_pack_weights(torch.randn(1, 300, 264, generator=g).to(DEV), "K")
+    plan = B.gmm_plan(530, 300, 264, 1, B.GMM_Q8)
+    dY = normal(g, 530, 264)
+    off = offsets_of([530])
+    assert torch.equal(B.gmm8_forward(plan, q, s, Wq, Ws), B.gmm8_forward(plan, q, s, Wq, Ws, off))
+    assert torch.equal(B.gmm8_backward_dw(plan, q, s, dY), B.gmm8_backward_dw(plan, q, s, dY, off))
+
+
+def test_all_experts_of_a_large_count():
+    check_bf16(0, 64, 72, ragged(2500, 1024, 9, 0.3))
+    check_q8(0, 130, 64, ragged(2500, 1000, 9, 0.3))
+
+
+def test_no_rows():
+    W, off = torch.randn(2, 16, 8, device=DEV).bfloat16(), offsets_of([0, 0])
+    x, dy = torch.empty(0, 16, dtype=torch.bfloat16, device=DEV), torch.empty(0, 8, dtype=torch.bfloat16, device=DEV)
+    plan = B.gmm_plan(0, 16, 8, 2)
+    assert B.gmm_forward(plan, x, W, off).numel() == 0 and B.gmm_backward_dx(plan, dy, W, off).numel() == 0
+    assert not B.gmm_backward_dw(plan, x, dy, off, dW=torch.ones(2, 16, 8, device=DEV)).any()
+    old = torch.ones(2, 16, 8, device=DEV)
+    assert bool((B.gmm_backward_dw(plan, x, dy, off, dW=old, accumulate=True) == 1).all())
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_bad_rows_spoil_their_expert_alone(q8):
+    """NaN in rows of one expert, and in rows of none: the neighbours' outputs are bit for bit as without."""
+    sizes, K, N = [50, 70, 0, 90], 136, 264
+    g = torch.Generator().manual_seed(2)
+    R = sum(sizes) + 30
+    X, dY, W = normal(g, R, K), normal(g, R, N), normal(g, 4, K, N)
+    off = offsets_of(sizes, 10)
+    plan = B.gmm_plan(R, K, N, 4, B.GMM_Q8 if q8 else B.GMM_BF16)
+    rp = B.q8_plan(R, K)
+    Wq, Ws = B.q8_pack_weights(W, "K")
+
+    def run():
+        if q8:
+            Xq, Xs = B.q8_pack(rp, X)
+            return B.gmm8_forward(plan, Xq, Xs, Wq, Ws, off), None, B.gmm8_backward_dw(plan, Xq, Xs, dY, off)
+        return B.gmm_forward(plan, X, W, off), B.gmm_backward_dx(plan, dY, W, off), B.gmm_backward_dw(plan, X, dY, off)
+
+    good = run()
+    for t in (X, dY):
+        t[:10] = float("nan")
+        t[-20:] = float("inf")
+        t[10 + 60] = float("nan")  # expert 1
+    bad = run()
+    rows = [r for r in range(10, R - 20) if r != 70]
+    for a, b in zip(good[:2], bad[:2]):
+        if a is not None:
+            assert torch.equal(a[rows], b[rows]) and torch.isnan(b[70]).all()
+    assert torch.equal(good[2][[0, 2, 3]], bad[2][[0, 2, 3]]) and torch.isnan(bad[2][1]).all()
+
+
+@pytest.mark.parametrize("operands", [B.GMM_BF16, B.GMM_Q8])
+def test_broken_offsets_stay_inside(operands):
+    """Descending, negative and far too large offsets: whatever the rows hold, nothing around the outputs is touched."""
+    R, K, N, E, pad = 300, 136, 72, 5, 4096
+    g = torch.Generator().manual_seed(3)
+    X, dY, W = normal(g, R, K), normal(g, R, N), normal(g, E, K, N)
+    plan = B.gmm_plan(R, K, N, E, operands)
+    Xq, Xs = B.q8_pack(B.q8_plan(R, K), X)
+    Wq, Ws = B.q8_pack_weights(W, "K")
+
+    def guarded(shape, dtype):
+        n = int(np.prod(shape))
+        buf = torch.full((n + 2 * pad,), 55.0, dtype=dtype, device=DEV)
+        return buf, buf[pad:pad + n].view(shape)
+
+    for broken in ([0, 500, 20, 300, -7, 2 ** 31 - 1], [-2 ** 31, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, 0, 300], [300, 200, 100, 50, 20, 0], [2 ** 31 - 1] * 6,
+                   [0, 300, 0, 300, 0, 300]):
+        off = torch.tensor(broken, dtype=torch.int32, device=DEV)
+        (by, Y), (bx, dX), (bw, dW) = guarded((R, N), torch.bfloat16), guarded((R, K), torch.bfloat16), guarded((E, K, N), torch.float32)
+        if operands == B.GMM_BF16:
+            B.gmm_forward(plan, X, W, off, Y=Y)
+            B.gmm_backward_dx(plan, dY, W, off, dX=dX)
+            B.gmm_backward_dw(plan, X, dY, off, dW=dW)
+        else:
+            B.gmm8_forward(plan, Xq, Xs, Wq, Ws, off, Y=Y)
+            B.gmm8_backward_dw(plan, Xq, Xs, dY, off, dW=dW)
+        torch.cuda.synchronize()
+        for b in (by, bx, bw):
+            assert bool((b[:pad] == 55).all()) and bool((b[-pad:] == 55).all())
+
+
+def test_scales_of_any_size():
+    """Scales far apart between rows, blocks and columns: each enters with its own power of two."""
+    g = torch.Generator().manual_seed(4)
+    R, K, N = 70, 700, 264
+    x = torch.randn(R, K, generator=g) * torch.exp2(torch.randint(-30, 30, (R, 1), generator=g).float())
+    x = x * torch.exp2(torch.randint(-8, 8, (1, K), generator=g).float())
+    plan8 = B.q8_plan(R, K, B.MOE_F32)
+    Xq, Xs = B.q8_pack(plan8, x.to(DEV))
+    X = B.q8_unpack(plan8, Xq, Xs).double()
+    W = torch.randn(1, K, N, generator=g) * torch.exp2(torch.randint(-20, 20, (1, 1, N), generator=g).float())
+    Wv = torch.from_numpy(Q.quantise_weights(W.numpy())[0])[0].to(DEV)
+    Wq, Ws = B.q8_pack_weights(W.to(DEV), "K")
+    Y = B.gmm8_forward(B.gmm_plan(R, K, N, 1, B.GMM_Q8), Xq, Xs, Wq, Ws)
+    close(Y, X @ Wv, X.abs() @ Wv.abs(), K, E16, "Y")
+
+
+@pytest.mark.parametrize("operands", [B.GMM_BF16, B.GMM_Q8])
+def test_repeats_on_streams_and_in_graphs(operands):
+    """Bit for bit: twice, on another stream, in two captured graphs with workspaces of their own, replayed in turn
+    between eager calls, and on new inputs in the same buffers."""
+    R, K, N, sizes = 700, 1000, 392, [300, 0, 250, 150]
+    g = torch.Generator().manual_seed(5)
+    X, dY, W, off = normal(g, R, K), normal(g, R, N), normal(g, 4, K, N), offsets_of(sizes)
+    plan = B.gmm_plan(R, K, N, 4, operands)
+    rp = B.q8_plan(R, K)
+    Xq, Xs = B.q8_pack(rp, X)
+    Wq, Ws = B.q8_pack_weights(W, "K")
+
+    def run(ws):
+        if operands == B.GMM_Q8:
+            return [B.gmm8_forward(plan, Xq, Xs, Wq, Ws, off, ws=ws), B.gmm8_backward_dw(plan, Xq, Xs, dY, off, ws=ws)]
+        return [B.gmm_forward(plan, X, W, off, ws=ws), B.gmm_backward_dx(plan, dY, W, off, ws=ws), B.gmm_backward_dw(plan, X, dY, off, ws=ws)]
+
+    spaces = [B.workspace(plan, "both", DEV) for _ in range(3)]
+    want = [t.clone() for t in run(spaces[0])]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = run(None)
+    side.synchronize()
+    assert all(map(torch.equal, want, other)) and all(map(torch.equal, want, run(None)))
+    graphs = []
+    for ws in spaces[1:]:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run(ws)
+        graphs.append((graph, out))
+    for turn in range(3):
+        if turn == 2:
+            X.mul_(0.5)
+            dY.copy_(dY.flip(0))
+            off.copy_(offsets_of([1, 500, 199, 0]))
+            B.q8_pack(rp, X, Xq, Xs)
+            want = [t.clone() for t in run(spaces[0])]
+        for graph, out in graphs:
+            for t in out:
+                t.fill_(9)
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(map(torch.equal, want, out)), turn
+            run(spaces[0])
+
+
+def test_gradients_are_the_adjoints():
+    """<dY, X W> = <dX, X> = <dW, W>, each to the outputs' roundings."""
+    g = torch.Generator().manual_seed(6)
+    sizes = [100, 0, 57, 343]
+    X, dY, W, off = normal(g, 500, 264), normal(g, 500, 136), normal(g, 4, 264, 136), offsets_of(sizes)
+    plan = B.gmm_plan(500, 264, 136, 4)
+    d = lambda a, b: float((a.double() * b.double()).sum())
+    y, dx, dw = B.gmm_forward(plan, X, W, off), B.gmm_backward_dx(plan, dY, W, off), B.gmm_backward_dw(plan, X, dY, off)
+    vals = d(y, dY), d(dx, X), d(dw, W)
+    scale = E16 * max(float((y.double() * dY.double()).abs().sum()), float((dx.double() * X.double()).abs().sum()))
+    assert max(vals) - min(vals) <= 2 * scale

@@ -1,0 +1,171 @@
+"""Rows in 8 bits and SwiGLU with 8-bit checkpoints on the GPU against fp64 on the same inputs.
+
+Packing rounds once from the given values, so numbers and scales equal the oracle's; unpacking to bfloat16 is exact.
+SwiGLU, u = 2^-24: 1 / (1 + e^-a) through a hardware exponential of a log2(e), whose rounded argument alone moves it by
+|a| u; that, the exponential, sum, quotient and products leave h off by at most (8 + |a|) u of itself (and 2^-120 where
+the exponential passes the type's range), so does dU; dA has the factor 1 + a (1 - g), off by |a| (6 + |a|) u and 4 u of
+its terms.  Then half a step of the output's type: e4m3 under the kernel's scale, or bf16 2^-8, fp32 u."""
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_common import DEV, B, dev_to_f64, needs_gpu, require_lib
+from oracle import q8_oracle as Q
+from test_gpu_rms import TYPES, check8, values8
+
+pytestmark = [pytest.mark.gpu, needs_gpu]
+U = 2.0 ** -24
+SIZES = [(1, 1), (1, 128), (3, 7), (5, 129), (777, 1111), (2, 65536), (64, 512), (33, 640), (1000, 72), (1, 4096), (4097, 136), (0, 5)]
+
+
+def rows(N, H, dtype, seed=0, spread=3.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(N, H, generator=g) * torch.exp(spread * torch.randn(N, 1, generator=g))).to(TYPES[dtype][0]).to(DEV)
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "%dx%d" % s)
+def test_pack_and_unpack(size, dtype):
+    require_lib()
+    N, H = size
+    x = rows(N, H, dtype)
+    plan = B.q8_plan(N, H, B.moe_dtype(x.dtype))
+    q, s = B.q8_pack(plan, x)
+    back = B.q8_unpack(plan, q, s)
+    torch.cuda.synchronize()
+    if N == 0:
+        return
+    want, e = Q.quantise(dev_to_f64(x))
+    got, _, ge = values8(q, s, H)
+    assert np.array_equal(ge, e) and np.array_equal(got, want)
+    assert np.array_equal(dev_to_f64(back), want)
+    assert np.array_equal(dev_to_f64(B.q8_unpack(B.q8_plan(N, H, B.MOE_BF16), q, s)), want)
+
+
+def test_pack_of_special_values():
+    """Ties, the largest of a block on the border between two scales, subnormal and huge values, infinities and NaN."""
+    x = torch.zeros(12, 200)
+    x[1, :8] = torch.tensor([448.0, 1.0625, 1.1875, -1.0625, 2.0 ** -7 * 1.5, 2.0 ** -10, 3 * 2.0 ** -10, 17.0])
+    x[2, 0], x[3, 0] = 448.0, 448.00003
+    x[4, 0], x[5, 0] = 3.3e38, 1e-38
+    x[6, 130] = 1e-45
+    x[7, 3], x[7, 4], x[7, 5], x[7, 150] = float("inf"), float("nan"), 5.0, -float("inf")
+    x[8, :] = float("nan")
+    x[9, 1], x[9, 2] = -448.0 * 2.0 ** -90, 2.0 ** -99 * 1.0625
+    x[10, 0], x[10, 1] = 1.75, 1.7500001
+    x = x.to(DEV)
+    plan = B.q8_plan(12, 200, B.MOE_F32)
+    q, s = B.q8_pack(plan, x)
+    back = B.q8_unpack(plan, q, s)
+    want, e = Q.quantise(dev_to_f64(x))
+    got, _, ge = values8(q, s, 200)
+    assert np.array_equal(ge, e) and np.array_equal(got, want, equal_nan=True)
+    # 3.3e38 = 248.3 * 2^120 lies nearest to 256 * 2^120 = 2^128, which fp32 does not hold
+    assert want[4, 0] == 2.0 ** 128
+    with np.errstate(over="ignore"):
+        assert np.array_equal(back.cpu().numpy(), want.astype(np.float32), equal_nan=True)
+
+
+def test_unpack_of_every_byte():
+    """All e4m3 codes under all scales: the value where fp32 holds it, NaN for NaN on either side."""
+    q = torch.arange(256, dtype=torch.uint8).repeat(256, 1)
+    s = torch.full((256, 4), 127, dtype=torch.uint8)
+    s[:, 0] = s[:, 1] = torch.arange(256, dtype=torch.uint8)
+    back = B.q8_unpack(B.q8_plan(256, 256, B.MOE_F32), q.view(B.E4M3).to(DEV), s.view(B.E8M0).to(DEV))
+    scale = 2.0 ** (np.arange(256.0) - 127)[:, None]
+    scale[255] = np.nan
+    with np.errstate(over="ignore"):
+        want = (Q.decode(q.numpy()) * scale).astype(np.float32)
+    assert np.array_equal(back.cpu().numpy(), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("shape", [(1, 1, 1), (2, 128, 128), (3, 130, 72), (1, 1000, 264), (2, 5, 300), (1, 257, 513), (5, 64, 640)], ids=str)
+def test_pack_weights(shape, dtype):
+    E, K, N = shape
+    w = rows(E * K, N, dtype, spread=0.5).view(E, K, N)
+    qt, st, q, s = B.q8_pack_weights(w)
+    only = B.q8_pack_weights(w, "K"), B.q8_pack_weights(w, "N")
+    torch.cuda.synchronize()
+    for a, b in zip((qt, st, q, s), (*only[0], *only[1])):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    want, e = Q.quantise_weights(dev_to_f64(w))
+    n = lambda t: t.view(torch.uint8).cpu().numpy()
+    kb, nb = -(-K // 128), -(-N // 128)
+    assert np.array_equal(n(s)[:, :, :nb].astype(int) - 127, e) and np.all(n(s)[:, :, nb:] == 127)
+    assert np.array_equal(n(st)[:, :, :kb].astype(int) - 127, e.transpose(0, 2, 1)) and np.all(n(st)[:, :, kb:] == 127)
+    full = np.repeat(np.repeat(2.0 ** e, 128, 1), 128, 2)[:, :K, :N]
+    assert np.array_equal(Q.decode(n(q)[:, :, :N]) * full, want) and np.all(n(q)[:, :, N:] & 127 == 0)
+    assert np.array_equal(Q.decode(n(qt)[:, :, :K]) * full.transpose(0, 2, 1), want.transpose(0, 2, 1)) and np.all(n(qt)[:, :, K:] & 127 == 0)
+
+
+def swiglu_inputs(N, H, dtype, seed=1):
+    a, u, dh = rows(N, H, dtype, seed, 0.5), rows(N, H, dtype, seed + 1, 0.5), rows(N, H, dtype, seed + 2, 0.5)
+    if H > 6:
+        a[0, :6] = torch.tensor([0.0, -0.0, 60.0, -60.0, -95.0, -300.0])
+    return a, u, dh
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "%dx%d" % s)
+def test_swiglu(size, dtype):
+    require_lib()
+    N, H = size
+    a, u, dh = swiglu_inputs(max(N, 1), H, dtype)
+    a, u, dh = a[:N], u[:N], dh[:N]
+    e = TYPES[dtype][1]
+    plan = B.q8_plan(N, H, B.moe_dtype(a.dtype))
+    hq, hs, kept = B.q8_swiglu_forward(plan, a, u)
+    hq2, hs2, none = B.q8_swiglu_forward(plan, a, u, keep=False)
+    dA, dU = B.q8_swiglu_backward(plan, kept, dh)
+    over = dh.clone()
+    dA2, dU2 = B.q8_swiglu_backward(plan, kept, over, dA=over)
+    torch.cuda.synchronize()
+    if N == 0:
+        return
+    assert none is None and torch.equal(dA, dA2) and torch.equal(dU, dU2)
+    assert torch.equal(hq.view(torch.uint8), hq2.view(torch.uint8)) and torch.equal(hs.view(torch.uint8), hs2.view(torch.uint8))
+    a64, u64, d64 = dev_to_f64(a), dev_to_f64(u), dev_to_f64(dh)
+    with np.errstate(over="ignore"):
+        h = Q.swiglu(a64, u64)
+    check8(hq, hs, h, (8 + np.abs(a64)) * U * np.abs(h) + 2.0 ** -120)
+    for pair, x in ((kept[:2], a), (kept[2:], u)):
+        want, se = Q.quantise(dev_to_f64(x))
+        got, _, ge = values8(*pair, H)
+        assert np.array_equal(got, want) and np.array_equal(ge, se)
+    a64, u64 = values8(*kept[:2], H)[0], values8(*kept[2:], H)[0]
+    with np.errstate(over="ignore"):
+        ra, ru = Q.swiglu_backward(a64, u64, d64)
+        g = 1 / (1 + np.exp(-a64))
+    t = np.abs(a64)
+    tol = np.abs(d64 * u64 * g) * ((t * (6 + t) + 4) + (8 + t) * np.abs(1 + a64 * (1 - g))) * U + 2.0 ** -120
+    assert np.all(np.abs(dev_to_f64(dA) - ra) <= tol * (1 + e) + e * np.abs(ra)), "dA"
+    assert np.all(np.abs(dev_to_f64(dU) - ru) <= (8 + t) * U * np.abs(ru) * (1 + e) + 2.0 ** -120 + e * np.abs(ru)), "dU"
+
+
+def test_swiglu_bad_values_spoil_their_place_alone():
+    a, u, dh = swiglu_inputs(8, 300, "bf16")
+    plan = B.q8_plan(8, 300)
+    good = B.q8_swiglu_forward(plan, a, u)
+    a[3, 20], u[5, 200] = float("nan"), float("inf")
+    hq, hs, kept = B.q8_swiglu_forward(plan, a, u)
+    for (x, y) in ((hq, good[0]), (kept[0], good[2][0]), (kept[2], good[2][2])):
+        x, y = x.view(torch.uint8), y.view(torch.uint8)
+        assert torch.equal(x[[0, 1, 2, 4, 6, 7]], y[[0, 1, 2, 4, 6, 7]])
+    assert torch.isnan(hq.float()[3, 20]) and torch.isnan(kept[0].float()[3, 20]) and torch.isnan(kept[2].float()[5, 200])
+    assert int(torch.isnan(hq.float()).sum()) == 2
+
+
+def test_blocks_past_32_bits():
+    """More than 2^31 values: the last rows are as in a call of their own."""
+    N, H = 600_000, 4096
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    x = torch.randn(64, H, device=DEV).bfloat16().repeat(N // 64, 1)
+    q, s = B.q8_pack(B.q8_plan(N, H), x)
+    q2, s2 = B.q8_pack(B.q8_plan(32, H), x[-32:].contiguous())
+    assert torch.equal(q[-32:].view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s[-32:].view(torch.uint8), s2.view(torch.uint8))
+    del x
+    back = B.q8_unpack(B.q8_plan(N, H), q, s)
+    assert torch.equal(back[-32:], B.q8_unpack(B.q8_plan(32, H), q2, s2))
