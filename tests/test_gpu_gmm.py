@@ -3,7 +3,13 @@
 A sum of n products in fp32 is off by at most 2 u per addition of the sum of its terms' sizes, u = 2^-24 (a whole step,
 since the matrix unit need not round its inner additions to nearest): 2 u n S.  The products of bfloat16 numbers, and
 those of e4m3 numbers times powers of two, are exact.  Y and dX are rounded once: 2^-8.  With accumulate, one more
-addition: u of the result."""
+addition: u of the result.
+
+gmm8_forward multiplies e4m3 numbers with the matrix instruction for them, which adds eight products at a time before
+they reach the fp32 accumulator, each cut where it lies 2^13 below the largest of the eight (measured: 2^16 - 2^16 + t
+of one eight keeps t from 2^3 on, of different eights from 2^-7 on).  The seven others lose less than 2^-13 of the
+largest each, so a sum loses less than 7 * 2^-13 S: TRUNC S below.  Cuts of many products do not all go one way, so
+over a whole matrix the 2-norm of the error stays under 2^-13 of S's beside the output's rounding."""
 
 import numpy as np
 import pytest
@@ -14,6 +20,7 @@ from oracle import q8_oracle as Q
 
 pytestmark = [pytest.mark.gpu, needs_gpu]
 U, E16 = 2.0 ** -24, 2.0 ** -8
+TRUNC = 7 * 2.0 ** -13
 
 
 def ragged(R, E, seed, skew=0.7):
@@ -35,10 +42,12 @@ def by_expert(offsets):
     return [(e, slice(o[e], o[e + 1])) for e in range(len(o) - 1)]
 
 
-def close(got, ref, size, n, e, what):
+def close(got, ref, size, n, e, what, cut=0.0):
     got = got.double()
-    bad = (got - ref).abs() > 2 * U * max(n, 1) * size * (1 + e) + e * ref.abs()
+    bad = (got - ref).abs() > (2 * U * max(n, 1) + cut) * size * (1 + e) + e * ref.abs()
     assert not bad.any(), (what, int(bad.sum()), float((got - ref).abs().max()))
+    if cut and len(ref):
+        assert float((got - ref).norm()) <= e * float(ref.norm()) + 2.0 ** -13 * float(size.norm()), what
 
 
 def check_bf16(R, K, N, sizes, seed=0, start=0, after=0, offsets="given"):
@@ -100,7 +109,7 @@ def check_q8(R, K, N, sizes, seed=0, start=0, after=0):
     assert nb == Ws.shape[1]
     for e, r in by_expert(off):
         x, d, w = X[r], dY[r].double(), Wv[e].T.contiguous()
-        close(Y[r], x @ w, x.abs() @ w.abs(), K, E16, ("Y", e))
+        close(Y[r], x @ w, x.abs() @ w.abs(), K, E16, ("Y", e), TRUNC)
         xt = x.T.contiguous()
         ref, size, n = xt @ d, xt.abs() @ d.abs(), r.stop - r.start
         close(dW[e], ref, size, n, 0, ("dW", e))
@@ -241,7 +250,7 @@ def test_scales_of_any_size():
     Wv = torch.from_numpy(Q.quantise_weights(W.numpy())[0])[0].to(DEV)
     Wq, Ws = B.q8_pack_weights(W.to(DEV), "K")
     Y = B.gmm8_forward(B.gmm_plan(R, K, N, 1, B.GMM_Q8), Xq, Xs, Wq, Ws)
-    close(Y, X @ Wv, X.abs() @ Wv.abs(), K, E16, "Y")
+    close(Y, X @ Wv, X.abs() @ Wv.abs(), K, E16, "Y", TRUNC)
 
 
 @pytest.mark.parametrize("operands", [B.GMM_BF16, B.GMM_Q8])
