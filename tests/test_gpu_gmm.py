@@ -141,11 +141,37 @@ def test_q8(K, N, sizes):
     check_q8(0, K, N, sizes)
 
 
+# (K, N, rows): every tile that a product can take, with tiles that end inside a matrix and inside an expert, and the
+# splits of k: over few tiles, into parts of which the last is shorter, and of an expert's rows
+TILES = [
+    (136, 4104, ragged(3000, 3, 10, 0.3)), (4104, 136, ragged(3000, 3, 11, 0.3)),  # 256 x 256
+    (200, 1032, ragged(2800, 40, 12, 0.1)), (1032, 200, ragged(2800, 40, 13, 0.1)),  # 128 x 128
+    (200, 1032, ragged(1300, 40, 14, 0.4)), (1032, 200, ragged(1300, 40, 15, 0.4)),  # 64 x 128
+    (200, 1032, ragged(500, 64, 16)), (1032, 200, ragged(500, 64, 17)),  # 16 or 32 x 128
+    (520, 520, ragged(900, 40, 18)),  # dW in 256 x 256
+    (2056, 72, [70]), (72, 2056, [70]), (5000, 136, [3, 0, 9]), (72, 64, [5000]), (64, 200, [3000, 0, 40, 1])]
+
+
+@pytest.mark.parametrize("check", [check_bf16, check_q8])
+@pytest.mark.parametrize("K,N,sizes", TILES, ids=lambda v: str(v) if isinstance(v, int) else "E%d_R%d" % (len(v), sum(v)))
+def test_every_tile_and_split(check, K, N, sizes):
+    check(0, K, N, sizes)
+
+
+def test_splits_are_taken():
+    """The cases above reach the joins of partial sums."""
+    assert B.gmm_plan(70, 2056, 72, 1).fwd_workspace_bytes > 0 and B.gmm_plan(70, 72, 2056, 1).fwd_workspace_bytes > 0
+    assert B.gmm_plan(12, 5000, 136, 3, B.GMM_Q8).fwd_workspace_bytes > 0
+    assert B.gmm_plan(5000, 72, 64, 1).bwd_workspace_bytes > 0 and B.gmm_plan(3041, 64, 200, 4).bwd_workspace_bytes > 0
+
+
 @pytest.mark.parametrize("check", [check_bf16, check_q8])
 def test_rows_of_no_expert_are_left(check):
     check(0, 136, 136, [40, 0, 100, 7], start=13, after=200)
     check(0, 136, 264, [0, 0, 0], start=5, after=9)
     check(0, 264, 136, [300], start=1, after=1)
+    check(0, 4096, 136, [5, 0, 6], start=3, after=2)
+    check(0, 72, 64, [2000, 0, 900], start=300, after=100)
 
 
 def test_without_offsets():
@@ -206,10 +232,11 @@ def test_bad_rows_spoil_their_expert_alone(q8):
     assert torch.equal(good[2][[0, 2, 3]], bad[2][[0, 2, 3]]) and torch.isnan(bad[2][1]).all()
 
 
+@pytest.mark.parametrize("rows", [300, 3, 4000])
 @pytest.mark.parametrize("operands", [B.GMM_BF16, B.GMM_Q8])
-def test_broken_offsets_stay_inside(operands):
+def test_broken_offsets_stay_inside(operands, rows):
     """Descending, negative and far too large offsets: whatever the rows hold, nothing around the outputs is touched."""
-    R, K, N, E, pad = 300, 136, 72, 5, 4096
+    R, K, N, E, pad = rows, 136, 72, 5, 4096
     g = torch.Generator().manual_seed(3)
     X, dY, W = normal(g, R, K), normal(g, R, N), normal(g, E, K, N)
     plan = B.gmm_plan(R, K, N, E, operands)
@@ -253,11 +280,14 @@ def test_scales_of_any_size():
     close(Y, X @ Wv, X.abs() @ Wv.abs(), K, E16, "Y", TRUNC)
 
 
+@pytest.mark.parametrize("split", [None, (220, 4096, 72, [100, 0, 100, 20]), (4000, 72, 64, [1500, 0, 2000, 500])], ids=str)
 @pytest.mark.parametrize("operands", [B.GMM_BF16, B.GMM_Q8])
-def test_repeats_on_streams_and_in_graphs(operands):
+def test_repeats_on_streams_and_in_graphs(operands, split):
     """Bit for bit: twice, on another stream, in two captured graphs with workspaces of their own, replayed in turn
     between eager calls, and on new inputs in the same buffers."""
     R, K, N, sizes = 700, 1000, 392, [300, 0, 250, 150]
+    if split:  # k in parts, forward or over the rows
+        R, K, N, sizes = split
     g = torch.Generator().manual_seed(5)
     X, dY, W, off = normal(g, R, K), normal(g, R, N), normal(g, 4, K, N), offsets_of(sizes)
     plan = B.gmm_plan(R, K, N, 4, operands)
@@ -288,7 +318,7 @@ def test_repeats_on_streams_and_in_graphs(operands):
         if turn == 2:
             X.mul_(0.5)
             dY.copy_(dY.flip(0))
-            off.copy_(offsets_of([1, 500, 199, 0]))
+            off.copy_(offsets_of([1, R - 200, 199, 0]))
             B.q8_pack(rp, X, Xq, Xs)
             want = [t.clone() for t in run(spaces[0])]
         for graph, out in graphs:
