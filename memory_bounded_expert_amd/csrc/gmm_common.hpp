@@ -39,6 +39,17 @@ template <int BM_, int BN_, int WGM_, int WGN_, int NS_>
 struct GShape {
   static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, WAVES = WGM_ * WGN_, THREADS = 64 * WAVES;
   static constexpr int WM = BM / WGM, WN = BN / WGN, NS = NS_;
+  // Where wave w's part of the tile lies.  Waves w and w + 4 share a SIMD: of eight,
+  // the second four are placed so that each half of the tile, upper or left, has one
+  // wave on every SIMD, and a tile of which the other half lies past the matrix takes
+  // half the multiplications' time.
+  static __device__ __forceinline__ int row(int w) {
+    return WGM == 4 && WGN == 2 ? (w >> 2) * 2 + (w & 1) : w / WGN;
+  }
+  static __device__ __forceinline__ int col(int w) {
+    if (WGM == 4 && WGN == 2) return ((w >> 1) & 1) ^ (w >> 2);
+    return WGM == 2 && WGN == 4 ? (w & 3) ^ ((w >> 2) * 2) : w % WGN;
+  }
 };
 
 // Rows of expert e, kept inside the matrix whatever the offsets say.

@@ -41,7 +41,7 @@ struct Tile {
 // in its L2 (65,536 x 4096 x 4096 in e4m3: 987 us without groups, 919 with groups
 // of 4, 903 of 8; 16,384 x 4096 x 4096 in bf16 435, 418 and 426).  Every wave finds
 // its tile for itself, an expert a lane, the tile counts added up over the lanes.
-template <int C>  // chunks of 64 experts held in registers
+template <int C>  // sets of 64 experts held in registers
 __device__ __forceinline__ bool find_tile_in(const int32_t* offsets, int E, int R, int bm, int ntiles, int side, int bid, Tile& t) {
   const int lane = threadIdx.x & 63;
   Segment s[C];
@@ -55,13 +55,7 @@ __device__ __forceinline__ bool find_tile_in(const int32_t* offsets, int E, int 
 #pragma unroll
   for (int c = 0; c < C; ++c) cum[c] = tiles[c] = (s[c].hi - s[c].lo + bm - 1) / bm;
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int v = __shfl_up(cum[c], o);
-      if (lane >= o) cum[c] += v;
-    }
-  }
+  for (int c = 0; c < C; ++c) cum[c] = wave_scan(cum[c]);
   int base[C + 1];
   base[0] = 0;
 #pragma unroll
@@ -124,7 +118,7 @@ __global__ __launch_bounds__(S::THREADS) void gmm_rows_kernel(const Args p, int 
   constexpr int RCB = S::BN / 8;
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / S::WGN, wn = wave % S::WGN;
+  const int wm = S::row(wave), wn = S::col(wave);
 
   Tile t;
   if (!find_tile(p.offsets, p.E, p.R, S::BM, ntiles, Q8 ? 8 : 4, blockIdx.x, t)) return;
@@ -271,7 +265,8 @@ __global__ __launch_bounds__(S::THREADS) void gmm_rows_kernel(const Args p, int 
   // ---- the sum.  Step t goes to stage t % NS.  Steps past the last are loads of
   // the last one again, never used, so that every wait counts the same loads (a wave
   // with more than PER_STEP of them waits for a few too many).
-  const bool active = m0 + wm * S::WM < m_end;  // a wave without rows only helps with the loads
+  // a wave without rows or columns only helps with the loads
+  const bool active = m0 + wm * S::WM < m_end && n0 + wn * S::WN < p.N;
 #pragma unroll
   for (int s = 0; s < NS; ++s) issue(min(s, last), s);
   wait_vmcnt<(NS - 1) * C::PER_STEP>();

@@ -54,7 +54,7 @@ __global__ __launch_bounds__(S::THREADS) void gmm_weights_kernel(const Args p, i
   constexpr int RCA = S::BM / 8, RCB = S::BN / 8;
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / S::WGN, wn = wave % S::WGN;
+  const int wm = S::row(wave), wn = S::col(wave);
 
   // an expert's tiles run on one XCD, whose L2 then holds its rows once
   const int per = mtiles * ntiles, lid = xcd_contiguous(blockIdx.x, gridDim.x);

@@ -32,6 +32,18 @@ __device__ __forceinline__ int row_shr(int v) {
   return __builtin_amdgcn_update_dpp(0, v, 0x110 + n, 0xf, 0xf, false);
 }
 
+// Sum over the wave's lanes up to and including this one: within rows of 16, then
+// row 0's last lane onto row 1 and row 2's onto row 3, then lane 31 onto both.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += row_shr<1>(v);
+  v += row_shr<2>(v);
+  v += row_shr<4>(v);
+  v += row_shr<8>(v);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
+  return v;
+}
+
 // Reductions over aligned runs of G = 16 or 64 lanes; every lane of the run ends
 // with the same bits.  Within a row of 16 by rotations, whose pairs are
 // combined commutatively step by step; the four rows through lanes 0, 16, 32,
