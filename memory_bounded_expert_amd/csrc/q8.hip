@@ -1,8 +1,8 @@
 // Rows in 8 bits, and SwiGLU with activation checkpoints in 8 bits (include/q8.h).
 //
 // All of it moves a few bytes per operation and is bound by HBM.  A block of 128
-// columns is 16 lanes with eight columns each, so its scale is a reduction over a
-// row of lanes; every value is read once.
+// columns is eight lanes with 16 columns each: 16 bytes of e4m3 a lane, and a scale by
+// three reductions in DPP operands.  Every value is read once.
 #include <algorithm>
 
 #include "device_common.hpp"
@@ -17,27 +17,27 @@ namespace moe {
 namespace {
 
 constexpr uint32_t kQ8Magic = 0x51385031u;  // "Q8P1"
-constexpr unsigned kMaxGroups = 1u << 16;
 
-// Eight values at p, of which n (maybe none) are there; the rest 0.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, float* v) {
+// NV values at p, of which n (maybe none) are there; the rest 0.
+template <int NV, typename T>
+__device__ __forceinline__ void load_some(const T* p, int n, float* v) {
   constexpr int EPC = Elem<T>::kPer16B;
 #pragma unroll
-  for (int c = 0; c < 8; c += EPC) {
+  for (int c = 0; c < NV; c += EPC) {
     if (n >= c + EPC) {
-      unpack16(*reinterpret_cast<const u32x4_any_t*>(p + c), v + c, T());
+      const u32x4_t w = *reinterpret_cast<const u32x4_any_t*>(p + c);
+      unpack16(w, v + c, T());
     } else {
 #pragma unroll
       for (int e = 0; e < EPC; ++e) v[c + e] = c + e < n ? Elem<T>::to_f(p[c + e]) : 0.f;
     }
   }
 }
-template <typename T>
-__device__ __forceinline__ void store8(T* p, int n, const float* v) {
+template <int NV, typename T>
+__device__ __forceinline__ void store_some(T* p, int n, const float* v) {
   constexpr int EPC = Elem<T>::kPer16B;
 #pragma unroll
-  for (int c = 0; c < 8; c += EPC) {
+  for (int c = 0; c < NV; c += EPC) {
     if (n >= c + EPC) {
       *reinterpret_cast<u32x4_any_t*>(p + c) = pack16(v + c, T());
     } else {
@@ -48,84 +48,90 @@ __device__ __forceinline__ void store8(T* p, int n, const float* v) {
   }
 }
 
-// Where a row of lanes' block goes.
+// Where blocks go.
 struct Packed {
   uint8_t *q, *s;
 };
+// A launch's blocks: `units` of them from row `first` on.  u / blocks is a product by
+// `magic` and a shift (units is below 2^31).
 struct Shape8 {
-  int64_t units;  // rows times blocks
+  int64_t first;
+  uint32_t units, magic, shift;
   int H, blocks, row_pitch, scale_pitch;
 };
+constexpr int kCols = 16, kLanes = kQBlock / kCols;  // columns of a lane, lanes of a block
 
-// Writes a lane's eight values of block b of row r, with the block's scale; the
-// row's last block writes the scales' padding too.
-__device__ __forceinline__ void put8(const Packed& to, const Shape8& sh, int64_t r, int b, int lane,
-                                     const float* v) {
-  float amax = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, q8_magnitude(v[e]));
-  const uint32_t byte = q8_scale_byte(run_maxf<16>(amax));
+// Writes a lane's values of block b of row r, with the block's scale; the row's last
+// block writes the scales' padding too.
+__device__ __forceinline__ void put(const Packed& to, const Shape8& sh, int64_t r, int b, int lane, const float* v) {
+  const uint32_t byte = q8_scale_byte(q8_amax<kCols>(v, [](float m) { return run8_maxf(m); }));
   const float inv = q8_inverse(byte);
-  *reinterpret_cast<uint2*>(to.q + r * sh.row_pitch + b * kQBlock + lane * 8) =
-      make_uint2(q8_round4(v, inv), q8_round4(v + 4, inv));
+  *reinterpret_cast<u32x4_t*>(to.q + r * sh.row_pitch + b * kQBlock + lane * kCols) =
+      u32x4_t{q8_round4(v, inv), q8_round4(v + 4, inv), q8_round4(v + 8, inv), q8_round4(v + 12, inv)};
   uint8_t* s = to.s + r * sh.scale_pitch;
   if (lane == 0) s[b] = (uint8_t)byte;
   if (b == sh.blocks - 1 && lane < sh.scale_pitch - sh.blocks) s[sh.blocks + lane] = kQOne;
 }
-__device__ __forceinline__ void get8(const uint8_t* q, const uint8_t* s, const Shape8& sh, int64_t r,
-                                     int b, int lane, float* v) {
+__device__ __forceinline__ void get(const uint8_t* q, const uint8_t* s, const Shape8& sh, int64_t r, int b, int lane,
+                                    float* v) {
   const float scale = q8_scale(s[r * sh.scale_pitch + b]);
-  const uint2 w = *reinterpret_cast<const uint2*>(q + r * sh.row_pitch + b * kQBlock + lane * 8);
-  q8_values4(w.x, scale, v);
-  q8_values4(w.y, scale, v + 4);
+  const u32x4_t w = *reinterpret_cast<const u32x4_t*>(q + r * sh.row_pitch + b * kQBlock + lane * kCols);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) q8_values4(w[e], scale, v + 4 * e);
 }
 
-// Calls f(row, block, lane of the block, column, columns there) for this thread's
-// share of all blocks.
+// Calls f(row, block, lane of the block, first value's place in a matrix, columns
+// there) for this thread's block.
 template <typename F>
-__device__ __forceinline__ void each_block(const Shape8& sh, F f) {
-  const int lane = threadIdx.x & 15;
-  for (int64_t u = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4); u < sh.units;
-       u += (int64_t)gridDim.x * (kThreads / 16)) {
-    const int64_t r = u / sh.blocks;
-    const int b = (int)(u - r * sh.blocks), col = b * kQBlock + lane * 8;
-    f(r, b, lane, col, sh.H - col);
-  }
+__device__ __forceinline__ void my_block(const Shape8& sh, F f) {
+  const int lane = threadIdx.x % kLanes;
+  const uint32_t u = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+  if (u >= sh.units) return;
+  const uint32_t row = (uint32_t)(((uint64_t)u * sh.magic) >> sh.shift);
+  const int b = (int)(u - row * sh.blocks), col = b * kQBlock + lane * kCols;
+  const int64_t r = sh.first + row;
+  f(r, b, lane, r * sh.H + col, sh.H - col);
 }
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void pack_kernel(const T* __restrict__ X, const Packed to, const Shape8 sh) {
-  each_block(sh, [&](int64_t r, int b, int lane, int col, int n) {
-    float v[8];
-    load8(X + r * sh.H + col, n, v);
-    put8(to, sh, r, b, lane, v);
+  my_block(sh, [&](int64_t r, int b, int lane, int64_t at, int n) {
+    float v[kCols];
+    load_some<kCols>(X + at, n, v);
+    put(to, sh, r, b, lane, v);
   });
 }
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void unpack_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
                                                           T* __restrict__ X, const Shape8 sh) {
-  each_block(sh, [&](int64_t r, int b, int lane, int col, int n) {
-    float v[8];
-    get8(q, s, sh, r, b, lane, v);
-    store8(X + r * sh.H + col, n, v);
+  my_block(sh, [&](int64_t r, int b, int lane, int64_t at, int n) {
+    float v[kCols];
+    get(q, s, sh, r, b, lane, v);
+    store_some<kCols>(X + at, n, v);
   });
 }
+
+// 1 / (1 + e^-a): in bf16 through the hardware's exponential and reciprocal, as the
+// layer's own SwiGLU does (an IEEE exponential and quotient take longer than the
+// bytes), in fp32 exactly rounded steps.
+__device__ __forceinline__ float gate(float a, bf16_t) { return logistic(a); }
+__device__ __forceinline__ float gate(float a, float) { return 1.f / (1.f + expf(-a)); }
 
 template <typename T, bool KEEP>
 __global__ __launch_bounds__(kThreads) void swiglu_forward_kernel(const T* __restrict__ A, const T* __restrict__ U,
                                                                   const Packed h, const Packed ka,
                                                                   const Packed ku, const Shape8 sh) {
-  each_block(sh, [&](int64_t r, int b, int lane, int col, int n) {
-    float a[8], u[8], v[8];
-    load8(A + r * sh.H + col, n, a);
-    load8(U + r * sh.H + col, n, u);
+  my_block(sh, [&](int64_t r, int b, int lane, int64_t at, int n) {
+    float a[kCols], u[kCols], v[kCols];
+    load_some<kCols>(A + at, n, a);
+    load_some<kCols>(U + at, n, u);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = a[e] / (1.f + expf(-a[e])) * u[e];
-    put8(h, sh, r, b, lane, v);
+    for (int e = 0; e < kCols; ++e) v[e] = a[e] * gate(a[e], T()) * u[e];
+    put(h, sh, r, b, lane, v);
     if constexpr (KEEP) {
-      put8(ka, sh, r, b, lane, a);
-      put8(ku, sh, r, b, lane, u);
+      put(ka, sh, r, b, lane, a);
+      put(ku, sh, r, b, lane, u);
     }
   });
 }
@@ -134,19 +140,19 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
     const uint8_t* __restrict__ Aq, const uint8_t* __restrict__ As, const uint8_t* __restrict__ Uq,
     const uint8_t* __restrict__ Us, const T* dH, T* dA, T* __restrict__ dU, const Shape8 sh) {
-  each_block(sh, [&](int64_t r, int b, int lane, int col, int n) {
-    float a[8], u[8], d[8];
-    get8(Aq, As, sh, r, b, lane, a);
-    get8(Uq, Us, sh, r, b, lane, u);
-    load8(dH + r * sh.H + col, n, d);
+  my_block(sh, [&](int64_t r, int b, int lane, int64_t at, int n) {
+    float a[kCols], u[kCols], d[kCols];
+    get(Aq, As, sh, r, b, lane, a);
+    get(Uq, Us, sh, r, b, lane, u);
+    load_some<kCols>(dH + at, n, d);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float g = 1.f / (1.f + expf(-a[e]));
-      u[e] = d[e] * u[e] * g * fmaf(a[e], 1.f - g, 1.f);
-      d[e] = d[e] * a[e] * g;
+    for (int e = 0; e < kCols; ++e) {
+      const float g = gate(a[e], T()), dg = d[e] * g;
+      u[e] = dg * u[e] * fmaf(a[e], 1.f - g, 1.f);
+      d[e] = dg * a[e];
     }
-    store8(dA + r * sh.H + col, n, u);
-    store8(dU + r * sh.H + col, n, d);
+    store_some<kCols>(dA + at, n, u);
+    store_some<kCols>(dU + at, n, d);
   });
 }
 
@@ -165,19 +171,19 @@ __global__ __launch_bounds__(kThreads) void pack_weights_kernel(
   const int kblocks = q8_blocks(K), nblocks = q8_blocks(N);
   const T* w = W + (int64_t)e * K * N;
   const int col = nb * kQBlock + lane * 8;
-  float v[8][8], amax = 0.f;
+  float v[8][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int k = kb * kQBlock + i * 16 + row;
-    load8(w + (int64_t)min(k, K - 1) * N + min(col, N), k < K ? N - col : 0, v[i]);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, q8_magnitude(v[i][j]));
+    load_some<8>(w + (int64_t)min(k, K - 1) * N + min(col, N), k < K ? N - col : 0, v[i]);
   }
-  amax = run_maxf<64>(amax);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
-  __syncthreads();
-  amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  const uint32_t byte = q8_scale_byte(amax);
+  const uint32_t byte = q8_scale_byte(q8_amax<64>(&v[0][0], [&](float m) {
+    m = run_maxf<64>(m);
+    __syncthreads();  // the reads of a first reduction are done
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+    __syncthreads();
+    return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  }));
   const float inv = q8_inverse(byte);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -219,12 +225,23 @@ __global__ __launch_bounds__(kThreads) void pack_weights_kernel(
   }
 }
 
-Shape8 shape_of(const q8_plan_t& P) {
+// Calls f(shape, work-groups) for launches of below 2^31 blocks that cover all rows.
+template <typename F>
+int in_launches(const q8_plan_t& P, F f) {
   const int blocks = q8_blocks(P.H);
-  return Shape8{P.N * blocks, P.H, blocks, P.row_pitch, P.scale_pitch};
-}
-unsigned groups_of(const Shape8& sh) {
-  return (unsigned)std::min<int64_t>(ceil_div(sh.units, kThreads / 16), kMaxGroups);
+  // u / blocks = u magic >> shift for u < 2^31: magic = ceil(2^shift / blocks), whose
+  // error, below blocks, times u stays below 2^shift = 2^31 times a power of two >= blocks
+  uint32_t shift = 31;
+  while ((1u << (shift - 31)) < (uint32_t)blocks) ++shift;
+  Shape8 sh{0, 0, (uint32_t)((((uint64_t)1 << shift) + blocks - 1) / blocks), shift, P.H, blocks, P.row_pitch, P.scale_pitch};
+  const int64_t most = (((int64_t)1 << 31) - 1) / blocks;
+  (void)hipGetLastError();
+  for (; sh.first < P.N; sh.first += most) {
+    sh.units = (uint32_t)(std::min(most, P.N - sh.first) * blocks);
+    f(sh, (unsigned)ceil_div(sh.units, kThreads / kLanes));
+    if (hipGetLastError() != hipSuccess) return MOE_EHIP;
+  }
+  return MOE_OK;
 }
 bool plan_ok(const q8_plan_t* p) { return p != nullptr && p->magic == kQ8Magic; }
 // q on a 16-byte step, s on a 4-byte step, both there
@@ -259,26 +276,24 @@ MOE_API int q8_pack(const q8_plan_t* plan, const void* X, void* q, void* s, void
   if (!plan_ok(plan)) return MOE_EINVAL;
   if (plan->N == 0) return MOE_OK;
   if (!elem_ok(*plan, X) || !pair_ok(q, s)) return MOE_EINVAL;
-  const Shape8 sh = shape_of(*plan);
-  (void)hipGetLastError();
-  if (plan->dtype == MOE_BF16)
-    pack_kernel<bf16_t><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>((const bf16_t*)X, packed(q, s), sh);
-  else
-    pack_kernel<float><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>((const float*)X, packed(q, s), sh);
-  return launched();
+  return in_launches(*plan, [&](const Shape8& sh, unsigned groups) {
+    if (plan->dtype == MOE_BF16)
+      pack_kernel<bf16_t><<<groups, kThreads, 0, (hipStream_t)stream>>>((const bf16_t*)X, packed(q, s), sh);
+    else
+      pack_kernel<float><<<groups, kThreads, 0, (hipStream_t)stream>>>((const float*)X, packed(q, s), sh);
+  });
 }
 
 MOE_API int q8_unpack(const q8_plan_t* plan, const void* q, const void* s, void* X, void* stream) {
   if (!plan_ok(plan)) return MOE_EINVAL;
   if (plan->N == 0) return MOE_OK;
   if (!elem_ok(*plan, X) || !pair_ok(q, s)) return MOE_EINVAL;
-  const Shape8 sh = shape_of(*plan);
-  (void)hipGetLastError();
-  if (plan->dtype == MOE_BF16)
-    unpack_kernel<bf16_t><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>((const uint8_t*)q, (const uint8_t*)s, (bf16_t*)X, sh);
-  else
-    unpack_kernel<float><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>((const uint8_t*)q, (const uint8_t*)s, (float*)X, sh);
-  return launched();
+  return in_launches(*plan, [&](const Shape8& sh, unsigned groups) {
+    if (plan->dtype == MOE_BF16)
+      unpack_kernel<bf16_t><<<groups, kThreads, 0, (hipStream_t)stream>>>((const uint8_t*)q, (const uint8_t*)s, (bf16_t*)X, sh);
+    else
+      unpack_kernel<float><<<groups, kThreads, 0, (hipStream_t)stream>>>((const uint8_t*)q, (const uint8_t*)s, (float*)X, sh);
+  });
 }
 
 MOE_API int q8_pack_weights(int32_t E, int32_t K, int32_t N, int32_t dtype, const void* W, void* q,
@@ -304,23 +319,21 @@ namespace {
 template <typename T>
 int swiglu_forward(const q8_plan_t& P, const void* A, const void* U, const Packed& h, const Packed& ka,
                    const Packed& ku, void* stream) {
-  const Shape8 sh = shape_of(P);
-  (void)hipGetLastError();
-  if (ka.q)
-    swiglu_forward_kernel<T, true><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>((const T*)A, (const T*)U, h, ka, ku, sh);
-  else
-    swiglu_forward_kernel<T, false><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>((const T*)A, (const T*)U, h, ka, ku, sh);
-  return launched();
+  return in_launches(P, [&](const Shape8& sh, unsigned groups) {
+    if (ka.q)
+      swiglu_forward_kernel<T, true><<<groups, kThreads, 0, (hipStream_t)stream>>>((const T*)A, (const T*)U, h, ka, ku, sh);
+    else
+      swiglu_forward_kernel<T, false><<<groups, kThreads, 0, (hipStream_t)stream>>>((const T*)A, (const T*)U, h, ka, ku, sh);
+  });
 }
 template <typename T>
 int swiglu_backward(const q8_plan_t& P, const void* Aq, const void* As, const void* Uq, const void* Us,
                     const void* dH, void* dA, void* dU, void* stream) {
-  const Shape8 sh = shape_of(P);
-  (void)hipGetLastError();
-  swiglu_backward_kernel<T><<<groups_of(sh), kThreads, 0, (hipStream_t)stream>>>(
-      (const uint8_t*)Aq, (const uint8_t*)As, (const uint8_t*)Uq, (const uint8_t*)Us, (const T*)dH,
-      (T*)dA, (T*)dU, sh);
-  return launched();
+  return in_launches(P, [&](const Shape8& sh, unsigned groups) {
+    swiglu_backward_kernel<T><<<groups, kThreads, 0, (hipStream_t)stream>>>(
+        (const uint8_t*)Aq, (const uint8_t*)As, (const uint8_t*)Uq, (const uint8_t*)Us, (const T*)dH,
+        (T*)dA, (T*)dU, sh);
+  });
 }
 }  // namespace
 

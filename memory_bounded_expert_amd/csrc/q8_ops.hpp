@@ -14,11 +14,6 @@ constexpr int q8_row_pitch(int H) { return (H + kQBlock - 1) / kQBlock * kQBlock
 constexpr int q8_blocks(int H) { return (H + kQBlock - 1) / kQBlock; }
 constexpr int q8_scale_pitch(int H) { return (q8_blocks(H) + 3) / 4 * 4; }
 
-// |v|, or 0 where v is not finite: what counts for a block's scale
-__device__ __forceinline__ float q8_magnitude(float v) {
-  return __builtin_isfinite(v) ? fabsf(v) : 0.f;
-}
-
 // The byte of the smallest power of two 2^e, e >= -110, with amax / 2^e <= 448 =
 // 1.75 * 2^8: with amax = 1.f * 2^x, e = x - 8, and one more where 1.f > 1.75.
 __device__ __forceinline__ uint32_t q8_scale_byte(float amax) {
@@ -33,11 +28,29 @@ __device__ __forceinline__ float q8_scale(uint32_t byte) {
   return byte == 0 ? __uint_as_float(0x00400000u) : byte == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(byte << 23);
 }
 
-// Four values as e4m3 (v_cvt_pk_fp8_f32: to nearest, ties to even).  The scale
-// leaves no finite quotient above 448; v - v is 0, or NaN where v is not finite.
+// The largest finite magnitude among n values of each of a run of lanes, by reduce().
+// A maximum passes NaN over; where it finds an infinity the values are gone through
+// again without it.
+template <int n, typename R>
+__device__ __forceinline__ float q8_amax(const float* v, R reduce) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < n; ++e) m = fmaxf(m, fabsf(v[e]));
+  m = reduce(m);
+  if (__builtin_isinf(m)) {  // the same in all lanes of the run
+    m = 0.f;
+#pragma unroll
+    for (int e = 0; e < n; ++e) m = fmaxf(m, __builtin_isinf(v[e]) ? 0.f : fabsf(v[e]));
+    m = reduce(m);
+  }
+  return m;
+}
+
+// Four values as e4m3 (v_cvt_pk_fp8_f32: to nearest, ties to even; infinities and NaN
+// to NaN).  The scale leaves no finite quotient above 448.
 __device__ __forceinline__ uint32_t q8_round4(const float* v, float inv) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(fmaf(v[0], inv, v[0] - v[0]), fmaf(v[1], inv, v[1] - v[1]), 0, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(fmaf(v[2], inv, v[2] - v[2]), fmaf(v[3], inv, v[3] - v[3]), w, true);
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, w, true);
   return (uint32_t)w;
 }
 // Four numbers of a word times the scale

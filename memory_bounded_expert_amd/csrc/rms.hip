@@ -86,18 +86,18 @@ __global__ __launch_bounds__(kGroup<W>) void rms_rows_forward_kernel(
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int at = (c * 64 * W + place) * EPC;
-        float v[EPC], amax = 0.f;
+        float v[EPC];
         cur.get(c, v);
 #pragma unroll
         for (int e = 0; e < EPC; ++e) {
           v[e] = v[e] * r * ga[c * EPC + e];
           // past the row's end x and gamma are 0, but r may be NaN
           if (at + e >= H) v[e] = 0.f;
-          amax = fmaxf(amax, q8_magnitude(v[e]));
         }
-        amax = run_maxf<16>(amax);
-        if constexpr (EPC == 4) amax = fmaxf(amax, __shfl_xor(amax, 16));
-        const uint32_t byte = q8_scale_byte(amax);
+        const uint32_t byte = q8_scale_byte(q8_amax<EPC>(v, [](float m) {
+          m = run_maxf<16>(m);
+          return EPC == 4 ? fmaxf(m, __shfl_xor(m, 16)) : m;
+        }));
         const float qi = q8_inverse(byte);
         if (at < out.row_pitch) {
           if constexpr (EPC == 8)
@@ -258,15 +258,13 @@ __global__ __launch_bounds__(kThreads) void rms_forward_kernel(
       const int blocks = q8_blocks(H);
       for (int b = threadIdx.x / 32; b < blocks; b += kThreads / 32) {
         const int at = b * kQBlock + (threadIdx.x & 31) * 4;
-        float v[4], amax = 0.f;
+        float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = at + e < H ? Elem<T>::to_f(x[at + e]) * r * gamma[at + e] : 0.f;
-          amax = fmaxf(amax, q8_magnitude(v[e]));
-        }
-        amax = run_maxf<16>(amax);
-        amax = fmaxf(amax, __shfl_xor(amax, 16));
-        const uint32_t byte = q8_scale_byte(amax);
+        for (int e = 0; e < 4; ++e) v[e] = at + e < H ? Elem<T>::to_f(x[at + e]) * r * gamma[at + e] : 0.f;
+        const uint32_t byte = q8_scale_byte(q8_amax<4>(v, [](float m) {
+          m = run_maxf<16>(m);
+          return fmaxf(m, __shfl_xor(m, 16));
+        }));
         *reinterpret_cast<uint32_t*>(qo + at) = q8_round4(v, q8_inverse(byte));
         if ((threadIdx.x & 31) == 0) sc[b] = (uint8_t)byte;
       }

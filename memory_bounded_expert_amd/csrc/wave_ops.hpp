@@ -3,6 +3,8 @@
 // wave's own LDS traffic.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.hpp"
 
 namespace moe {
@@ -60,6 +62,15 @@ __device__ __forceinline__ V run_reduce(V v, Op op) {
     v = op(op(lane(0), lane(16)), op(lane(32), lane(48)));
   }
   return v;
+}
+// The largest of an aligned run of 8 lanes: pairs, quads, and the quad mirrored.
+__device__ __forceinline__ float run8_maxf(float v) {
+  auto dpp = [](float x, auto ctrl) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl.value, 0xf, 0xf, false));
+  };
+  v = fmaxf(v, dpp(v, std::integral_constant<int, 0xB1>()));   // quad_perm [1,0,3,2]
+  v = fmaxf(v, dpp(v, std::integral_constant<int, 0x4E>()));   // quad_perm [2,3,0,1]
+  return fmaxf(v, dpp(v, std::integral_constant<int, 0x141>()));  // row_half_mirror
 }
 template <int G>
 __device__ __forceinline__ float run_sum(float v) {
