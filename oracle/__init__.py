@@ -53,3 +53,5 @@ from .distill_oracle import (  # noqa: F401,E402
     kd_dlogits,
     kd_backward,
 )
+
+from . import q8_oracle  # noqa: F401,E402

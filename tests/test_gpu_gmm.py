@@ -232,6 +232,83 @@ def test_bad_rows_spoil_their_expert_alone(q8):
     assert torch.equal(good[2][[0, 2, 3]], bad[2][[0, 2, 3]]) and torch.isnan(bad[2][1]).all()
 
 
+@pytest.mark.parametrize("K,N", [(136, 264), (200, 72), (64, 1032)])
+@pytest.mark.parametrize("q8", [False, True])
+def test_a_bad_matrix_spoils_its_expert_alone(q8, K, N):
+    """NaN and infinities in one expert's W: tiles and steps that end inside a matrix read nothing of the next."""
+    sizes = [60, 70, 0, 90]
+    g = torch.Generator().manual_seed(7)
+    X, dY, W, off = normal(g, 220, K), normal(g, 220, N), normal(g, 4, K, N), offsets_of(sizes)
+    plan = B.gmm_plan(220, K, N, 4, B.GMM_Q8 if q8 else B.GMM_BF16)
+
+    def run():
+        if q8:
+            return [B.gmm8_forward(plan, *B.q8_pack(B.q8_plan(220, K), X), *B.q8_pack_weights(W, "K"), off)]
+        return [B.gmm_forward(plan, X, W, off), B.gmm_backward_dx(plan, dY, W, off)]
+
+    good = run()
+    W[1], W[2] = float("nan"), float("inf")  # (expert 2 has no rows)
+    for a, b in zip(good, run()):
+        assert torch.equal(a[:60], b[:60]) and torch.equal(a[130:], b[130:]) and torch.isnan(b[60:130]).all()
+
+
+def test_scale_bytes_at_their_ends():
+    """NaN's byte makes its row (in dW its block of columns) NaN and nothing else; the least and largest scales hold."""
+    R, K, N = 40, 300, 136
+    g = torch.Generator().manual_seed(8)
+    q, s, _ = rows8(g, R, K)
+    W = torch.randn(1, K, N, generator=g).to(DEV)
+    Wq, Ws = B.q8_pack_weights(W, "K")
+    dY = normal(g, R, N)
+    plan = B.gmm_plan(R, K, N, 1, B.GMM_Q8)
+    good, dgood = B.gmm8_forward(plan, q, s, Wq, Ws), B.gmm8_backward_dw(plan, q, s, dY)
+    b = s.view(torch.uint8)
+    b[7, 1] = 255
+    y, dw = B.gmm8_forward(plan, q, s, Wq, Ws), B.gmm8_backward_dw(plan, q, s, dY)
+    rows = [r for r in range(R) if r != 7]
+    assert torch.equal(y[rows], good[rows]) and torch.isnan(y[7]).all()
+    assert torch.isnan(dw[0, 128:256]).all() and torch.equal(dw[0, :128], dgood[0, :128]) and torch.equal(dw[0, 256:], dgood[0, 256:])
+    for byte in (17, 0, 237):  # 2^-110; 2^-127, whose values no longer show; 2^110
+        b[:] = byte
+        x = q.double()[:, :K] * 2.0 ** (byte - 127)
+        w = (Wq[0, :, :K].double() * torch.exp2(Ws.view(torch.uint8)[0, :, :3].double() - 127).repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]).T.contiguous()
+        ref, size = x @ w, x.abs() @ w.abs()
+        tiny = 2.0 ** -126 if byte == 0 else 0.0  # what underflows in fp32
+        got = B.gmm8_forward(plan, q, s, Wq, Ws).double()
+        assert not ((got - ref).abs() > (2 * U * K + TRUNC) * size * (1 + E16) + E16 * ref.abs() + tiny).any(), byte
+
+
+def test_matrices_past_32_bits():
+    """More than 2^31 values in X, dY and dX: the last expert's rows and matrix."""
+    R, K, N = 270_000, 8192, 64
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g = torch.Generator().manual_seed(9)
+    part = normal(g, 1000, K)
+    X = part.repeat(R // 1000, 1)
+    W, dY, off = normal(g, 2, K, N, std=0.05), normal(g, 1000, N).repeat(R // 1000, 1), offsets_of([R - 700, 700])
+    plan = B.gmm_plan(R, K, N, 2)
+    last = slice(R - 700, R)
+    x, d, w = X[last].double(), dY[last].double(), W[1].double()
+    close(B.gmm_forward(plan, X, W, off)[last], x @ w, x.abs() @ w.abs(), K, E16, "Y")
+    dX = B.gmm_backward_dx(plan, dY, W, off)
+    close(dX[last], d @ w.T.contiguous(), d.abs() @ w.abs().T.contiguous(), N, E16, "dX")
+    del dX
+    dW = B.gmm_backward_dw(plan, X, dY, off)
+    xt = x.T.contiguous()
+    close(dW[1], xt @ d, xt.abs() @ d.abs(), 700, 0, "dW")
+    Xq, Xs = B.q8_pack(B.q8_plan(R, K), X)
+    del X
+    plan = B.gmm_plan(R, K, N, 2, B.GMM_Q8)
+    Wq, Ws = B.q8_pack_weights(W, "K")
+    xv = B.q8_unpack(B.q8_plan(700, K), Xq[last].contiguous(), Xs[last].contiguous()).double()
+    s8 = torch.exp2(Ws.view(torch.uint8)[1, :, :64].double() - 127).repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)
+    w = (Wq[1].double() * s8).T.contiguous()
+    close(B.gmm8_forward(plan, Xq, Xs, Wq, Ws, off)[last], xv @ w, xv.abs() @ w.abs(), K, E16, "Y", TRUNC)
+    xt = xv.T.contiguous()
+    close(B.gmm8_backward_dw(plan, Xq, Xs, dY, off)[1], xt @ d, xt.abs() @ d.abs(), 700, 0, "dW")
+
+
 @pytest.mark.parametrize("rows", [300, 3, 4000])
 @pytest.mark.parametrize("operands", [B.GMM_BF16, B.GMM_Q8])
 def test_broken_offsets_stay_inside(operands, rows):
