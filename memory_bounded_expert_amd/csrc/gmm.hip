@@ -135,7 +135,7 @@ int rows_product(Args a, void* workspace, hipStream_t st) {
 template <Form F, class S>
 int weights_launch(const Args& a, const Choice& c, hipStream_t st) {
   const int mtiles = (int)ceil_div(a.K, S::BM), ntiles = (int)ceil_div(a.N, S::BN);
-  const dim3 grid((unsigned)((int64_t)a.E * mtiles * ntiles), c.splits);
+  const dim3 grid((unsigned)weights_groups((int64_t)a.E * mtiles * ntiles), c.splits);
   constexpr int lds = WeightsCfg<F, S>::LDS;
   static uint64_t whole = 0;
   (void)hipGetLastError();

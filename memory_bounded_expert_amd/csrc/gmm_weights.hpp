@@ -45,6 +45,65 @@ struct WeightsCfg {
   }
 };
 
+// An expert's tiles run in blocks of 4 x 2, whose work-groups share row panels in an
+// XCD's L2; the tiles go to the XCDs in turn, eight at a time, so that every XCD has
+// its part of each expert's rows, however they are spread.  With an expert's tiles on
+// one XCD instead (each pass on other operands): 32,768 rows, 2048 x 1408, over 64
+// experts whose shares fall by r^-0.2 302 us where these take 281, by r^-1 487 and
+// 300; 65,536 rows, 4096 x 1536, 32 experts, r^-0.5 1020 and 755.
+// Experts of more than twice the mean rows come first: their tiles take longest.
+// (128 experts, 1024 x 1024, r^-1, the same operands every pass: 214 us in the
+// experts' order, 139.)
+constexpr int kBlockM = 4, kBlockN = 2, kDeal = 8;
+inline int64_t weights_groups(int64_t tiles) { return ceil_div(tiles, 8 * kDeal) * 8 * kDeal; }
+struct WeightsTile {
+  int e, mt, nt;
+  Segment rows;
+};
+template <int C>  // sets of 64 experts, one a lane
+__device__ __forceinline__ bool find_weights_tile_in(const int32_t* offsets, int E, int R, int place, WeightsTile& t) {
+  const int lane = threadIdx.x & 63;
+  Segment s[C];
+  unsigned long long large[C];
+  int first = 0;  // large experts
+#pragma unroll
+  for (int c = 0; c < C; ++c) s[c] = segment(offsets, min(c * 64 + lane, E - 1), R);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    large[c] = __ballot(c * 64 + lane < E && (int64_t)(s[c].hi - s[c].lo) * E > 2 * (int64_t)R);
+    first += __popcll(large[c]);
+  }
+  int at = place < first ? place : place - first;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const unsigned long long there = __ballot(c * 64 + lane < E), of = place < first ? large[c] : there & ~large[c];
+    const int here = __popcll(of);
+    if (at < here) {
+      const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(of >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)of, 0));
+      const int l = __ffsll((long long)__ballot((of >> lane & 1) && before == at)) - 1;
+      t.e = c * 64 + l;
+      t.rows = Segment{__builtin_amdgcn_readlane(s[c].lo, l), __builtin_amdgcn_readlane(s[c].hi, l)};
+      return true;
+    }
+    at -= here;
+  }
+  return false;
+}
+__device__ __forceinline__ bool find_weights_tile(const int32_t* offsets, int E, int R, int mtiles, int ntiles, int bid,
+                                                  WeightsTile& t) {
+  const int slot = bid >> 3, lid = (slot / kDeal * 8 + (bid & 7)) * kDeal + slot % kDeal;
+  const int per = mtiles * ntiles, place = lid / per;
+  if (place >= E) return false;
+  const int local = lid - place * per, pair = local / (kBlockN * mtiles), wide = min(kBlockN, ntiles - pair * kBlockN);
+  const int r = local - pair * kBlockN * mtiles, block = r / (kBlockM * wide), in_block = r - block * kBlockM * wide;
+  const int high = min(kBlockM, mtiles - block * kBlockM);
+  t.nt = pair * kBlockN + in_block / high;
+  t.mt = block * kBlockM + in_block % high;
+  if (E <= 64) return find_weights_tile_in<1>(offsets, E, R, place, t);
+  if (E <= 256) return find_weights_tile_in<4>(offsets, E, R, place, t);
+  return find_weights_tile_in<16>(offsets, E, R, place, t);
+}
+
 // Split over the rows (PART): work-group (x, y) sums part y of its expert's steps
 // of gridDim.y, into p.part [y][E][K][N].
 template <Form F, class S, bool PART>
@@ -56,14 +115,12 @@ __global__ __launch_bounds__(S::THREADS) void gmm_weights_kernel(const Args p, i
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = S::row(wave), wn = S::col(wave);
 
-  // an expert's tiles run on one XCD, whose L2 then holds its rows once
-  const int per = mtiles * ntiles, lid = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int e = __builtin_amdgcn_readfirstlane(lid / per), rem = lid - e * per;
-  const int n0 = __builtin_amdgcn_readfirstlane(rem / mtiles) * S::BN;
-  const int m0 = __builtin_amdgcn_readfirstlane(rem % mtiles) * S::BM;
-  const Segment seg = segment(p.offsets, e, p.R);
-  int64_t k0 = __builtin_amdgcn_readfirstlane(seg.lo);
-  int k_len = __builtin_amdgcn_readfirstlane(seg.hi - seg.lo);
+  WeightsTile t;
+  if (!find_weights_tile(p.offsets, p.E, p.R, mtiles, ntiles, blockIdx.x, t)) return;
+  const int e = __builtin_amdgcn_readfirstlane(t.e);
+  const int m0 = __builtin_amdgcn_readfirstlane(t.mt) * S::BM, n0 = __builtin_amdgcn_readfirstlane(t.nt) * S::BN;
+  int64_t k0 = __builtin_amdgcn_readfirstlane(t.rows.lo);
+  int k_len = __builtin_amdgcn_readfirstlane(t.rows.hi - t.rows.lo);
   if constexpr (PART) {
     const int each = ((k_len + KT - 1) / KT + gridDim.y - 1) / gridDim.y * KT;
     const int from = min(k_len, each * (int)blockIdx.y);

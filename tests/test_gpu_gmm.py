@@ -158,6 +158,25 @@ def test_every_tile_and_split(check, K, N, sizes):
     check(0, K, N, sizes)
 
 
+# experts of more than twice the mean rows, which go first in dW, among others, in every set of 64 experts, with even and
+# odd counts of tiles along both
+def hot(E, where, rows=400):
+    sizes = ragged(2 * E, E, 21, 0.3)
+    for e in where:
+        sizes[e] += rows
+    return sizes
+
+
+HOT = [(520, 264, hot(70, [0, 3, 63, 64, 69])), (1288, 648, hot(10, [9])), (264, 72, hot(300, [17, 128, 255, 256, 299], 90)),
+       (72, 136, hot(1024, [5, 600, 1023], 300)), (136, 200, hot(3, [2], 2000))]
+
+
+@pytest.mark.parametrize("check", [check_bf16, check_q8])
+@pytest.mark.parametrize("K,N,sizes", HOT, ids=lambda v: str(v) if isinstance(v, int) else "E%d_R%d" % (len(v), sum(v)))
+def test_large_experts_among_others(check, K, N, sizes):
+    check(0, K, N, sizes)
+
+
 def test_splits_are_taken():
     """The cases above reach the joins of partial sums."""
     assert B.gmm_plan(70, 2056, 72, 1).fwd_workspace_bytes > 0 and B.gmm_plan(70, 72, 2056, 1).fwd_workspace_bytes > 0
