@@ -4,6 +4,7 @@
 
 #include "gmm.h"
 #include "gmm_rows.hpp"
+#include "gmm_single.hpp"
 #include "gmm_weights.hpp"
 #include "moe_internal.h"
 
@@ -33,7 +34,7 @@ int launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP; }
 int64_t row_tiles(int64_t R, int E, int bm) { return R / bm + std::min<int64_t>(E, R); }
 
 // Tiles, and into how many parts k is split.
-enum class Size { Large, Middle, Small, Few, Tiny };
+enum class Size { Large, Middle, Small, Few, Tiny, Single };
 struct Choice {
   Size size;
   int splits, steps;  // steps: of a part
@@ -48,6 +49,8 @@ int64_t tiles_of(int64_t R, int E, int N, int bm, int bn) {
 }
 
 // Microseconds with one tile and the other, in bf16 forward / dX and in e4m3:
+//  * Single (dot products) for up to 4 rows in e4m3: 1 x 7168 x 2048 5.6 us in a graph
+//    (Few in parts 8.4), 4 rows 8.5 (8.8), 8 rows 13.9 (8.9); 1 x 2048 x 1408 3.0 (6.6).
 //  * Few (64 x 64, four stages) where there are fewer 64 x 128 tiles than CUs, so
 //    that a step's latency counts: 64 x 4096 x 4096 17 / 15, 10 (Small 35 / 35, 13).
 //  * Tiny (16 or 32 rows) for up to 16 rows an expert: 128 x 2048 x 1408 over 64
@@ -62,6 +65,7 @@ int64_t tiles_of(int64_t R, int E, int N, int bm, int bn) {
 // Few tiles and a long k: parts of at least eight steps, up to a work-group a CU (1 x
 // 7168 x 2048 21 -> 11.5; 64 x 4096 x 4096 17.3 -> 16.6).
 Choice choose_rows(bool q8, int64_t R, int K, int N, int E) {
+  if (q8 && R <= 4) return Choice{Size::Single, 1, 0};
   const int64_t rows = ceil_div(R, std::max<int64_t>(std::min<int64_t>(E, R), 1));
   const int64_t few = tiles_of(R, E, N, 64, 64);
   if (tiles_of(R, E, N, 64, 128) <= kCus) {
@@ -116,10 +120,22 @@ int rows_launch(const Args& a, const Choice& c, hipStream_t st) {
   return launched();
 }
 
+int single_launch(const Args& a, hipStream_t st) {
+  (void)hipGetLastError();
+  const unsigned grid = (unsigned)(ceil_div(ceil_div(a.N, kSingleCols * (kThreads / 64)), 8) * 8 * a.R);
+  // (1 x 2048 x 1408 2.96 us with two KiB of a row in flight, 3.22 with four; 1 x 7168 x
+  // 2048 6.3 and 6.1)
+  auto kern = a.K <= 4096 ? gmm_single_kernel<2> : gmm_single_kernel<4>;
+  kern<<<grid, kThreads, 0, st>>>(a);
+  return launched();
+}
+
 template <Form F>
 int rows_product(Args a, void* workspace, hipStream_t st) {
   const Choice c = choose_rows(F == Form::Q8, a.R, a.K, a.N, a.E);
   a.part = (float*)workspace;
+  if constexpr (F == Form::Q8)
+    if (c.size == Size::Single) return single_launch(a, st);
   switch (c.size) {
     // (waves of 64 x 128, or in bf16 128 x 64, of which the transposing reads want
     // fewer columns: 16,384 x 4096 x 4096 forward 410 us and 397)

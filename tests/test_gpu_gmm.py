@@ -177,6 +177,19 @@ def test_large_experts_among_others(check, K, N, sizes):
     check(0, K, N, sizes)
 
 
+# one to four rows: K on both sides of a KiB and of its multiples, more experts than rows, rows of no expert
+SINGLE = [(1, 8, [1]), (100, 72, [1, 0, 1]), (128, 264, [0, 2]), (1000, 136, [1]), (1024, 136, [3]), (1025, 24, [1, 1, 1, 1]),
+          (2049, 72, [0, 0, 4, 0]), (4096, 264, [2]), (4097, 136, [1, 2]), (7168, 520, [1]), (10000, 40, [0] * 200 + [1, 0, 2])]
+
+
+@pytest.mark.parametrize("start,after", [(0, 0), (1, 0), (0, 1)])
+@pytest.mark.parametrize("K,N,sizes", SINGLE, ids=lambda v: str(v) if isinstance(v, int) else "E%d_R%d" % (len(v), sum(v)))
+def test_few_rows_in_8_bits(K, N, sizes, start, after):
+    if sum(sizes) + start + after > 4:
+        sizes = [min(n, 1) for n in sizes]
+    check_q8(0, K, N, sizes, start=start, after=after)
+
+
 def test_splits_are_taken():
     """The cases above reach the joins of partial sums."""
     assert B.gmm_plan(70, 2056, 72, 1).fwd_workspace_bytes > 0 and B.gmm_plan(70, 72, 2056, 1).fwd_workspace_bytes > 0
@@ -295,6 +308,37 @@ def test_scale_bytes_at_their_ends():
         tiny = 2.0 ** -126 if byte == 0 else 0.0  # what underflows in fp32
         got = B.gmm8_forward(plan, q, s, Wq, Ws).double()
         assert not ((got - ref).abs() > (2 * U * K + TRUNC) * size * (1 + E16) + E16 * ref.abs() + tiny).any(), byte
+
+
+def test_few_rows_with_bad_values():
+    """The product of few rows: NaN in a row or its scale, and in another expert's matrix, stay there; the least and
+    largest scales hold; the same bits on every pass and whatever the other rows are."""
+    R, K, N = 4, 1300, 136
+    g = torch.Generator().manual_seed(9)
+    q, s, _ = rows8(g, R, K)
+    W = torch.randn(3, K, N, generator=g).to(DEV)
+    Wq, Ws = B.q8_pack_weights(W, "K")
+    off = offsets_of([1, 0, 3])
+    plan = B.gmm_plan(R, K, N, 3, B.GMM_Q8)
+    good = B.gmm8_forward(plan, q, s, Wq, Ws, off)
+    Wq2 = Wq.clone().view(torch.uint8)
+    Wq2[0, 5, 1290], Wq2[1] = 127, 127  # NaN in expert 0's column 5, and all over expert 1, which has no rows
+    q2, s2 = q.clone().view(torch.uint8), s.clone().view(torch.uint8)
+    q2[2, 1299], s2[3, 10] = 127, 255
+    got = B.gmm8_forward(plan, q2.view(q.dtype), s2.view(s.dtype), Wq2.view(Wq.dtype), Ws, off)
+    assert torch.isnan(got[0, 5]) and torch.isnan(got[2:]).all()
+    keep = [n for n in range(N) if n != 5]
+    assert torch.equal(got[0, keep], good[0, keep]) and torch.equal(got[1], good[1])
+    wb = Ws.view(torch.uint8)[:, :, :11].double() - 127
+    w = Wq[:, :, :K].double() * torch.exp2(wb).repeat_interleave(128, 1)[:, :N].repeat_interleave(128, 2)[:, :, :K]
+    for byte in (17, 0, 237):
+        s2[:] = byte
+        got = B.gmm8_forward(plan, q, s2.view(s.dtype), Wq, Ws, off).double()
+        x = q.double()[:, :K] * 2.0 ** (byte - 127)
+        for r, e in enumerate((0, 2, 2, 2)):
+            ref, size = w[e] @ x[r], w[e].abs() @ x[r].abs()
+            tiny = 2.0 ** -126 if byte == 0 else 0.0  # what underflows in fp32
+            assert not ((got[r] - ref).abs() > 2 * U * K * size * (1 + E16) + E16 * ref.abs() + tiny).any(), (byte, r)
 
 
 def test_matrices_past_32_bits():
