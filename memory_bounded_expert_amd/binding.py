@@ -323,6 +323,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
+# A new tensor on the current device without the public call's reading of its arguments
+# (0.7 us for 1.3, and a call has up to six).
+_empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
 def _stream(device, stream):
     if stream is None:
         if _raw_stream is not None and device.type == "cuda" and device.index is not None:
@@ -357,8 +362,12 @@ def _workspace(ws, plan, kind, device):
 
 
 def _out(t, name, shape, dtype, device):
-    """The output tensor given, checked, or a new one."""
+    """The output tensor given, checked, or a new one (on the current device, see _on)."""
     if t is None:
+        if _empty_strided is not None and len(shape) < 4:
+            row = shape[-1] or 1
+            strides = (row, 1) if len(shape) == 2 else (1,) if len(shape) == 1 else ((shape[1] or 1) * row, row, 1)
+            return _empty_strided(shape, strides, dtype)
         return torch.empty(*shape, dtype=dtype, device=device)  # sizes one by one: 1.2 us, a tuple 1.6
     _expect(t, name, shape, dtype, device)
     return t
