@@ -79,8 +79,8 @@ __device__ __forceinline__ void step_barrier() {
 }
 
 // A resource over whatever lies from base on: every offset used with it is inside
-// its tensor, or kOob.
-__device__ __forceinline__ i32x4_t open_srd(const void* base) { return make_srd(base, 0x7FFFFFF0); }
+// its tensor, or kOob.  Not there: its loads give zeros and touch no memory.
+__device__ __forceinline__ i32x4_t open_srd(const void* base, bool there = true) { return make_srd(base, there ? 0x7FFFFFF0 : 0); }
 
 // One wave's share of an operand's loads of a step: 1 KiB per instruction, the
 // waves in turn.

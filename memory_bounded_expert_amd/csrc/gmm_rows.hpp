@@ -165,13 +165,13 @@ __global__ __launch_bounds__(S::THREADS) void gmm_rows_kernel(const Args p, int 
   };
   auto issue = [&](int kt, int stage) __attribute__((always_inline)) {
     const uint32_t at = lds0 + (uint32_t)stage * C::STAGE;
-    const i32x4_t ra = open_srd(ap + (int64_t)kt * C::STEP), rb = open_srd(bp + kt * b_step);
+    const i32x4_t ra = open_srd(ap + (int64_t)kt * C::STEP, kt <= last), rb = open_srd(bp + kt * b_step, kt <= last);
 #pragma unroll
     for (int u = 0; u < decltype(la)::PW; ++u) la.issue(u, ra, at, wave, kt == last);
 #pragma unroll
     for (int u = 0; u < decltype(lb)::PW; ++u) lb.issue(u, rb, at + C::A_BYTES, wave, kt == last);
     if constexpr (Q8)
-      if (kt % 4 == 0) issue_scales(kt / 4);
+      if (kt % 4 == 0) issue_scales(min(kt, last) / 4);
   };
 
   // ---- fragments
@@ -263,12 +263,12 @@ __global__ __launch_bounds__(S::THREADS) void gmm_rows_kernel(const Args p, int 
   };
 
   // ---- the sum.  Step t goes to stage t % NS.  Steps past the last are loads of
-  // the last one again, never used, so that every wait counts the same loads (a wave
-  // with more than PER_STEP of them waits for a few too many).
+  // nothing, so that every wait counts the same loads (a wave with more than PER_STEP
+  // of them waits for a few too many).
   // a wave without rows or columns only helps with the loads
   const bool active = m0 + wm * S::WM < m_end && n0 + wn * S::WN < p.N;
 #pragma unroll
-  for (int s = 0; s < NS; ++s) issue(min(s, last), s);
+  for (int s = 0; s < NS; ++s) issue(s, s);
   wait_vmcnt<(NS - 1) * C::PER_STEP>();
   step_barrier();
   if (active) {
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(S::THREADS) void gmm_rows_kernel(const Args p, int 
     }
     wait_vmcnt<(NS - 2) * C::PER_STEP>();  // this wave's loads of step kt + 1
     step_barrier();
-    issue(min(kt + NS, last), stage);
+    issue(kt + NS, stage);
     launder();
     if (active) {
       read_half((stage + 1) % NS, 0);

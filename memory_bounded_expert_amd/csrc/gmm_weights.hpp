@@ -45,16 +45,18 @@ struct WeightsCfg {
   }
 };
 
-// An expert's tiles run in blocks of 4 x 2, whose work-groups share row panels in an
-// XCD's L2; the tiles go to the XCDs in turn, eight at a time, so that every XCD has
+// An expert's tiles run in blocks of 4 x 4, whose work-groups share row panels in an
+// XCD's L2; the tiles go to the XCDs in turn, sixteen at a time, so that every XCD has
 // its part of each expert's rows, however they are spread.  With an expert's tiles on
 // one XCD instead (each pass on other operands): 32,768 rows, 2048 x 1408, over 64
 // experts whose shares fall by r^-0.2 302 us where these take 281, by r^-1 487 and
-// 300; 65,536 rows, 4096 x 1536, 32 experts, r^-0.5 1020 and 755.
+// 309; 65,536 rows, 4096 x 1536, 32 experts, r^-0.5 1020 and 766.  (Eight at a time in
+// blocks of 4 x 2 283, 301, 771, but one matrix of 4096 x 4096 from 16,384 rows 455 us
+// where these take 421.)
 // Experts of more than twice the mean rows come first: their tiles take longest.
 // (128 experts, 1024 x 1024, r^-1, the same operands every pass: 214 us in the
 // experts' order, 139.)
-constexpr int kBlockM = 4, kBlockN = 2, kDeal = 8;
+constexpr int kBlockM = 4, kBlockN = 4, kDeal = 16;
 inline int64_t weights_groups(int64_t tiles) { return ceil_div(tiles, 8 * kDeal) * 8 * kDeal; }
 struct WeightsTile {
   int e, mt, nt;
@@ -153,8 +155,8 @@ __global__ __launch_bounds__(S::THREADS) void gmm_weights_kernel(const Args p, i
   }
   auto issue_raw = [&](int kt, int stage) __attribute__((always_inline)) {
     if constexpr (C::RAW) {
-      const i32x4_t rq = open_srd(ap + (int64_t)kt * KT * kp);
-      const i32x4_t rs = open_srd((const unsigned char*)p.As + (k0 + (int64_t)kt * KT) * sp);
+      const i32x4_t rq = open_srd(ap + (int64_t)kt * KT * kp, kt <= last);
+      const i32x4_t rs = open_srd((const unsigned char*)p.As + (k0 + (int64_t)kt * KT) * sp, kt <= last);
       const bool in = kt * KT + wave * (64 / LR) + lane / LR < k_len;
       const uint32_t at = lds0 + C::raw_at(stage, wave);
       lds_load16_at(rq, at, in ? raw_off : kOob);
@@ -185,11 +187,11 @@ __global__ __launch_bounds__(S::THREADS) void gmm_weights_kernel(const Args p, i
     if constexpr (C::RAW) {
       issue_raw(kt, stage);
     } else {
-      const i32x4_t ra = open_srd(ap + (int64_t)kt * KT * lda);
+      const i32x4_t ra = open_srd(ap + (int64_t)kt * KT * lda, kt <= last);
 #pragma unroll
       for (int u = 0; u < decltype(la)::PW; ++u) la.issue(u, ra, lds0 + C::a_at(stage), wave, kt == last);
     }
-    const i32x4_t rb = open_srd(bp + (int64_t)kt * KT * ldb);
+    const i32x4_t rb = open_srd(bp + (int64_t)kt * KT * ldb, kt <= last);
 #pragma unroll
     for (int u = 0; u < decltype(lb)::PW; ++u) lb.issue(u, rb, lds0 + C::b_at(stage), wave, kt == last);
   };
@@ -233,12 +235,12 @@ __global__ __launch_bounds__(S::THREADS) void gmm_weights_kernel(const Args p, i
                                                             __builtin_bit_cast(bf16x8_t, fa[set][i]), acc[i][j], 0, 0, 0);
   };
 
-  // ---- the sum, as in gmm_rows.hpp: step t in stage t % NS, steps past the last
-  // loaded again and never used
+  // ---- the sum, as in gmm_rows.hpp: step t in stage t % NS, steps past the last load
+  // nothing
   const bool active = m0 + wm * S::WM < p.K && n0 + wn * S::WN < p.N;
   if (nk > 0) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s) issue(min(s, last), s);
+    for (int s = 0; s < NS; ++s) issue(s, s);
     wait_vmcnt<(NS - 1) * C::PER_STEP>();
     place_raw(0, 0);
     step_barrier();
@@ -248,7 +250,7 @@ __global__ __launch_bounds__(S::THREADS) void gmm_weights_kernel(const Args p, i
       place_raw(u.value + 1, (u.value + 1) % NS);
       step_barrier();
       launder();
-      issue(min(kt + NS, last), u.value);
+      issue(kt + NS, u.value);
       if (active) {
         read((u.value + 1) % NS, (u.value + 1) & 1);
         multiply(u.value & 1);
