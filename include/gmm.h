@@ -31,8 +31,11 @@
  *   offsets: int32 [E+1] on the device, ascending, in [0, R].  Rows outside
  *   [offsets[0], offsets[E]) are neither read nor written.  Offsets that break
  *   this give unspecified rows, but nothing outside the tensors is touched.
+ *   A workspace serves one call at a time: calls that may overlap, on other
+ *   streams or in graphs replayed side by side, each take their own.
  *   NaN or Inf in a row of X spoils that row of Y and its expert's dW; in W its
- *   expert's rows; nothing else.
+ *   expert's rows; nothing else.  A scale byte of 255 (E8M0's NaN) makes its
+ *   block's numbers NaN.
  */
 #ifndef GMM_H
 #define GMM_H
@@ -68,8 +71,8 @@ typedef struct gmm_plan {
  * backward dW still writes zeros).
  * Errors: MOE_EINVAL if out is NULL, R < 0, K < 1, N < 1, E < 0, operands
  *   unknown, N (and K in bfloat16) not a multiple of 8, or E = 0 with R > 0.
- *   MOE_EUNSUPPORTED if K or N > 65536, E > 1024, R >= 2^31 - 65536, or 2 K N (the
- *   bytes of a matrix) >= 2^31.
+ *   MOE_EUNSUPPORTED if K or N > 65536, E > 1024, R >= 2^31 - 65536, 2 K N (the
+ *   bytes of a matrix) >= 2^31, or R max(K, N) >= 2^40.
  */
 int gmm_plan(int64_t R, int32_t K, int32_t N, int32_t E, int32_t operands, gmm_plan_t* out);
 

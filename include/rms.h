@@ -84,7 +84,8 @@ int rms_forward_q8(const rms_plan_t* plan, const void* X, const void* residual,
  * Outputs (device, overwritten): dX [N][H], the gradient of X and of the
  *   residual alike (may be dY or dS itself); dgamma [H].
  * workspace: at least plan->bwd_workspace_bytes bytes, 256-byte aligned;
- *   contents on entry do not matter.  It holds the partial sums over rows.
+ *   contents on entry do not matter.  It holds the partial sums over rows, and
+ *   serves one call at a time: calls that may overlap each take their own.
  * Errors: as rms_forward; MOE_EINVAL also for a workspace that is not
  *   256-byte aligned, MOE_EWORKSPACE for one that is too small.
  */

@@ -9,6 +9,13 @@
 // of k, the second while the first is multiplied, the first of the next step while
 // the second is: the stage can be filled again from the middle of its step on.
 //
+// What bounds it: a 256 x 256 step takes 1.45 us in e4m3, its multiplications 1.0, its
+// LDS traffic (192 KB read, 64 KB written, 128 bytes a cycle) as long; a tile's first
+// loads and its output 13% of 16 us to 100.  65,536 x 4096 x 4096 in e4m3 876 us, 2.5
+// PFLOP/s; in bf16 16,384 x 4096 x 4096 405 us, 1.36 PFLOP/s.  With 512 rows an expert
+// (32,768 x 2048 x 1408, 64 experts, 595 MB) a tile's rows and columns come out of HBM
+// and its last ones are part empty: 225 us, 840 TFLOP/s.
+//
 //  * Operands along k (X, dY; W in dX; all of the 8-bit product) lie in LDS as rows
 //    of 128 bytes; 16-byte chunk c of row r sits at c ^ (r / 2 % 8), so that 16
 //    rows' reads of one chunk cover all 64 banks.

@@ -9,6 +9,10 @@
 // (Two stages of 64 rows: 388 us where these take 358 for 64 experts of 512 rows,
 // 2048 x 1408, whose 738 MB of dW alone take 110 us to fill.)
 //
+// What bounds it: with few rows an expert, HBM.  Those 64 experts with operands out of
+// HBM take 281 us for 964 MB, 1.17 GB with what XCDs read twice, near what a copy of as
+// much takes; 16,384 rows and one matrix of 4096 x 4096 421 us, 1.31 PFLOP/s.
+//
 // X in 8 bits lands in LDS as it is, each lane's 16 numbers of one row with the word
 // of their scale; one step before they are read, the lane makes them bf16, which
 // holds them, and writes them to the stage.
