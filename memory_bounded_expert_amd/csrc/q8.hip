@@ -18,32 +18,59 @@ namespace {
 
 constexpr uint32_t kQ8Magic = 0x51385031u;  // "Q8P1"
 
-// NV values at p, of which n (maybe none) are there; the rest 0.
-template <int NV, typename T>
-__device__ __forceinline__ void load_some(const T* p, int n, float* v) {
+constexpr int kCols = 16, kLanes = kQBlock / kCols;  // columns of a lane, lanes of a block
+
+// The column of vector c (16 bytes) of a lane in its block.  Either a lane's vectors
+// are neighbours, and its 16 numbers of e4m3, or (TURN) the lanes' vectors lie in turn,
+// so that a store fills whole lines of memory, and the numbers of e4m3 in pieces.
+//  * fp32: in turn (131,072 x 1536 SwiGLU backward 496 us, neighbours 700; unpacked 167,
+//    292; 98,304 x 1000 281, 393).
+//  * bf16, where 8-bit rows are read and rows start on whole lines: in turn (131,072 x
+//    1536 backward 288, 301; unpacked 101, 111); on other widths neighbours (98,304 x
+//    1000 167, 153; 65, 57).
+//  * bf16, where 8-bit rows are written: neighbours (98,304 x 1000 forward 136, 127; on
+//    131,072 x 1536 the same).
+template <typename T>
+constexpr bool kTurn = Elem<T>::kPer16B == 4;
+template <typename T, bool TURN>
+__device__ __forceinline__ int column(int lane, int c) {
   constexpr int EPC = Elem<T>::kPer16B;
+  return TURN ? (c * kLanes + lane) * EPC : lane * kCols + c * EPC;
+}
+// The EPC values of a vector at p, of which n (maybe none) are there; the rest 0.
+template <typename T>
+__device__ __forceinline__ void load_vec(const T* p, int n, float* v) {
+  constexpr int EPC = Elem<T>::kPer16B;
+  if (n >= EPC) {
+    const u32x4_t w = *reinterpret_cast<const u32x4_any_t*>(p);
+    unpack16(w, v, T());
+  } else {
 #pragma unroll
-  for (int c = 0; c < NV; c += EPC) {
-    if (n >= c + EPC) {
-      const u32x4_t w = *reinterpret_cast<const u32x4_any_t*>(p + c);
-      unpack16(w, v + c, T());
-    } else {
-#pragma unroll
-      for (int e = 0; e < EPC; ++e) v[c + e] = c + e < n ? Elem<T>::to_f(p[c + e]) : 0.f;
-    }
+    for (int e = 0; e < EPC; ++e) v[e] = e < n ? Elem<T>::to_f(p[e]) : 0.f;
   }
 }
-template <int NV, typename T>
-__device__ __forceinline__ void store_some(T* p, int n, const float* v) {
+// A lane's values of a block at p, of which n columns are there; the rest 0.
+template <typename T, bool TURN>
+__device__ __forceinline__ void load_some(const T* p, int lane, int n, float* v) {
   constexpr int EPC = Elem<T>::kPer16B;
 #pragma unroll
-  for (int c = 0; c < NV; c += EPC) {
-    if (n >= c + EPC) {
-      *reinterpret_cast<u32x4_any_t*>(p + c) = pack16(v + c, T());
+  for (int c = 0; c < kCols / EPC; ++c) {
+    const int at = column<T, TURN>(lane, c);
+    load_vec(p + at, n - at, v + c * EPC);
+  }
+}
+template <typename T, bool TURN>
+__device__ __forceinline__ void store_some(T* p, int lane, int n, const float* v) {
+  constexpr int EPC = Elem<T>::kPer16B;
+#pragma unroll
+  for (int c = 0; c < kCols / EPC; ++c) {
+    const int at = column<T, TURN>(lane, c);
+    if (n >= at + EPC) {
+      *reinterpret_cast<u32x4_any_t*>(p + at) = pack16(v + c * EPC, T());
     } else {
 #pragma unroll
       for (int e = 0; e < EPC; ++e)
-        if (c + e < n) p[c + e] = Elem<T>::from_f(v[c + e]);
+        if (at + e < n) p[at + e] = Elem<T>::from_f(v[c * EPC + e]);
     }
   }
 }
@@ -59,36 +86,57 @@ struct Shape8 {
   uint32_t units, magic, shift;
   int H, blocks, row_pitch, scale_pitch;
 };
-constexpr int kCols = 16, kLanes = kQBlock / kCols;  // columns of a lane, lanes of a block
-
 // Writes a lane's values of block b of row r, with the block's scale; the row's last
 // block writes the scales' padding too.
+template <typename T>
 __device__ __forceinline__ void put(const Packed& to, const Shape8& sh, int64_t r, int b, int lane, const float* v) {
   const uint32_t byte = q8_scale_byte(q8_amax<kCols>(v, [](float m) { return run8_maxf(m); }));
   const float inv = q8_inverse(byte);
-  *reinterpret_cast<u32x4_t*>(to.q + r * sh.row_pitch + b * kQBlock + lane * kCols) =
-      u32x4_t{q8_round4(v, inv), q8_round4(v + 4, inv), q8_round4(v + 8, inv), q8_round4(v + 12, inv)};
+  uint8_t* q = to.q + r * sh.row_pitch + b * kQBlock;
+  if constexpr (!kTurn<T>) {
+    *reinterpret_cast<u32x4_t*>(q + lane * kCols) =
+        u32x4_t{q8_round4(v, inv), q8_round4(v + 4, inv), q8_round4(v + 8, inv), q8_round4(v + 12, inv)};
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) *reinterpret_cast<uint32_t*>(q + column<T, true>(lane, c)) = q8_round4(v + 4 * c, inv);
+  }
   uint8_t* s = to.s + r * sh.scale_pitch;
   if (lane == 0) s[b] = (uint8_t)byte;
   if (b == sh.blocks - 1 && lane < sh.scale_pitch - sh.blocks) s[sh.blocks + lane] = kQOne;
 }
+template <typename T, bool TURN>
 __device__ __forceinline__ void get(const uint8_t* q, const uint8_t* s, const Shape8& sh, int64_t r, int b, int lane,
                                     float* v) {
+  constexpr int WORDS = Elem<T>::kPer16B / 4;  // of a vector's numbers
   const float scale = q8_scale(s[r * sh.scale_pitch + b]);
-  const u32x4_t w = *reinterpret_cast<const u32x4_t*>(q + r * sh.row_pitch + b * kQBlock + lane * kCols);
+  q += r * sh.row_pitch + b * kQBlock;
+  u32x4_t w;
+  if constexpr (!TURN) {
+    w = *reinterpret_cast<const u32x4_t*>(q + lane * kCols);
+  } else if constexpr (WORDS == 2) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint2 x = *reinterpret_cast<const uint2*>(q + column<T, true>(lane, c));
+      w[2 * c] = x.x;
+      w[2 * c + 1] = x.y;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint32_t*>(q + column<T, true>(lane, c));
+  }
 #pragma unroll
   for (int e = 0; e < 4; ++e) q8_values4(w[e], scale, v + 4 * e);
 }
 
-// Calls f(row, block, lane of the block, first value's place in a matrix, columns
-// there) for this thread's block.
+// Calls f(row, block, lane of the block, the block's place in a matrix, columns there
+// from it on) for this thread's block.
 template <typename F>
 __device__ __forceinline__ void my_block(const Shape8& sh, F f) {
   const int lane = threadIdx.x % kLanes;
   const uint32_t u = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
   if (u >= sh.units) return;
   const uint32_t row = (uint32_t)(((uint64_t)u * sh.magic) >> sh.shift);
-  const int b = (int)(u - row * sh.blocks), col = b * kQBlock + lane * kCols;
+  const int b = (int)(u - row * sh.blocks), col = b * kQBlock;
   const int64_t r = sh.first + row;
   f(r, b, lane, r * sh.H + col, sh.H - col);
 }
@@ -98,20 +146,19 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void pack_kernel(const T* __restrict__ X, const Packed to, const Shape8 sh) {
   my_block(sh, [&](int64_t r, int b, int lane, int64_t at, int n) {
     float v[kCols];
-    load_some<kCols>(X + at, n, v);
-    put(to, sh, r, b, lane, v);
+    load_some<T, kTurn<T>>(X + at, lane, n, v);
+    put<T>(to, sh, r, b, lane, v);
   });
 }
 
-// 65,536 x 2048 to bf16: 73 us, 5.5 TB/s (to fp32 196 us, 3.4 TB/s: a lane's 64 bytes go
-// out in four stores of 16).
-template <typename T>
+// 65,536 x 2048 to bf16: 67 us, 6.0 TB/s; 131,072 x 1536 to fp32 167 us, 6.0 TB/s.
+template <typename T, bool TURN>
 __global__ __launch_bounds__(kThreads) void unpack_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
                                                           T* __restrict__ X, const Shape8 sh) {
   my_block(sh, [&](int64_t r, int b, int lane, int64_t at, int n) {
     float v[kCols];
-    get(q, s, sh, r, b, lane, v);
-    store_some<kCols>(X + at, n, v);
+    get<T, TURN>(q, s, sh, r, b, lane, v);
+    store_some<T, TURN>(X + at, lane, n, v);
   });
 }
 
@@ -128,36 +175,36 @@ __global__ __launch_bounds__(kThreads) void swiglu_forward_kernel(const T* __res
                                                                   const Packed ku, const Shape8 sh) {
   my_block(sh, [&](int64_t r, int b, int lane, int64_t at, int n) {
     float a[kCols], u[kCols], v[kCols];
-    load_some<kCols>(A + at, n, a);
-    load_some<kCols>(U + at, n, u);
+    load_some<T, kTurn<T>>(A + at, lane, n, a);
+    load_some<T, kTurn<T>>(U + at, lane, n, u);
 #pragma unroll
     for (int e = 0; e < kCols; ++e) v[e] = a[e] * gate(a[e], T()) * u[e];
-    put(h, sh, r, b, lane, v);
+    put<T>(h, sh, r, b, lane, v);
     if constexpr (KEEP) {
-      put(ka, sh, r, b, lane, a);
-      put(ku, sh, r, b, lane, u);
+      put<T>(ka, sh, r, b, lane, a);
+      put<T>(ku, sh, r, b, lane, u);
     }
   });
 }
 
-// 131,072 x 1536 bf16: 308 us, 5.2 TB/s.
-template <typename T>
+// 131,072 x 1536 bf16: 284 us, 5.7 TB/s; fp32 483 us, 5.9 TB/s.
+template <typename T, bool TURN>
 __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
     const uint8_t* __restrict__ Aq, const uint8_t* __restrict__ As, const uint8_t* __restrict__ Uq,
     const uint8_t* __restrict__ Us, const T* dH, T* dA, T* __restrict__ dU, const Shape8 sh) {
   my_block(sh, [&](int64_t r, int b, int lane, int64_t at, int n) {
     float a[kCols], u[kCols], d[kCols];
-    get(Aq, As, sh, r, b, lane, a);
-    get(Uq, Us, sh, r, b, lane, u);
-    load_some<kCols>(dH + at, n, d);
+    get<T, TURN>(Aq, As, sh, r, b, lane, a);
+    get<T, TURN>(Uq, Us, sh, r, b, lane, u);
+    load_some<T, TURN>(dH + at, lane, n, d);
 #pragma unroll
     for (int e = 0; e < kCols; ++e) {
       const float g = gate(a[e], T()), dg = d[e] * g;
       u[e] = dg * u[e] * fmaf(a[e], 1.f - g, 1.f);
       d[e] = dg * a[e];
     }
-    store_some<kCols>(dA + at, n, u);
-    store_some<kCols>(dU + at, n, d);
+    store_some<T, TURN>(dA + at, lane, n, u);
+    store_some<T, TURN>(dU + at, lane, n, d);
   });
 }
 
@@ -180,7 +227,10 @@ __global__ __launch_bounds__(kThreads) void pack_weights_kernel(
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int k = kb * kQBlock + i * 16 + row;
-    load_some<8>(w + (int64_t)min(k, K - 1) * N + min(col, N), k < K ? N - col : 0, v[i]);
+    const T* from = w + (int64_t)min(k, K - 1) * N + min(col, N);
+    const int there = k < K ? N - col : 0;
+#pragma unroll
+    for (int c = 0; c < 8; c += Elem<T>::kPer16B) load_vec(from + c, there - c, v[i] + c);
   }
   const uint32_t byte = q8_scale_byte(q8_amax<64>(&v[0][0], [&](float m) {
     m = run_maxf<64>(m);
@@ -230,6 +280,12 @@ __global__ __launch_bounds__(kThreads) void pack_weights_kernel(
   }
 }
 
+// Whether a lane's vectors lie in turn where 8-bit rows are read (see column).
+template <typename T>
+bool in_turn(const q8_plan_t& P) {
+  return kTurn<T> || P.H % 64 == 0;
+}
+
 // Calls f(shape, work-groups) for launches of below 2^31 blocks that cover all rows.
 template <typename F>
 int in_launches(const q8_plan_t& P, F f) {
@@ -249,6 +305,14 @@ int in_launches(const q8_plan_t& P, F f) {
   return MOE_OK;
 }
 bool plan_ok(const q8_plan_t* p) { return p != nullptr && p->magic == kQ8Magic; }
+template <typename T>
+int unpack(const q8_plan_t& P, const void* q, const void* s, void* X, void* stream) {
+  return in_launches(P, [&](const Shape8& sh, unsigned groups) {
+    auto kern = in_turn<T>(P) ? unpack_kernel<T, true> : unpack_kernel<T, kTurn<T>>;
+    kern<<<groups, kThreads, 0, (hipStream_t)stream>>>((const uint8_t*)q, (const uint8_t*)s, (T*)X, sh);
+  });
+}
+
 // q on a 16-byte step, s on a 4-byte step, both there
 bool pair_ok(const void* q, const void* s) {
   return q && s && (uintptr_t)q % 16 == 0 && (uintptr_t)s % 4 == 0;
@@ -293,12 +357,7 @@ MOE_API int q8_unpack(const q8_plan_t* plan, const void* q, const void* s, void*
   if (!plan_ok(plan)) return MOE_EINVAL;
   if (plan->N == 0) return MOE_OK;
   if (!elem_ok(*plan, X) || !pair_ok(q, s)) return MOE_EINVAL;
-  return in_launches(*plan, [&](const Shape8& sh, unsigned groups) {
-    if (plan->dtype == MOE_BF16)
-      unpack_kernel<bf16_t><<<groups, kThreads, 0, (hipStream_t)stream>>>((const uint8_t*)q, (const uint8_t*)s, (bf16_t*)X, sh);
-    else
-      unpack_kernel<float><<<groups, kThreads, 0, (hipStream_t)stream>>>((const uint8_t*)q, (const uint8_t*)s, (float*)X, sh);
-  });
+  return plan->dtype == MOE_BF16 ? unpack<bf16_t>(*plan, q, s, X, stream) : unpack<float>(*plan, q, s, X, stream);
 }
 
 MOE_API int q8_pack_weights(int32_t E, int32_t K, int32_t N, int32_t dtype, const void* W, void* q,
@@ -335,9 +394,9 @@ template <typename T>
 int swiglu_backward(const q8_plan_t& P, const void* Aq, const void* As, const void* Uq, const void* Us,
                     const void* dH, void* dA, void* dU, void* stream) {
   return in_launches(P, [&](const Shape8& sh, unsigned groups) {
-    swiglu_backward_kernel<T><<<groups, kThreads, 0, (hipStream_t)stream>>>(
-        (const uint8_t*)Aq, (const uint8_t*)As, (const uint8_t*)Uq, (const uint8_t*)Us, (const T*)dH,
-        (T*)dA, (T*)dU, sh);
+    auto kern = in_turn<T>(P) ? swiglu_backward_kernel<T, true> : swiglu_backward_kernel<T, kTurn<T>>;
+    kern<<<groups, kThreads, 0, (hipStream_t)stream>>>((const uint8_t*)Aq, (const uint8_t*)As, (const uint8_t*)Uq,
+                                                       (const uint8_t*)Us, (const T*)dH, (T*)dA, (T*)dU, sh);
   });
 }
 }  // namespace
