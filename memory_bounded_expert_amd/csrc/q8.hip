@@ -25,11 +25,14 @@ constexpr int kCols = 16, kLanes = kQBlock / kCols;  // columns of a lane, lanes
 // so that a store fills whole lines of memory, and the numbers of e4m3 in pieces.
 //  * fp32: in turn (131,072 x 1536 SwiGLU backward 496 us, neighbours 700; unpacked 167,
 //    292; 98,304 x 1000 281, 393).
-//  * bf16, where 8-bit rows are read and rows start on whole lines: in turn (131,072 x
-//    1536 backward 288, 301; unpacked 101, 111); on other widths neighbours (98,304 x
+//  * bf16, where 8-bit rows are read and rows are whole lines (LINES): in turn (131,072
+//    x 1536 backward 288, 301; unpacked 101, 111); on other widths neighbours (98,304 x
 //    1000 167, 153; 65, 57).
 //  * bf16, where 8-bit rows are written: neighbours (98,304 x 1000 forward 136, 127; on
 //    131,072 x 1536 the same).
+// Stores of whole lines, which no kernel here reads again, go past L2 (131,072 x 1536
+// bf16 unpacked 101 us, 85 so; backward 288, 280; of 8-bit rows, forward 252, 240), parts
+// of lines through it (98,304 x 1000 fp32 backward 285, past L2 405).
 template <typename T>
 constexpr bool kTurn = Elem<T>::kPer16B == 4;
 template <typename T, bool TURN>
@@ -59,14 +62,18 @@ __device__ __forceinline__ void load_some(const T* p, int lane, int n, float* v)
     load_vec(p + at, n - at, v + c * EPC);
   }
 }
-template <typename T, bool TURN>
+template <typename T, bool LINES>
 __device__ __forceinline__ void store_some(T* p, int lane, int n, const float* v) {
   constexpr int EPC = Elem<T>::kPer16B;
 #pragma unroll
   for (int c = 0; c < kCols / EPC; ++c) {
-    const int at = column<T, TURN>(lane, c);
+    const int at = column<T, LINES || kTurn<T>>(lane, c);
     if (n >= at + EPC) {
-      *reinterpret_cast<u32x4_any_t*>(p + at) = pack16(v + c * EPC, T());
+      const u32x4_any_t w = pack16(v + c * EPC, T());
+      if constexpr (LINES)
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any_t*>(p + at));
+      else
+        *reinterpret_cast<u32x4_any_t*>(p + at) = w;
     } else {
 #pragma unroll
       for (int e = 0; e < EPC; ++e)
@@ -94,11 +101,12 @@ __device__ __forceinline__ void put(const Packed& to, const Shape8& sh, int64_t 
   const float inv = q8_inverse(byte);
   uint8_t* q = to.q + r * sh.row_pitch + b * kQBlock;
   if constexpr (!kTurn<T>) {
-    *reinterpret_cast<u32x4_t*>(q + lane * kCols) =
-        u32x4_t{q8_round4(v, inv), q8_round4(v + 4, inv), q8_round4(v + 8, inv), q8_round4(v + 12, inv)};
+    const u32x4_t w{q8_round4(v, inv), q8_round4(v + 4, inv), q8_round4(v + 8, inv), q8_round4(v + 12, inv)};
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_t*>(q + lane * kCols));
   } else {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) *reinterpret_cast<uint32_t*>(q + column<T, true>(lane, c)) = q8_round4(v + 4 * c, inv);
+    for (int c = 0; c < 4; ++c)
+      __builtin_nontemporal_store(q8_round4(v + 4 * c, inv), reinterpret_cast<uint32_t*>(q + column<T, true>(lane, c)));
   }
   uint8_t* s = to.s + r * sh.scale_pitch;
   if (lane == 0) s[b] = (uint8_t)byte;
@@ -152,13 +160,14 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(const T* __restrict__ X,
 }
 
 // 65,536 x 2048 to bf16: 67 us, 6.0 TB/s; 131,072 x 1536 to fp32 167 us, 6.0 TB/s.
-template <typename T, bool TURN>
+template <typename T, bool LINES>
 __global__ __launch_bounds__(kThreads) void unpack_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ s,
                                                           T* __restrict__ X, const Shape8 sh) {
+  constexpr bool TURN = LINES || kTurn<T>;
   my_block(sh, [&](int64_t r, int b, int lane, int64_t at, int n) {
     float v[kCols];
     get<T, TURN>(q, s, sh, r, b, lane, v);
-    store_some<T, TURN>(X + at, lane, n, v);
+    store_some<T, LINES>(X + at, lane, n, v);
   });
 }
 
@@ -188,10 +197,11 @@ __global__ __launch_bounds__(kThreads) void swiglu_forward_kernel(const T* __res
 }
 
 // 131,072 x 1536 bf16: 284 us, 5.7 TB/s; fp32 483 us, 5.9 TB/s.
-template <typename T, bool TURN>
+template <typename T, bool LINES>
 __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
     const uint8_t* __restrict__ Aq, const uint8_t* __restrict__ As, const uint8_t* __restrict__ Uq,
     const uint8_t* __restrict__ Us, const T* dH, T* dA, T* __restrict__ dU, const Shape8 sh) {
+  constexpr bool TURN = LINES || kTurn<T>;
   my_block(sh, [&](int64_t r, int b, int lane, int64_t at, int n) {
     float a[kCols], u[kCols], d[kCols];
     get<T, TURN>(Aq, As, sh, r, b, lane, a);
@@ -203,8 +213,8 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(
       u[e] = dg * u[e] * fmaf(a[e], 1.f - g, 1.f);
       d[e] = dg * a[e];
     }
-    store_some<T, TURN>(dA + at, lane, n, u);
-    store_some<T, TURN>(dU + at, lane, n, d);
+    store_some<T, LINES>(dA + at, lane, n, u);
+    store_some<T, LINES>(dU + at, lane, n, d);
   });
 }
 
@@ -280,10 +290,10 @@ __global__ __launch_bounds__(kThreads) void pack_weights_kernel(
   }
 }
 
-// Whether a lane's vectors lie in turn where 8-bit rows are read (see column).
+// Whether the rows of a matrix are whole lines of memory.
 template <typename T>
-bool in_turn(const q8_plan_t& P) {
-  return kTurn<T> || P.H % 64 == 0;
+bool whole_lines(const q8_plan_t& P, const void* a, const void* b) {
+  return P.H * sizeof(T) % 128 == 0 && ((uintptr_t)a | (uintptr_t)b) % 128 == 0;
 }
 
 // Calls f(shape, work-groups) for launches of below 2^31 blocks that cover all rows.
@@ -308,7 +318,7 @@ bool plan_ok(const q8_plan_t* p) { return p != nullptr && p->magic == kQ8Magic; 
 template <typename T>
 int unpack(const q8_plan_t& P, const void* q, const void* s, void* X, void* stream) {
   return in_launches(P, [&](const Shape8& sh, unsigned groups) {
-    auto kern = in_turn<T>(P) ? unpack_kernel<T, true> : unpack_kernel<T, kTurn<T>>;
+    auto kern = whole_lines<T>(P, X, X) ? unpack_kernel<T, true> : unpack_kernel<T, false>;
     kern<<<groups, kThreads, 0, (hipStream_t)stream>>>((const uint8_t*)q, (const uint8_t*)s, (T*)X, sh);
   });
 }
@@ -394,7 +404,7 @@ template <typename T>
 int swiglu_backward(const q8_plan_t& P, const void* Aq, const void* As, const void* Uq, const void* Us,
                     const void* dH, void* dA, void* dU, void* stream) {
   return in_launches(P, [&](const Shape8& sh, unsigned groups) {
-    auto kern = in_turn<T>(P) ? swiglu_backward_kernel<T, true> : swiglu_backward_kernel<T, kTurn<T>>;
+    auto kern = whole_lines<T>(P, dA, dU) ? swiglu_backward_kernel<T, true> : swiglu_backward_kernel<T, false>;
     kern<<<groups, kThreads, 0, (hipStream_t)stream>>>((const uint8_t*)Aq, (const uint8_t*)As, (const uint8_t*)Uq,
                                                        (const uint8_t*)Us, (const T*)dH, (T*)dA, (T*)dU, sh);
   });
