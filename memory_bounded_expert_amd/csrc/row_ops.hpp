@@ -61,9 +61,15 @@ struct RowPart {
     }
   }
   __device__ __forceinline__ void get(int c, float* v) const { unpack16(raw[c], v, T()); }
+  // PAST: past L2, for rows that the call does not read again
+  template <bool PAST = false>
   __device__ static __forceinline__ void put(T* row, int at, int H, const float* v) {
     if (at + EPC <= H) {
-      *reinterpret_cast<u32x4_any_t*>(row + at) = pack16(v, T());
+      const u32x4_any_t w = pack16(v, T());
+      if constexpr (PAST)
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any_t*>(row + at));
+      else
+        *reinterpret_cast<u32x4_any_t*>(row + at) = w;
     } else if constexpr (TAIL) {
 #pragma unroll
       for (int e = 0; e < EPC; ++e)
