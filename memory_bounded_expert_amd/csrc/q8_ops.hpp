@@ -46,6 +46,21 @@ __device__ __forceinline__ float q8_amax(const float* v, R reduce) {
   return m;
 }
 
+// Whether v is within eight of its last places of where e4m3 or a scale turn, under any
+// power of two: a value with at most four bits after its first.  There 32 bits do not say
+// which side a computed value is on, and it is formed again in 64.
+__device__ __forceinline__ bool q8_border(float v) {
+  return ((__float_as_uint(v) + 8u) & 0x7ffffu) <= 16u && v != 0.f;
+}
+// x in 32 bits to odd (a value between two numbers becomes the one whose last bit is 1),
+// so that rounding it once more gives what rounding x would.
+__device__ __forceinline__ float q8_to_odd(double x) {
+  const float f = (float)x;
+  const uint32_t b = __float_as_uint(f);
+  if (!(fabsf(f) < __builtin_inff()) || (double)f == x || (b & 1)) return f;
+  return __uint_as_float(fabs(x) > fabs((double)f) ? b + 1 : b - 1);
+}
+
 // Four values as e4m3 (v_cvt_pk_fp8_f32: to nearest, ties to even; infinities and NaN
 // to NaN).  The scale leaves no finite quotient above 448.
 __device__ __forceinline__ uint32_t q8_round4(const float* v, float inv) {

@@ -169,3 +169,15 @@ def test_blocks_past_32_bits():
     del x
     back = B.q8_unpack(B.q8_plan(N, H), q, s)
     assert torch.equal(back[-32:], B.q8_unpack(B.q8_plan(32, H), q2, s2))
+
+
+def test_fp32_swiglu_is_rounded_once():
+    """Values next to where e4m3 or a scale turn are formed in 64 bits: all numbers and scales are those of the fp64 h."""
+    require_lib()
+    N, H = 2000, 1500
+    a, u = rows(N, H, "f32", 5, 0.5), rows(N, H, "f32", 6, 0.5)
+    a[3], u[4], a[5], u[5] = 0.0, -0.0, -200.0, 1e30
+    hq, hs, _ = B.q8_swiglu_forward(B.q8_plan(N, H, B.MOE_F32), a, u)
+    want, e = Q.quantise(Q.swiglu(dev_to_f64(a), dev_to_f64(u)))
+    got, _, ge = values8(hq, hs, H)
+    assert np.array_equal(got, want) and np.array_equal(ge, e)

@@ -167,3 +167,25 @@ def test_no_rows():
     Y, S, rstd = B.rms_forward(plan, x, gamma)
     dX, dg = B.rms_backward(plan, x, gamma, x, rstd, dgamma=torch.full((40,), 7.0, device=DEV))
     assert Y.numel() == 0 and not dg.any()
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_values_next_to_borders(dtype):
+    """Values next to where e4m3 or a scale turn are formed in 64 bits from the row's sum, whose fp32 part (eight products a
+    chain, up to four such, four steps over 16 lanes) is off by 16 u at most, u = 2^-24: rstd by 8 u.  Of values spread over
+    their logarithm, 8 borders an octave have 8 * 2 * 8 u / ln 2 = 185 u within that: 46 of 2048 x 2048.  (fp32 products
+    would be off by another 2 u to 5 u; a value on the wrong side is one step away, never more.)"""
+    require_lib()
+    N = H = 2048
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(N, H, generator=g).to(TYPES[dtype][0]).to(DEV)
+    gamma = (1 + 0.1 * torch.randn(H, generator=g)).to(DEV)
+    plan = B.rms_plan(N, H, B.moe_dtype(x.dtype), 1e-6)
+    q, s, _, _ = B.rms_forward_q8(plan, x, gamma)
+    v = dev_to_f64(x)
+    y = v / np.sqrt(np.mean(v * v, axis=1, keepdims=True) + float(np.float32(1e-6))) * dev_to_f64(gamma)
+    want, e = Q.quantise(y)
+    got, _, ge = values8(q, s, H)
+    assert np.array_equal(ge, e)
+    assert int((got != want).sum()) <= 46
+    assert (np.abs(got - want) <= np.exp2(np.floor(np.log2(np.maximum(np.abs(want), 1e-30))) - 3)).all()
