@@ -49,14 +49,17 @@ __device__ __forceinline__ double row_sum64(float v, double (*red)[16], int& hal
   }
   return s;
 }
-// A value for 8 bits: v r g, r = 1 / sqrt(m).  (65,536 x 2048: 15 to 23 of 134 million
-// numbers are not those of 64 bits; all in 32 bits 67 to 109, and 178 us for 180.)
-__device__ __forceinline__ float normed8(float v, float r, float g, double m) {
-  const float y = v * r * g;
-  return q8_border(y) ? q8_to_odd((double)v / sqrt(m) * (double)g) : y;
+// 1 / sqrt(m) from r, which is that in 32 bits, by a Newton step.
+__device__ __forceinline__ double rstd64(double m, float r) {
+  return fma(0.5 * r, fma(-m * r, (double)r, 1.0), (double)r);
+}
+// A value for 8 bits, y = v r g in 32 bits.  (65,536 x 2048: 15 to 23 of 134 million numbers are not
+// those of 64 bits; all in 32 bits 67 to 109, and 178 us for 182.)
+__device__ __forceinline__ float exact8(float y, float v, float g, double r64) {
+  return q8_border(y) ? q8_to_odd((double)v * r64 * (double)g) : y;
 }
 
-// 65,536 x 2048 bf16 with a residual into 8 bits: 180 us, 5.2 TB/s.
+// 65,536 x 2048 bf16 with a residual into 8 bits: 182 us, 5.2 TB/s.
 template <typename T, int W, int C, bool TAIL, bool Q8>
 __global__ __launch_bounds__(kGroup<W>) void rms_rows_forward_kernel(
     const T* X, const T* residual, const float* __restrict__ gamma, T* S, const RowsOut out,
@@ -107,6 +110,7 @@ __global__ __launch_bounds__(kGroup<W>) void rms_rows_forward_kernel(
     }
     const double m = fma(row_sum64<W>(sum, red, half), inv, (double)eps);
     const float r = 1.f / sqrtf((float)m);
+    const double r64 = rstd64(m, r);
     if (place == 0) rstd[t] = r;
     if constexpr (Q8) {
       uint8_t* q = (uint8_t*)out.q + t * out.row_pitch;
@@ -117,23 +121,30 @@ __global__ __launch_bounds__(kGroup<W>) void rms_rows_forward_kernel(
         const int at = (c * 64 * W + place) * EPC;
         float v[EPC];
         cur.get(c, v);
+        float y[EPC];
+        bool border = false;
 #pragma unroll
         for (int e = 0; e < EPC; ++e) {
-          v[e] = normed8(v[e], r, ga[c * EPC + e], m);
+          y[e] = v[e] * r * ga[c * EPC + e];
           // past the row's end x and gamma are 0, but r may be NaN
-          if (at + e >= H) v[e] = 0.f;
+          if (at + e >= H) y[e] = 0.f;
+          border |= q8_border(y[e]);
         }
-        const uint32_t byte = q8_scale_byte(q8_amax<EPC>(v, [](float m) {
+        if (border) {
+#pragma unroll
+          for (int e = 0; e < EPC; ++e) y[e] = exact8(y[e], v[e], ga[c * EPC + e], r64);
+        }
+        const uint32_t byte = q8_scale_byte(q8_amax<EPC>(y, [](float m) {
           m = run_maxf<16>(m);
           return EPC == 4 ? fmaxf(m, __shfl_xor(m, 16)) : m;
         }));
         const float qi = q8_inverse(byte);
         if (at < out.row_pitch) {
           if constexpr (EPC == 8)
-            __builtin_nontemporal_store((uint64_t)q8_round4(v, qi) | (uint64_t)q8_round4(v + 4, qi) << 32,
+            __builtin_nontemporal_store((uint64_t)q8_round4(y, qi) | (uint64_t)q8_round4(y + 4, qi) << 32,
                                         reinterpret_cast<uint64_t*>(q + at));
           else
-            __builtin_nontemporal_store(q8_round4(v, qi), reinterpret_cast<uint32_t*>(q + at));
+            __builtin_nontemporal_store(q8_round4(y, qi), reinterpret_cast<uint32_t*>(q + at));
           if (at % kQBlock == 0) sc[at / kQBlock] = (uint8_t)byte;
         }
       }
@@ -282,6 +293,7 @@ __global__ __launch_bounds__(kThreads) void rms_forward_kernel(
     if (residual) x = S + t * H;  // each thread reads back what it wrote
     const double m = (double)group_sum(q, red) / H + (double)eps;
     const float r = 1.f / sqrtf((float)m);
+    const double r64 = rstd64(m, r);
     if (threadIdx.x == 0) rstd[t] = r;
     if constexpr (Q8) {
       // a block of 128 columns in 32 lanes, four columns each; the sum's rows are
@@ -294,7 +306,10 @@ __global__ __launch_bounds__(kThreads) void rms_forward_kernel(
         const int at = b * kQBlock + (threadIdx.x & 31) * 4;
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = at + e < H ? normed8(Elem<T>::to_f(x[at + e]), r, gamma[at + e], m) : 0.f;
+        for (int e = 0; e < 4; ++e) {
+          const float xe = at + e < H ? Elem<T>::to_f(x[at + e]) : 0.f, g = at + e < H ? gamma[at + e] : 0.f;
+          v[e] = at + e < H ? exact8(xe * r * g, xe, g, r64) : 0.f;
+        }
         const uint32_t byte = q8_scale_byte(q8_amax<4>(v, [](float m) {
           m = run_maxf<16>(m);
           return fmaxf(m, __shfl_xor(m, 16));
