@@ -35,6 +35,7 @@ BSTAGES = {"zero": 0, "transpose": 1, "plan": 2, "recompute": 3, "dh": 4, "wgrad
            "wgrad_gate_up": 6, "dx": 7, "combine_bwd": 8, "dwr": 9}
 MOE_F32, MOE_BF16 = 0, 1
 GMM_BF16, GMM_Q8 = 0, 1
+GMM8_CUT = 7.0 / 8192  # of the products' magnitudes: gmm8_forward's sums of more than four rows
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 CCE_STAGES = {"logits": 0, "fold": 1, "grad": 2, "dx": 3, "dw": 4}
 
@@ -1098,7 +1099,8 @@ def _expect_gmm8_rows(plan, Xq, Xs, dev):
 
 def gmm8_forward(plan: GmmPlan, Xq, Xs, Wq, Ws, offsets=None, Y=None, ws=None, stream=None):
     """Returns Y [R, N] bfloat16 from rows in 8 bits (q8_pack) and weights in 8 bits along K
-    (q8_pack_weights(W, "K"))."""
+    (q8_pack_weights(W, "K")).  Sums of more than four rows are off by up to GMM8_CUT of their
+    products' magnitudes."""
     dev = Xq.device
     R, K, N, E = plan.R, plan.K, plan.N, plan.E
     _expect_gmm8_rows(plan, Xq, Xs, dev)

@@ -49,6 +49,15 @@ def test_struct_layout_matches_c(struct, tmp_path):
         assert int(off) == getattr(cls, n).offset, n
 
 
+def test_what_the_8_bit_product_cuts_is_stated(tmp_path):
+    """The header's bound of gmm8_forward's sums is the binding's: 2^-13 for each of seven products of eight."""
+    c, exe = str(tmp_path / "t.c"), str(tmp_path / "t")
+    open(c, "w").write('#include <stdio.h>\n#include "gmm.h"\nint main(void) { printf("%.17g\\n", GMM8_CUT); return 0; }\n')
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-I", os.path.join(ROOT, "include"), c, "-o", exe], check=True)
+    out = subprocess.run([exe], capture_output=True, text=True, check=True).stdout
+    assert float(out) == B.GMM8_CUT == 7 * 2.0 ** -13
+
+
 CALLS = {
     "rms": ("rms", "rms.h", "ROWS(N) SIZES(H) for (int d = -1; d < 3; ++d) { rms_plan_t p; ok += rms_plan(N, H, d, 1e-5f, &p) == MOE_OK; }"),
     "q8": ("q8", "q8.h", "ROWS(N) SIZES(H) for (int d = -1; d < 3; ++d) { q8_plan_t p; ok += q8_plan(N, H, d, &p) == MOE_OK; }"),

@@ -482,3 +482,47 @@ def test_gradients_are_the_adjoints():
     vals = d(y, dY), d(dx, X), d(dw, W)
     scale = E16 * max(float((y.double() * dY.double()).abs().sum()), float((dx.double() * X.double()).abs().sum()))
     assert max(vals) - min(vals) <= 2 * scale
+
+
+# rows, K, N, experts: dot products; 64 x 64 tiles, whole and with k in parts; 32, 64 and 128 rows; 256 x 256
+CUTS = [(4, 300, 72, 1), (4, 2056, 72, 2), (5, 300, 72, 1), (40, 300, 72, 1), (70, 2056, 72, 1), (500, 200, 1032, 64), (1300, 200, 1032, 40),
+        (2800, 200, 1032, 40), (3000, 136, 4104, 3)]
+
+
+@pytest.mark.parametrize("R,K,N,E", CUTS)
+def test_8_bit_sums_that_cancel(R, K, N, E):
+    """Sums whose products cancel in pairs of one eight but for small ones, under the header's bound: fp32's roundings for
+    up to four rows, GMM8_CUT of the products' magnitudes beside them for more."""
+    g = torch.Generator().manual_seed(11)
+    x, w = torch.randn(R, K, generator=g), torch.randn(E, K, N, generator=g)
+    x[:, 1::4], w[:, 1::4] = -x[:, 0::4][:, :x[:, 1::4].shape[1]], w[:, 0::4][:, :w[:, 1::4].shape[1]]
+    for c in (2, 3):  # and between the pairs products of 2^-10 to 2^-15 of theirs
+        x[:, c::4] *= torch.exp2(-torch.randint(10, 16, x[:, c::4].shape, generator=g).float())
+    x, w = x.to(DEV), w.to(DEV)
+    p8 = B.q8_plan(R, K, B.MOE_F32)
+    Xq, Xs = B.q8_pack(p8, x)
+    Wq, Ws = B.q8_pack_weights(w, "K")
+    X = B.q8_unpack(p8, Xq, Xs).double()
+    s = torch.exp2(Ws.view(torch.uint8)[:, :, :-(-K // 128)].double() - 127)
+    Wv = (Wq[:, :, :K].double() * s.repeat_interleave(128, 1)[:, :N].repeat_interleave(128, 2)[:, :, :K]).transpose(1, 2).contiguous()
+    sizes = ragged(R, E, 3, 0.1)
+    off = offsets_of(sizes)
+    Y = B.gmm8_forward(B.gmm_plan(R, K, N, E, B.GMM_Q8), Xq, Xs, Wq, Ws, off).double()
+    cut = 0.0 if R <= 4 else B.GMM8_CUT
+    for e, r in by_expert(off):
+        ref, size = X[r] @ Wv[e], X[r].abs() @ Wv[e].abs()
+        bad = (Y[r] - ref).abs() > (2 * U * K + cut) * size * (1 + E16) + E16 * ref.abs()
+        assert not bad.any(), (e, int(bad.sum()))
+
+
+def test_a_row_of_an_8_bit_product_does_not_depend_on_the_others():
+    """In calls of the same sizes a row has the same bits whatever the other rows hold."""
+    for R, K, N in ((4, 700, 136), (9, 700, 136), (200, 700, 136)):
+        g = torch.Generator().manual_seed(12)
+        Xq, Xs, _ = rows8(g, R, K)
+        Wq, Ws = B.q8_pack_weights(torch.randn(1, K, N, generator=g).to(DEV), "K")
+        plan = B.gmm_plan(R, K, N, 1, B.GMM_Q8)
+        a = B.gmm8_forward(plan, Xq, Xs, Wq, Ws)
+        other, scales, _ = rows8(g, R, K)
+        other.view(torch.uint8)[R // 2], scales.view(torch.uint8)[R // 2] = Xq.view(torch.uint8)[R // 2], Xs.view(torch.uint8)[R // 2]
+        assert torch.equal(a[R // 2], B.gmm8_forward(plan, other, scales, Wq, Ws)[R // 2])
