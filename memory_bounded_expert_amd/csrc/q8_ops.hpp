@@ -46,11 +46,11 @@ __device__ __forceinline__ float q8_amax(const float* v, R reduce) {
   return m;
 }
 
-// Whether v is within eight of its last places of where e4m3 or a scale turn, under any
+// Whether v is within `off` of its last places of where e4m3 or a scale turn, under any
 // power of two: a value with at most four bits after its first.  There 32 bits do not say
 // which side a computed value is on, and it is formed again in 64.
-__device__ __forceinline__ bool q8_border(float v) {
-  return ((__float_as_uint(v) + 8u) & 0x7ffffu) <= 16u && v != 0.f;
+__device__ __forceinline__ bool q8_border(float v, uint32_t off = 8) {
+  return ((__float_as_uint(v) + off) & 0x7ffffu) <= 2 * off && v != 0.f;
 }
 // x in 32 bits to odd (a value between two numbers becomes the one whose last bit is 1),
 // so that rounding it once more gives what rounding x would.

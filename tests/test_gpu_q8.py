@@ -181,3 +181,36 @@ def test_fp32_swiglu_is_rounded_once():
     want, e = Q.quantise(Q.swiglu(dev_to_f64(a), dev_to_f64(u)))
     got, _, ge = values8(hq, hs, H)
     assert np.array_equal(got, want) and np.array_equal(ge, e)
+
+
+def all_classes():
+    """a [N][1] and u [1][128] of every bfloat16 mantissa: a of both signs with 2^-9 <= |a| < 2^6, u in [1, 2)."""
+    a = (torch.arange(118 << 7, 133 << 7, dtype=torch.int32) << 16).view(torch.float32)
+    u = (((127 << 7) | torch.arange(128, dtype=torch.int32)) << 16).view(torch.float32)
+    return torch.cat([a, -a])[:, None], u[None]
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_swiglu_of_every_mantissa_is_rounded_once(dtype):
+    """h next to where e4m3 turns is formed in 64 bits in bfloat16 too: from a = 17 on silu(a) is a to within fp32, so that
+    a u, which may be a tie, stands for an h below it; for other a the 32-bit h is off by its exponential's argument.  All
+    numbers and scales are those of the fp64 h."""
+    require_lib()
+    a, u = (t.expand(3840, 128).contiguous().to(TYPES[dtype][0]).to(DEV) for t in all_classes())
+    for x, y in ((a, u), (a, -u * 2.0 ** -20), (a[:, :1].expand(-1, 128).contiguous(), u[:, :1] * torch.exp2(torch.arange(128.0, device=DEV) - 64).to(u.dtype))):
+        hq, hs, _ = B.q8_swiglu_forward(B.q8_plan(3840, 128, B.moe_dtype(a.dtype)), x, y.contiguous())
+        want, e = Q.quantise(Q.swiglu(dev_to_f64(x), dev_to_f64(y)))
+        got, _, ge = values8(hq, hs, 128)
+        assert int((got != want).sum()) == 0 and np.array_equal(ge, e)
+
+
+@pytest.mark.parametrize("H", [1536, 1000])
+def test_bf16_swiglu_is_rounded_once(H):
+    """As test_fp32_swiglu_is_rounded_once, of ordinary rows, with ones whose gates are all past 17."""
+    a, u = rows(2000, H, "bf16", 5, 0.5), rows(2000, H, "bf16", 6, 0.5)
+    a[:40] = (a[:40].abs() + 17).bfloat16()
+    a[50], u[51], a[52], u[52] = 0.0, -0.0, -200.0, 1e30
+    hq, hs, _ = B.q8_swiglu_forward(B.q8_plan(2000, H), a, u)
+    want, e = Q.quantise(Q.swiglu(dev_to_f64(a), dev_to_f64(u)))
+    got, _, ge = values8(hq, hs, H)
+    assert np.array_equal(got, want) and np.array_equal(ge, e)
