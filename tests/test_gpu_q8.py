@@ -214,3 +214,28 @@ def test_bf16_swiglu_is_rounded_once(H):
     want, e = Q.quantise(Q.swiglu(dev_to_f64(a), dev_to_f64(u)))
     got, _, ge = values8(hq, hs, H)
     assert np.array_equal(got, want) and np.array_equal(ge, e)
+
+
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_swiglu_where_the_32_bit_exponential_ends(dtype):
+    """Gates so far below zero that e^-a leaves fp32's range (-87.3 for its reciprocal, -88.7 for itself), under factors
+    that bring the products back: h, dA and dU are those of fp64, not 0.  The gradients are rounded to fp32 and to the
+    output's type: half a step of each, or of the least number."""
+    require_lib()
+    dt, e = TYPES[dtype]
+    a = torch.tensor([-80.0, -87.0, -87.5, -88.0, -89.0, -95.0, -100.0, -104.0, -120.0, -300.0, -700.0, -800.0])[:, None].expand(-1, 300)
+    n = len(a)
+    for u, d in ((torch.linspace(1e30, 3e38, 300), 1.0), (torch.linspace(-3.0, 3.0, 300), 1e30), (torch.full((300,), 1e38), 1e-3)):
+        x, y, dh = a.to(dt).contiguous().to(DEV), u.expand(n, -1).to(dt).contiguous().to(DEV), torch.full((n, 300), d).to(dt).to(DEV)
+        plan = B.q8_plan(n, 300, B.moe_dtype(dt))
+        hq, hs, kept = B.q8_swiglu_forward(plan, x, y)
+        dA, dU = B.q8_swiglu_backward(plan, kept, dh)
+        with np.errstate(over="ignore"):
+            want, se = Q.quantise(Q.swiglu(dev_to_f64(x), dev_to_f64(y)))
+            got, _, ge = values8(hq, hs, 300)
+            assert np.array_equal(got, want) and np.array_equal(ge, se)
+            refs = Q.swiglu_backward(values8(*kept[:2], 300)[0], values8(*kept[2:], 300)[0], dev_to_f64(dh))
+        far = dev_to_f64(x) < -87
+        for t, ref in zip((dA, dU), refs):
+            tol = (e + 2 * U) * np.abs(ref) + (2.0 ** -134 if dtype == "bf16" else 2.0 ** -150)
+            assert np.all(np.abs(dev_to_f64(t) - ref)[far] <= tol[far])
