@@ -9,6 +9,7 @@
 #include "moe_internal.h"
 #include "q8.h"
 #include "q8_ops.hpp"
+#include "q8_shapes.hpp"
 #include "wave_ops.hpp"
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
@@ -87,7 +88,7 @@ struct Packed {
   uint8_t *q, *s;
 };
 // A launch's blocks: `units` of them from row `first` on.  u / blocks is a product by
-// `magic` and a shift (units is below 2^31).
+// `magic` and a shift (q8_shapes.hpp).
 struct Shape8 {
   int64_t first;
   uint32_t units, magic, shift;
@@ -347,21 +348,17 @@ bool whole_lines(const q8_plan_t& P, const void* a, const void* b) {
   return P.H * sizeof(T) % 128 == 0 && ((uintptr_t)a | (uintptr_t)b) % 128 == 0;
 }
 
-// Calls f(shape, work-groups) for launches of below 2^31 blocks that cover all rows.
+// Calls f(shape, work-groups) for the launches that cover all rows.
 template <typename F>
 int in_launches(const q8_plan_t& P, F f) {
+  static_assert(kThreads == kQ8GroupThreads && kThreads / kLanes == kQ8GroupBlocks, "a work-group's blocks");
   const int blocks = q8_blocks(P.H);
-  // u / blocks = u magic >> shift for u < 2^31: magic = ceil(2^shift / blocks), whose
-  // error, below blocks, times u stays below 2^shift = 2^31 times a power of two >= blocks
-  uint32_t shift = 31;
-  while ((1u << (shift - 31)) < (uint32_t)blocks) ++shift;
-  Shape8 sh{0, 0, (uint32_t)((((uint64_t)1 << shift) + blocks - 1) / blocks), shift, P.H, blocks, P.row_pitch, P.scale_pitch};
-  const int64_t most = (((int64_t)1 << 31) - 1) / blocks;
   (void)hipGetLastError();
-  for (; sh.first < P.N; sh.first += most) {
-    sh.units = (uint32_t)(std::min(most, P.N - sh.first) * blocks);
-    f(sh, (unsigned)ceil_div(sh.units, kThreads / kLanes));
+  for (int64_t first = 0; first < P.N;) {
+    const Q8Launch l = q8_launch(P.N - first, blocks);
+    f(Shape8{first, l.units, l.magic, l.shift, P.H, blocks, P.row_pitch, P.scale_pitch}, l.groups);
     if (hipGetLastError() != hipSuccess) return MOE_EHIP;
+    first += l.rows;
   }
   return MOE_OK;
 }

@@ -239,3 +239,35 @@ def test_swiglu_where_the_32_bit_exponential_ends(dtype):
         for t, ref in zip((dA, dU), refs):
             tol = (e + 2 * U) * np.abs(ref) + (2.0 ** -134 if dtype == "bf16" else 2.0 ** -150)
             assert np.all(np.abs(dev_to_f64(t) - ref)[far] <= tol[far])
+
+
+def test_rows_past_one_launch():
+    """More blocks than a launch has (2^29 - 32, HIP's 2^32 threads): the rows of the second are as those of the first."""
+    require_lib()
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 140 << 30:
+        pytest.skip("needs 140 GB")
+    H, n = 8, 1 << 16
+    N = (1 << 29) + n
+    x = torch.randn(n, H, device=DEV).bfloat16()
+    X, few, many = x.repeat(N // n, 1), B.q8_plan(n, H), B.q8_plan(N, H)
+    raw = lambda t: t.view(torch.uint8)
+
+    def same(q, s, q1, s1):
+        for part in (slice(0, n), slice(N - 2 * n, N - n), slice(N - n, N)):
+            assert torch.equal(raw(q)[part], raw(q1)) and torch.equal(raw(s)[part], raw(s1))
+
+    q, s = B.q8_pack(many, X)
+    q1, s1 = B.q8_pack(few, x)
+    same(q, s, q1, s1)
+    back = B.q8_unpack(many, q, s)
+    assert bool((back.view(-1, n, H) == B.q8_unpack(few, q1, s1)).all())
+    dA, dU = B.q8_swiglu_backward(many, (q, s, q, s), X, dA=X, dU=back)
+    dA1, dU1 = B.q8_swiglu_backward(few, (q1, s1, q1, s1), x)
+    assert bool((dA.view(-1, n, H) == dA1).all()) and bool((dU.view(-1, n, H) == dU1).all())
+    del back, dU
+    X.copy_(x.repeat(N // n, 1))
+    B.q8_swiglu_forward(many, X, X, keep=False, H=(q, s))
+    same(q, s, *B.q8_swiglu_forward(few, x, x, keep=False)[:2])
+    del q, s, X, dA
+    torch.cuda.empty_cache()
