@@ -83,7 +83,9 @@ typedef struct gmm_plan {
  * Errors: MOE_EINVAL if out is NULL, R < 0, K < 1, N < 1, E < 0, operands
  *   unknown, N (and K in bfloat16) not a multiple of 8, or E = 0 with R > 0.
  *   MOE_EUNSUPPORTED if K or N > 65536, E > 1024, R >= 2^31 - 65536, 2 K N (the
- *   bytes of a matrix) >= 2^31, or R max(K, N) >= 2^40.
+ *   bytes of a matrix) >= 2^31, R max(K, N) >= 2^40, or a launch would have 2^32
+ *   threads (within the limits before only near them: R past 2^31 - 2^19 over
+ *   hundreds of experts).
  */
 int gmm_plan(int64_t R, int32_t K, int32_t N, int32_t E, int32_t operands, gmm_plan_t* out);
 

@@ -130,22 +130,46 @@ int single_launch(const Args& a, hipStream_t st) {
   return launched();
 }
 
+// Calls g with the tile of a size.
+template <Form F, typename G>
+auto with_rows_shape(Size size, G g) {
+  switch (size) {
+    // (waves of 64 x 128, or in bf16 128 x 64, of which the transposing reads want
+    // fewer columns: 16,384 x 4096 x 4096 forward 410 us and 397)
+    case Size::Large: return g(std::conditional_t<F == Form::Q8, GShape<256, 256, 4, 2, 2>, GShape<256, 256, 2, 4, 2>>());
+    case Size::Middle: return g(GShape<128, 128, 2, 2, 2>());
+    case Size::Small: return g(GShape<64, 128, 2, 2, 2>());
+    case Size::Few: return g(GShape<64, 64, 2, 2, 4>());
+    default: return g(GShape<F == Form::Q8 ? 32 : 16, 128, 1, 4, 2>());
+  }
+}
+template <typename G>
+auto with_weights_shape(Size size, G g) {
+  if (size == Size::Large) return g(GShape<256, 256, 4, 2, 4>());
+  return g(GShape<128, 128, 2, 2, 4>());
+}
+
+// Whether a product's launch has fewer than 2^32 threads along x (HIP refuses others).
+constexpr int64_t kLaunchThreads = (int64_t)1 << 32;
+template <Form F>
+bool rows_launchable(const Choice& c, int64_t R, int N, int E) {
+  return c.size == Size::Single || with_rows_shape<F>(c.size, [&](auto s) {
+           return row_tiles(R, E, s.BM) * ceil_div(N, s.BN) * s.THREADS < kLaunchThreads;
+         });
+}
+bool weights_launchable(const Choice& c, int K, int N, int E) {
+  return with_weights_shape(c.size, [&](auto s) {
+    return weights_groups(E * ceil_div(K, s.BM) * ceil_div(N, s.BN)) * s.THREADS < kLaunchThreads;
+  });
+}
+
 template <Form F>
 int rows_product(Args a, void* workspace, hipStream_t st) {
   const Choice c = choose_rows(F == Form::Q8, a.R, a.K, a.N, a.E);
   a.part = (float*)workspace;
   if constexpr (F == Form::Q8)
     if (c.size == Size::Single) return single_launch(a, st);
-  switch (c.size) {
-    // (waves of 64 x 128, or in bf16 128 x 64, of which the transposing reads want
-    // fewer columns: 16,384 x 4096 x 4096 forward 410 us and 397)
-    case Size::Large:
-      return rows_launch<F, std::conditional_t<F == Form::Q8, GShape<256, 256, 4, 2, 2>, GShape<256, 256, 2, 4, 2>>>(a, c, st);
-    case Size::Middle: return rows_launch<F, GShape<128, 128, 2, 2, 2>>(a, c, st);
-    case Size::Small: return rows_launch<F, GShape<64, 128, 2, 2, 2>>(a, c, st);
-    case Size::Few: return rows_launch<F, GShape<64, 64, 2, 2, 4>>(a, c, st);
-    default: return rows_launch<F, GShape<F == Form::Q8 ? 32 : 16, 128, 1, 4, 2>>(a, c, st);
-  }
+  return with_rows_shape<F>(c.size, [&](auto s) { return rows_launch<F, decltype(s)>(a, c, st); });
 }
 
 template <Form F, class S>
@@ -178,8 +202,7 @@ template <Form F>
 int weights_product(Args a, void* workspace, hipStream_t st) {
   const Choice c = choose_weights(a.R, a.K, a.N, a.E);
   a.part = (float*)workspace;
-  if (c.size == Size::Large) return weights_launch<F, GShape<256, 256, 4, 2, 4>>(a, c, st);
-  return weights_launch<F, GShape<128, 128, 2, 2, 4>>(a, c, st);
+  return with_weights_shape(c.size, [&](auto s) { return weights_launch<F, decltype(s)>(a, c, st); });
 }
 
 }  // namespace
@@ -202,10 +225,18 @@ MOE_API int gmm_plan(int64_t R, int32_t K, int32_t N, int32_t E, int32_t operand
   p.E = E;
   p.row_pitch = operands == GMM_BF16 ? 2 * K : q8_row_pitch(K);
   const bool q8 = operands == GMM_Q8;
+  const Choice dw = choose_weights(R, K, N, E);
+  if (!weights_launchable(dw, K, N, E)) return MOE_EUNSUPPORTED;
   if (R > 0) {
-    p.fwd_workspace_bytes = part_bytes(choose_rows(q8, R, K, N, E), R * N);
-    if (!q8) p.fwd_workspace_bytes = std::max(p.fwd_workspace_bytes, part_bytes(choose_rows(false, R, N, K, E), R * K));
-    p.bwd_workspace_bytes = part_bytes(choose_weights(R, K, N, E), (int64_t)E * K * N);
+    const Choice y = choose_rows(q8, R, K, N, E);
+    if (!(q8 ? rows_launchable<Form::Q8>(y, R, N, E) : rows_launchable<Form::NN>(y, R, N, E))) return MOE_EUNSUPPORTED;
+    p.fwd_workspace_bytes = part_bytes(y, R * N);
+    if (!q8) {
+      const Choice dx = choose_rows(false, R, N, K, E);
+      if (!rows_launchable<Form::NT>(dx, R, K, E)) return MOE_EUNSUPPORTED;
+      p.fwd_workspace_bytes = std::max(p.fwd_workspace_bytes, part_bytes(dx, R * K));
+    }
+    p.bwd_workspace_bytes = part_bytes(dw, (int64_t)E * K * N);
   }
   *out = p;
   return MOE_OK;

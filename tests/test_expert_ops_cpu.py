@@ -120,6 +120,26 @@ def test_gmm_plan_errors(a, status):
     assert B.lib().gmm_plan(*a, None) == B.MOE_EINVAL
 
 
+@pytest.mark.parametrize("operands", [B.GMM_BF16, B.GMM_Q8])
+def test_gmm_plans_whose_launch_would_be_refused(operands):
+    """256 rows of one column tile are 512 threads, and an expert's rows may end in a tile of their own: HIP takes fewer
+    than 2^32 threads of a launch."""
+    plan = lambda R, K, N, E: B.lib().gmm_plan(R, K, N, E, operands, ref(B.GmmPlan()))
+    most = 2 ** 31 - 65536 - 1
+    for E in (1, 64, 255):
+        assert (most // 256 + E) * 512 < 2 ** 32 and plan(most, 8, 8, E) == B.MOE_OK
+    for E in (257, 512, 1024):
+        assert (most // 256 + E) * 512 >= 2 ** 32 and plan(most, 8, 8, E) == B.MOE_EUNSUPPORTED
+    R = 2 ** 31 - 512 * 1024 // 2 - 256
+    assert (R // 256 + 1024) * 512 < 2 ** 32 and plan(R, 8, 8, 1024) == B.MOE_OK
+    assert plan(2 ** 31 - 512 * 1024 // 2, 8, 8, 1024) == B.MOE_EUNSUPPORTED
+    for R in (0, 1, 300, 100_000):  # and of dW's, whatever the rows
+        assert plan(R, 32768, 32760, 1024) == (B.MOE_EUNSUPPORTED if 16384 * 1024 * 512 >= 2 ** 32 else B.MOE_OK)
+    # dX's columns are K
+    if operands == B.GMM_BF16:
+        assert plan(2 ** 30, 512, 8, 1024) == B.MOE_EUNSUPPORTED and plan(2 ** 30, 256, 8, 1024) == B.MOE_OK
+
+
 # ---- calls
 
 
