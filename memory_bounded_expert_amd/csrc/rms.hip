@@ -49,6 +49,18 @@ __device__ __forceinline__ double row_sum64(float v, double (*red)[16], int& hal
   }
   return s;
 }
+// Sum over the work-group, in 64 bits; `red` as in row_sum64.
+__device__ __forceinline__ double group_sum64(double v, double (*red)[16], int& half) {
+#pragma unroll
+  for (int n = 32; n > 0; n /= 2) v += __shfl_xor(v, n);
+  if ((threadIdx.x & 63) == 0) red[half][threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) v += red[half][w];
+  half ^= 1;
+  return v;
+}
 // 1 / sqrt(m) from r, which is that in 32 bits, by a Newton step.
 __device__ __forceinline__ double rstd64(double m, float r) {
   return fma(0.5 * r, fma(-m * r, (double)r, 1.0), (double)r);
@@ -272,15 +284,17 @@ __global__ __launch_bounds__(kGroup<W>) void rms_rows_backward_kernel(
   }
 }
 
-// Rows wider than the registers hold.
+// Rows wider than the registers hold, their sums in 64 bits throughout (a lane adds up to 256
+// numbers).
 template <typename T, bool Q8>
 __global__ __launch_bounds__(kThreads) void rms_forward_kernel(
     const T* X, const T* residual, const float* __restrict__ gamma, T* S, const RowsOut out,
     float* __restrict__ rstd, int64_t N, int H, float eps) {
-  __shared__ float red[kThreads / 64];
+  __shared__ double red[2][16];
+  int half = 0;
   for (int64_t t = blockIdx.x; t < N; t += gridDim.x) {
     const T* x = X + t * H;
-    float q = 0.f;
+    double q = 0.0;
     for (int h = threadIdx.x; h < H; h += kThreads) {
       float v = Elem<T>::to_f(x[h]);
       if (residual) {
@@ -288,10 +302,10 @@ __global__ __launch_bounds__(kThreads) void rms_forward_kernel(
         S[t * H + h] = sum;
         v = Elem<T>::to_f(sum);
       }
-      q = fmaf(v, v, q);
+      q = fma((double)v, (double)v, q);
     }
     if (residual) x = S + t * H;  // each thread reads back what it wrote
-    const double m = (double)group_sum(q, red) / H + (double)eps;
+    const double m = group_sum64(q, red, half) / H + (double)eps;
     const float r = 1.f / sqrtf((float)m);
     const double r64 = rstd64(m, r);
     if (threadIdx.x == 0) rstd[t] = r;

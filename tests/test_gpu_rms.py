@@ -189,3 +189,21 @@ def test_values_next_to_borders(dtype):
     assert np.array_equal(ge, e)
     assert int((got != want).sum()) <= 46
     assert (np.abs(got - want) <= np.exp2(np.floor(np.log2(np.maximum(np.abs(want), 1e-30))) - 3)).all()
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dtype", sorted(TYPES))
+def test_wide_rows_next_to_borders(dtype, residual):
+    """Rows past 16,384 columns are summed in 64 bits throughout, so that values formed in 64 bits are those of the fp64
+    norm: all numbers and scales.  (From sums in 32 bits up to three of four million are not.)"""
+    require_lib()
+    N, H = 200, 20_000
+    g = torch.Generator().manual_seed(10)
+    x, r = (torch.randn(N, H, generator=g).to(TYPES[dtype][0]).to(DEV) for _ in range(2))
+    gamma = (1 + 0.1 * torch.randn(H, generator=g)).to(DEV)
+    q, s, S, _ = B.rms_forward_q8(B.rms_plan(N, H, B.moe_dtype(x.dtype), 1e-6), x, gamma, r if residual else None)
+    v = dev_to_f64(S)
+    y = v / np.sqrt(np.mean(v * v, axis=1, keepdims=True) + float(np.float32(1e-6))) * dev_to_f64(gamma)
+    want, e = Q.quantise(y)
+    got, _, ge = values8(q, s, H)
+    assert np.array_equal(ge, e) and int((got != want).sum()) == 0
