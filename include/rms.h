@@ -9,9 +9,12 @@
  * with xh_h = s_h rstd and d_h = dy_h gamma_h:
  *   dx_h     = ds_h + rstd (d_h - xh_h sum_j d_j xh_j / H)   (dr = dx)
  *   dgamma_h = sum over rows of dy_h xh_h
- * Every sum is fp32, and y and dx are rounded once.  y can come as rows of 8 bits
- * with scales (q8.h), formed from the fp32 y.  Every output is deterministic:
- * sums run in a fixed order, without atomics.
+ * The sum of squares is fp32 within 16 lanes (512 columns at most) and 64 bits from
+ * there on, of rows past 16,384 columns 64 bits throughout; the backward pass's sums
+ * are fp32.  y and dx are rounded once.  y can come as rows of 8 bits with scales
+ * (q8.h): formed in fp32, and again in 64 bits where that lies next to where e4m3 or
+ * a scale turn, so that it is rounded to 8 bits as the 64-bit value is.  Every output
+ * is deterministic: sums run in a fixed order, without atomics.
  *
  * Conventions: as moebound.h (row-major contiguous device tensors, caller-
  * owned memory and workspace, no allocation or synchronisation, work enqueued
