@@ -325,8 +325,13 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 
 
 # A new tensor on the current device without the public call's reading of its arguments
-# (0.7 us for 1.3, and a call has up to six).
+# (0.8 us for 1.3, and a call has up to six).  Only where torch.empty does no more than that:
+# it fills new memory under deterministic algorithms, and dispatch modes see it.
 _empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+_deterministic = getattr(torch._C, "_get_deterministic_algorithms", torch.are_deterministic_algorithms_enabled)
+_dispatch_modes = getattr(torch._C, "_len_torch_dispatch_stack", None)
+if _dispatch_modes is None:
+    _empty_strided = None
 
 
 def _stream(device, stream):
@@ -365,10 +370,15 @@ def _workspace(ws, plan, kind, device):
 def _out(t, name, shape, dtype, device):
     """The output tensor given, checked, or a new one (on the current device, see _on)."""
     if t is None:
-        if _empty_strided is not None and len(shape) < 4:
-            row = shape[-1] or 1
-            strides = (row, 1) if len(shape) == 2 else (1,) if len(shape) == 1 else ((shape[1] or 1) * row, row, 1)
-            return _empty_strided(shape, strides, dtype)
+        if _empty_strided is not None and not _deterministic() and not _dispatch_modes():
+            n = len(shape)
+            if n == 2:
+                return _empty_strided(shape, (shape[1] or 1, 1), dtype)
+            if n == 1:
+                return _empty_strided(shape, (1,), dtype)
+            if n == 3:
+                row = shape[2] or 1
+                return _empty_strided(shape, ((shape[1] or 1) * row, row, 1), dtype)
         return torch.empty(*shape, dtype=dtype, device=device)  # sizes one by one: 1.2 us, a tuple 1.6
     _expect(t, name, shape, dtype, device)
     return t
