@@ -526,3 +526,29 @@ def test_a_row_of_an_8_bit_product_does_not_depend_on_the_others():
         other, scales, _ = rows8(g, R, K)
         other.view(torch.uint8)[R // 2], scales.view(torch.uint8)[R // 2] = Xq.view(torch.uint8)[R // 2], Xs.view(torch.uint8)[R // 2]
         assert torch.equal(a[R // 2], B.gmm8_forward(plan, other, scales, Wq, Ws)[R // 2])
+
+
+def check_q8_dx(R, K, N, sizes, seed=0):
+    """dX in 8 bits: gmm8_forward of a plan (R, N, K, E) on dY's rows in 8 bits and on W in 8 bits along N, to the bound of
+    the forward product."""
+    g = torch.Generator().manual_seed(seed)
+    E, R = len(sizes), sum(sizes)
+    Dq, Ds, D = rows8(g, R, N)
+    W = (torch.randn(E, K, N, generator=g) * 0.05 * torch.exp(torch.randn(1, K, 1, generator=g)) * torch.exp(torch.randn(E, 1, N, generator=g))).to(DEV)
+    Wq, Ws = B.q8_pack_weights(W, "N")
+    s = torch.exp2(Ws.view(torch.uint8)[:, :, :-(-N // 128)].double() - 127)
+    Wv = Wq[:, :, :N].double() * s.repeat_interleave(128, 1)[:, :K].repeat_interleave(128, 2)[:, :, :N]
+    off = offsets_of(sizes)
+    dX = B.gmm8_forward(B.gmm_plan(R, N, K, E, B.GMM_Q8), Dq, Ds, Wq, Ws, off)
+    for e, r in by_expert(off):
+        w = Wv[e].T.contiguous()
+        close(dX[r], D[r] @ w, D[r].abs() @ w.abs(), N, E16, ("dX", e), 0.0 if R <= 4 else TRUNC)
+        # nothing but roundings of the given W: every number within half a step of e4m3 of it
+        scale = s[e].repeat_interleave(128, 0)[:K].repeat_interleave(128, 1)[:, :N]
+        assert bool(((Wv[e] - W[e].double()).abs() <= torch.maximum(2.0 ** -4 * W[e].double().abs(), 2.0 ** -10 * scale)).all())
+
+
+@pytest.mark.parametrize("K,N,sizes", CASES + TILES, ids=lambda v: str(v) if isinstance(v, int) else "E%d_R%d" % (len(v), sum(v)))
+def test_dx_in_8_bits(K, N, sizes):
+    check_q8_dx(0, K, N, sizes)
+    check_q8_dx(0, K, max(N - 3, 1), sizes, 1)
