@@ -283,3 +283,64 @@ def test_binding_refuses_wrong_tensors():
         with pytest.raises(ValueError):
             call()
             print("call", i, "passed")
+
+
+def test_binding_says_what_is_wrong():
+    """Each refusal by its own check: the name of the tensor and what does not fit, before the look at the device."""
+    z = lambda *s, d=torch.bfloat16: torch.zeros(*s, dtype=d)
+    q = lambda *s: z(*s, d=torch.uint8).view(B.E4M3)
+    s8 = lambda *s: z(*s, d=torch.uint8).view(B.E8M0)
+    f32 = torch.float32
+    rp, qp, gp, g8 = B.rms_plan(4, 16), B.q8_plan(4, 16), B.gmm_plan(4, 16, 8, 2), B.gmm_plan(4, 16, 8, 2, B.GMM_Q8)
+    x, dy, ga, w, of = z(4, 16), z(4, 8), z(16, d=f32), z(2, 16, 8), z(3, d=torch.int32)
+    xq, xs, wq, ws = q(4, 128), s8(4, 4), q(2, 8, 128), s8(2, 1, 4)
+    odd = z(16, 4).t()  # 4 x 16, not in one piece
+    kept = (xq, xs, xq, xs)
+    meta = lambda t: t.to("meta")
+    for message, call in (
+            ("^X: shape", lambda: B.rms_forward(rp, x[:3], ga)), ("^X: dtype", lambda: B.rms_forward(rp, x.float(), ga)),
+            ("^X must be contiguous", lambda: B.rms_forward(rp, odd, ga)), ("^gamma: dtype", lambda: B.rms_forward(rp, x, ga.bfloat16())),
+            ("^gamma: shape", lambda: B.rms_forward(rp, x, ga[:8])), ("^gamma: device", lambda: B.rms_forward(rp, x, meta(ga))),
+            ("^residual: shape", lambda: B.rms_forward(rp, x, ga, residual=x[:2])), ("^residual: dtype", lambda: B.rms_forward_q8(rp, x, ga, x.float())),
+            ("^S is X itself", lambda: B.rms_forward(rp, x, ga, S=x)), ("^S is X itself", lambda: B.rms_forward_q8(rp, x, ga, S=x)),
+            ("^dY: shape", lambda: B.rms_backward(rp, x, ga, x[:1], ga[:4])), ("^rstd: dtype", lambda: B.rms_backward(rp, x, ga, x, z(4))),
+            ("^rstd: shape", lambda: B.rms_backward(rp, x, ga, x, ga)), ("^dS: dtype", lambda: B.rms_backward(rp, x, ga, x, ga[:4], dS=x.float())),
+            ("^S must be contiguous", lambda: B.rms_backward(rp, odd, ga, x, ga[:4])),
+            ("^X must be contiguous", lambda: B.q8_pack(qp, odd)), ("^X: dtype", lambda: B.q8_pack(B.q8_plan(4, 16, B.MOE_F32), x)),
+            ("^q: shape", lambda: B.q8_unpack(qp, q(4, 16), xs)), ("^s: shape", lambda: B.q8_unpack(qp, xq, s8(4, 1))),
+            ("^q: dtype", lambda: B.q8_unpack(qp, z(4, 128, d=torch.uint8), xs)), ("^s: dtype", lambda: B.q8_unpack(qp, xq, z(4, 4, d=torch.uint8))),
+            ("^along: 'M'", lambda: B.q8_pack_weights(w, "M")), ("^W: 2 dimensions", lambda: B.q8_pack_weights(x)),
+            ("^unsupported dtype", lambda: B.q8_pack_weights(w.half())), ("^W must be contiguous", lambda: B.q8_pack_weights(z(2, 8, 16).transpose(1, 2))),
+            ("^A: shape", lambda: B.q8_swiglu_forward(qp, x[:3], x)), ("^U: shape", lambda: B.q8_swiglu_forward(qp, x, x[:3])),
+            ("^U: dtype", lambda: B.q8_swiglu_forward(qp, x, x.float())), ("^As: shape", lambda: B.q8_swiglu_backward(qp, (xq, s8(4, 3), xq, xs), x)),
+            ("^Uq: dtype", lambda: B.q8_swiglu_backward(qp, (xq, xs, z(4, 128), xs), x)),
+            ("^Us: shape", lambda: B.q8_swiglu_backward(qp, (xq, xs, xq, s8(4, 3)), x)), ("^dH: dtype", lambda: B.q8_swiglu_backward(qp, kept, x.float())),
+            ("^offsets are required", lambda: B.gmm_forward(gp, x, w)), ("^offsets are required", lambda: B.gmm8_forward(g8, xq, xs, wq, ws)),
+            ("^offsets: dtype", lambda: B.gmm_forward(gp, x, w, of.long())), ("^offsets: shape", lambda: B.gmm_backward_dx(gp, dy, w, of[:2])),
+            ("^offsets: device", lambda: B.gmm_backward_dw(gp, x, dy, meta(of))), ("^offsets: shape", lambda: B.gmm8_backward_dw(g8, xq, xs, dy, of[:2])),
+            ("^W: shape", lambda: B.gmm_forward(gp, x, z(2, 8, 16), of)), ("^W must be contiguous", lambda: B.gmm_forward(gp, x, z(2, 8, 16).transpose(1, 2), of)),
+            ("^dY: shape", lambda: B.gmm_backward_dx(gp, x, w, of)), ("^W: dtype", lambda: B.gmm_backward_dx(gp, dy, w.float(), of)),
+            ("^dY: shape", lambda: B.gmm_backward_dw(gp, x, x, of)), ("^X: dtype", lambda: B.gmm_backward_dw(gp, x.float(), dy, of)),
+            ("^accumulate needs", lambda: B.gmm_backward_dw(gp, x, dy, of, accumulate=True)),
+            ("^accumulate needs", lambda: B.gmm8_backward_dw(g8, xq, xs, dy, of, accumulate=True)),
+            ("^Xq: shape", lambda: B.gmm8_forward(gp, xq, xs, wq, ws, of)), ("^Xs: shape", lambda: B.gmm8_forward(g8, xq, s8(4, 8), wq, ws, of)),
+            ("^Wq: shape", lambda: B.gmm8_forward(g8, xq, xs, q(2, 16, 128), ws, of)), ("^Ws: shape", lambda: B.gmm8_forward(g8, xq, xs, wq, s8(2, 2, 4), of)),
+            ("^Xq: dtype", lambda: B.gmm8_backward_dw(g8, z(4, 128), xs, dy, of)), ("^dY: shape", lambda: B.gmm8_backward_dw(g8, xq, xs, x, of))):
+        with pytest.raises(ValueError, match=message):
+            call()
+    # and what passes every check is refused for its device alone
+    for call in (lambda: B.rms_forward(rp, x, ga), lambda: B.rms_forward_q8(rp, x, ga, x), lambda: B.rms_backward(rp, x, ga, x, ga[:4], x),
+                 lambda: B.q8_pack(qp, x), lambda: B.q8_unpack(qp, xq, xs), lambda: B.q8_pack_weights(w), lambda: B.q8_swiglu_forward(qp, x, x),
+                 lambda: B.q8_swiglu_backward(qp, kept, x), lambda: B.gmm_forward(gp, x, w, of), lambda: B.gmm_backward_dx(gp, dy, w, of),
+                 lambda: B.gmm_backward_dw(gp, x, dy, of), lambda: B.gmm8_forward(g8, xq, xs, wq, ws, of), lambda: B.gmm8_backward_dw(g8, xq, xs, dy, of)):
+        with pytest.raises(ValueError, match="^tensors must be on a GPU, not on cpu$"):
+            call()
+
+
+def test_plans_ask_for_workspaces():
+    """The sizes that test_gmm_workspaces goes through: which of them need one, so that its refusals are reached."""
+    for name, (operands, _, _) in GMM.items():
+        kind = "bwd_workspace_bytes" if name.endswith("dw") else "fwd_workspace_bytes"
+        asked = [(R, K, E) for R in (1, 8, 64, 300, 5000) for K in (64, 2048, 16384) for E in (1, 4)
+                 if getattr(B.gmm_plan(R, K, 2048, E, operands), kind) > 0]
+        assert len(asked) >= 2, name
