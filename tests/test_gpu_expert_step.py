@@ -10,10 +10,14 @@ number (2^-10 of a scale that is at most 2^-8 of the block's largest: 2^-17 of i
 8 * 2^-4 bounds the relative 2-norm of what such roundings make of a gradient to first order; in bfloat16 at most 12
 roundings of 2^-8."""
 
+import numpy as np
 import pytest
 import torch
 
-from gpu_common import DEV, B, needs_gpu, require_lib, say
+from gpu_common import DEV, B, dev_to_f64, needs_gpu, require_lib, say
+from oracle import q8_oracle as Q
+from test_gpu_gmm import TRUNC, close
+from test_gpu_rms import check8, values8
 
 pytestmark = [pytest.mark.gpu, needs_gpu]
 
@@ -167,3 +171,135 @@ def test_a_step_on_another_stream_by_argument():
     a2 = B.gmm8_forward(s.up, xq, xs, *s.wg[:2], s.offsets)
     da2, _ = B.q8_swiglu_backward(s.rows_f, B.q8_swiglu_forward(s.rows_f, a2, a2)[2], a2)
     assert torch.equal(a, a2) and torch.equal(da, da2) and torch.equal(dw, B.gmm8_backward_dw(s.up, xq, xs, da2, s.offsets))
+
+
+U, E16 = 2.0 ** -24, 2.0 ** -8
+
+
+@pytest.mark.parametrize("eight", [True, False], ids=["8 bits", "bf16"])
+def test_step_beside_the_residual(eight):
+    """As test_step_against_autograd, of what the experts add to out and to dx, which the residual's S and dout hide there,
+    and with the roundings of a value taken as independent: of numbers spread over their logarithm one to e4m3 is off by
+    2^-4 sqrt(0.54 / 3) (uniform in its cell, 0.54 the mean of 1 / m^2), eight by 0.075, twelve to bfloat16 by 0.0057; the
+    bound is twice that, and the two roundings of the whole out, or of the whole dx.  (In fp64 a step whose dA has no
+    1 + a (1 - g) is 0.18 to 0.25 off in dx, dgamma and dWg, one without its up product's share of dx 0.69 to 0.73.)"""
+    require_lib()
+    s = Step(eight=eight)
+    out, ref = s.run(), s.reference()
+    torch.cuda.synchronize()
+    x, r, dout = (getattr(s, n).double().cpu() for n in ("x", "r", "dout"))
+    tol = 2 * (8 ** 0.5 * 2.0 ** -4 if eight else 12 ** 0.5 * E16) * (0.54 / 3) ** 0.5
+    off = {}
+    for k, v in ref.items():
+        rest = {"out": x + r, "x": dout}.get(k, torch.zeros(()))
+        part = (v - rest).norm()
+        off[k] = float((out[k].double().cpu() - v).norm() / part), tol + (2 * E16 * float(v.norm() / part) if k in ("out", "x") else 0.0)
+    say("expert step beside the residual: relative 2-norm errors", {k: "%.1e of %.1e" % v for k, v in off.items()})
+    assert all(v <= t for v, t in off.values()), off
+
+
+class Calls:
+    """Every call that the step makes, with its arguments and what it returned."""
+
+    NAMES = ("rms_forward", "rms_forward_q8", "rms_backward", "q8_pack", "q8_swiglu_forward", "q8_swiglu_backward", "gmm_forward",
+             "gmm_backward_dx", "gmm_backward_dw", "gmm8_forward", "gmm8_backward_dw")
+
+    def __init__(self, monkeypatch):
+        self.made = []
+        for name in self.NAMES:
+            monkeypatch.setattr(B, name, self.recorded(name, getattr(B, name)))
+
+    def recorded(self, name, f):
+        def call(plan, *args, **kw):
+            out = f(plan, *args, **kw)
+            self.made.append((name, plan, args, out))
+            return out
+        return call
+
+
+def weights64(q, s, cols):
+    """Values [E][rows][cols] of weights in 8 bits."""
+    e = torch.exp2(s.view(torch.uint8)[:, :, :-(-cols // 128)].double() - 127)
+    return q[:, :, :cols].double() * e.repeat_interleave(128, 1)[:, :q.shape[1]].repeat_interleave(128, 2)[:, :, :cols]
+
+
+def rows64(q, s, cols):
+    return torch.from_numpy(values8(q, s, cols)[0]).to(DEV)
+
+
+def by_row(x, w, offsets):
+    """Rows of each expert by its matrix [E][columns summed][columns], and by magnitudes."""
+    o = offsets.tolist()
+    parts = [(x[o[e]:o[e + 1]], w[e].contiguous()) for e in range(len(o) - 1)]
+    return torch.cat([a @ b for a, b in parts]), torch.cat([a.abs() @ b.abs() for a, b in parts])
+
+
+def by_matrix(x, d, offsets):
+    o = offsets.tolist()
+    parts = [(x[o[e]:o[e + 1]].T.contiguous(), d[o[e]:o[e + 1]]) for e in range(len(o) - 1)]
+    return torch.stack([a @ b for a, b in parts]), torch.stack([a.abs() @ b.abs() for a, b in parts])
+
+
+def check_call(name, plan, a, out):
+    if name in ("gmm_forward", "gmm_backward_dx"):
+        ref, size = by_row(a[0].double(), a[1].double() if name == "gmm_forward" else a[1].double().transpose(1, 2), a[2])
+        close(out, ref, size, max(plan.K, plan.N), E16, name)
+    elif name == "gmm8_forward":
+        ref, size = by_row(rows64(a[0], a[1], plan.K), weights64(a[2], a[3], plan.K).transpose(1, 2), a[4])
+        close(out, ref, size, plan.K, E16, name, TRUNC)
+    elif name in ("gmm_backward_dw", "gmm8_backward_dw"):
+        x, d, off = (a[0].double(), a[1], a[2]) if name == "gmm_backward_dw" else (rows64(a[0], a[1], plan.K), a[2], a[3])
+        ref, size = by_matrix(x, d.double(), off)
+        close(out, ref, size, plan.R, 0, name)
+    elif name in ("rms_forward", "rms_forward_q8"):
+        S, rstd = out[-2:]
+        assert torch.equal(S, (a[0].double() + a[2].double()).bfloat16())
+        y, r = Q.rms(dev_to_f64(S), dev_to_f64(a[1]), EPS)
+        off = (256 + 24) * U
+        assert np.all(np.abs(dev_to_f64(rstd) - r) <= off * r)
+        if name == "rms_forward":
+            assert np.all(np.abs(dev_to_f64(out[0]) - y) <= (off + E16) * np.abs(y))
+        else:
+            check8(out[0], out[1], y, off * np.abs(y))
+    elif name == "rms_backward":
+        S, gamma, dy, r, ds = (dev_to_f64(t) for t in a[:5])
+        dx, dg = Q.rms_backward(S, gamma, dy, r, ds)
+        xh, d = np.abs(S * r[:, None]), np.abs(dy * gamma)
+        inner = r[:, None] * (d + xh * (xh * d).mean(1, keepdims=True))
+        assert np.all(np.abs(dev_to_f64(out[0]) - dx) <= E16 * np.abs(dx) + (256 + 24) * U * (inner + np.abs(ds)))
+        assert np.all(np.abs(dev_to_f64(out[1]) - dg) <= (256 + 24) * U * (np.abs(dy) * xh).sum(0))
+    elif name == "q8_pack":
+        assert np.array_equal(values8(*out, plan.H)[0], Q.quantise(dev_to_f64(a[0]))[0])
+    elif name == "q8_swiglu_forward":
+        g, u = dev_to_f64(a[0]), dev_to_f64(a[1])
+        assert np.array_equal(values8(*out[:2], plan.H)[0], Q.quantise(Q.swiglu(g, u))[0])
+        for pair, x in ((out[2][:2], g), (out[2][2:], u)):
+            assert np.array_equal(values8(*pair, plan.H)[0], Q.quantise(x)[0])
+    elif name == "q8_swiglu_backward":
+        g, u, d = values8(*a[0][:2], plan.H)[0], values8(*a[0][2:], plan.H)[0], dev_to_f64(a[1])
+        t, terms = np.abs(g), np.abs(d * u) / (1 + np.exp(-g))
+        for x, ref, size in zip(out, Q.swiglu_backward(g, u, d), (terms * (1 + t), 0.0)):
+            assert np.all(np.abs(dev_to_f64(x) - ref) <= E16 * np.abs(ref) + (16 + 2 * t) * U * (np.abs(ref) + size))
+    else:
+        raise AssertionError(name)
+
+
+@pytest.mark.parametrize("eight", [True, False], ids=["8 bits", "bf16"])
+def test_every_call_of_the_step(eight, monkeypatch):
+    """Each call's outputs against the formula in fp64 on the values that this call was given, to the bounds of the
+    operators' own tests: a term that is left out anywhere is far outside (the mean of the norm's gradient is 0.1 of dx)."""
+    require_lib()
+    s = Step(4, eight)
+    calls = Calls(monkeypatch)
+    out = s.run()
+    torch.cuda.synchronize()
+    for c in calls.made:
+        check_call(*c)
+    names = [c[0] for c in calls.made]
+    assert len(names) == (16 if eight else 11)
+    # the sum onto the residual: fp32 sums of K terms, rounded once
+    first, y = calls.made[0], [c[3] for c in calls.made if c[0] in ("gmm8_forward", "gmm_forward")][2]
+    S, g = first[3][-2].double(), s.gates.flatten()[s.order][:, None].double()
+    terms = (y.double() * g)[s.back].view(N, K, H)
+    want, size = S + terms.sum(1), S.abs() + terms.abs().sum(1)
+    assert bool(((out["out"].double() - want).abs() <= E16 * want.abs() + 8 * U * size).all())
