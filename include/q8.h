@@ -97,7 +97,9 @@ int q8_pack_weights(int32_t E, int32_t K, int32_t N, int32_t dtype, const void* 
  * Inputs (device): A, U [N][H].
  * Outputs (device, overwritten): Hq, Hs; Aq, As, Uq, Us, each pair [N][row_pitch],
  *   [N][scale_pitch].  The four of the checkpoint may be NULL together (no
- *   backward pass).  h is formed from A and U themselves, not from the checkpoint.
+ *   backward pass).  h is formed from A and U themselves, not from the checkpoint,
+ *   and rounded to 8 bits as its 64-bit value is: in fp32, and again in 64 bits
+ *   where that lies next to a border of e4m3 or of a scale.
  * Errors: as q8_pack; MOE_EINVAL also for a part of a checkpoint.
  */
 int q8_swiglu_forward(const q8_plan_t* plan, const void* A, const void* U, void* Hq, void* Hs,

@@ -13,8 +13,8 @@
  * there on, of rows past 16,384 columns 64 bits throughout; the backward pass's sums
  * are fp32.  y and dx are rounded once.  y can come as rows of 8 bits with scales
  * (q8.h): formed in fp32, and again in 64 bits where that lies next to where e4m3 or
- * a scale turn, so that it is rounded to 8 bits as the 64-bit value is.  Every output
- * is deterministic: sums run in a fixed order, without atomics.
+ * a scale turn, so that it is rounded to 8 bits as the 64-bit value of that sum is.
+ * Every output is deterministic: sums run in a fixed order, without atomics.
  *
  * Conventions: as moebound.h (row-major contiguous device tensors, caller-
  * owned memory and workspace, no allocation or synchronisation, work enqueued

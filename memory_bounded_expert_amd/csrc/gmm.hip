@@ -51,6 +51,7 @@ int64_t tiles_of(int64_t R, int E, int N, int bm, int bn) {
 // Microseconds with one tile and the other, in bf16 forward / dX and in e4m3:
 //  * Single (dot products) for up to 4 rows in e4m3: 1 x 7168 x 2048 5.6 us in a graph
 //    (Few in parts 8.4), 4 rows 8.5 (8.8), 8 rows 13.9 (8.9); 1 x 2048 x 1408 3.0 (6.6).
+//    All of one matrix, which the rows share; not measured over several.
 //  * Few (64 x 64, four stages) where there are fewer 64 x 128 tiles than CUs, so
 //    that a step's latency counts: 64 x 4096 x 4096 17 / 15, 10 (Small 35 / 35, 13).
 //  * Tiny (16 or 32 rows) for up to 16 rows an expert: 128 x 2048 x 1408 over 64

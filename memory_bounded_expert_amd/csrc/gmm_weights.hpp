@@ -15,7 +15,8 @@
 //
 // X in 8 bits lands in LDS as it is, each lane's 16 numbers of one row with the word
 // of their scale; one step before they are read, the lane makes them bf16, which
-// holds them, and writes them to the stage.
+// holds them, and writes them to the stage.  That stands between a step's wait and its
+// barrier, with no multiplication beside it: the same experts take 290 us so for 1.04 GB.
 #pragma once
 
 #include "gmm_common.hpp"
