@@ -184,8 +184,8 @@ def test_fp32_swiglu_is_rounded_once():
 
 
 def all_classes():
-    """a [N][1] and u [1][128] of every bfloat16 mantissa: a of both signs with 2^-9 <= |a| < 2^6, u in [1, 2)."""
-    a = (torch.arange(118 << 7, 133 << 7, dtype=torch.int32) << 16).view(torch.float32)
+    """a [N][1] and u [1][128] of every bfloat16 mantissa: a of both signs with 2^-9 <= |a| < 2^7, u in [1, 2)."""
+    a = (torch.arange(118 << 7, 134 << 7, dtype=torch.int32) << 16).view(torch.float32)
     u = (((127 << 7) | torch.arange(128, dtype=torch.int32)) << 16).view(torch.float32)
     return torch.cat([a, -a])[:, None], u[None]
 
@@ -196,9 +196,9 @@ def test_swiglu_of_every_mantissa_is_rounded_once(dtype):
     a u, which may be a tie, stands for an h below it; for other a the 32-bit h is off by its exponential's argument.  All
     numbers and scales are those of the fp64 h."""
     require_lib()
-    a, u = (t.expand(3840, 128).contiguous().to(TYPES[dtype][0]).to(DEV) for t in all_classes())
+    a, u = (t.expand(4096, 128).contiguous().to(TYPES[dtype][0]).to(DEV) for t in all_classes())
     for x, y in ((a, u), (a, -u * 2.0 ** -20), (a[:, :1].expand(-1, 128).contiguous(), u[:, :1] * torch.exp2(torch.arange(128.0, device=DEV) - 64).to(u.dtype))):
-        hq, hs, _ = B.q8_swiglu_forward(B.q8_plan(3840, 128, B.moe_dtype(a.dtype)), x, y.contiguous())
+        hq, hs, _ = B.q8_swiglu_forward(B.q8_plan(4096, 128, B.moe_dtype(a.dtype)), x, y.contiguous())
         want, e = Q.quantise(Q.swiglu(dev_to_f64(x), dev_to_f64(y)))
         got, _, ge = values8(hq, hs, 128)
         assert int((got != want).sum()) == 0 and np.array_equal(ge, e)
