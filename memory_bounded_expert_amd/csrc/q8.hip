@@ -194,7 +194,7 @@ __device__ __forceinline__ bool unsure(float h, float a, bf16_t) {
 __device__ __forceinline__ bool unsure(float h, float, float) { return q8_border(h); }
 // h for 8 bits.  (32,768 x 1536 fp32: all numbers are those of 64 bits; all in 32 bits 29 to
 // 41 are not.  Of the 491,520 pairs of bf16 mantissas with 2^-9 <= |a| < 2^6 11 are not.
-// 131,072 x 1536 bf16 take as long either way, 779 x 1000 4.9 us for 4.3.)
+// 131,072 x 1536 bf16 take as long either way, 779 x 1000 5.1 us for 4.3.)
 template <typename T>
 __device__ __forceinline__ void swiglu_for8(const float* a, const float* u, float* h) {
   bool again = false;
